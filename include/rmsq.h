@@ -35,7 +35,11 @@
  * unfused two-op sequence the fusion replaces (rmsq_fused_add_rmsnorm,
  * rmsq_quant); and QK-norm + RoPE on the attention input
  * (rmsq_qk_norm_rope, the docs page's "QK Norm + RoPE
- * (enable_qk_norm_rope_fusion)").
+ * (enable_qk_norm_rope_fusion)").  Around that input it has the serving
+ * operators of an attention block: slot maps from request lengths
+ * (rmsq_build_slot_map), a paged key / value cache in NVFP4
+ * (rmsq_kv_cache_store_nvfp4, rmsq_kv_cache_load_nvfp4) and causal attention
+ * over it (rmsq_paged_attention_nvfp4).
  *
  * Conventions for every entry point:
  *   - Pointers marked "device" must be addressable by the current CUDA device
@@ -325,6 +329,137 @@ int rmsq_qk_norm_rope_ex(void *qkv, const int64_t *positions, const float *cos_s
                          int64_t max_positions, const void *q_weight, const void *k_weight, float eps,
                          int64_t n_tokens, int num_q_heads, int num_kv_heads, int head_dim, int is_neox,
                          int dtype, void *stream, int variant);
+
+/* Most requests of rmsq_build_slot_map and rmsq_paged_attention_nvfp4. */
+#define RMSQ_MAX_REQUESTS 8192
+
+/* Bits of rmsq_build_slot_map's status. */
+#define RMSQ_SLOT_NO_PAGES 1         /* the free list is shorter than the pages needed */
+#define RMSQ_SLOT_TABLE_FULL 2       /* a request needs more than table_width pages */
+#define RMSQ_SLOT_TOO_MANY_TOKENS 4  /* the query lengths add up to more than max_tokens */
+#define RMSQ_SLOT_BAD_LENGTH 8       /* a negative length, or num_free outside [0, free_capacity] */
+
+/*
+ * rmsq_build_slot_map — block tables and slot map of one step, from the
+ * requests' lengths, on the device (no length has to be known to the host, so
+ * a captured graph can be replayed for every step).  Request r has
+ * context_lens[r] tokens in the cache and brings query_lens[r] new ones.
+ * Pages are taken from the end of the free list, in request order, and
+ * appended to the request's row of the block table; token i of request r gets
+ *   position = context_lens[r] + i,
+ *   slot     = block_table[r, position / page_size] * page_size + position % page_size
+ * (slot -1 where the table holds a negative page).
+ *  context_lens, query_lens  device, int32[num_requests].
+ *  block_table   device, int32[num_requests, table_width], updated in place:
+ *                only the entries of the new pages are written.
+ *  free_pages    device, int32[free_capacity]; the first num_free[0] are free.
+ *  num_free      device, int32[1].
+ *  page_size     16, 32, 64, 128 or 256 tokens.
+ *  slot_map, positions  device, int64[max_tokens]: tokens in request order;
+ *                entries behind the last token are -1 (the store skips such a
+ *                slot, rmsq_qk_norm_rope such a position).
+ *  query_start   device, int32[num_requests + 1]: first token of each request,
+ *                and their number.
+ *  seq_lens      device, int32[num_requests]: context + query length.
+ *  num_free_out  device, int32[1]: pages still free (the next call's num_free).
+ *  status        device, int32[1]: 0, or RMSQ_SLOT_* bits.  Then nothing was
+ *                assigned: every slot and position is -1, query_start 0,
+ *                seq_lens the context lengths, num_free_out num_free, the
+ *                table unchanged.
+ * int32 buffers 4-byte, int64 buffers 8-byte aligned.  num_requests at most
+ * RMSQ_MAX_REQUESTS, max_tokens below 2^30; 0 requests are allowed.  No output
+ * may overlap an input or another output.  Asynchronous on `stream`.
+ */
+int rmsq_build_slot_map(const int32_t *context_lens, const int32_t *query_lens, int32_t *block_table,
+                        int64_t table_width, const int32_t *free_pages, int64_t free_capacity,
+                        const int32_t *num_free, int64_t page_size, int64_t num_requests, int64_t max_tokens,
+                        int64_t *slot_map, int64_t *positions, int32_t *query_start, int32_t *seq_lens,
+                        int32_t *num_free_out, int32_t *status, void *stream);
+
+/*
+ * The paged NVFP4 cache: device, u8 [num_pages, 2, num_kv_heads, tile],
+ * 16-byte aligned, with keys at index 0 and values at index 1 of the second
+ * axis and tiles of page_size * head_dim * 9 / 16 bytes: first the codes
+ * [page_size, head_dim / 2] (E2M1, element 2j in the low nibble of byte j),
+ * then the E4M3 scales of the 16-element blocks [page_size, head_dim / 16].
+ * Slot s is token s % page_size of page s / page_size.  An element stands for
+ * code * scale / global scale; a scale byte's sign is ignored and its NaN code
+ * counts as 0.
+ *
+ * rmsq_kv_cache_store_nvfp4 — quantises the key and value heads of n_tokens
+ * tokens into the cache, bit for bit as RMSQ_NVFP4 does (rmsq_quant).
+ * rmsq_kv_cache_load_nvfp4 — reads tokens back: T((code * scale) / global
+ * scale), one fp32 division, rounded once to T.
+ *  k, v          device, T[n_tokens, num_kv_heads, head_dim], heads contiguous,
+ *                tokens k_stride / v_stride elements apart (so k and v may be
+ *                column ranges of a qkv buffer); 16-byte aligned, strides
+ *                multiples of 8, at least num_kv_heads * head_dim.
+ *  slot_map      device, int64[n_tokens].  A token whose slot lies outside
+ *                [0, num_pages * page_size) is skipped by the store and read
+ *                as zeros by the load.  The store's slots must differ: of two
+ *                tokens with one slot either may be kept, block by block.
+ *  k_global_scale, v_global_scale  device, one fp32 each, finite and > 0
+ *                (not checked): 448 * 6 / the largest magnitude expected.
+ *  head_dim      64, 128 or 256; page_size 16, 32, 64, 128 or 256.
+ *  n_tokens      >= 0 (0 returns RMSQ_OK without a launch).
+ * No output may overlap an input; the load's k and v rows may interleave in
+ * one buffer.  Asynchronous on `stream`.
+ */
+int rmsq_kv_cache_store_nvfp4(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                              const int64_t *slot_map, const float *k_global_scale, const float *v_global_scale,
+                              void *kv_cache, int64_t num_pages, int64_t page_size, int64_t n_tokens,
+                              int num_kv_heads, int head_dim, int dtype, void *stream);
+int rmsq_kv_cache_load_nvfp4(const void *kv_cache, int64_t num_pages, int64_t page_size, const int64_t *slot_map,
+                             const float *k_global_scale, const float *v_global_scale, void *k, int64_t k_stride,
+                             void *v, int64_t v_stride, int64_t n_tokens, int num_kv_heads, int head_dim, int dtype,
+                             void *stream);
+
+/*
+ * rmsq_paged_attention_nvfp4 — causal attention of ragged queries over the
+ * paged NVFP4 cache, grouped query heads (num_heads a multiple of
+ * num_kv_heads: query head h reads kv head h / (num_heads / num_kv_heads)).
+ * Request r has the query tokens query_start[r] .. query_start[r+1] - 1, the
+ * last of them at position seq_lens[r] - 1; their keys must be in the cache
+ * already.  Query token i of request r, at position p = seq_lens[r] -
+ * query_len + i, attends keys 0 .. p, with window > 0 only the last `window`
+ * of them (p included):
+ *   out = sum_j softmax_j(softmax_scale * q.k_j) v_j,
+ *   lse = ln sum_j exp(softmax_scale * q.k_j).
+ * A query that sees no key (an empty request, p < 0) gets zeros and -inf.
+ * A key on a page outside [0, num_pages) is left out.
+ *  q             device, T[n_tokens, num_heads, head_dim], tokens q_stride
+ *                elements apart (a multiple of 8), 16-byte aligned.
+ *  kv_cache, num_pages, page_size, head_dim, global scales: as above.
+ *  block_table   device, int32[num_requests, table_width]; page of key j of
+ *                request r: block_table[r, j / page_size].
+ *  query_start   device, int32[num_requests + 1], ascending from 0;
+ *  seq_lens      device, int32[num_requests].  Values outside the buffers
+ *                (rows beyond n_tokens, lengths beyond the table) are clamped.
+ *  softmax_scale finite, > 0.   window >= 0, 0 for none.
+ *  out           device, T[n_tokens, num_heads, head_dim], 16-byte aligned;
+ *                rows behind query_start[num_requests] are left as they were.
+ *  lse           device, fp32[n_tokens, num_heads], or NULL.
+ *  workspace     device, 16-byte aligned, at least
+ *                rmsq_paged_attention_workspace_bytes(...) bytes of scratch;
+ *                contents on entry do not matter.  Two calls in flight at the
+ *                same time must not share one.
+ * Sums, maxima and the log-sum-exp are fp32; probabilities are rounded to f16
+ * before they meet the values.  Results are deterministic.  n_tokens *
+ * num_heads below 2^31; 0 tokens or requests return RMSQ_OK without a launch.
+ * No output may overlap an input.  Asynchronous on `stream`.
+ */
+int rmsq_paged_attention_nvfp4(const void *q, int64_t q_stride, const void *kv_cache, int64_t num_pages,
+                               int64_t page_size, const int32_t *block_table, int64_t table_width,
+                               const int32_t *query_start, const int32_t *seq_lens, const float *k_global_scale,
+                               const float *v_global_scale, float softmax_scale, int64_t window, void *out,
+                               float *lse, void *workspace, size_t workspace_bytes, int64_t n_tokens,
+                               int64_t num_requests, int num_heads, int num_kv_heads, int head_dim, int dtype,
+                               void *stream);
+
+/* Bytes of workspace rmsq_paged_attention_nvfp4 needs (0 for arguments it
+ * refuses). */
+size_t rmsq_paged_attention_workspace_bytes(int64_t n_tokens, int64_t num_requests, int num_heads,
+                                            int num_kv_heads, int head_dim);
 
 /* Most ranks rmsq_allreduce_add_rmsnorm_quant sums. */
 #define RMSQ_MAX_ALLREDUCE_RANKS 8

@@ -61,6 +61,8 @@ EXPORTS = ("rmsq_fused_add_rmsnorm_quant", "rmsq_fused_add_rmsnorm_quant_ex",
            "rmsq_fused_add_rmsnorm_nvfp4_dynamic_noalloc", "rmsq_silu_mul_quant",
            "rmsq_fused_add_rmsnorm", "rmsq_quant", "rmsq_qk_norm_rope", "rmsq_qk_norm_rope_ex",
            "rmsq_allreduce_add_rmsnorm_quant",
+           "rmsq_build_slot_map", "rmsq_kv_cache_store_nvfp4", "rmsq_kv_cache_load_nvfp4",
+           "rmsq_paged_attention_nvfp4", "rmsq_paged_attention_workspace_bytes",
            "rmsq_set_pipeline_config", "rmsq_set_programmatic_launch", "rmsq_take_fault_flags",
            "rmsq_query_sizes", "rmsq_query_launch", "rmsq_debug_convert", "rmsq_debug_activation", "rmsq_debug_bounded_wait",
            "rmsq_status_string", "rmsq_last_cuda_error", "rmsq_version")
@@ -109,6 +111,17 @@ def load(path: str | None = None):
         L.rmsq_allreduce_add_rmsnorm_quant.argtypes = [ctypes.POINTER(vp), ci, vp, vp, f32, ci, vp, vp, vp, vp,
                                                        i64, i64, ci, vp]
         L.rmsq_allreduce_add_rmsnorm_quant.restype = ci
+        L.rmsq_build_slot_map.argtypes = [vp, vp, vp, i64, vp, i64, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp]
+        L.rmsq_build_slot_map.restype = ci
+        L.rmsq_kv_cache_store_nvfp4.argtypes = [vp, i64, vp, i64, vp, vp, vp, vp, i64, i64, i64, ci, ci, ci, vp]
+        L.rmsq_kv_cache_store_nvfp4.restype = ci
+        L.rmsq_kv_cache_load_nvfp4.argtypes = [vp, i64, i64, vp, vp, vp, vp, i64, vp, i64, i64, ci, ci, ci, vp]
+        L.rmsq_kv_cache_load_nvfp4.restype = ci
+        L.rmsq_paged_attention_nvfp4.argtypes = [vp, i64, vp, i64, i64, vp, i64, vp, vp, vp, vp, f32, i64, vp, vp, vp,
+                                                 ctypes.c_size_t, i64, i64, ci, ci, ci, ci, vp]
+        L.rmsq_paged_attention_nvfp4.restype = ci
+        L.rmsq_paged_attention_workspace_bytes.argtypes = [i64, i64, ci, ci, ci]
+        L.rmsq_paged_attention_workspace_bytes.restype = ctypes.c_size_t
         L.rmsq_quant.argtypes = [vp, ci, vp, vp, vp, i64, i64, ci, vp]
         L.rmsq_quant.restype = ci
         L.rmsq_silu_mul_quant.argtypes = [vp, ci, vp, vp, vp, i64, i64, ci, vp]
@@ -340,6 +353,233 @@ def qk_norm_rope(qkv: torch.Tensor, positions: torch.Tensor, cos_sin_cache: torc
     if st:
         raise RmsqError(st, "rmsq_qk_norm_rope_ex")
     return qkv
+
+
+def _check_tensors(named, dtypes) -> None:
+    """Every tensor of `named` (name -> tensor) on one device, the current one
+    if it is a CUDA device, and of the type `dtypes` says for its name."""
+    device = None
+    for name, t in named.items():
+        if t is None:
+            continue
+        if t.dtype != dtypes[name]:
+            raise TypeError(f"{name} must be {dtypes[name]}, got {t.dtype}")
+        if device is None:
+            device = t.device
+            if device.type == "cuda":
+                if device.index != torch.cuda.current_device():
+                    raise ValueError(f"{name} is on {device}, not on the current device")
+            elif torch.cuda.is_available():
+                raise ValueError(f"{name} must be a CUDA tensor")
+        elif t.device != device:
+            raise ValueError(f"{name} is on {t.device}, the others on {device}")
+
+
+def _want_shape(name: str, t: torch.Tensor, *shape) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _token_rows(name: str, t: torch.Tensor) -> int:
+    """The token stride of a [n, heads, D] tensor whose heads are contiguous."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
+    n, h, d = t.shape
+    if (t.stride(2) != 1 and d > 1) or (t.stride(1) != d and h > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(0) if n > 1 else h * d
+
+
+_I32, _I64, _F32, _U8 = torch.int32, torch.int64, torch.float32, torch.uint8
+_SLOT_TYPES = {"context_lens": _I32, "query_lens": _I32, "block_table": _I32, "free_pages": _I32, "num_free": _I32,
+               "slot_map": _I64, "positions": _I64, "query_start": _I32, "seq_lens": _I32, "num_free_out": _I32,
+               "status": _I32}
+SLOT_NO_PAGES, SLOT_TABLE_FULL, SLOT_TOO_MANY_TOKENS, SLOT_BAD_LENGTH = 1, 2, 4, 8
+MAX_REQUESTS = 8192
+
+
+def build_slot_map(context_lens: torch.Tensor, query_lens: torch.Tensor, block_table: torch.Tensor,
+                   free_pages: torch.Tensor, num_free: torch.Tensor, page_size: int, max_tokens: int, *,
+                   slot_map: torch.Tensor | None = None, positions: torch.Tensor | None = None,
+                   query_start: torch.Tensor | None = None, seq_lens: torch.Tensor | None = None,
+                   num_free_out: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None):
+    """rmsq_build_slot_map: pages, slots and positions of a step's new tokens.
+
+    context_lens, query_lens: int32 [R]; block_table: int32 [R, width], updated
+    in place; free_pages: int32 [capacity]; num_free: int32 [1].  Missing
+    outputs are allocated.  Returns (slot_map [max_tokens], positions
+    [max_tokens], query_start [R + 1], seq_lens [R], num_free_out [1],
+    status [1]); status holds SLOT_* bits, 0 when the pages were assigned.
+    """
+    L = load()
+    R, width = block_table.shape
+    dev = block_table.device
+    given = {"context_lens": context_lens, "query_lens": query_lens, "block_table": block_table,
+             "free_pages": free_pages, "num_free": num_free, "slot_map": slot_map, "positions": positions,
+             "query_start": query_start, "seq_lens": seq_lens, "num_free_out": num_free_out, "status": status}
+    _check_tensors(given, _SLOT_TYPES)
+    if max_tokens < 0:
+        raise ValueError("max_tokens must be >= 0")
+    sizes = {"context_lens": (R,), "query_lens": (R,), "block_table": (R, width), "free_pages": (free_pages.numel(),),
+             "num_free": (1,), "slot_map": (max_tokens,), "positions": (max_tokens,), "query_start": (R + 1,),
+             "seq_lens": (R,), "num_free_out": (1,), "status": (1,)}
+    for name, t in given.items():
+        if t is not None:
+            _want_shape(name, t, *sizes[name])
+    if slot_map is None:
+        slot_map = torch.empty(max_tokens, dtype=_I64, device=dev)
+    if positions is None:
+        positions = torch.empty(max_tokens, dtype=_I64, device=dev)
+    if query_start is None:
+        query_start = torch.empty(R + 1, dtype=_I32, device=dev)
+    if seq_lens is None:
+        seq_lens = torch.empty(R, dtype=_I32, device=dev)
+    if num_free_out is None:
+        num_free_out = torch.empty(1, dtype=_I32, device=dev)
+    if status is None:
+        status = torch.empty(1, dtype=_I32, device=dev)
+    st = L.rmsq_build_slot_map(_p(context_lens), _p(query_lens), _p(block_table), width, _p(free_pages),
+                               free_pages.numel(), _p(num_free), page_size, R, max_tokens, _p(slot_map), _p(positions),
+                               _p(query_start), _p(seq_lens), _p(num_free_out), _p(status), _stream(stream))
+    if st:
+        raise RmsqError(st, "rmsq_build_slot_map")
+    return slot_map, positions, query_start, seq_lens, num_free_out, status
+
+
+def kv_cache_shape(num_pages: int, num_kv_heads: int, head_dim: int, page_size: int) -> tuple[int, int, int, int]:
+    """Shape of the uint8 tensor that holds a paged NVFP4 cache."""
+    return num_pages, 2, num_kv_heads, page_size * head_dim * 9 // 16
+
+
+def _check_cache(cache: torch.Tensor, num_kv_heads: int, head_dim: int, page_size: int) -> int:
+    _want_shape("cache", cache, *kv_cache_shape(cache.shape[0], num_kv_heads, head_dim, page_size))
+    return cache.shape[0]
+
+
+def _act_types(t: torch.Tensor) -> torch.dtype:
+    if t.dtype not in DTYPES:
+        raise TypeError(f"unsupported activation dtype {t.dtype}")
+    return t.dtype
+
+
+def kv_cache_store_nvfp4(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, k_global_scale: torch.Tensor,
+                         v_global_scale: torch.Tensor, cache: torch.Tensor, page_size: int, *, stream=None) -> None:
+    """rmsq_kv_cache_store_nvfp4: k, v [n, kv heads, D] (token stride free, so
+    slices of a qkv buffer serve) quantised into `cache` (kv_cache_shape) at
+    slot_map (int64 [n]); a slot outside the cache skips its token.  The global
+    scales are one-element fp32 tensors."""
+    L = load()
+    dt = _act_types(k)
+    ks, vs = _token_rows("k", k), _token_rows("v", v)
+    n, h, d = k.shape
+    if v.shape != k.shape:
+        raise ValueError("k and v must have one shape")
+    _check_tensors({"k": k, "v": v, "slot_map": slot_map, "k_global_scale": k_global_scale,
+                    "v_global_scale": v_global_scale, "cache": cache},
+                   {"k": dt, "v": dt, "slot_map": _I64, "k_global_scale": _F32, "v_global_scale": _F32, "cache": _U8})
+    _want_shape("slot_map", slot_map, n)
+    pages = _check_cache(cache, h, d, page_size)
+    if k_global_scale.numel() != 1 or v_global_scale.numel() != 1:
+        raise ValueError("a global scale is one element")
+    st = L.rmsq_kv_cache_store_nvfp4(_p(k), ks, _p(v), vs, _p(slot_map), _p(k_global_scale), _p(v_global_scale),
+                                     _p(cache), pages, page_size, n, h, d, DTYPES[dt], _stream(stream))
+    if st:
+        raise RmsqError(st, "rmsq_kv_cache_store_nvfp4")
+
+
+def kv_cache_load_nvfp4(cache: torch.Tensor, slot_map: torch.Tensor, k_global_scale: torch.Tensor,
+                        v_global_scale: torch.Tensor, head_dim: int, page_size: int, dtype: torch.dtype = torch.bfloat16, *,
+                        k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None, stream=None):
+    """rmsq_kv_cache_load_nvfp4: the tokens at slot_map (int64 [n]) as two
+    [n, kv heads, D] tensors of `dtype`; zeros for a slot outside the cache.
+    Missing outputs are allocated.  Returns (k, v)."""
+    L = load()
+    if dtype not in DTYPES:
+        raise TypeError(f"unsupported activation dtype {dtype}")
+    if cache.dim() != 4:
+        raise ValueError("cache must be [pages, 2, kv heads, bytes of a tile]")
+    n, h = slot_map.shape[0], cache.shape[2]
+    _check_tensors({"cache": cache, "slot_map": slot_map, "k_global_scale": k_global_scale,
+                    "v_global_scale": v_global_scale, "k_out": k_out, "v_out": v_out},
+                   {"cache": _U8, "slot_map": _I64, "k_global_scale": _F32, "v_global_scale": _F32, "k_out": dtype,
+                    "v_out": dtype})
+    _want_shape("slot_map", slot_map, n)
+    pages = _check_cache(cache, h, head_dim, page_size)
+    if k_global_scale.numel() != 1 or v_global_scale.numel() != 1:
+        raise ValueError("a global scale is one element")
+    if k_out is None:
+        k_out = torch.empty(n, h, head_dim, dtype=dtype, device=cache.device)
+    if v_out is None:
+        v_out = torch.empty(n, h, head_dim, dtype=dtype, device=cache.device)
+    ks, vs = _token_rows("k_out", k_out), _token_rows("v_out", v_out)
+    if tuple(k_out.shape) != (n, h, head_dim) or tuple(v_out.shape) != (n, h, head_dim):
+        raise ValueError(f"outputs must have shape {(n, h, head_dim)}")
+    st = L.rmsq_kv_cache_load_nvfp4(_p(cache), pages, page_size, _p(slot_map), _p(k_global_scale), _p(v_global_scale),
+                                    _p(k_out), ks, _p(v_out), vs, n, h, head_dim, DTYPES[dtype], _stream(stream))
+    if st:
+        raise RmsqError(st, "rmsq_kv_cache_load_nvfp4")
+    return k_out, v_out
+
+
+def paged_attention_workspace_bytes(n_tokens: int, num_requests: int, num_heads: int, num_kv_heads: int,
+                                    head_dim: int) -> int:
+    return load().rmsq_paged_attention_workspace_bytes(n_tokens, num_requests, num_heads, num_kv_heads, head_dim)
+
+
+def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Tensor, query_start: torch.Tensor,
+                          seq_lens: torch.Tensor, k_global_scale: torch.Tensor, v_global_scale: torch.Tensor,
+                          page_size: int, softmax_scale: float | None = None, *, window: int = 0,
+                          return_lse: bool = False, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None):
+    """rmsq_paged_attention_nvfp4: causal attention of q [tokens, heads, D]
+    (token stride free) over the paged NVFP4 cache.
+
+    block_table: int32 [R, width]; query_start: int32 [R + 1]; seq_lens: int32
+    [R], the lengths with this step's tokens, which are in the cache already.
+    softmax_scale: 1 / sqrt(D) by default; window > 0 limits a query to its
+    last `window` keys.  Missing outputs and the workspace are allocated (rows
+    of q behind query_start[R] are not computed).  Returns out [tokens, heads,
+    D], or (out, lse [tokens, heads] fp32) with return_lse or a given lse.
+    """
+    L = load()
+    dt = _act_types(q)
+    qs = _token_rows("q", q)
+    n, heads, d = q.shape
+    if cache.dim() != 4 or block_table.dim() != 2:
+        raise ValueError("cache must be [pages, 2, kv heads, bytes of a tile], block_table [requests, width]")
+    kv, (R, width) = cache.shape[2], block_table.shape
+    if out is None:
+        out = torch.empty(n, heads, d, dtype=dt, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty(n, heads, dtype=_F32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(paged_attention_workspace_bytes(n, R, heads, kv, d), dtype=_U8, device=q.device)
+    _check_tensors({"q": q, "cache": cache, "block_table": block_table, "query_start": query_start,
+                    "seq_lens": seq_lens, "k_global_scale": k_global_scale, "v_global_scale": v_global_scale,
+                    "out": out, "lse": lse, "workspace": workspace},
+                   {"q": dt, "cache": _U8, "block_table": _I32, "query_start": _I32, "seq_lens": _I32,
+                    "k_global_scale": _F32, "v_global_scale": _F32, "out": dt, "lse": _F32, "workspace": _U8})
+    pages = _check_cache(cache, kv, d, page_size)
+    _want_shape("block_table", block_table, R, width)
+    _want_shape("query_start", query_start, R + 1)
+    _want_shape("seq_lens", seq_lens, R)
+    _want_shape("out", out, n, heads, d)
+    if lse is not None:
+        _want_shape("lse", lse, n, heads)
+    _want_shape("workspace", workspace, workspace.numel())
+    if k_global_scale.numel() != 1 or v_global_scale.numel() != 1:
+        raise ValueError("a global scale is one element")
+    if softmax_scale is None:
+        softmax_scale = d ** -0.5
+    st = L.rmsq_paged_attention_nvfp4(_p(q), qs, _p(cache), pages, page_size, _p(block_table), width, _p(query_start),
+                                      _p(seq_lens), _p(k_global_scale), _p(v_global_scale), softmax_scale, window, _p(out),
+                                      _p(lse), _p(workspace), workspace.numel(), n, R, heads, kv, d, DTYPES[dt],
+                                      _stream(stream))
+    if st:
+        raise RmsqError(st, "rmsq_paged_attention_nvfp4")
+    return out if lse is None else (out, lse)
 
 
 def silu_mul_quant(gate_up: torch.Tensor, mode: str, scale_in: torch.Tensor | None = None, *,

@@ -122,18 +122,10 @@ void sizes_of(int quant_mode, int64_t n, int64_t hidden, size_t* q, size_t* sc) 
     }
 }
 
-struct Span {
-    uintptr_t lo, hi;   // [lo, hi); empty when lo == hi
-};
-
-Span span(const void* p, size_t bytes) {
-    const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-    return {a, p ? a + bytes : a};
-}
-
-bool overlaps(Span a, Span b) { return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi; }
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+using rmsq_abi::aligned;
+using rmsq_abi::overlaps;
+using rmsq_abi::Span;
+using rmsq_abi::span;
 
 std::atomic<int> g_tune_j{0}, g_tune_stages{0}, g_tune_cps{0}, g_tune_rows{0};
 std::atomic<bool> g_pdl{true};

@@ -1,0 +1,162 @@
+// Attention over the paged NVFP4 cache: argument checks and launches.
+#include <cmath>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "rmsq.h"
+#include "rmsq_abi.h"
+#include "rmsq_attn.cuh"
+#include "rmsq_host.cuh"
+
+namespace rmsq {
+namespace {
+
+// Row blocks of 8: two (16 rows share a pass over the keys) where a request
+// has more than 8 rows on average; one for D = 256, whose accumulators for 16
+// rows would not fit the registers.
+int row_blocks(int64_t tokens, int64_t requests, int group, int head_dim) {
+    return head_dim <= 128 && tokens * group > 8 * requests ? 2 : 1;
+}
+
+size_t part_floats(int head_dim, int nb) { return static_cast<size_t>(8) * nb * (head_dim + 2); }
+
+template <class E, int D, int NB>
+cudaError_t launch_split(AttnArgs a, int64_t max_tiles, cudaStream_t stream) {
+    cudaError_t e;
+    const int sms = sm_count(&e);
+    if (e != cudaSuccess) return e;
+    const void* split = (const void*)&attn_split_kernel<E, D, NB>;
+    const void* join = (const void*)&attn_join_kernel<E, D, NB>;
+    const int smem = (a.requests + 1) * 8;
+    if (smem > 12 * 1024) {   // beyond what the default 48 KB leave beside the static part
+        const int most = (RMSQ_MAX_REQUESTS + 1) * 8;
+        e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        if (e != cudaSuccess) return e;
+    }
+    int per_sm = 0;
+    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, split, kAttnThreads, smem);
+    if (e != cudaSuccess) return e;
+    if (per_sm < 1) return cudaErrorInvalidConfiguration;
+    int64_t workers = static_cast<int64_t>(per_sm) * sms;
+    if (workers > kAttnMaxWorkers) workers = kAttnMaxWorkers;
+    if (workers > max_tiles) workers = max_tiles;
+    a.workers = static_cast<int>(workers);
+    void* params[] = {&a};
+    e = launch_kernel(split, dim3(a.workers), dim3(kAttnThreads), params, smem, stream);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(join, dim3(a.workers), dim3(kAttnThreads), params, smem, stream);
+}
+
+template <class E>
+cudaError_t launch_attn(const AttnArgs& a, int head_dim, int64_t max_tiles, cudaStream_t stream) {
+    const int nb = row_blocks(a.tokens, a.requests, a.group, head_dim);
+    switch (head_dim) {
+    case 64: return nb == 2 ? launch_split<E, 64, 2>(a, max_tiles, stream) : launch_split<E, 64, 1>(a, max_tiles, stream);
+    case 128: return nb == 2 ? launch_split<E, 128, 2>(a, max_tiles, stream) : launch_split<E, 128, 1>(a, max_tiles, stream);
+    default: return launch_split<E, 256, 1>(a, max_tiles, stream);
+    }
+}
+
+int attn_shape(int64_t tokens, int64_t requests, int heads, int kv_heads, int head_dim) {
+    if (tokens < 0 || requests < 0 || heads <= 0 || kv_heads <= 0) return RMSQ_ERR_INVALID_ARG;
+    if (heads % kv_heads != 0 || heads > 4096 || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+        requests > RMSQ_MAX_REQUESTS || tokens * heads > INT32_MAX)
+        return RMSQ_ERR_UNSUPPORTED_SHAPE;
+    return RMSQ_OK;
+}
+
+}  // namespace
+}  // namespace rmsq
+
+extern "C" {
+
+size_t rmsq_paged_attention_workspace_bytes(int64_t n_tokens, int64_t num_requests, int num_heads, int num_kv_heads,
+                                            int head_dim) {
+    if (rmsq::attn_shape(n_tokens, num_requests, num_heads, num_kv_heads, head_dim) != RMSQ_OK) return 0;
+    const int nb = rmsq::row_blocks(n_tokens, num_requests, num_heads / num_kv_heads, head_dim);
+    return static_cast<size_t>(rmsq::kAttnMaxWorkers) * 2 * rmsq::part_floats(head_dim, nb) * 4;
+}
+
+int rmsq_paged_attention_nvfp4(const void* q, int64_t q_stride, const void* kv_cache, int64_t num_pages, int64_t page_size,
+                               const int32_t* block_table, int64_t table_width, const int32_t* query_start,
+                               const int32_t* seq_lens, const float* k_global_scale, const float* v_global_scale,
+                               float softmax_scale, int64_t window, void* out, float* lse, void* workspace,
+                               size_t workspace_bytes, int64_t n_tokens, int64_t num_requests, int num_heads,
+                               int num_kv_heads, int head_dim, int dtype, void* stream) {
+    using rmsq_abi::aligned;
+    using rmsq_abi::overlaps;
+    using rmsq_abi::Span;
+    using rmsq_abi::span;
+    if (dtype != RMSQ_BF16 && dtype != RMSQ_FP16) return RMSQ_ERR_INVALID_ARG;
+    int st = rmsq::attn_shape(n_tokens, num_requests, num_heads, num_kv_heads, head_dim);
+    if (st != RMSQ_OK) return st;
+    if (!std::isfinite(softmax_scale) || softmax_scale <= 0.0f || window < 0 || num_pages < 0 || table_width < 0)
+        return RMSQ_ERR_INVALID_ARG;
+    int shift = -1;
+    for (int s = 4; s <= 8; ++s)
+        if (page_size == (1 << s)) shift = s;
+    if (shift < 0 || num_pages > INT32_MAX || table_width > (INT32_MAX >> (shift + 1))) return RMSQ_ERR_UNSUPPORTED_SHAPE;
+    const int64_t row = static_cast<int64_t>(num_heads) * head_dim;
+    if (q_stride < row || q_stride > INT32_MAX) return RMSQ_ERR_INVALID_ARG;
+    if (n_tokens == 0 || num_requests == 0) return RMSQ_OK;
+    if (!q || !query_start || !seq_lens || !k_global_scale || !v_global_scale || !out || !workspace ||
+        (num_pages > 0 && !kv_cache) || (table_width > 0 && !block_table))
+        return RMSQ_ERR_INVALID_ARG;
+    const size_t need = rmsq_paged_attention_workspace_bytes(n_tokens, num_requests, num_heads, num_kv_heads, head_dim);
+    if (workspace_bytes < need) return RMSQ_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || q_stride % 8 || !aligned(kv_cache, 16) || !aligned(block_table, 4) || !aligned(query_start, 4) ||
+        !aligned(seq_lens, 4) || !aligned(k_global_scale, 4) || !aligned(v_global_scale, 4) || !aligned(out, 16) ||
+        !aligned(lse, 4) || !aligned(workspace, 16))
+        return RMSQ_ERR_ALIGNMENT;
+    const size_t tile = static_cast<size_t>(head_dim) * 9 / 16 << shift;
+    const Span ins[7] = {span(q, (static_cast<size_t>(n_tokens - 1) * q_stride + row) * 2),
+                         span(kv_cache, static_cast<size_t>(num_pages) * 2 * num_kv_heads * tile),
+                         span(block_table, static_cast<size_t>(num_requests) * table_width * 4),
+                         span(query_start, static_cast<size_t>(num_requests + 1) * 4),
+                         span(seq_lens, static_cast<size_t>(num_requests) * 4), span(k_global_scale, 4),
+                         span(v_global_scale, 4)};
+    const Span outs[3] = {span(out, static_cast<size_t>(n_tokens) * row * 2),
+                          span(lse, static_cast<size_t>(n_tokens) * num_heads * 4), span(workspace, need)};
+    for (int i = 0; i < 3; ++i) {
+        for (const Span& in : ins)
+            if (overlaps(outs[i], in)) return RMSQ_ERR_ALIAS;
+        for (int j = i + 1; j < 3; ++j)
+            if (overlaps(outs[i], outs[j])) return RMSQ_ERR_ALIAS;
+    }
+    st = rmsq_abi::check_device();
+    if (st != RMSQ_OK) return st;
+    rmsq::AttnArgs a = {};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.cache = static_cast<const uint8_t*>(kv_cache);
+    a.table = block_table;
+    a.q_start = query_start;
+    a.seq_lens = seq_lens;
+    a.k_gs = k_global_scale;
+    a.v_gs = v_global_scale;
+    a.out = out;
+    a.lse = lse;
+    a.part = static_cast<float*>(workspace);
+    a.requests = static_cast<int>(num_requests);
+    a.width = static_cast<int>(table_width);
+    a.tokens = static_cast<int>(n_tokens);
+    a.heads = num_heads;
+    a.kv_heads = num_kv_heads;
+    a.group = num_heads / num_kv_heads;
+    a.page_shift = shift;
+    a.num_pages = static_cast<int>(num_pages);
+    a.window = window > INT32_MAX / 2 ? 0 : static_cast<int>(window);
+    a.scale_log2 = softmax_scale * 1.44269504088896341f;
+    // most (row tile, kv head, key tile) tiles these sizes can hold
+    const int64_t ktiles = (static_cast<int64_t>(table_width) << shift) / rmsq::kAttnKeyTile + 1;
+    constexpr int64_t kMaxTiles = int64_t(1) << 40;
+    const int64_t qtiles = n_tokens * a.group / 8 + num_requests;
+    const int64_t max_tiles = qtiles > kMaxTiles / ktiles / num_kv_heads ? kMaxTiles : qtiles * ktiles * num_kv_heads;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == RMSQ_BF16 ? rmsq::launch_attn<rmsq::Bf16T>(a, head_dim, max_tiles, s)
+                                             : rmsq::launch_attn<rmsq::Fp16T>(a, head_dim, max_tiles, s);
+    return e == cudaSuccess ? RMSQ_OK : rmsq_abi::fail_cuda(e);
+}
+
+}  // extern "C"

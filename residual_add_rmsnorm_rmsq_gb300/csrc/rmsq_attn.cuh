@@ -1,0 +1,647 @@
+// Attention over the paged NVFP4 cache, for few queries per request (decode).
+//
+//   o_i = sum_j p_ij v_j,  p_ij = exp(scale q_i.k_j) / sum_j' exp(scale q_i.k_j'),
+//   keys j <= pos_i (and j > pos_i - window), pos_i = seq_len - query_len + i.
+//
+// The G query heads of a kv head read the same keys, so the rows of one
+// matrix product are (query token, head of the group): row = i * G + g, taken
+// ROWS = 8 * NB at a time.  One pass over the keys with a running maximum.
+//
+// Matrix instructions (m16n8k16, f16 operands, fp32 sums), transposed so that
+// the 16-row operand is the cache and the rows are the 8 columns:
+//   S^T[key, row] = K[key, :] . Q[row, :]      O^T[dim, row] += V[:, dim] . P[row, :]
+// f16 holds the cached values exactly: an E2M1 code times its E4M3 scale has
+// at most 6 significant bits and lies in [2^-10, 2688] (or is 0).  The global
+// scales are factors of the logits and of the output.  bf16 queries are scaled
+// by a power of two per row into f16's range, exact unless an element is
+// 2^-28 of the row's largest (then off by 2^-39 of it).  Probabilities are
+// rounded to f16 (11 bits; 8 would be as many as a bf16 output has), scaled by
+// 2^kPShift so that those down to 2^-23 of the maximum keep all their bits.
+//
+// Layout: contractions may take their index in any order, so every lane loads
+// the piece of the cache it needs straight into registers, 16 bytes at a time,
+// with no shared memory and no shuffle.  Lane (g, t) = (lane / 4, lane % 4):
+//   K: dims t * D/4 .. of keys kappa(g) and kappa(g) + 8;
+//   V: dims g * D/8 .. of keys t, t + 4, t + 8, t + 12 (one scale block for
+//      D = 128), whose nibbles are interleaved pairwise so that one
+//      conversion yields the same dim of two keys, the pair a register of the
+//      operand holds;
+// kappa is the order of the keys that makes S^T's accumulator, transposed by
+// movmatrix, the second product's operand.
+//
+// Bound by HBM for long caches (9/16 byte per element, K and V): see the
+// table of measurements beside the launch.  Work is split evenly over the
+// CTAs whatever the lengths: the (request, row tile, kv head, 128-key tile)
+// tiles form one sequence, cut into equal runs; a CTA writes the items its
+// run holds whole, and leaves (O, m, l) in the workspace for the two that its
+// ends may cut, which a second launch joins in order.
+#pragma once
+
+#include "rmsq_device.cuh"
+#include "rmsq_kv.cuh"
+
+namespace rmsq {
+
+constexpr int kAttnWarps = 4;
+constexpr int kAttnThreads = kAttnWarps * 32;
+constexpr int kAttnKeyTile = kAttnWarps * 32;   // keys per CTA step: 32 per warp
+constexpr int kAttnMaxWorkers = 1216;           // CTAs of the split launch: 8 per SM of 152
+constexpr float kPShift = 9.0f;                 // probabilities are scaled by 2^9 ...
+constexpr float kLazy = 6.0f;                   // ... and by up to 2^6 more while the maximum lags: < 2^16 in f16
+
+struct AttnArgs {
+    const void* q;
+    int64_t q_stride;       // elements between tokens
+    const uint8_t* cache;
+    const int* table;       // [requests, width]
+    const int* q_start;     // [requests + 1]
+    const int* seq_lens;    // [requests]
+    const float* k_gs;
+    const float* v_gs;
+    void* out;              // [tokens, heads, D]
+    float* lse;             // [tokens, heads] or null
+    float* part;            // [workers][2][ROWS][D + 2]
+    int requests, width, tokens, heads, kv_heads, group;
+    int page_shift, num_pages, window, workers;
+    float scale_log2;       // softmax scale * log2(e)
+};
+
+// One request as the kernels see it: every value is clamped so that no
+// length or offset in device memory can lead outside the buffers.
+struct Req {
+    int q0, qlen, seq, tile0, ktiles, qtiles;
+};
+
+template <int ROWS>
+__device__ __forceinline__ Req load_request(const AttnArgs& a, int r) {
+    Req x;
+    x.q0 = min(max(__ldg(a.q_start + r), 0), a.tokens);
+    x.qlen = min(max(__ldg(a.q_start + r + 1), x.q0), a.tokens) - x.q0;
+    x.seq = min(max(__ldg(a.seq_lens + r), 0), a.width << a.page_shift);
+    const int first = a.window > 0 ? max(x.seq - x.qlen - a.window + 1, 0) : 0;
+    x.tile0 = min(first, max(x.seq - 1, 0)) / kAttnKeyTile;
+    x.ktiles = max((x.seq + kAttnKeyTile - 1) / kAttnKeyTile - x.tile0, 1);
+    x.qtiles = static_cast<int>((static_cast<int64_t>(x.qlen) * a.group + ROWS - 1) / ROWS);
+    return x;
+}
+
+// prefix[r] = tiles (per kv head) of the requests before r, prefix[requests]
+// = all, in shared memory.  Ends with a barrier.
+template <int ROWS>
+__device__ __forceinline__ void scan_requests(const AttnArgs& a, int64_t* prefix) {
+    __shared__ int64_t wsum[kAttnWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (a.requests + kAttnThreads - 1) / kAttnThreads;
+    const int r0 = min(tid * per, a.requests), r1 = min(r0 + per, a.requests);
+    int64_t sum = 0;
+    for (int r = r0; r < r1; ++r) {
+        const Req x = load_request<ROWS>(a, r);
+        const int64_t c = static_cast<int64_t>(x.qtiles) * x.ktiles;
+        prefix[r + 1] = c;
+        sum += c;
+    }
+    int64_t inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(kFull, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) wsum[warp] = inc;
+    __syncthreads();
+    int64_t run = inc - sum;
+    for (int w = 0; w < warp; ++w) run += wsum[w];
+    for (int r = r0; r < r1; ++r) {
+        const int64_t c = prefix[r + 1];
+        run += c;
+        prefix[r + 1] = run;
+    }
+    if (tid == 0) prefix[0] = 0;
+    __syncthreads();
+}
+
+// Where tile x of the whole sequence lies.
+struct Place {
+    int r, head, qtile, tile;   // tile: index inside the item
+    int64_t item0;              // first tile of the item in the sequence
+};
+
+template <int ROWS>
+__device__ __forceinline__ Place locate(const AttnArgs& a, const int64_t* prefix, int64_t x, Req& req) {
+    int lo = 0, hi = a.requests;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] * a.kv_heads <= x) lo = mid;
+        else hi = mid;
+    }
+    req = load_request<ROWS>(a, lo);
+    const int64_t rest = x - prefix[lo] * a.kv_heads;
+    const int64_t item = rest / req.ktiles;
+    Place p;
+    p.r = lo;
+    p.tile = static_cast<int>(rest - item * req.ktiles);
+    p.qtile = static_cast<int>(item / a.kv_heads);
+    p.head = static_cast<int>(item - static_cast<int64_t>(p.qtile) * a.kv_heads);
+    p.item0 = x - p.tile;
+    return p;
+}
+
+// Tiles per CTA of the even split.
+__device__ __forceinline__ int64_t run_length(int64_t total, int workers) {
+    return total <= workers ? 1 : (total + workers - 1) / workers;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four scale bytes with sign bits cleared and NaN codes (0x7f) turned to 0.
+__device__ __forceinline__ uint32_t clean_scales(uint32_t w) {
+    w &= 0x7f7f7f7fu;
+    const uint32_t nan = (w + 0x01010101u) & 0x80808080u;
+    return w & ~(nan - (nan >> 7));
+}
+
+// Two E4M3 codes (low half of w) as an f16 pair; every E4M3 value is exact.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
+    return r;
+}
+
+// A lane's share of 16 keys: codes and scale bytes.
+template <int D>
+struct KeyRegs {
+    static constexpr int KW = D / 32;           // words of K codes per key (D/4 dims)
+    static constexpr int VW = D / 64;           // words of V codes per key (D/8 dims)
+    static constexpr int KS = D / 64;           // K scale bytes per key
+    static constexpr int VS = D == 256 ? 2 : 1; // V scale bytes per key
+    uint32_t k[2][KW], v[4][VW];
+    uint32_t ks[2];     // KS bytes each
+    uint32_t vs[4];     // VS bytes each
+    int base;           // first key; < 0: nothing here
+};
+
+template <int D>
+__device__ __forceinline__ void load_keys(KeyRegs<D>& x, const AttnArgs& a, int base, int page, int head, int g, int t) {
+    x.base = page < 0 ? -1 : base;
+    if (page < 0) return;
+    using K = KeyRegs<D>;
+    const int P = 1 << a.page_shift;
+    const int64_t tile = static_cast<int64_t>(D / 16 * 9) << a.page_shift;
+    const uint8_t* kt = a.cache + (static_cast<int64_t>(page) * 2 * a.kv_heads + head) * tile;
+    const uint8_t* vt = kt + a.kv_heads * tile;
+    const int in = base & (P - 1);
+    const int kappa = (g >> 1) + ((g & 1) << 2);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint8_t* p = kt + (in + kappa + 8 * i) * (D / 2) + t * (D / 8);
+        if constexpr (D == 64) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+            x.k[i][0] = u.x; x.k[i][1] = u.y;
+        } else {
+#pragma unroll
+            for (int j = 0; j < K::KW; j += 4) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + j / 4);
+                x.k[i][j] = u.x; x.k[i][j + 1] = u.y; x.k[i][j + 2] = u.z; x.k[i][j + 3] = u.w;
+            }
+        }
+        const uint8_t* s = kt + P * (D / 2) + (in + kappa + 8 * i) * (D / 16) + t * K::KS;
+        if constexpr (D == 64) x.ks[i] = __ldg(s);
+        else if constexpr (D == 128) x.ks[i] = __ldg(reinterpret_cast<const uint16_t*>(s));
+        else x.ks[i] = __ldg(reinterpret_cast<const uint32_t*>(s));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint8_t* p = vt + (in + t + 4 * i) * (D / 2) + g * (D / 16);
+        if constexpr (D == 64) {
+            x.v[i][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+        } else if constexpr (D == 128) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+            x.v[i][0] = u.x; x.v[i][1] = u.y;
+        } else {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+            x.v[i][0] = u.x; x.v[i][1] = u.y; x.v[i][2] = u.z; x.v[i][3] = u.w;
+        }
+        const uint8_t* s = vt + P * (D / 2) + (in + t + 4 * i) * (D / 16) + (D == 64 ? g / 2 : g * K::VS);
+        if constexpr (D == 256) x.vs[i] = __ldg(reinterpret_cast<const uint16_t*>(s));
+        else x.vs[i] = __ldg(s);
+    }
+}
+
+// f16 pair (s, s) from half `hi` of an f16 pair.
+__device__ __forceinline__ uint32_t dup_half(uint32_t pair, int hi) { return __byte_perm(pair, 0, hi ? 0x3232 : 0x1010); }
+
+// A warp's running state over its keys for one item.
+template <int D, int NB>
+struct WarpState {
+    float o[D / 16][NB][4];
+    float m[NB][2], l[NB][2];
+};
+
+// One step: 16 keys.  pos / lo: last and first key each of the lane's columns
+// may see; `full`: every key of the step is inside for every row.
+template <int D, int NB>
+__device__ __forceinline__ void attend16(WarpState<D, NB>& w, const KeyRegs<D>& x, const uint32_t (&qf)[D / 16][NB][2],
+                                         const float (&fs)[NB][2], const int (&pos)[NB][2], const int (&lo)[NB][2],
+                                         bool full, int g) {
+    using K = KeyRegs<D>;
+    float s[NB][4];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[b][j] = 0.0f;
+    // scale bytes of both keys: D = 64: one each, 128: two each, 256: four each
+    uint32_t kscale[2][K::KS];      // duplicated f16 pair per block
+    if constexpr (D == 64) {
+        const uint32_t p = e4m3x2_f16x2(clean_scales(x.ks[0] | (x.ks[1] << 8)));
+        kscale[0][0] = dup_half(p, 0);
+        kscale[1][0] = dup_half(p, 1);
+    } else if constexpr (D == 128) {
+        const uint32_t c = clean_scales(x.ks[0] | (x.ks[1] << 16));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t p = e4m3x2_f16x2(c >> (16 * i));
+            kscale[i][0] = dup_half(p, 0);
+            kscale[i][1] = dup_half(p, 1);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t c = clean_scales(x.ks[i]);
+            const uint32_t p0 = e4m3x2_f16x2(c), p1 = e4m3x2_f16x2(c >> 16);
+            kscale[i][0] = dup_half(p0, 0);
+            kscale[i][1] = dup_half(p0, 1);
+            kscale[i][2] = dup_half(p1, 0);
+            kscale[i][3] = dup_half(p1, 1);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < K::KW; ++j) {   // a word of codes: 8 dims, two k-steps
+        uint32_t k0[4], k1[4];
+        e2m1x8_f16x2(x.k[0][j], k0);
+        e2m1x8_f16x2(x.k[1][j], k1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            k0[i] = mul_f16x2(k0[i], kscale[0][j / 2]);
+            k1[i] = mul_f16x2(k1[i], kscale[1][j / 2]);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            mma_f16(s[b], k0[0], k1[0], k0[1], k1[1], qf[2 * j][b][0], qf[2 * j][b][1]);
+            mma_f16(s[b], k0[2], k1[2], k0[3], k1[3], qf[2 * j + 1][b][0], qf[2 * j + 1][b][1]);
+        }
+    }
+    // logits in units of log2; s[b][0..1]: key kappa(g), rows 2t, 2t+1; s[b][2..3]: key + 8
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[b][j] *= fs[b][j & 1];
+    if (!full) {
+        const int key = x.base + (g >> 1) + ((g & 1) << 2);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = key + (j >> 1) * 8;
+                if (k > pos[b][j & 1] || k < lo[b][j & 1]) s[b][j] = -INFINITY;
+            }
+    }
+    // The maximum is moved only when some logit passes it by more than kLazy.
+    bool grow = false;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) grow |= fmaxf(s[b][j], s[b][j + 2]) > w.m[b][j] + kLazy;
+    if (__any_sync(kFull, grow)) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float top = fmaxf(s[b][j], s[b][j + 2]);
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+                const float m = fmaxf(top, w.m[b][j]);
+                const float f = m == -INFINITY ? 1.0f : exp2_approx(w.m[b][j] - m);
+                w.m[b][j] = m;
+                w.l[b][j] *= f;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    w.o[i][b][j] *= f;
+                    w.o[i][b][j + 2] *= f;
+                }
+            }
+    }
+    uint32_t pf[NB][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        float p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float m = w.m[b][j & 1];
+            p[j] = exp2_approx(s[b][j] - (m == -INFINITY ? 0.0f : m - kPShift));
+        }
+        w.l[b][0] += p[0] + p[2];
+        w.l[b][1] += p[1] + p[3];
+        pf[b][0] = transpose8x8(Fp16T::pack(p[0], p[1]));
+        pf[b][1] = transpose8x8(Fp16T::pack(p[2], p[3]));
+    }
+    // V: pair (key t, key t + 4) and (t + 8, t + 12)
+    uint32_t vscale[2][K::VS];
+    if constexpr (D == 256) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t c = clean_scales(__byte_perm(x.vs[2 * i], x.vs[2 * i + 1], 0x5140));
+            vscale[i][0] = e4m3x2_f16x2(c);
+            vscale[i][1] = e4m3x2_f16x2(c >> 16);
+        }
+    } else {
+        const uint32_t c = clean_scales(__byte_perm(x.vs[0], x.vs[1], 0x1140) |
+                                        (__byte_perm(x.vs[2], x.vs[3], 0x1140) << 16));
+        vscale[0][0] = e4m3x2_f16x2(c);
+        vscale[1][0] = e4m3x2_f16x2(c >> 16);
+    }
+#pragma unroll
+    for (int j = 0; j < K::VW; ++j) {   // 8 dims: four m-tiles
+        uint32_t even[2][4], odd[2][4];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t A = x.v[2 * i][j], B = x.v[2 * i + 1][j];
+            e2m1x8_f16x2((A & 0x0f0f0f0fu) | ((B << 4) & 0xf0f0f0f0u), even[i]);
+            e2m1x8_f16x2(((A >> 4) & 0x0f0f0f0fu) | (B & 0xf0f0f0f0u), odd[i]);
+            const uint32_t sc = vscale[i][K::VS == 2 ? j / 2 : 0];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                even[i][c] = mul_f16x2(even[i][c], sc);
+                odd[i][c] = mul_f16x2(odd[i][c], sc);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+                mma_f16(w.o[4 * j + c][b], even[0][c], odd[0][c], even[1][c], odd[1][c], pf[b][0], pf[b][1]);
+    }
+}
+
+template <int D, int NB>
+struct AttnSmem {
+    float o[kAttnWarps][8 * NB][D + 4];
+    float m[kAttnWarps][8 * NB], l[kAttnWarps][8 * NB];
+};
+
+// Writes row `row` of an item: out = o / l / gs and the log-sum-exp.  A row
+// that sees no key gets zeros and -inf.
+template <class E>
+__device__ __forceinline__ void store_quad(void* out, int64_t at, float4 o, float inv) {
+    reinterpret_cast<uint2*>(out)[at / 4] =
+        make_uint2(E::pack(o.x * inv, o.y * inv), E::pack(o.z * inv, o.w * inv));
+}
+
+template <class E, int D, int NB>
+__global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
+    constexpr int ROWS = 8 * NB;
+    extern __shared__ int64_t prefix[];
+    __shared__ __align__(16) AttnSmem<D, NB> sm;
+    allow_dependents();
+    grid_dependency_wait();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    scan_requests<ROWS>(a, prefix);
+    const int64_t total = prefix[a.requests] * a.kv_heads;
+    const int64_t run = run_length(total, a.workers);
+    int64_t x = blockIdx.x * run;
+    const int64_t end = x + run < total ? x + run : total;
+    const float k_gs = __ldg(a.k_gs), v_gs = __ldg(a.v_gs);
+
+    while (x < end) {
+        Req rq;
+        const Place at = locate<ROWS>(a, prefix, x, rq);
+        const int ntiles = static_cast<int>(min(static_cast<int64_t>(rq.ktiles - at.tile), end - x));
+        const int rows = rq.qlen * a.group;      // of the request
+        const int row0 = at.qtile * ROWS;
+
+        // Query fragments: column n = g of block b is row row0 + 8 b + g.
+        uint32_t qf[D / 16][NB][2];
+        float fs[NB][2];
+        int pos[NB][2], lo[NB][2];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int row = row0 + 8 * b + g;
+            uint32_t w[D / 8];
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) w[i] = 0u;
+            if (row < rows) {
+                const int i = row / a.group, h = at.head * a.group + row % a.group;
+                const uint16_t* p = static_cast<const uint16_t*>(a.q) + (rq.q0 + i) * a.q_stride + h * D + t * (D / 4);
+#pragma unroll
+                for (int j = 0; j < D / 32; ++j) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + j);
+                    w[4 * j] = u.x; w[4 * j + 1] = u.y; w[4 * j + 2] = u.z; w[4 * j + 3] = u.w;
+                }
+            }
+            float f = a.scale_log2 / k_gs;
+            if constexpr (E::kBits87 == Bf16T::kBits87) {
+                float top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) top = max_abs3(top, E::lo(w[i]), E::hi(w[i]));
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+                // 2^e brings the row's largest magnitude into [2^14, 2^15)
+                const int e = min(14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 126);
+                const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+                f *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) w[i] = Fp16T::pack(E::lo(w[i]) * up, E::hi(w[i]) * up);
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                qf[i][b][0] = w[2 * i];
+                qf[i][b][1] = w[2 * i + 1];
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                fs[b][j] = __shfl_sync(kFull, f, (2 * t + j) * 4);
+                const int col = row0 + 8 * b + 2 * t + j;
+                pos[b][j] = col < rows ? rq.seq - rq.qlen + col / a.group : -1;
+                lo[b][j] = a.window > 0 ? pos[b][j] - a.window + 1 : 0;
+            }
+        }
+        // Range of the tile's rows: last key any row sees, and the keys every row sees.
+        const int last_row = min(row0 + ROWS, rows) - 1;
+        const int pos_min = rq.seq - rq.qlen + row0 / a.group, pos_max = rq.seq - rq.qlen + last_row / a.group;
+        const int lo_min = a.window > 0 ? pos_min - a.window + 1 : 0, lo_max = a.window > 0 ? pos_max - a.window + 1 : 0;
+
+        WarpState<D, NB> w;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                w.m[b][j] = -INFINITY;
+                w.l[b][j] = 0.0f;
+            }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w.o[i][b][j] = 0.0f;
+
+        // The warp's steps: 16 keys each, two per tile, loaded one step ahead.
+        const int first_key = (rq.tile0 + at.tile) * kAttnKeyTile + warp * 32;
+        const int* row_table = a.table + static_cast<int64_t>(at.r) * a.width;
+        auto key_of = [&](int j) { return first_key + (j >> 1) * kAttnKeyTile + (j & 1) * 16; };
+        auto page_of = [&](int j) {
+            const int k = key_of(j);
+            if (j >= 2 * ntiles || k > pos_max || k + 15 < lo_min) return -1;
+            const int p = __ldg(row_table + (k >> a.page_shift));
+            return p < a.num_pages ? p : -1;
+        };
+        KeyRegs<D> cur, nxt;
+        int p1 = page_of(1);
+        load_keys<D>(cur, a, key_of(0), page_of(0), at.head, g, t);
+        for (int j = 0; j < 2 * ntiles; ++j) {
+            const int p2 = page_of(j + 2);
+            load_keys<D>(nxt, a, key_of(j + 1), p1, at.head, g, t);
+            p1 = p2;
+            if (cur.base >= 0) {
+                const bool full = cur.base + 15 <= pos_min && cur.base >= lo_max;
+                attend16<D, NB>(w, cur, qf, fs, pos, lo, full, g);
+            }
+            cur = nxt;
+        }
+
+        // Join the warps.
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float l = w.l[b][j];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(kFull, l, o);
+                if (g == 0) {
+                    sm.m[warp][8 * b + 2 * t + j] = w.m[b][j];
+                    sm.l[warp][8 * b + 2 * t + j] = l;
+                }
+            }
+        __syncthreads();
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int row = 8 * b + 2 * t + j;
+                float top = sm.m[0][row];
+#pragma unroll
+                for (int i = 1; i < kAttnWarps; ++i) top = fmaxf(top, sm.m[i][row]);
+                const float f = w.m[b][j] == -INFINITY ? 0.0f : exp2_approx(w.m[b][j] - top);
+                float* dst = &sm.o[warp][row][g * (D / 8)];
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    dst[2 * i] = w.o[i][b][j] * f;
+                    dst[2 * i + 1] = w.o[i][b][j + 2] * f;
+                }
+            }
+        __syncthreads();
+        const bool whole = at.tile == 0 && ntiles == rq.ktiles;
+        float* part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (x == blockIdx.x * run ? 0 : 1)) * ROWS * (D + 2);
+        for (int i = tid; i < ROWS * (D / 4); i += kAttnThreads) {
+            const int row = i / (D / 4), d = i % (D / 4) * 4;
+            float top = sm.m[0][row], l = 0.0f;
+#pragma unroll
+            for (int k = 1; k < kAttnWarps; ++k) top = fmaxf(top, sm.m[k][row]);
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < kAttnWarps; ++k) {
+                const float4 u = *reinterpret_cast<const float4*>(&sm.o[k][row][d]);
+                o.x += u.x; o.y += u.y; o.z += u.z; o.w += u.w;
+                const float mk = sm.m[k][row];
+                l += mk == -INFINITY ? 0.0f : sm.l[k][row] * exp2_approx(mk - top);
+            }
+            if (whole) {
+                if (row0 + row < rows) {
+                    const int64_t tok = rq.q0 + (row0 + row) / a.group;
+                    const int64_t oh = tok * a.heads + at.head * a.group + (row0 + row) % a.group;
+                    store_quad<E>(a.out, oh * D + d, o, l > 0.0f ? 1.0f / (l * v_gs) : (l == 0.0f ? 0.0f : l));
+                    if (a.lse && d == 0) a.lse[oh] = l == 0.0f ? -INFINITY : (top + log2f(l) - kPShift) * 0.693147180559945309f;
+                }
+            } else {
+                *reinterpret_cast<float2*>(part + row * (D + 2) + d) = make_float2(o.x, o.y);
+                *reinterpret_cast<float2*>(part + row * (D + 2) + d + 2) = make_float2(o.z, o.w);
+                if (d == 0) *reinterpret_cast<float2*>(part + row * (D + 2) + D) = make_float2(top, l);
+            }
+        }
+        __syncthreads();
+        x += ntiles;
+    }
+}
+
+// Joins the parts of the items that the runs cut: CTA b takes the item that
+// starts in run b and goes past its end.
+template <class E, int D, int NB>
+__global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(AttnArgs a) {
+    constexpr int ROWS = 8 * NB;
+    extern __shared__ int64_t prefix[];
+    allow_dependents();
+    grid_dependency_wait();
+    scan_requests<ROWS>(a, prefix);
+    const int64_t total = prefix[a.requests] * a.kv_heads;
+    const int64_t run = run_length(total, a.workers);
+    const int64_t end = (blockIdx.x + 1) * run;
+    if (end >= total) return;
+    Req rq;
+    const Place at = locate<ROWS>(a, prefix, end - 1, rq);
+    const int64_t item_end = at.item0 + rq.ktiles;
+    if (item_end <= end || at.item0 < end - run) return;
+    const int w1 = static_cast<int>((item_end - 1) / run);
+    const float v_gs = __ldg(a.v_gs);
+    const int rows = rq.qlen * a.group, row0 = at.qtile * ROWS;
+    const int64_t slot = ROWS * (D + 2);
+    const float* first = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (at.item0 == end - run ? 0 : 1)) * slot;
+    for (int i = threadIdx.x; i < ROWS * (D / 4); i += kAttnThreads) {
+        const int row = i / (D / 4), d = i % (D / 4) * 4;
+        if (row0 + row >= rows) continue;
+        const float* p = first + row * (D + 2);
+        float top = p[D], l = p[D + 1];
+        const float2 u0 = *reinterpret_cast<const float2*>(p + d), u1 = *reinterpret_cast<const float2*>(p + d + 2);
+        float4 o = make_float4(u0.x, u0.y, u1.x, u1.y);
+        for (int w = blockIdx.x + 1; w <= w1; ++w) {
+            p = a.part + static_cast<int64_t>(w) * 2 * slot + row * (D + 2);
+            const float m = fmaxf(top, p[D]);
+            const float f0 = top == -INFINITY ? 0.0f : exp2_approx(top - m);
+            const float f1 = p[D] == -INFINITY ? 0.0f : exp2_approx(p[D] - m);
+            const float2 v0 = *reinterpret_cast<const float2*>(p + d), v1 = *reinterpret_cast<const float2*>(p + d + 2);
+            o.x = o.x * f0 + v0.x * f1;
+            o.y = o.y * f0 + v0.y * f1;
+            o.z = o.z * f0 + v1.x * f1;
+            o.w = o.w * f0 + v1.y * f1;
+            l = l * f0 + p[D + 1] * f1;
+            top = m;
+        }
+        const int64_t tok = rq.q0 + (row0 + row) / a.group;
+        const int64_t oh = tok * a.heads + at.head * a.group + (row0 + row) % a.group;
+        store_quad<E>(a.out, oh * D + d, o, l > 0.0f ? 1.0f / (l * v_gs) : (l == 0.0f ? 0.0f : l));
+        if (a.lse && d == 0) a.lse[oh] = l == 0.0f ? -INFINITY : (top + log2f(l) - kPShift) * 0.693147180559945309f;
+    }
+}
+
+}  // namespace rmsq

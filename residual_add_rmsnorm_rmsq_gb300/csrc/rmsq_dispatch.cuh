@@ -18,6 +18,7 @@
 #include <atomic>
 #include <mutex>
 
+#include "rmsq_host.cuh"
 #include "rmsq_launch.h"
 #include "rmsq_nvfp4_dyn.cuh"
 #include "rmsq_pipe.cuh"
@@ -121,24 +122,6 @@ const void* pick_kernel(int mode, bool res, bool pipe, int J) {
     }
 }
 
-// One kernel launch, with programmatic stream serialisation unless it is
-// switched off: the kernel may then start while the previous kernel of the
-// stream finishes; the kernels wait for it before any memory access.
-inline cudaError_t launch_kernel(const void* fn, dim3 grid, dim3 block, void** params, size_t smem,
-                                 cudaStream_t stream) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = programmatic_launch() ? 1 : 0;
-    return cudaLaunchKernelExC(&cfg, fn, params);
-}
-
 // Occupancy of a pipelined instantiation for a given ring size, cached per
 // device.
 struct OccEntry {
@@ -228,20 +211,6 @@ inline int pipe_blocks_per_sm(const void* fn, int threads, int smem, cudaError_t
     *err = set_smem_attributes(fn);
     if (*err != cudaSuccess) return 0;
     return occupancy_blocks(fn, threads, smem, err);
-}
-
-inline int sm_count(cudaError_t* err) {
-    static std::atomic<int> cached[128];
-    int dev = 0;
-    *err = cudaGetDevice(&dev);
-    if (*err != cudaSuccess || dev < 0 || dev >= 128) return 0;
-    int v = cached[dev].load(std::memory_order_acquire);
-    if (v == 0) {
-        *err = cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
-        if (*err != cudaSuccess) return 0;
-        cached[dev].store(v, std::memory_order_release);
-    }
-    return v;
 }
 
 // Default ring: two stages (one row computed while the next is in flight),

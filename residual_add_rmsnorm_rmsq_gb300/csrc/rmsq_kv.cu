@@ -1,0 +1,479 @@
+// Paged key / value cache: slot maps from request lengths, and the NVFP4
+// cache's store and load.
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "rmsq.h"
+#include "rmsq_abi.h"
+#include "rmsq_device.cuh"
+#include "rmsq_host.cuh"
+#include "rmsq_kv.cuh"
+
+namespace rmsq {
+
+// ---------------------------------------------------------------------------
+// Slot map.  With q_r new and c_r cached tokens of request r, page size P:
+//   start_r = q_0 + .. + q_{r-1},   held_r = ceil(c_r / P),
+//   new_r = ceil((c_r + q_r) / P) - held_r,   off_r = new_0 + .. + new_{r-1}
+//   table[r][held_r + k] = free[num_free - 1 - off_r - k]       (k < new_r)
+//   token i of r: position c_r + i, slot = table[r][pos / P] * P + pos % P.
+//
+// Bound by latency (64 requests) or by launch and scan (1000): 8 bytes read
+// per request and 16 written per token.  Every CTA scans all lengths itself
+// (an L2-resident array, two loads per request), so one launch is enough and
+// no CTA waits for another; then the CTAs share out the tokens and the new
+// pages, each finding its request by binary search in the scanned offsets in
+// shared memory.  A token on a new page takes the page from the free list
+// itself, not from the table entry another CTA may not have written yet; the
+// table entries read (pages held before) are written by nobody.
+// ---------------------------------------------------------------------------
+struct SlotArgs {
+    const int* ctx;
+    const int* qlen;
+    int* table;
+    const int* free_pages;
+    const int* num_free;
+    int64_t* slots;
+    int64_t* positions;
+    int* q_start;
+    int* seq_lens;
+    int* num_free_out;
+    int* status;
+    int requests, width, free_capacity, page_shift, tokens;
+};
+
+constexpr int kSlotThreads = 512;
+
+// Exclusive scan of one pair of 64-bit values per thread over the CTA;
+// total_* receive the sums.
+__device__ __forceinline__ void block_scan_pair(int64_t& a, int64_t& b, int64_t& total_a, int64_t& total_b) {
+    __shared__ int64_t wa[kSlotThreads / 32], wb[kSlotThreads / 32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t ia = a, ib = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t ua = __shfl_up_sync(kFull, ia, o), ub = __shfl_up_sync(kFull, ib, o);
+        if (lane >= o) {
+            ia += ua;
+            ib += ub;
+        }
+    }
+    if (lane == 31) {
+        wa[warp] = ia;
+        wb[warp] = ib;
+    }
+    __syncthreads();
+    int64_t pa = 0, pb = 0;
+    total_a = total_b = 0;
+#pragma unroll
+    for (int w = 0; w < kSlotThreads / 32; ++w) {
+        if (w == warp) {
+            pa = total_a;
+            pb = total_b;
+        }
+        total_a += wa[w];
+        total_b += wb[w];
+    }
+    a = pa + ia - a;
+    b = pb + ib - b;
+}
+
+// Largest r in [0, n) with start[r] <= x, for start[0] = 0 <= x < start[n]
+// and ascending starts.
+__device__ __forceinline__ int find_request(const int* start, int n, int x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(SlotArgs a) {
+    extern __shared__ int smem[];
+    int* start = smem;                     // [requests + 1]
+    int* page_off = smem + a.requests + 1; // [requests + 1]
+    __shared__ int err_sh;
+    const int tid = threadIdx.x, R = a.requests, P = 1 << a.page_shift;
+    allow_dependents();
+    grid_dependency_wait();
+    if (tid == 0) err_sh = 0;
+    __syncthreads();
+
+    // Thread t owns `per` consecutive requests: local sums, one scan over the
+    // CTA, then the offsets.  Lengths are staged through the offset arrays so
+    // that the global reads are coalesced.
+    for (int r = tid; r < R; r += kSlotThreads) {
+        start[r] = __ldg(a.qlen + r);
+        page_off[r] = __ldg(a.ctx + r);
+    }
+    const int nf = __ldg(a.num_free);
+    __syncthreads();
+    const int per = (R + kSlotThreads - 1) / kSlotThreads;
+    const int r0 = min(tid * per, R), r1 = min(r0 + per, R);
+    int64_t sq = 0, sp = 0;
+    int err = 0;
+    for (int r = r0; r < r1; ++r) {
+        const int q = start[r], c = page_off[r];
+        if (q < 0 || c < 0) {
+            err |= RMSQ_SLOT_BAD_LENGTH;
+            continue;
+        }
+        const int64_t want = (static_cast<int64_t>(c) + q + P - 1) >> a.page_shift;
+        if (want > a.width) err |= RMSQ_SLOT_TABLE_FULL;
+        sq += q;
+        sp += want - ((static_cast<int64_t>(c) + P - 1) >> a.page_shift);
+    }
+    int64_t tq, tp;
+    block_scan_pair(sq, sp, tq, tp);
+    if (tid == 0) {
+        if (nf < 0 || nf > a.free_capacity) err |= RMSQ_SLOT_BAD_LENGTH;
+        else if (tp > nf) err |= RMSQ_SLOT_NO_PAGES;
+        if (tq > a.tokens) err |= RMSQ_SLOT_TOO_MANY_TOKENS;
+    }
+    if (err) atomicOr(&err_sh, err);
+    __syncthreads();
+    err = err_sh;
+    const int stride = gridDim.x * kSlotThreads, first = blockIdx.x * kSlotThreads + tid;
+    if (first == 0) {
+        *a.status = err;
+        *a.num_free_out = err ? nf : nf - static_cast<int>(tp);
+    }
+    if (err) {   // nothing is assigned; every output is still defined
+        for (int t = first; t < a.tokens; t += stride) a.slots[t] = a.positions[t] = -1;
+        for (int r = first; r <= R; r += stride) {
+            a.q_start[r] = 0;
+            if (r < R) a.seq_lens[r] = __ldg(a.ctx + r);
+        }
+        return;
+    }
+    // Totals fit int32 here: tokens <= a.tokens, pages <= nf.
+    for (int r = r0; r < r1; ++r) {
+        const int q = start[r], c = page_off[r];
+        start[r] = static_cast<int>(sq);
+        page_off[r] = static_cast<int>(sp);
+        sq += q;
+        sp += ((c + q + P - 1) >> a.page_shift) - ((c + P - 1) >> a.page_shift);
+    }
+    if (tid == 0) {
+        start[R] = static_cast<int>(tq);
+        page_off[R] = static_cast<int>(tp);
+    }
+    __syncthreads();
+    for (int t = first; t < a.tokens; t += stride) {
+        int64_t slot = -1, pos = -1;
+        if (t < start[R]) {
+            const int r = find_request(start, R, t);
+            const int c = __ldg(a.ctx + r);
+            const int held = (c + P - 1) >> a.page_shift;
+            const int p = c + (t - start[r]), idx = p >> a.page_shift;
+            const int page = idx < held ? a.table[static_cast<int64_t>(r) * a.width + idx]
+                                        : __ldg(a.free_pages + (nf - 1 - page_off[r] - (idx - held)));
+            pos = p;
+            slot = page < 0 ? -1 : (static_cast<int64_t>(page) << a.page_shift) + (p & (P - 1));
+        }
+        a.slots[t] = slot;
+        a.positions[t] = pos;
+    }
+    for (int k = first; k < page_off[R]; k += stride) {
+        const int r = find_request(page_off, R, k);
+        const int held = (__ldg(a.ctx + r) + P - 1) >> a.page_shift;
+        a.table[static_cast<int64_t>(r) * a.width + held + (k - page_off[r])] = __ldg(a.free_pages + (nf - 1 - k));
+    }
+    for (int r = first; r <= R; r += stride) {
+        a.q_start[r] = start[r];
+        if (r < R) a.seq_lens[r] = __ldg(a.ctx + r) + (start[r + 1] - start[r]);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Store.  One thread per 16-element block: two 16-byte loads, the block's
+// largest magnitude, its E4M3 scale and 16 E2M1 codes with the same steps (and
+// so the same bits) as the RMSQ_NVFP4 quantisation of the row ops.  Bound by
+// HBM: 2 bytes read and 9/16 written per element.  Consecutive threads take
+// consecutive blocks of a token, so a warp reads 1 KB in one piece and writes
+// whole 32-byte sectors of codes; the eight scale bytes of a head are
+// adjacent bytes of one store.
+// ---------------------------------------------------------------------------
+struct CacheArgs {
+    const uint4* k;            // source (store) / destination (load) of the keys
+    const uint4* v;
+    int64_t k_stride, v_stride;   // 16-byte chunks per token
+    const int64_t* slots;
+    const float* k_gs;
+    const float* v_gs;
+    uint8_t* cache;
+    int64_t slots_total;       // pages * page size
+    int n, heads, blocks;      // tokens, kv heads, 16-element blocks per head
+    int page_shift;
+};
+
+template <class E>
+__device__ __forceinline__ void unpack16(const uint4& lo, const uint4& hi, float (&a)[8], float (&b)[8]) {
+    const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        a[2 * i] = E::lo(w[i]);
+        a[2 * i + 1] = E::hi(w[i]);
+        b[2 * i] = E::lo(w[4 + i]);
+        b[2 * i + 1] = E::hi(w[4 + i]);
+    }
+}
+
+// Byte offset of a (page, key or value, head) tile in the cache.
+__device__ __forceinline__ int64_t tile_offset(const CacheArgs& a, int64_t page, int side, int head) {
+    const int64_t tile = (static_cast<int64_t>(a.blocks) * 9) << a.page_shift;
+    return ((page * 2 + side) * a.heads + head) * tile;
+}
+
+template <class E>
+__global__ void __launch_bounds__(256) cache_store_kernel(CacheArgs a) {
+    allow_dependents();
+    grid_dependency_wait();
+    const float gs[2] = {__ldg(a.k_gs), __ldg(a.v_gs)};
+    const int per_side = a.heads * a.blocks, per_token = 2 * per_side;
+    const int64_t total = static_cast<int64_t>(a.n) * per_token;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int t = static_cast<int>(i / per_token);
+        int rest = static_cast<int>(i - static_cast<int64_t>(t) * per_token);
+        const int64_t slot = __ldg(reinterpret_cast<const long long*>(a.slots) + t);
+        if (slot < 0 || slot >= a.slots_total) continue;
+        const int side = rest >= per_side;
+        rest -= side * per_side;
+        const int head = rest / a.blocks, blk = rest - head * a.blocks;
+        const uint4* src = (side ? a.v + t * a.v_stride : a.k + t * a.k_stride) + 2 * rest;
+        const uint4 lo = ld_act(src), hi = ld_act(src + 1);
+        float x[8], y[8];
+        unpack16<E>(lo, hi, x, y);
+        const float amax = max_abs8(max_abs8(0.0f, x), y);
+        const float g = gs[side];
+        const uint32_t sb = e4m3x2(__fmul_rn(__fdiv_rn(amax, 6.0f), g), 0.0f) & 0x7fu;
+        const float r = sb == 0u ? 0.0f : __fdiv_rn(g, e4m3_value_nonneg(sb));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            x[j] = __fmul_rn(x[j], r);
+            y[j] = __fmul_rn(y[j], r);
+        }
+        const int64_t page = slot >> a.page_shift;
+        const int in_page = static_cast<int>(slot & ((1 << a.page_shift) - 1));
+        uint8_t* tile = a.cache + tile_offset(a, page, side, head);
+        *reinterpret_cast<uint2*>(tile + (in_page * a.blocks + blk) * 8) = make_uint2(e2m1x8(x), e2m1x8(y));
+        tile[((a.blocks * 8) << a.page_shift) + in_page * a.blocks + blk] = static_cast<uint8_t>(sb);
+    }
+}
+
+// Load: value = T((q * d) / gs), q * d exact in fp32; zero for a token whose
+// slot is outside the cache.  Same split as the store, bytes the other way.
+template <class E>
+__global__ void __launch_bounds__(256) cache_load_kernel(CacheArgs a) {
+    allow_dependents();
+    grid_dependency_wait();
+    const float gs[2] = {__ldg(a.k_gs), __ldg(a.v_gs)};
+    const int per_side = a.heads * a.blocks, per_token = 2 * per_side;
+    const int64_t total = static_cast<int64_t>(a.n) * per_token;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
+         i += static_cast<int64_t>(gridDim.x) * 256) {
+        const int t = static_cast<int>(i / per_token);
+        int rest = static_cast<int>(i - static_cast<int64_t>(t) * per_token);
+        const int64_t slot = __ldg(reinterpret_cast<const long long*>(a.slots) + t);
+        const int side = rest >= per_side;
+        rest -= side * per_side;
+        uint4* dst = const_cast<uint4*>(side ? a.v + t * a.v_stride : a.k + t * a.k_stride) + 2 * rest;
+        uint32_t w[8] = {};
+        if (slot >= 0 && slot < a.slots_total) {
+            const int head = rest / a.blocks, blk = rest - head * a.blocks;
+            const int64_t page = slot >> a.page_shift;
+            const int in_page = static_cast<int>(slot & ((1 << a.page_shift) - 1));
+            const uint8_t* tile = a.cache + tile_offset(a, page, side, head);
+            const uint2 c = __ldg(reinterpret_cast<const uint2*>(tile + (in_page * a.blocks + blk) * 8));
+            const float d = nvfp4_scale_value(
+                __ldg(tile + ((a.blocks * 8) << a.page_shift) + in_page * a.blocks + blk));
+            const float g = gs[side];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t word = j < 4 ? c.x : c.y;
+                const uint32_t pair = e2m1x2_f16x2(word >> (8 * (j & 3)));
+                w[j] = E::pack(__fdiv_rn(__fmul_rn(Fp16T::lo(pair), d), g), __fdiv_rn(__fmul_rn(Fp16T::hi(pair), d), g));
+            }
+        }
+        st_stream(dst, make_uint4(w[0], w[1], w[2], w[3]));
+        st_stream(dst + 1, make_uint4(w[4], w[5], w[6], w[7]));
+    }
+}
+
+namespace {
+
+int page_shift_of(int64_t page_size) {
+    for (int s = 4; s <= 8; ++s)
+        if (page_size == (1 << s)) return s;
+    return -1;
+}
+
+// The checks the store and the load share; fills the launch arguments.
+int cache_args(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int64_t* slot_map, const float* k_gs,
+               const float* v_gs, const void* cache, int64_t num_pages, int64_t page_size, int64_t n, int heads,
+               int head_dim, int dtype, CacheArgs* a) {
+    if (dtype != RMSQ_BF16 && dtype != RMSQ_FP16) return RMSQ_ERR_INVALID_ARG;
+    if (n < 0 || heads <= 0 || num_pages <= 0) return RMSQ_ERR_INVALID_ARG;
+    if (page_shift_of(page_size) < 0 || (head_dim != 64 && head_dim != 128 && head_dim != 256) || heads > 4096 ||
+        n > INT32_MAX || num_pages > INT32_MAX)
+        return RMSQ_ERR_UNSUPPORTED_SHAPE;
+    const int64_t row = static_cast<int64_t>(heads) * head_dim;
+    if (k_stride < row || v_stride < row || k_stride > INT32_MAX || v_stride > INT32_MAX) return RMSQ_ERR_INVALID_ARG;
+    if (n == 0) return RMSQ_OK;
+    if (!k || !v || !slot_map || !k_gs || !v_gs || !cache) return RMSQ_ERR_INVALID_ARG;
+    using rmsq_abi::aligned;
+    if (!aligned(k, 16) || !aligned(v, 16) || k_stride % 8 || v_stride % 8 || !aligned(slot_map, 8) || !aligned(k_gs, 4) ||
+        !aligned(v_gs, 4) || !aligned(cache, 16))
+        return RMSQ_ERR_ALIGNMENT;
+    a->k = static_cast<const uint4*>(k);
+    a->v = static_cast<const uint4*>(v);
+    a->k_stride = k_stride / 8;
+    a->v_stride = v_stride / 8;
+    a->slots = slot_map;
+    a->k_gs = k_gs;
+    a->v_gs = v_gs;
+    a->cache = static_cast<uint8_t*>(const_cast<void*>(cache));
+    a->slots_total = num_pages * page_size;
+    a->n = static_cast<int>(n);
+    a->heads = heads;
+    a->blocks = head_dim / 16;
+    a->page_shift = page_shift_of(page_size);
+    return RMSQ_OK;
+}
+
+// Spans of the token rows [n, stride], of the cache and of the small inputs.
+struct CacheSpans {
+    rmsq_abi::Span k, v, cache, small[3];
+};
+CacheSpans cache_spans(const CacheArgs& a, const float* k_gs, const float* v_gs) {
+    const size_t row = static_cast<size_t>(a.heads) * a.blocks * 32;
+    auto rows = [&](const uint4* p, int64_t stride) {
+        return rmsq_abi::span(p, static_cast<size_t>(a.n - 1) * stride * 16 + row);
+    };
+    const size_t tile = static_cast<size_t>(a.blocks) * 9 << a.page_shift;
+    return {rows(a.k, a.k_stride), rows(a.v, a.v_stride),
+            rmsq_abi::span(a.cache, (a.slots_total >> a.page_shift) * 2 * a.heads * tile),
+            {rmsq_abi::span(a.slots, static_cast<size_t>(a.n) * 8), rmsq_abi::span(k_gs, 4), rmsq_abi::span(v_gs, 4)}};
+}
+
+cudaError_t launch_cache(const void* fn, CacheArgs& a, cudaStream_t stream) {
+    cudaError_t e;
+    const int sms = sm_count(&e);
+    if (e != cudaSuccess) return e;
+    const int64_t threads = static_cast<int64_t>(a.n) * 2 * a.heads * a.blocks;
+    int64_t grid = (threads + 255) / 256;
+    if (grid > static_cast<int64_t>(sms) * 32) grid = static_cast<int64_t>(sms) * 32;
+    void* params[] = {&a};
+    return launch_kernel(fn, dim3(static_cast<unsigned>(grid)), dim3(256), params, 0, stream);
+}
+
+}  // namespace
+}  // namespace rmsq
+
+extern "C" {
+
+int rmsq_build_slot_map(const int32_t* context_lens, const int32_t* query_lens, int32_t* block_table, int64_t table_width,
+                        const int32_t* free_pages, int64_t free_capacity, const int32_t* num_free, int64_t page_size,
+                        int64_t num_requests, int64_t max_tokens, int64_t* slot_map, int64_t* positions,
+                        int32_t* query_start, int32_t* seq_lens, int32_t* num_free_out, int32_t* status, void* stream) {
+    using rmsq_abi::aligned;
+    using rmsq_abi::overlaps;
+    using rmsq_abi::Span;
+    using rmsq_abi::span;
+    if (num_requests < 0 || max_tokens < 0 || table_width < 0 || free_capacity < 0) return RMSQ_ERR_INVALID_ARG;
+    const int shift = rmsq::page_shift_of(page_size);
+    // positions and slots inside a request stay below 2^31
+    if (shift < 0 || num_requests > RMSQ_MAX_REQUESTS || max_tokens > INT32_MAX / 2 || free_capacity > INT32_MAX ||
+        table_width > (INT32_MAX >> shift))
+        return RMSQ_ERR_UNSUPPORTED_SHAPE;
+    if (!num_free || !query_start || !num_free_out || !status) return RMSQ_ERR_INVALID_ARG;
+    if (num_requests > 0 && (!context_lens || !query_lens || !seq_lens || (table_width > 0 && !block_table)))
+        return RMSQ_ERR_INVALID_ARG;
+    if ((free_capacity > 0 && !free_pages) || (max_tokens > 0 && (!slot_map || !positions))) return RMSQ_ERR_INVALID_ARG;
+    if (!aligned(context_lens, 4) || !aligned(query_lens, 4) || !aligned(block_table, 4) || !aligned(free_pages, 4) ||
+        !aligned(num_free, 4) || !aligned(slot_map, 8) || !aligned(positions, 8) || !aligned(query_start, 4) ||
+        !aligned(seq_lens, 4) || !aligned(num_free_out, 4) || !aligned(status, 4))
+        return RMSQ_ERR_ALIGNMENT;
+    const size_t R = static_cast<size_t>(num_requests), T = static_cast<size_t>(max_tokens);
+    const Span ins[4] = {span(context_lens, R * 4), span(query_lens, R * 4),
+                         span(free_pages, static_cast<size_t>(free_capacity) * 4), span(num_free, 4)};
+    const Span outs[7] = {span(block_table, R * static_cast<size_t>(table_width) * 4), span(slot_map, T * 8),
+                          span(positions, T * 8), span(query_start, (R + 1) * 4), span(seq_lens, R * 4),
+                          span(num_free_out, 4), span(status, 4)};
+    for (int i = 0; i < 7; ++i) {
+        for (const Span& in : ins)
+            if (overlaps(outs[i], in)) return RMSQ_ERR_ALIAS;
+        for (int j = i + 1; j < 7; ++j)
+            if (overlaps(outs[i], outs[j])) return RMSQ_ERR_ALIAS;
+    }
+    const int st = rmsq_abi::check_device();
+    if (st != RMSQ_OK) return st;
+    rmsq::SlotArgs a = {context_lens, query_lens, block_table, free_pages, num_free, slot_map, positions, query_start,
+                        seq_lens, num_free_out, status, static_cast<int>(num_requests), static_cast<int>(table_width),
+                        static_cast<int>(free_capacity), shift, static_cast<int>(max_tokens)};
+    const void* fn = (const void*)&rmsq::slot_map_kernel;
+    const int smem = static_cast<int>(2 * (num_requests + 1) * 4);
+    cudaError_t e;
+    const int sms = rmsq::sm_count(&e);
+    if (e == cudaSuccess && smem > 40 * 1024)
+        e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, 2 * (RMSQ_MAX_REQUESTS + 1) * 4);
+    if (e != cudaSuccess) return rmsq_abi::fail_cuda(e);
+    const int64_t most = max_tokens > num_requests + 1 ? max_tokens : num_requests + 1;
+    int64_t grid = (most + rmsq::kSlotThreads - 1) / rmsq::kSlotThreads;
+    if (grid > sms) grid = sms;
+    void* params[] = {&a};
+    e = rmsq::launch_kernel(fn, dim3(static_cast<unsigned>(grid)), dim3(rmsq::kSlotThreads), params, smem,
+                            static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RMSQ_OK : rmsq_abi::fail_cuda(e);
+}
+
+int rmsq_kv_cache_store_nvfp4(const void* k, int64_t k_stride, const void* v, int64_t v_stride, const int64_t* slot_map,
+                              const float* k_global_scale, const float* v_global_scale, void* kv_cache, int64_t num_pages,
+                              int64_t page_size, int64_t n_tokens, int num_kv_heads, int head_dim, int dtype,
+                              void* stream) {
+    rmsq::CacheArgs a = {};
+    int st = rmsq::cache_args(k, k_stride, v, v_stride, slot_map, k_global_scale, v_global_scale, kv_cache, num_pages,
+                              page_size, n_tokens, num_kv_heads, head_dim, dtype, &a);
+    if (st != RMSQ_OK || n_tokens == 0) return st;
+    const rmsq::CacheSpans s = rmsq::cache_spans(a, k_global_scale, v_global_scale);
+    if (rmsq_abi::overlaps(s.cache, s.k) || rmsq_abi::overlaps(s.cache, s.v)) return RMSQ_ERR_ALIAS;
+    for (const rmsq_abi::Span& in : s.small)
+        if (rmsq_abi::overlaps(s.cache, in)) return RMSQ_ERR_ALIAS;
+    st = rmsq_abi::check_device();
+    if (st != RMSQ_OK) return st;
+    const void* fn = dtype == RMSQ_BF16 ? (const void*)&rmsq::cache_store_kernel<rmsq::Bf16T>
+                                        : (const void*)&rmsq::cache_store_kernel<rmsq::Fp16T>;
+    const cudaError_t e = rmsq::launch_cache(fn, a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RMSQ_OK : rmsq_abi::fail_cuda(e);
+}
+
+int rmsq_kv_cache_load_nvfp4(const void* kv_cache, int64_t num_pages, int64_t page_size, const int64_t* slot_map,
+                             const float* k_global_scale, const float* v_global_scale, void* k, int64_t k_stride, void* v,
+                             int64_t v_stride, int64_t n_tokens, int num_kv_heads, int head_dim, int dtype, void* stream) {
+    rmsq::CacheArgs a = {};
+    int st = rmsq::cache_args(k, k_stride, v, v_stride, slot_map, k_global_scale, v_global_scale, kv_cache, num_pages,
+                              page_size, n_tokens, num_kv_heads, head_dim, dtype, &a);
+    if (st != RMSQ_OK || n_tokens == 0) return st;
+    const rmsq::CacheSpans s = rmsq::cache_spans(a, k_global_scale, v_global_scale);
+    // k and v may be two column ranges of one token-major buffer: their rows
+    // interleave without sharing an element
+    const bool columns = a.k_stride == a.v_stride && rmsq::disjoint_columns(a.k, a.v, a.k_stride, a.heads * a.blocks * 2);
+    if (rmsq_abi::overlaps(s.k, s.v) && !columns) return RMSQ_ERR_ALIAS;
+    const rmsq_abi::Span outs[2] = {s.k, s.v};
+    for (const rmsq_abi::Span& o : outs) {
+        if (rmsq_abi::overlaps(o, s.cache)) return RMSQ_ERR_ALIAS;
+        for (const rmsq_abi::Span& in : s.small)
+            if (rmsq_abi::overlaps(o, in)) return RMSQ_ERR_ALIAS;
+    }
+    st = rmsq_abi::check_device();
+    if (st != RMSQ_OK) return st;
+    const void* fn = dtype == RMSQ_BF16 ? (const void*)&rmsq::cache_load_kernel<rmsq::Bf16T>
+                                        : (const void*)&rmsq::cache_load_kernel<rmsq::Fp16T>;
+    const cudaError_t e = rmsq::launch_cache(fn, a, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? RMSQ_OK : rmsq_abi::fail_cuda(e);
+}
+
+}  // extern "C"

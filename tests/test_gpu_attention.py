@@ -1,0 +1,269 @@
+"""Attention over the paged NVFP4 cache on the GPU, against float64 with
+tolerances derived beside the reference (tests/_serve_ref.py)."""
+import numpy as np
+import pytest
+import torch
+
+import _serve_ref as ref
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+
+
+def make(q_lens, seq_lens, heads, kv, D, page, dtype, *, seed=0, extra_rows=0, sigma=1.0, spare=3):
+    rng = np.random.default_rng(seed)
+    need = [max(1, -(-s // page)) for s in seq_lens]
+    pages, width = sum(need) + spare, max(need) + 1
+    ids = rng.permutation(pages).astype(np.int32)
+    table = np.full((len(seq_lens), width), -1, np.int32)
+    at = 0
+    for r, m in enumerate(need):
+        table[r, :m] = ids[at: at + m]
+        at += m
+    cache = ref.random_cache(rng, pages, kv, page, D)
+    T = sum(q_lens) + extra_rows
+    q, q64 = ref.act(rng.normal(0, sigma, (T, heads, D)), DT[dtype])
+    return {"q": q, "q64": q64, "cache": cache, "table": table, "q_lens": q_lens, "seq": seq_lens, "page": page, "D": D,
+            "heads": heads, "kv": kv, "dtype": dtype, "k_gs": np.float32(611.3), "v_gs": np.float32(57.9)}
+
+
+def run(rq, c, *, window=0, scale=None, stream=None, **kw):
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    start = np.concatenate([[0], np.cumsum(c["q_lens"])]).astype(np.int32)
+    return rq.paged_attention_nvfp4(kw.pop("q", c["q"].cuda()), dev(c["cache"]), dev(c["table"]), dev(start),
+                                    dev(np.array(c["seq"], np.int32)), torch.tensor([c["k_gs"]], device="cuda"),
+                                    torch.tensor([c["v_gs"]], device="cuda"), c["page"], scale, window=window,
+                                    return_lse=True, stream=stream, **kw)
+
+
+def check(rq, c, *, window=0, scale=None, **kw):
+    n = sum(c["q_lens"])
+    out, lse = run(rq, c, window=window, scale=scale, **kw)
+    eps = torch.finfo(DT[c["dtype"]]).eps
+    w_out, w_lse, tol, tol_lse = ref.attention(c["q64"][:n], c["cache"], c["table"], c["q_lens"], c["seq"],
+                                               float(c["k_gs"]), float(c["v_gs"]), c["page"],
+                                               c["D"] ** -0.5 if scale is None else scale, window, eps)
+    o, s = out[:n].double().cpu().numpy(), lse[:n].double().cpu().numpy()
+    empty = np.isinf(w_lse)
+    assert np.array_equal(np.isinf(s), empty) and (s[empty] < 0).all() and (o[empty] == 0).all()
+    bad = np.abs(o - w_out) - tol
+    assert bad.max(initial=0) <= 0, f"out off by up to {np.abs(o - w_out).max()}, {(bad > 0).sum()} beyond"
+    bad = np.abs(s - w_lse)[~empty] - tol_lse[~empty]
+    assert bad.max(initial=0) <= 0, f"lse beyond by {bad.max()}"
+    return out, lse
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D, page", [(64, 16), (64, 128), (128, 16), (128, 32), (128, 64), (256, 256), (256, 16)])
+@pytest.mark.parametrize("heads, kv", [(1, 1), (4, 4), (8, 2), (5, 1), (16, 1), (6, 2), (8, 1)])
+def test_decode(rmsq_gpu, dtype, D, page, heads, kv):
+    """One query per request: one key, around tile and page ends, longer ones."""
+    seq = [1, 15, 16, 17, 127, 128, 129, 300]
+    check(rmsq_gpu, make([1] * len(seq), seq, heads, kv, D, page, dtype, seed=D + heads))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D, heads, kv, page", [(64, 8, 1, 16), (128, 8, 2, 64), (128, 3, 1, 16), (256, 4, 2, 32)])
+@pytest.mark.parametrize("window", [0, 1, 16, 100])
+def test_several_queries(rmsq_gpu, dtype, D, heads, kv, page, window):
+    """Speculative tokens and prompts of odd lengths, with and without a
+    window; a request without queries, one that is nothing but queries."""
+    c = make([4, 1, 0, 33, 130], [77, 300, 20, 33, 391], heads, kv, D, page, dtype, seed=window)
+    check(rmsq_gpu, c, window=window)
+
+
+@pytest.mark.parametrize("heads, kv", [(16, 1), (32, 4)])
+def test_prompt(rmsq_gpu, heads, kv):
+    check(rmsq_gpu, make([150, 1], [150, 201], heads, kv, 128, 16, "bf16", seed=5))
+
+
+def test_rows_without_keys(rmsq_gpu):
+    """Empty requests and more queries than keys: zeros and -inf."""
+    c = make([1, 3, 5, 1], [0, 2, 0, 40], 8, 2, 128, 16, "bf16")
+    out, lse = check(rmsq_gpu, c)
+    assert torch.isinf(lse[0]).all() and torch.isinf(lse[1]).all() and torch.isfinite(lse[2]).all()
+
+
+def test_bad_pages_are_left_out(rmsq_gpu):
+    """Negative and too large page numbers, at ends and in the middle."""
+    c = make([1, 1, 2], [200, 90, 130], 8, 2, 128, 16, "bf16", seed=2)
+    c["table"][0, 3], c["table"][0, 12], c["table"][1, 0] = -1, len(c["cache"]), 2**31 - 1
+    c["table"][2, :] = -5                      # a request with no page at all
+    out, lse = check(rmsq_gpu, c)
+    assert torch.isinf(lse[2:]).all()
+
+
+def test_garbage_behind_the_last_key(rmsq_gpu):
+    """Unwritten slots of the last page and spare pages hold 0xff (NaN scales)."""
+    c = make([1, 2], [37, 130], 8, 2, 128, 64, "bf16", seed=4)
+    clean = [t.clone() for t in run(rmsq_gpu, c)]
+    codes, scales = ref.tiles(c["cache"], 64, 128)
+    for r, n in enumerate(c["seq"]):
+        last = c["table"][r, (n - 1) // 64]
+        codes[last, :, :, (n - 1) % 64 + 1:] = 0xff
+        scales[last, :, :, (n - 1) % 64 + 1:] = 0xff
+    for a, b in zip(clean, run(rmsq_gpu, c)):
+        assert torch.equal(a, b)
+
+
+def test_rows_behind_the_last_request_stay(rmsq_gpu):
+    c = make([1, 2, 1], [30, 40, 50], 8, 4, 64, 16, "fp16", extra_rows=9)
+    out = torch.full((13, 8, 64), 3.0, dtype=torch.float16, device="cuda")
+    lse = torch.full((13, 8), 5.0, device="cuda")
+    check(rmsq_gpu, c, out=out, lse=lse)
+    assert (out[4:] == 3).all() and (lse[4:] == 5).all()
+
+
+@pytest.mark.parametrize("dtype, big", [("bf16", 1e30), ("bf16", 1e-30), ("fp16", 6e4), ("fp16", 6e-8)])
+def test_extreme_queries(rmsq_gpu, dtype, big):
+    """Query magnitudes at the ends of their type, one row unlike the next;
+    the softmax scale keeps the logits ordinary."""
+    c = make([1, 1, 1], [50, 260, 33], 4, 2, 64, 16, dtype, seed=8)
+    x = np.random.default_rng(1).normal(0, 1, (3, 4, 64)) * big / 4
+    c["q"], c["q64"] = ref.act(x, DT[dtype])
+    check(rmsq_gpu, c, scale=float(np.float32(0.1 / big)) if big > 1 else min(0.1 / big, 1e20))
+
+
+def test_infinite_and_nan_queries_stay_in_their_rows(rmsq_gpu):
+    c = make([1, 1, 1, 1], [50, 60, 70, 80], 4, 1, 128, 16, "bf16", seed=6)
+    good, good_lse = run(rmsq_gpu, c)
+    q = c["q"].clone()
+    q[1, 2, 5], q[2, 0, 0] = float("inf"), float("nan")
+    out, lse = run(rmsq_gpu, c, q=q.cuda())
+    hit = torch.zeros(4, 4, dtype=torch.bool)
+    hit[1, 2] = hit[2, 0] = True
+    assert torch.equal(out[~hit], good[~hit]) and torch.equal(lse[~hit], good_lse[~hit])
+    assert torch.isnan(out[1, 2]).any() and torch.isnan(out[2, 0]).all()
+
+
+@pytest.mark.parametrize("sigma", [0.0, 30.0])
+def test_flat_and_peaked_weights(rmsq_gpu, sigma):
+    check(rmsq_gpu, make([1, 2, 1], [500, 130, 1], 8, 2, 128, 16, "bf16", sigma=sigma, seed=9))
+
+
+def test_rising_logits_move_the_maximum(rmsq_gpu):
+    """Keys that grow along the sequence: the running maximum moves at every step."""
+    c = make([1], [1000], 4, 1, 64, 16, "fp16", seed=3)
+    codes, scales = ref.tiles(c["cache"], 16, 64)
+    codes[:, 0] = 0x22                                    # every element 1.0
+    for j in range(1000):
+        scales[c["table"][0, j // 16], 0, :, j % 16] = 0x10 + j // 10
+    c["q"], c["q64"] = ref.act(np.abs(c["q64"]) + 0.5, torch.float16)
+    check(rmsq_gpu, c, scale=0.5)
+
+
+def test_a_long_sequence_split_over_the_card(rmsq_gpu):
+    """One head over 20000 keys next to short ones; only a few rows are
+    compared with float64, all of them with a second run bit for bit."""
+    c = make([1, 1, 2], [20000, 3, 700], 4, 2, 128, 128, "bf16", seed=11)
+    a = check(rmsq_gpu, c)
+    b = run(rmsq_gpu, c)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_strided_queries_shared_pages_and_reused_workspace(rmsq_gpu):
+    """q as a column range of a qkv buffer; two requests on the same pages; a
+    workspace full of NaN."""
+    rq = rmsq_gpu
+    c = make([1, 1], [90, 90], 8, 2, 128, 16, "bf16", seed=12)
+    c["table"][1] = c["table"][0]
+    wide = torch.randn(2, 12 * 128).bfloat16()
+    wide[:, :1024] = c["q"].flatten(1)
+    ws = torch.full((rq.paged_attention_workspace_bytes(2, 2, 8, 2, 128),), 0xff, dtype=torch.uint8, device="cuda")
+    check(rq, c, q=wide.cuda()[:, :1024].unflatten(1, (8, 128)), workspace=ws)
+
+
+def test_lengths_outside_the_buffers_are_clamped(rmsq_gpu):
+    """Device-side lengths and offsets beyond the table, the tokens or below
+    zero read nothing outside."""
+    rq = rmsq_gpu
+    c = make([1, 1, 1], [40, 40, 40], 4, 2, 64, 16, "bf16")
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    one = torch.ones(1, device="cuda")
+    for start, seq in (([0, 1, 2, 3], [2**31 - 1, -5, 40]), ([-9, 1, 2**31 - 1, 5], [40, 40, 40]), ([3, 2, 1, 0], [40] * 3)):
+        out = rq.paged_attention_nvfp4(c["q"].cuda(), dev(c["cache"]), dev(c["table"]), dev(np.array(start, np.int32)),
+                                       dev(np.array(seq, np.int32)), one, one, 16, out=torch.zeros_like(c["q"]).cuda())
+        torch.cuda.synchronize()
+        assert out.shape == (3, 4, 64)
+
+
+def test_most_requests(rmsq_gpu):
+    """As many requests as there may be, one key each: out is that value."""
+    rq = rmsq_gpu
+    R, page = rq.MAX_REQUESTS, 16
+    cache = torch.zeros(rq.kv_cache_shape(R // 16, 1, 64, page), dtype=torch.uint8, device="cuda")
+    k = torch.randn(R, 1, 64, device="cuda").bfloat16()
+    slots = torch.arange(R, device="cuda")
+    gs = torch.tensor([336.0], device="cuda")
+    rq.kv_cache_store_nvfp4(k, k, slots, gs, gs, cache, page)
+    _, v = rq.kv_cache_load_nvfp4(cache, slots, gs, gs, 64, page)
+    # request r sees exactly slot r: window 1 at position r % 16 of page r / 16
+    table = (torch.arange(R, device="cuda") // 16).int()[:, None].contiguous()
+    seq = (torch.arange(R, device="cuda") % 16 + 1).int()
+    start = torch.arange(R + 1, device="cuda").int()
+    out = rq.paged_attention_nvfp4(k, cache, table, start, seq, gs, gs, page, window=1)
+    assert torch.equal(out, v)
+
+
+def test_graph_replay_follows_the_device_lengths(rmsq_gpu):
+    rq = rmsq_gpu
+    c = make([1, 1, 1], [30, 200, 64], 8, 2, 128, 16, "bf16", seed=21)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    q, cache, table = c["q"].cuda(), dev(c["cache"]), dev(c["table"])
+    start, seq = torch.arange(4, dtype=torch.int32, device="cuda"), dev(np.array(c["seq"], np.int32))
+    g1, g2 = torch.tensor([c["k_gs"]], device="cuda"), torch.tensor([c["v_gs"]], device="cuda")
+    ws = torch.empty(rq.paged_attention_workspace_bytes(3, 3, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(3, 8, device="cuda")
+
+    def call():
+        rq.paged_attention_nvfp4(q, cache, table, start, seq, g1, g2, 16, out=out, lse=lse, workspace=ws)
+
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for lens in ([1, 1, 1], [17, 208, 3], [30, 200, 64]):
+        seq.copy_(torch.tensor(lens, dtype=torch.int32))
+        q.neg_()
+        graph.replay()
+        got = out.clone(), lse.clone()
+        call()
+        assert torch.equal(got[0], out) and torch.equal(got[1], lse)
+
+
+def test_a_decode_loop_of_the_operators_together(rmsq_gpu):
+    """Slot map, QK-norm + RoPE, store, attention over a prompt step and three
+    decode steps, against float64 attention over what the cache holds."""
+    rq = rmsq_gpu
+    import rmsq_inputs as ri
+    R, nq, nkv, D, page, width, cap = 3, 8, 2, 128, 16, 6, 16
+    torch.manual_seed(0)
+    ctx = torch.zeros(R, dtype=torch.int32, device="cuda")
+    table = torch.full((R, width), -1, dtype=torch.int32, device="cuda")
+    free = torch.randperm(cap, device="cuda").int()
+    left = torch.tensor([cap], dtype=torch.int32, device="cuda")
+    cos_sin = torch.from_numpy(ri.rope_table(256, D)).cuda()
+    w = (1 + 0.1 * torch.randn(D)).bfloat16().cuda()
+    cache = torch.full(rq.kv_cache_shape(cap, nkv, D, page), 0xff, dtype=torch.uint8, device="cuda")
+    gs = torch.tensor([2688 / 12.0], device="cuda")
+    seq_host = [0] * R
+    for q_lens in ([20, 1, 37], [1, 1, 1], [1, 1, 1], [2, 1, 0]):
+        n = sum(q_lens)
+        tokens = n + 2                                     # padded, as a captured step would be
+        slots, pos, start, seq, left, status = rq.build_slot_map(
+            ctx, torch.tensor(q_lens, dtype=torch.int32, device="cuda"), table, free, left, page, tokens)
+        assert status.item() == 0
+        qkv = torch.randn(tokens, (nq + 2 * nkv) * D, device="cuda").bfloat16()
+        rq.qk_norm_rope(qkv, pos, cos_sin, w, w, 1e-6, nq, nkv, D)
+        heads = qkv.unflatten(1, (nq + 2 * nkv, D))
+        rq.kv_cache_store_nvfp4(heads[:, nq: nq + nkv], heads[:, nq + nkv:], slots, gs, gs, cache, page)
+        out, lse = rq.paged_attention_nvfp4(heads[:, :nq], cache, table, start, seq, gs, gs, page, return_lse=True)
+        seq_host = [a + b for a, b in zip(seq_host, q_lens)]
+        assert seq.tolist() == seq_host
+        q64 = heads[:n, :nq].double().cpu().numpy()
+        w_out, w_lse, tol, tol_lse = ref.attention(q64, cache.cpu().numpy(), table.cpu().numpy(), q_lens, seq_host,
+                                                   float(gs.item()), float(gs.item()), page, D ** -0.5, 0,
+                                                   torch.finfo(torch.bfloat16).eps)
+        assert (np.abs(out[:n].double().cpu().numpy() - w_out) <= tol).all()
+        assert (np.abs(lse[:n].double().cpu().numpy() - w_lse) <= tol_lse).all()
+        ctx = seq

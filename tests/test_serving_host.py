@@ -1,0 +1,174 @@
+"""Refusals of the serving operators (no GPU needed, no kernel runs): every
+bad argument is an error before anything is launched."""
+import ctypes
+
+import pytest
+import torch
+
+import residual_add_rmsnorm_rmsq_gb300 as rq
+
+A = [0x10000000 * k for k in range(1, 16)]   # far-apart fake addresses
+I32, F32 = torch.int32, torch.float32
+
+
+@pytest.fixture(scope="module")
+def L():
+    from residual_add_rmsnorm_rmsq_gb300 import _build
+    _build.build()
+    return rq.load()
+
+
+def vp(x):
+    return ctypes.c_void_p(x) if x else None
+
+
+def slots(L, ctx=A[0], ql=A[1], table=A[2], width=8, free=A[3], cap=100, nf=A[4], page=16, R=4, T=64, sm=A[5], pos=A[6],
+          start=A[7], seq=A[8], out=A[9], st=A[10]):
+    return L.rmsq_build_slot_map(vp(ctx), vp(ql), vp(table), width, vp(free), cap, vp(nf), page, R, T, vp(sm), vp(pos),
+                                 vp(start), vp(seq), vp(out), vp(st), None)
+
+
+NO_GPU = (rq.ERR_NO_DEVICE, rq.ERR_UNSUPPORTED_DEVICE)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="fake addresses")
+def test_valid_calls_reach_the_device_check(L):
+    assert slots(L) in NO_GPU
+    assert slots(L, R=0, ctx=0, ql=0, seq=0, table=0) in NO_GPU
+    assert store(L) in NO_GPU and load(L) in NO_GPU and attn(L) in NO_GPU
+    # k and v as columns of one buffer
+    assert store(L, k=A[0], v=A[0] + 1024, ks=2048, vs=2048) in NO_GPU
+    assert load(L, k=A[0], v=A[0] + 1024, ks=1024, vs=1024) in NO_GPU
+    assert attn(L, lse=0) in NO_GPU
+
+
+def test_slot_map_refusals(L):
+    for kw in ("ctx", "ql", "table", "free", "nf", "sm", "pos", "start", "seq", "out", "st"):
+        assert slots(L, **{kw: 0}) == rq.ERR_INVALID_ARG, kw
+        assert slots(L, **{kw: A[12] + 2}) == rq.ERR_ALIGNMENT, kw
+    assert slots(L, sm=A[12] + 4) == rq.ERR_ALIGNMENT
+    for kw in ({"R": -1}, {"T": -1}, {"width": -1}, {"cap": -1}):
+        assert slots(L, **kw) == rq.ERR_INVALID_ARG, kw
+    for kw in ({"page": 0}, {"page": 8}, {"page": 24}, {"page": 512}, {"R": rq.MAX_REQUESTS + 1}, {"T": 1 << 30},
+               {"cap": 1 << 31}, {"width": 1 << 28}):
+        assert slots(L, **kw) == rq.ERR_UNSUPPORTED_SHAPE, kw
+    assert slots(L, seq=A[0]) == rq.ERR_ALIAS             # seq_lens over context_lens
+    assert slots(L, out=A[4]) == rq.ERR_ALIAS             # num_free in place
+    assert slots(L, sm=A[5], pos=A[5] + 64) == rq.ERR_ALIAS
+    assert slots(L, table=A[3]) == rq.ERR_ALIAS
+
+
+def store(L, k=A[0], ks=256, v=A[1], vs=256, sm=A[2], kg=A[3], vg=A[4], cache=A[5], pages=10, page=16, n=4, h=2, d=128,
+          dt=0):
+    return L.rmsq_kv_cache_store_nvfp4(vp(k), ks, vp(v), vs, vp(sm), vp(kg), vp(vg), vp(cache), pages, page, n, h, d, dt,
+                                       None)
+
+
+def load(L, k=A[0], ks=256, v=A[1], vs=256, sm=A[2], kg=A[3], vg=A[4], cache=A[5], pages=10, page=16, n=4, h=2, d=128,
+         dt=0):
+    return L.rmsq_kv_cache_load_nvfp4(vp(cache), pages, page, vp(sm), vp(kg), vp(vg), vp(k), ks, vp(v), vs, n, h, d, dt,
+                                      None)
+
+
+@pytest.mark.parametrize("call", [store, load])
+def test_cache_refusals(L, call):
+    for kw in ("k", "v", "sm", "kg", "vg", "cache"):
+        assert call(L, **{kw: 0}) == rq.ERR_INVALID_ARG, kw
+        assert call(L, **{kw: A[12] + 2}) == rq.ERR_ALIGNMENT, kw
+    for kw in ({"n": -1}, {"h": 0}, {"pages": 0}, {"dt": 2}, {"ks": 255}, {"vs": 128}, {"ks": 1 << 32}):
+        assert call(L, **kw) == rq.ERR_INVALID_ARG, kw
+    for kw in ({"d": 96}, {"d": 0}, {"d": 512}, {"page": 8}, {"page": 48}, {"h": 4097}, {"n": 1 << 31}):
+        assert call(L, **(kw | {"ks": 1 << 30, "vs": 1 << 30})) == rq.ERR_UNSUPPORTED_SHAPE, kw
+    assert call(L, ks=260) == rq.ERR_ALIGNMENT
+    assert call(L, n=0) == rq.OK
+    assert call(L, cache=A[0] + 512) == rq.ERR_ALIAS
+    assert call is load or call(L, cache=A[2]) == rq.ERR_ALIAS   # (two inputs of the load)
+
+
+def test_load_outputs_must_not_overlap(L):
+    assert load(L, v=A[0]) == rq.ERR_ALIAS
+    assert load(L, v=A[0] + 256, ks=512, vs=512) == rq.ERR_ALIAS      # columns that share elements
+    assert load(L, v=A[0] + 512, ks=384, vs=384) == rq.ERR_ALIAS      # ... that wrap into the next row
+    assert load(L, k=A[3]) == rq.ERR_ALIAS
+
+
+def attn(L, q=A[0], qs=1024, cache=A[1], pages=10, page=16, table=A[2], width=8, start=A[3], seq=A[4], kg=A[5], vg=A[6],
+         scale=0.1, window=0, out=A[7], lse=A[8], ws=A[9], wsb=1 << 27, T=4, R=3, h=8, kv=2, d=128, dt=0):
+    return L.rmsq_paged_attention_nvfp4(vp(q), qs, vp(cache), pages, page, vp(table), width, vp(start), vp(seq), vp(kg),
+                                        vp(vg), scale, window, vp(out), vp(lse), vp(ws), wsb, T, R, h, kv, d, dt, None)
+
+
+def test_attention_refusals(L):
+    for kw in ("q", "cache", "table", "start", "seq", "kg", "vg", "out", "ws"):
+        assert attn(L, **{kw: 0}) == rq.ERR_INVALID_ARG, kw
+        assert attn(L, **{kw: A[12] + 2}) == rq.ERR_ALIGNMENT, kw
+    assert attn(L, lse=A[12] + 2) == rq.ERR_ALIGNMENT and attn(L, qs=1028) == rq.ERR_ALIGNMENT
+    nan, inf = float("nan"), float("inf")
+    for kw in ({"dt": 2}, {"T": -1}, {"R": -1}, {"h": 0}, {"kv": 0}, {"scale": 0.0}, {"scale": -1.0}, {"scale": nan},
+               {"scale": inf}, {"window": -1}, {"qs": 1016}, {"pages": -1}, {"width": -1}, {"wsb": 100}):
+        assert attn(L, **kw) == rq.ERR_INVALID_ARG, kw
+    for kw in ({"kv": 3}, {"d": 80}, {"d": 512}, {"page": 8}, {"R": rq.MAX_REQUESTS + 1}, {"T": 1 << 28},
+               {"h": 8192, "kv": 8192}, {"width": 1 << 27}):
+        assert attn(L, **kw) == rq.ERR_UNSUPPORTED_SHAPE, kw
+    assert attn(L, T=0) == rq.OK and attn(L, R=0) == rq.OK
+    for kw in ({"out": A[0]}, {"lse": A[7] + 64}, {"ws": A[1]}, {"out": A[4]}, {"lse": A[9] + 64}):
+        assert attn(L, **kw) == rq.ERR_ALIAS, kw
+
+
+def test_attention_workspace_size(L):
+    small = rq.paged_attention_workspace_bytes(8, 8, 8, 1, 128)
+    assert small > 0 and rq.paged_attention_workspace_bytes(8, 8, 16, 1, 128) >= small
+    assert rq.paged_attention_workspace_bytes(8, 8, 8, 3, 128) == 0
+    assert rq.paged_attention_workspace_bytes(8, 8, 8, 1, 100) == 0
+
+
+def _attn_args(**kw):
+    a = {"q": torch.zeros(4, 8, 128).bfloat16(), "cache": torch.zeros(rq.kv_cache_shape(10, 2, 128, 16), dtype=torch.uint8),
+         "block_table": torch.zeros(3, 8, dtype=I32), "query_start": torch.zeros(4, dtype=I32),
+         "seq_lens": torch.zeros(3, dtype=I32), "k_global_scale": torch.ones(1), "v_global_scale": torch.ones(1),
+         "page_size": 16, "stream": 0}
+    return a | kw
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="CPU tensors")
+def test_binding_refusals(L):
+    with pytest.raises(rq.RmsqError) as e:
+        rq.paged_attention_nvfp4(**_attn_args())
+    assert e.value.status == rq.ERR_NO_DEVICE
+    z = torch.zeros
+    for kw in ({"q": z(4, 8, 128)}, {"block_table": z(3, 8, dtype=torch.int64)}, {"seq_lens": z(3)},
+               {"k_global_scale": torch.ones(1).double()}, {"cache": z(10, 2, 2, 1152)},
+               {"lse": z(4, 8, dtype=torch.float64)}, {"out": z(4, 8, 128)}):
+        with pytest.raises(TypeError):
+            rq.paged_attention_nvfp4(**_attn_args(**kw))
+    u8 = torch.uint8
+    for kw in ({"q": z(4, 8, 256).bfloat16()[..., ::2]}, {"q": z(4, 128).bfloat16()}, {"page_size": 32},
+               {"cache": z(10, 2, 2, 1151, dtype=u8)}, {"cache": z(10, 2, 2, 2304, dtype=u8)[..., ::2]},
+               {"query_start": z(3, dtype=I32)}, {"seq_lens": z(4, dtype=I32)}, {"block_table": z(3, dtype=I32)},
+               {"k_global_scale": torch.ones(2)}, {"out": z(5, 8, 128).bfloat16()}, {"lse": z(4, 9)}):
+        with pytest.raises(ValueError):
+            rq.paged_attention_nvfp4(**_attn_args(**kw))
+    k = z(4, 2, 128).bfloat16()
+    sm, one, cache = torch.arange(4), torch.ones(1), z(rq.kv_cache_shape(10, 2, 128, 16), dtype=u8)
+    for bad in ((k, k[:3], sm, one, one, cache, 16), (k, k, sm[:3], one, one, cache, 16), (k, k, sm, one, one, cache, 32),
+                (k.transpose(0, 1), k.transpose(0, 1), sm[:2], one, one, cache, 16)):
+        with pytest.raises(ValueError):
+            rq.kv_cache_store_nvfp4(*bad, stream=0)
+    with pytest.raises(TypeError):
+        rq.kv_cache_store_nvfp4(k, k.half(), sm, one, one, cache, 16, stream=0)
+    with pytest.raises(TypeError):
+        rq.kv_cache_load_nvfp4(cache, sm, one, one, 128, 16, torch.float32, stream=0)
+    with pytest.raises(ValueError):
+        rq.kv_cache_load_nvfp4(cache, sm, one, one, 64, 16, stream=0)
+    i = lambda *s: z(*s, dtype=I32)  # noqa: E731
+    with pytest.raises(ValueError):
+        rq.build_slot_map(i(3), i(2), i(3, 4), i(9), i(1), 16, 8, stream=0)
+    with pytest.raises(ValueError):
+        rq.build_slot_map(i(3), i(3), i(3, 4), i(9), i(1), 16, -1, stream=0)
+    with pytest.raises(TypeError):
+        rq.build_slot_map(i(3), i(3).long(), i(3, 4), i(9), i(1), 16, 8, stream=0)
+    with pytest.raises(TypeError):
+        rq.build_slot_map(i(3), i(3), i(3, 4), i(9), i(1), 16, 8, slot_map=i(8), stream=0)
+    with pytest.raises(rq.RmsqError) as e:
+        rq.build_slot_map(i(3), i(3), i(3, 4), i(9), i(1), 24, 8, stream=0)
+    assert e.value.status == rq.ERR_UNSUPPORTED_SHAPE
