@@ -39,7 +39,8 @@
  * operators of an attention block: slot maps from request lengths
  * (rmsq_build_slot_map), a paged key / value cache in NVFP4
  * (rmsq_kv_cache_store_nvfp4, rmsq_kv_cache_load_nvfp4) and causal attention
- * over it (rmsq_paged_attention_nvfp4).
+ * over it (rmsq_paged_attention_nvfp4); and the FP8 matrix product that
+ * consumes the group-128 modes' outputs (rmsq_fp8_block_matmul).
  *
  * Conventions for every entry point:
  *   - Pointers marked "device" must be addressable by the current CUDA device
@@ -537,6 +538,31 @@ int rmsq_silu_mul_quant(const void *gate_up, int quant_mode, const float *scale_
                         void *out_scales, int64_t n_tokens, int64_t d, int dtype, void *stream);
 
 /*
+ * rmsq_fp8_block_matmul — the matrix product that consumes what the FP8
+ * group-128 modes write: a linear layer with E4M3 activations (one scale per
+ * row and 128 columns) and E4M3 weights (one scale per 128 x 128 block):
+ *   out[i, j] = T( sum_kb sa[i, kb] * sb[j / 128, kb] * sum_{l in block kb} a[i, l] * b[j, l] )
+ *  a_codes      device, u8 (E4M3) [m, k], 16-byte aligned.
+ *  a_scales     device, as rmsq_fused_add_rmsnorm_quant / rmsq_silu_mul_quant
+ *               write them for
+ *  quant_mode   RMSQ_FP8_GROUP128_ROW or RMSQ_FP8_GROUP128_COL with their
+ *               options (hidden = k, n_tokens = m); any other mode is
+ *               RMSQ_ERR_INVALID_ARG.
+ *  b_codes      device, u8 (E4M3) [n, k], 16-byte aligned.
+ *  b_scales     device, fp32 [ceil(n / 128), k / 128], 4-byte aligned.
+ *  out          device, T[m, n], 16-byte aligned, overlapping no input.
+ *  m            >= 0 (0 returns RMSQ_OK without a launch);
+ *  n            > 0, a multiple of 8;  k > 0, a multiple of 128, at most
+ *               RMSQ_ACT_MAX_D (else RMSQ_ERR_UNSUPPORTED_SHAPE).
+ * The 128 products of a block are summed by the tensor cores in fp32, the
+ * blocks in fp32 registers; out is rounded once.  Deterministic.  NaN codes
+ * give NaN in their row or column.  Asynchronous on `stream`.
+ */
+int rmsq_fp8_block_matmul(const void *a_codes, const void *a_scales, int quant_mode, const void *b_codes,
+                          const float *b_scales, void *out, int64_t m, int64_t n, int64_t k, int dtype,
+                          void *stream);
+
+/*
  * rmsq_set_pipeline_config — process-wide tuning of the PIPELINED variant:
  * chunks_per_thread (16-byte chunks of a row per thread: 1, 2, 4 or 8),
  * stages (rows in flight per CTA: 1..8) and ctas_per_sm (cap on resident
@@ -567,7 +593,7 @@ int rmsq_set_programmatic_launch(int enable);
 
 /*
  * rmsq_take_fault_flags — reads and clears, on the current device, the flag a
- * pipelined launch (norm or QK-norm + RoPE) sets if it ever gives up
+ * pipelined launch (norm or QK-norm + RoPE) or a matrix product sets if it ever gives up
  * waiting (after 100 ms) for its own shared-memory copies; the outputs of
  * such a launch are incomplete.
  * *flags = 0 when no launch gave up.  Synchronous with respect to the device:

@@ -62,7 +62,7 @@ EXPORTS = ("rmsq_fused_add_rmsnorm_quant", "rmsq_fused_add_rmsnorm_quant_ex",
            "rmsq_fused_add_rmsnorm", "rmsq_quant", "rmsq_qk_norm_rope", "rmsq_qk_norm_rope_ex",
            "rmsq_allreduce_add_rmsnorm_quant",
            "rmsq_build_slot_map", "rmsq_kv_cache_store_nvfp4", "rmsq_kv_cache_load_nvfp4",
-           "rmsq_paged_attention_nvfp4", "rmsq_paged_attention_workspace_bytes",
+           "rmsq_paged_attention_nvfp4", "rmsq_paged_attention_workspace_bytes", "rmsq_fp8_block_matmul",
            "rmsq_set_pipeline_config", "rmsq_set_programmatic_launch", "rmsq_take_fault_flags",
            "rmsq_query_sizes", "rmsq_query_launch", "rmsq_debug_convert", "rmsq_debug_activation", "rmsq_debug_bounded_wait",
            "rmsq_status_string", "rmsq_last_cuda_error", "rmsq_version")
@@ -122,6 +122,8 @@ def load(path: str | None = None):
         L.rmsq_paged_attention_nvfp4.restype = ci
         L.rmsq_paged_attention_workspace_bytes.argtypes = [i64, i64, ci, ci, ci]
         L.rmsq_paged_attention_workspace_bytes.restype = ctypes.c_size_t
+        L.rmsq_fp8_block_matmul.argtypes = [vp, vp, ci, vp, vp, vp, i64, i64, i64, ci, vp]
+        L.rmsq_fp8_block_matmul.restype = ci
         L.rmsq_quant.argtypes = [vp, ci, vp, vp, vp, i64, i64, ci, vp]
         L.rmsq_quant.restype = ci
         L.rmsq_silu_mul_quant.argtypes = [vp, ci, vp, vp, vp, i64, i64, ci, vp]
@@ -580,6 +582,53 @@ def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: tor
     if st:
         raise RmsqError(st, "rmsq_paged_attention_nvfp4")
     return out if lse is None else (out, lse)
+
+
+_CODE_TYPES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def fp8_block_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, mode: str, b_codes: torch.Tensor,
+                     b_scales: torch.Tensor, dtype: torch.dtype = torch.bfloat16, *, out: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """rmsq_fp8_block_matmul: out [m, n] = a . b^T of E4M3 codes with block scales.
+
+    a_codes [m, k] and a_scales as fused_add_rmsnorm_quant or silu_mul_quant
+    return them for `mode` ("fp8_group128_row" / "fp8_group128_col" with their
+    options); b_codes [n, k] (uint8 or float8_e4m3fn) with b_scales fp32
+    [ceil(n / 128), k / 128].  out is bf16 or fp16, allocated if missing.
+    """
+    L = load()
+    if dtype not in DTYPES:
+        raise TypeError(f"unsupported activation dtype {dtype}")
+    if a_codes.dtype not in _CODE_TYPES or b_codes.dtype not in _CODE_TYPES:
+        raise TypeError("codes must be uint8 or float8_e4m3fn")
+    code = mode_code(mode)
+    if code & 15 not in (MODES["fp8_group128_row"], MODES["fp8_group128_col"]):
+        raise ValueError(f"the matrix product takes group-128 scales, not {mode!r}")
+    if a_codes.dim() != 2 or b_codes.dim() != 2 or a_codes.shape[1] != b_codes.shape[1]:
+        raise ValueError("codes must be [m, k] and [n, k]")
+    (m, k), n = a_codes.shape, b_codes.shape[0]
+    st_dtype = _U8 if code & OPTIONS["ue8m0"] else _F32
+    if out is None:
+        out = torch.empty(m, n, dtype=dtype, device=a_codes.device)
+    _check_tensors({"a_codes": a_codes, "a_scales": a_scales, "b_codes": b_codes, "b_scales": b_scales, "out": out},
+                   {"a_codes": a_codes.dtype, "a_scales": st_dtype, "b_codes": b_codes.dtype, "b_scales": _F32,
+                    "out": dtype})
+    if code & 15 == MODES["fp8_group128_row"]:
+        shape = (m, k // 128)
+    else:
+        per16 = 16 if code & OPTIONS["ue8m0"] else 4
+        shape = (k // 128, (m + per16 - 1) // per16 * per16 if code & OPTIONS["tma"] else m)
+    _want_shape("a_codes", a_codes, m, k)
+    _want_shape("b_codes", b_codes, n, k)
+    _want_shape("a_scales", a_scales, *shape)
+    _want_shape("b_scales", b_scales, (n + 127) // 128, k // 128)
+    _want_shape("out", out, m, n)
+    st = L.rmsq_fp8_block_matmul(_p(a_codes), _p(a_scales), code, _p(b_codes), _p(b_scales), _p(out), m, n, k,
+                                 DTYPES[dtype], _stream(stream))
+    if st:
+        raise RmsqError(st, "rmsq_fp8_block_matmul")
+    return out
 
 
 def silu_mul_quant(gate_up: torch.Tensor, mode: str, scale_in: torch.Tensor | None = None, *,

@@ -1,0 +1,181 @@
+// FP8 block-scaled matrix product: argument checks, tensor maps, launches.
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "rmsq.h"
+#include "rmsq_abi.h"
+#include "rmsq_host.cuh"
+#include "rmsq_matmul.cuh"
+
+namespace rmsq {
+
+cudaError_t take_mm_fault(unsigned int* out) {
+    const unsigned int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_mm_fault, sizeof(unsigned int));
+    if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(g_mm_fault, &zero, sizeof(zero));
+    return e;
+}
+
+namespace {
+
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// The driver's tensor-map encoder, looked up once.
+EncodeTiled encoder() {
+    static const EncodeTiled fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// A row-major [rows, cols] matrix in boxes of box_rows x 128 bytes, swizzled.
+bool make_map(CUtensorMap* map, const void* p, bool codes, int64_t rows, int64_t cols, int box_rows) {
+    const EncodeTiled enc = encoder();
+    if (!enc) return false;
+    const int elem = codes ? 1 : 2;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * elem};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), static_cast<cuuint32_t>(box_rows)}, one[2] = {1, 1};
+    return enc(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(p), dims,
+               strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct MmCall {
+    const void *a, *b;
+    int64_t m, n, k;
+    MmArgs args;
+};
+
+template <class E, int BN>
+cudaError_t launch_rows(const MmCall& c, int sms, cudaStream_t stream) {
+    using Tile = RowsTile<BN>;
+    const void* fn = (const void*)&mm_rows_kernel<E, BN>;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile::smem);
+    if (e != cudaSuccess) return e;
+    CUtensorMap ma, mb, mo;
+    if (!make_map(&ma, c.a, true, c.m, c.k, 128) || !make_map(&mb, c.b, true, c.n, c.k, BN) ||
+        !make_map(&mo, c.args.out, false, c.m, c.n, 128))
+        return cudaErrorInvalidValue;
+    const int64_t tiles = (c.m + 127) / 128 * ((c.n + BN - 1) / BN);
+    MmArgs args = c.args;
+    void* params[] = {&ma, &mb, &mo, &args};
+    return launch_kernel(fn, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kRowsThreads), params, Tile::smem,
+                         stream);
+}
+
+template <class E, int NT>
+cudaError_t launch_tokens(const MmCall& c, int sms, cudaStream_t stream) {
+    using Tile = TokTile<NT>;
+    const void* fn = (const void*)&mm_tokens_kernel<E, NT>;
+    const int64_t blocks = (c.n + 127) / 128, mt = (c.m + NT - 1) / NT, kb = c.k / 128;
+    // K split in two as long as the CTAs are not two per SM and each keeps two blocks
+    int splits = 1;
+    while (splits < 8 && blocks * mt * splits * 2 <= 2 * sms && kb >= splits * 4) splits *= 2;
+    const int64_t most_kb = (kb + splits - 1) / splits;
+    int stages = static_cast<int>((kTokSmem - 1024 - most_kb * NT * 4) / Tile::stage_bytes);
+    if (stages > Tile::max_stages) stages = Tile::max_stages;
+    // a long run of K leaves too little room for the ring: half as many tokens per CTA
+    if constexpr (NT > 16) {
+        if (stages < 3) return launch_tokens<E, NT / 2>(c, sms, stream);
+    }
+    if (stages < 2) return cudaErrorInvalidConfiguration;
+    CUtensorMap ma, mb;
+    if (!make_map(&ma, c.a, true, c.m, c.k, NT) || !make_map(&mb, c.b, true, c.n, c.k, 128)) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTokSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks * splits), static_cast<unsigned>(mt));
+    cfg.blockDim = dim3(kTokThreads);
+    cfg.dynamicSmemBytes = kTokSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = programmatic_launch() ? 2 : 1;
+    MmArgs args = c.args;
+    void* params[] = {&ma, &mb, &args, &splits, &stages};
+    return cudaLaunchKernelExC(&cfg, fn, params);
+}
+
+template <class E>
+cudaError_t launch_matmul(const MmCall& c, cudaStream_t stream) {
+    cudaError_t e;
+    const int sms = sm_count(&e);
+    if (e != cudaSuccess) return e;
+    const int64_t mt = (c.m + 127) / 128;
+    if (c.m > 128 && mt * ((c.n + 255) / 256) >= sms) return launch_rows<E, 256>(c, sms, stream);
+    if (c.m > 128 && mt * ((c.n + 127) / 128) * 3 >= 2 * sms) return launch_rows<E, 128>(c, sms, stream);
+    if (c.m <= 16) return launch_tokens<E, 16>(c, sms, stream);
+    if (c.m <= 32) return launch_tokens<E, 32>(c, sms, stream);
+    if (c.m <= 64) return launch_tokens<E, 64>(c, sms, stream);
+    return launch_tokens<E, 128>(c, sms, stream);
+}
+
+}  // namespace
+}  // namespace rmsq
+
+extern "C" int rmsq_fp8_block_matmul(const void* a_codes, const void* a_scales, int quant_mode, const void* b_codes,
+                                     const float* b_scales, void* out, int64_t m, int64_t n, int64_t k, int dtype,
+                                     void* stream) {
+    using rmsq_abi::aligned;
+    using rmsq_abi::overlaps;
+    using rmsq_abi::Span;
+    using rmsq_abi::span;
+    if (dtype != RMSQ_BF16 && dtype != RMSQ_FP16) return RMSQ_ERR_INVALID_ARG;
+    const int mode = quant_mode & RMSQ_QUANT_MODE_MASK;
+    if (quant_mode < 0 || (mode != RMSQ_FP8_GROUP128_ROW && mode != RMSQ_FP8_GROUP128_COL)) return RMSQ_ERR_INVALID_ARG;
+    if (m < 0 || n <= 0 || k <= 0) return RMSQ_ERR_INVALID_ARG;
+    // the scale options are the quantisation's; K is its hidden size
+    size_t q_bytes = 0, sa_bytes = 0;
+    int st = rmsq_query_sizes(quant_mode, m, k <= RMSQ_MAX_HIDDEN ? k : 128, &q_bytes, &sa_bytes);
+    if (st != RMSQ_OK) return st;
+    if (k % 128 != 0 || k > RMSQ_ACT_MAX_D || n % 8 != 0 || n > INT32_MAX / 2 || m > INT32_MAX / 2 ||
+        (m + 127) / 128 * ((n + 127) / 128) > INT32_MAX / 2)
+        return RMSQ_ERR_UNSUPPORTED_SHAPE;
+    if (m == 0) return RMSQ_OK;
+    if (!a_codes || !a_scales || !b_codes || !b_scales || !out) return RMSQ_ERR_INVALID_ARG;
+    const bool ue8m0 = (quant_mode & RMSQ_QUANT_UE8M0) != 0, col = mode == RMSQ_FP8_GROUP128_COL;
+    if (!aligned(a_codes, 16) || !aligned(b_codes, 16) || !aligned(out, 16) || !aligned(a_scales, ue8m0 ? 1 : 4) ||
+        !aligned(b_scales, 4))
+        return RMSQ_ERR_ALIGNMENT;
+    const int64_t kb = k / 128, per16 = ue8m0 ? 16 : 4;
+    const int64_t stride = (quant_mode & RMSQ_QUANT_TMA_ALIGNED) ? (m + per16 - 1) / per16 * per16 : m;
+    const size_t width = ue8m0 ? 1 : 4;
+    const Span ins[4] = {span(a_codes, static_cast<size_t>(m) * k),
+                         span(a_scales, static_cast<size_t>(col ? kb * stride : m * kb) * width),
+                         span(b_codes, static_cast<size_t>(n) * k), span(b_scales, static_cast<size_t>((n + 127) / 128) * kb * 4)};
+    const Span O = span(out, static_cast<size_t>(m) * n * 2);
+    for (const Span& in : ins)
+        if (overlaps(O, in)) return RMSQ_ERR_ALIAS;
+    st = rmsq_abi::check_device();
+    if (st != RMSQ_OK) return st;
+    rmsq::MmCall c = {a_codes, b_codes, m, n, k, {}};
+    c.args.sa = a_scales;
+    c.args.sb = b_scales;
+    c.args.out = out;
+    c.args.sa_row = col ? 1 : kb;
+    c.args.sa_kb = col ? stride : 1;
+    c.args.m = static_cast<int>(m);
+    c.args.n = static_cast<int>(n);
+    c.args.kb = static_cast<int>(kb);
+    c.args.ue8m0 = ue8m0;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == RMSQ_BF16 ? rmsq::launch_matmul<rmsq::Bf16T>(c, s) : rmsq::launch_matmul<rmsq::Fp16T>(c, s);
+    return e == cudaSuccess ? RMSQ_OK : rmsq_abi::fail_cuda(e);
+}

@@ -1,0 +1,484 @@
+// FP8 matrix product with block scales on the fifth-generation tensor cores.
+//
+//   out[m, n] = T( sum_kb sa[m, kb] * sb[n / 128, kb] * sum_{k in block kb} a[m, k] * b[n, k] )
+//
+// a: E4M3 codes [M, K] with one scale per row and 128 columns (what the
+// FP8 group-128 modes of this library write), b: E4M3 codes [N, K] with one
+// scale per 128 x 128 block.  The scales are general fp32 numbers, so they
+// cannot be folded into the operands: the matrix unit sums one block of 128
+// products (four K = 32 instructions, accumulator cleared by the first) into
+// tensor memory, and the CTA's other warps read that block sum, multiply it by
+// its scale and add it to the running sum in fp32 registers, while the matrix
+// unit works on the next block in the other half of tensor memory.  That also
+// keeps each chain of matrix-unit additions at 128 terms.
+//
+// Two kernels:
+//  mm_rows_kernel    many rows.  Tile 128 rows x BN columns, accumulator lane =
+//                    row of a, so a thread owns one row: its scale is one
+//                    number per block.  Persistent, one CTA per SM.
+//  mm_tokens_kernel  few rows (decode).  Bound by the bytes of b, so b's 128
+//                    rows are the accumulator's lanes and the tokens its
+//                    16 .. 128 columns, and the blocks of K are split over a
+//                    cluster of up to eight CTAs to occupy the card; the
+//                    partial sums are joined through distributed shared memory,
+//                    in a fixed order.
+//
+// Both: one thread keeps a ring of operand tiles in flight (tensor-map copies,
+// 128-byte swizzle), one thread issues the products, the other warps promote.
+// Every wait is bounded; a role whose wait runs out records it in a flag the
+// host can read, and the CTA drains what it has in flight, frees its tensor
+// memory and returns with its output incomplete.
+#pragma once
+
+#include <cuda.h>
+
+#include "rmsq_device.cuh"
+
+namespace rmsq {
+
+static __device__ unsigned int g_mm_fault;
+
+struct MmArgs {
+    const void* sa;          // fp32 or UE8M0 bytes
+    const float* sb;         // [ceil(N / 128), KB]
+    void* out;               // T[M, N]
+    int64_t sa_row, sa_kb;   // element strides of sa
+    int m, n, kb;            // rows of a, rows of b, blocks of 128 along K
+    bool ue8m0;
+};
+
+// ---------------------------------------------------------------------------
+// PTX
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];"
+                 :: "r"(smem_u32(dst)), "l"(map), "r"(x), "r"(y), "r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];"
+                 :: "l"(map), "r"(smem_u32(src)), "r"(x), "r"(y) : "memory");
+}
+
+__device__ __forceinline__ void tmem_alloc(uint32_t* dst, uint32_t cols) {   // one full warp
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" :: "r"(smem_u32(dst)), "r"(cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t base, uint32_t cols) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(base), "r"(cols) : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// Arrives on `bar` when every product issued before has completed.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" :: "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// Matrix descriptor of a K-major tile of 128-byte rows under the 128-byte
+// swizzle (1024-byte aligned): 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t tile_desc(const void* p) {
+    return static_cast<uint64_t>((smem_u32(p) >> 4) & 0x3fffu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptor: E4M3 x E4M3 -> fp32, both K-major, 128 x N.
+template <int N>
+constexpr uint32_t kMmIdesc = (1u << 4) | (static_cast<uint32_t>(N / 8) << 17) | ((128u / 16u) << 24);
+
+// One block of 128 along K: D = A . B^T as four K = 32 products.
+__device__ __forceinline__ void mma_block(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(a + 2 * i), "l"(b + 2 * i), "r"(idesc), "r"(i) : "memory");
+    }
+}
+
+// Sixteen accumulator columns of the warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld16(float (&r)[16], uint32_t addr) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+                 "%15}, [%16];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+                   "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15])
+                 : "r"(addr));
+}
+
+// Waits for the thread's loads; the registers pass through it, so that no use
+// of them can be moved ahead of the wait.
+__device__ __forceinline__ void tmem_wait(float (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(r[0]), "+f"(r[1]), "+f"(r[2]), "+f"(r[3]), "+f"(r[4]), "+f"(r[5]), "+f"(r[6]), "+f"(r[7]),
+                   "+f"(r[8]), "+f"(r[9]), "+f"(r[10]), "+f"(r[11]), "+f"(r[12]), "+f"(r[13]), "+f"(r[14]), "+f"(r[15])
+                 :: "memory");
+}
+
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The whole warp's answer to a bounded wait of each lane.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    return __all_sync(kFull, mbar_wait_bounded(bar, parity));
+}
+
+__device__ __forceinline__ float load_sa(const MmArgs& a, int row, int kb) {
+    const int64_t i = row * a.sa_row + kb * a.sa_kb;
+    if (a.ue8m0) {
+        const uint32_t e = __ldg(static_cast<const uint8_t*>(a.sa) + i);
+        return __uint_as_float(e ? e << 23 : 0x00400000u);
+    }
+    return __ldg(static_cast<const float*>(a.sa) + i);
+}
+
+constexpr int kMmTile = 128 * 128;   // bytes of a 128-row operand tile
+
+// Waits (bounded) for the copies of the last `stages` of `issued` fills.
+__device__ __forceinline__ void drain_copies(uint64_t* full, int stages, int issued) {
+    for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+        mbar_wait_bounded(&full[i % stages], (i / stages) & 1);
+}
+
+// ---------------------------------------------------------------------------
+// Many rows
+// ---------------------------------------------------------------------------
+template <int BN>
+struct RowsTile {
+    static constexpr int stage_bytes = kMmTile + BN * 128;
+    static constexpr int stages = 196608 / stage_bytes;     // 4 (BN = 256), 6 (BN = 128)
+    static constexpr int staging = 128 * 128;               // 128 rows x 64 columns of T, per warpgroup
+    static constexpr int smem = 1024 + stages * stage_bytes + 2 * staging;
+};
+constexpr int kRowsThreads = 320;   // 8 promoting warps, the copying warp, the issuing warp
+constexpr int kRasterRows = 16;     // row tiles per raster group
+
+// Tile `i` of the raster: groups of kRasterRows row tiles, columns outermost
+// inside a group, so that the tiles in flight share rows and columns in L2.
+__device__ __forceinline__ void raster(int i, int mt, int nt, int& tm, int& tn) {
+    const int per = kRasterRows * nt, group = i / per, rest = i - group * per;
+    const int rows = min(kRasterRows, mt - group * kRasterRows);
+    tn = rest / rows;
+    tm = group * kRasterRows + rest - tn * rows;
+}
+
+template <class E, int BN>
+__global__ void __launch_bounds__(kRowsThreads, 1)
+mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
+               const __grid_constant__ CUtensorMap map_out, const MmArgs a) {
+    using Tile = RowsTile<BN>;
+    constexpr int S = Tile::stages, HALF = BN / 2;
+    extern __shared__ unsigned char dyn[];
+    __shared__ __align__(8) uint64_t full[S], empty[S], tfull[2], tempty[2], drained;
+    __shared__ uint32_t tmem_base;
+    unsigned char* ring = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+    unsigned char* staging = ring + S * Tile::stage_bytes;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < S; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 8);
+        }
+        mbar_init(&drained, 1);
+        fence_mbar_init();
+    }
+    // Tensor memory is taken only once the previous kernel of the stream has
+    // ended, and the next one may start only after that: neither can hold
+    // columns the other still waits for.
+    grid_dependency_wait();
+    if (warp == 9) tmem_alloc(&tmem_base, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    allow_dependents();
+    const uint32_t tmem = tmem_base;
+    const int mt = (a.m + 127) / 128, nt = (a.n + BN - 1) / BN, tiles = mt * nt;
+    bool ok = true;
+
+    if (warp == 8) {
+        if (lane == 0) {
+            int it = 0;
+            for (int i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+                int tm, tn;
+                raster(i, mt, nt, tm, tn);
+                for (int kb = 0; kb < a.kb; ++kb, ++it) {
+                    const int s = it % S;
+                    ok = mbar_wait_bounded(&empty[s], ((it / S) & 1) ^ 1);
+                    if (!ok) break;
+                    unsigned char* st = ring + s * Tile::stage_bytes;
+                    mbar_arrive_expect_tx(&full[s], Tile::stage_bytes);
+                    tma_load_2d(st, &map_a, kb * 128, tm * 128, &full[s]);
+                    tma_load_2d(st + kMmTile, &map_b, kb * 128, tn * BN, &full[s]);
+                }
+            }
+            if (!ok) drain_copies(full, S, it);
+        }
+    } else if (warp == 9) {
+        if (lane == 0) {
+            int it = 0;
+            for (int i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+                for (int kb = 0; kb < a.kb; ++kb, ++it) {
+                    const int s = it % S, b = it & 1;
+                    ok = mbar_wait_bounded(&tempty[b], ((it >> 1) & 1) ^ 1) && mbar_wait_bounded(&full[s], (it / S) & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const unsigned char* st = ring + s * Tile::stage_bytes;
+                    mma_block(tmem + b * BN, tile_desc(st), tile_desc(st + kMmTile), kMmIdesc<BN>);
+                    mma_commit(&empty[s]);
+                    mma_commit(&tfull[b]);
+                }
+            }
+            if (!ok) {
+                mma_commit(&drained);
+                mbar_wait_bounded(&drained, 0);
+            }
+        }
+    } else {
+        const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
+        unsigned char* stage = staging + wg * Tile::staging;
+        int it = 0;
+        // A warp whose wait ran out keeps walking the loop (the warpgroup's
+        // barriers need every warp) without waiting or reading any more.
+        for (int i = blockIdx.x; i < tiles; i += gridDim.x) {
+            int tm, tn;
+            raster(i, mt, nt, tm, tn);
+            const int m = tm * 128 + row, n0 = tn * BN + wg * HALF;
+            const bool live = m < a.m;
+            const float* sb = a.sb + static_cast<int64_t>(min(n0, a.n - 1) / 128) * a.kb;
+            float2 acc[HALF / 2];
+#pragma unroll
+            for (int j = 0; j < HALF / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
+            float scale = live ? load_sa(a, m, 0) * __ldg(sb) : 0.0f;
+            for (int kb = 0; kb < a.kb; ++kb, ++it) {
+                const int b = it & 1;
+                float next = 0.0f;
+                if (live && kb + 1 < a.kb) next = load_sa(a, m, kb + 1) * __ldg(sb + kb + 1);
+                ok = ok && warp_wait(&tfull[b], (it >> 1) & 1);
+                if (!ok) continue;
+                tc_fence_after();
+                const uint32_t addr = tmem + b * BN + wg * HALF + (static_cast<uint32_t>(quad * 32) << 16);
+                const float2 s2 = make_float2(scale, scale);
+                float d[2][16];
+                tmem_ld16(d[0], addr);
+#pragma unroll
+                for (int c = 0; c < HALF / 16; ++c) {
+                    tmem_wait(d[c & 1]);
+                    if (c + 1 < HALF / 16) {
+                        tmem_ld16(d[(c + 1) & 1], addr + (c + 1) * 16);
+                    } else {   // the accumulator has been read: hand it back
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&tempty[b]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        acc[c * 8 + j] = fma2_rn(make_float2(d[c & 1][2 * j], d[c & 1][2 * j + 1]), s2, acc[c * 8 + j]);
+                }
+                scale = next;
+            }
+            // Round to T, through shared memory (swizzled as the tensor map
+            // says) into 64-column stores; rows and columns beyond the matrix
+            // are clipped by the copy.
+#pragma unroll
+            for (int h = 0; h < HALF / 64; ++h) {
+                if (quad == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                named_sync(1 + wg, 128);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    const float2* v = &acc[h * 32 + c * 4];
+                    *reinterpret_cast<uint4*>(stage + row * 128 + ((c ^ (row & 7)) << 4)) =
+                        make_uint4(E::pack(v[0].x, v[0].y), E::pack(v[1].x, v[1].y), E::pack(v[2].x, v[2].y),
+                                   E::pack(v[3].x, v[3].y));
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                named_sync(1 + wg, 128);
+                if (quad == 0 && lane == 0) {
+                    if (ok && n0 + h * 64 < a.n) tma_store_2d(&map_out, stage, n0 + h * 64, tm * 128);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                }
+            }
+        }
+        if (quad == 0 && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+    if (!ok) atomicOr(&g_mm_fault, 1u);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_free(tmem, 512);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows
+// ---------------------------------------------------------------------------
+constexpr int kTokThreads = 192;    // 4 promoting warps, the copying warp, the issuing warp
+constexpr int kTokSmem = 110 * 1024;   // two CTAs per SM, never three: their tensor memory then always fits together
+
+// Shared memory: the ring, then the scales [blocks of this CTA][NT].  The
+// ring's space later holds the partial sums [NT][128].
+template <int NT>
+struct TokTile {
+    static constexpr int stage_bytes = kMmTile + NT * 128;
+    static constexpr int sums = NT * 128 * 4;
+    static constexpr uint32_t cols = 2 * NT < 32 ? 32 : 2 * NT;
+    static constexpr int max_stages = 8;
+};
+
+template <class E, int NT>
+__global__ void __launch_bounds__(kTokThreads)
+mm_tokens_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b, const MmArgs a,
+                 const int splits, const int stages) {
+    using Tile = TokTile<NT>;
+    extern __shared__ unsigned char dyn[];
+    __shared__ __align__(8) uint64_t full[Tile::max_stages], empty[Tile::max_stages], tfull[2], tempty[2], drained;
+    __shared__ uint32_t tmem_base;
+    unsigned char* ring = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+    float* scales = reinterpret_cast<float*>(ring + stages * Tile::stage_bytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // The cluster spans blockIdx.x: its CTAs share a block of b's rows and
+    // divide K.
+    const int part = blockIdx.x % splits, tn = blockIdx.x / splits, m0 = blockIdx.y * NT;
+    const int kb0 = static_cast<int>(static_cast<int64_t>(a.kb) * part / splits);
+    const int nkb = static_cast<int>(static_cast<int64_t>(a.kb) * (part + 1) / splits) - kb0;
+    if (tid == 0) {
+        for (int i = 0; i < stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&tfull[i], 1);
+            mbar_init(&tempty[i], 4);
+        }
+        mbar_init(&drained, 1);
+        fence_mbar_init();
+    }
+    grid_dependency_wait();
+    if (warp == 5) tmem_alloc(&tmem_base, Tile::cols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    allow_dependents();
+    const uint32_t tmem = tmem_base;
+    bool ok = true;
+    if (warp == 4) {
+        if (lane == 0) {
+            int kb = 0;
+            for (; kb < nkb; ++kb) {
+                const int s = kb % stages;
+                ok = mbar_wait_bounded(&empty[s], ((kb / stages) & 1) ^ 1);
+                if (!ok) break;
+                unsigned char* st = ring + s * Tile::stage_bytes;
+                mbar_arrive_expect_tx(&full[s], Tile::stage_bytes);
+                tma_load_2d(st, &map_b, (kb0 + kb) * 128, tn * 128, &full[s]);
+                tma_load_2d(st + kMmTile, &map_a, (kb0 + kb) * 128, m0, &full[s]);
+            }
+            if (!ok) drain_copies(full, stages, kb);
+        }
+    } else if (warp == 5) {
+        if (lane == 0) {
+            for (int kb = 0; kb < nkb; ++kb) {
+                const int s = kb % stages, b = kb & 1;
+                ok = mbar_wait_bounded(&tempty[b], ((kb >> 1) & 1) ^ 1) && mbar_wait_bounded(&full[s], (kb / stages) & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const unsigned char* st = ring + s * Tile::stage_bytes;
+                mma_block(tmem + b * NT, tile_desc(st), tile_desc(st + kMmTile), kMmIdesc<NT>);
+                mma_commit(&empty[s]);
+                mma_commit(&tfull[b]);
+            }
+            if (!ok) {
+                mma_commit(&drained);
+                mbar_wait_bounded(&drained, 0);
+            }
+        }
+    } else {
+        // sa * sb of the CTA's blocks, while the first tiles are on their way
+        for (int i = tid; i < nkb * NT; i += 128) {
+            const int kb = i / NT, m = m0 + i % NT;
+            scales[i] = m < a.m ? load_sa(a, m, kb0 + kb) * __ldg(a.sb + static_cast<int64_t>(tn) * a.kb + kb0 + kb) : 0.0f;
+        }
+        named_sync(1, 128);
+        float2 acc[NT / 2];
+#pragma unroll
+        for (int j = 0; j < NT / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
+        for (int kb = 0; kb < nkb; ++kb) {
+            const int b = kb & 1;
+            ok = warp_wait(&tfull[b], (kb >> 1) & 1);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t addr = tmem + b * NT + (static_cast<uint32_t>(warp * 32) << 16);
+            const float4* sc = reinterpret_cast<const float4*>(scales + kb * NT);
+            float d[2][16];
+            tmem_ld16(d[0], addr);
+#pragma unroll
+            for (int c = 0; c < NT / 16; ++c) {
+                tmem_wait(d[c & 1]);
+                if (c + 1 < NT / 16) {
+                    tmem_ld16(d[(c + 1) & 1], addr + (c + 1) * 16);
+                } else {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&tempty[b]);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float4 s = sc[c * 4 + j];
+                    const float* v = &d[c & 1][4 * j];
+                    acc[c * 8 + 2 * j] = fma2_rn(make_float2(v[0], v[1]), make_float2(s.x, s.y), acc[c * 8 + 2 * j]);
+                    acc[c * 8 + 2 * j + 1] = fma2_rn(make_float2(v[2], v[3]), make_float2(s.z, s.w), acc[c * 8 + 2 * j + 1]);
+                }
+            }
+        }
+        if (ok) {   // every product has completed, so nothing reads the ring any more
+            float* sums = reinterpret_cast<float*>(ring);
+            const int row = warp * 32 + lane;
+#pragma unroll
+            for (int j = 0; j < NT / 2; ++j) {
+                sums[(2 * j) * 128 + row] = acc[j].x;
+                sums[(2 * j + 1) * 128 + row] = acc[j].y;
+            }
+        }
+    }
+    if (!ok) atomicOr(&g_mm_fault, 1u);
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 5) tmem_free(tmem, Tile::cols);
+    // Join: CTA `part` sums its share of the columns over the cluster, in
+    // order of K, two rows of b per thread.
+    const int c0 = NT * part / splits, c1 = min(NT * (part + 1) / splits, a.m - m0);
+    const uint32_t sums = smem_u32(ring);
+    for (int i = tid; i < (c1 - c0) * 64; i += kTokThreads) {
+        const int c = c0 + i / 64, r = i % 64 * 2, n = tn * 128 + r;
+        if (n >= a.n) continue;
+        float x = 0.0f, y = 0.0f;
+        for (int p = 0; p < splits; ++p) {
+            uint32_t at;
+            float u, v;
+            asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(sums + (c * 128 + r) * 4), "r"(p));
+            asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(u), "=f"(v) : "r"(at) : "memory");
+            x += u;
+            y += v;
+        }
+        static_cast<uint32_t*>(a.out)[(static_cast<int64_t>(m0 + c) * a.n + n) >> 1] = E::pack(x, y);
+    }
+    cluster_sync();   // the sums stay until every CTA has read them
+}
+
+}  // namespace rmsq

@@ -40,6 +40,7 @@ def test_valid_calls_reach_the_device_check(L):
     assert store(L, k=A[0], v=A[0] + 1024, ks=2048, vs=2048) in NO_GPU
     assert load(L, k=A[0], v=A[0] + 1024, ks=1024, vs=1024) in NO_GPU
     assert attn(L, lse=0) in NO_GPU
+    assert matmul(L) in NO_GPU and matmul(L, mode=3 | 0x40 | 0x20, sa=A[1] + 1) in NO_GPU
 
 
 def test_slot_map_refusals(L):
@@ -120,6 +121,50 @@ def test_attention_workspace_size(L):
     assert small > 0 and rq.paged_attention_workspace_bytes(8, 8, 16, 1, 128) >= small
     assert rq.paged_attention_workspace_bytes(8, 8, 8, 3, 128) == 0
     assert rq.paged_attention_workspace_bytes(8, 8, 8, 1, 100) == 0
+
+
+def matmul(L, a=A[0], sa=A[1], mode=2, b=A[2], sb=A[3], out=A[4], m=4, n=256, k=512, dt=0):
+    return L.rmsq_fp8_block_matmul(vp(a), vp(sa), mode, vp(b), vp(sb), vp(out), m, n, k, dt, None)
+
+
+def test_matmul_refusals(L):
+    for kw in ("a", "sa", "b", "sb", "out"):
+        assert matmul(L, **{kw: 0}) == rq.ERR_INVALID_ARG, kw
+        assert matmul(L, **{kw: A[12] + 2}) == rq.ERR_ALIGNMENT, kw
+    # every mode without a scale per 128 columns, unknown bits, options that do not apply
+    for mode in (0, 1, 4, 5, 6, 7, -1, 2 | 0x80, 2 | 0x20):
+        assert matmul(L, mode=mode) == rq.ERR_INVALID_ARG, mode
+    for kw in ({"dt": 2}, {"m": -1}, {"n": 0}, {"k": 0}):
+        assert matmul(L, **kw) == rq.ERR_INVALID_ARG, kw
+    for kw in ({"n": 257}, {"n": 252}, {"k": 64}, {"k": 500}, {"k": 32768 + 128}, {"m": 1 << 31}, {"n": 1 << 31}):
+        assert matmul(L, **kw) == rq.ERR_UNSUPPORTED_SHAPE, kw
+    assert matmul(L, m=0) == rq.OK
+    for kw in ({"out": A[0]}, {"out": A[1]}, {"out": A[2] + 256}, {"out": A[3]}):
+        assert matmul(L, **kw) == rq.ERR_ALIAS, kw
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="CPU tensors")
+def test_matmul_binding_refusals(L):
+    u8 = torch.uint8
+    a, b = torch.zeros(5, 256, dtype=u8), torch.zeros(200, 256, dtype=u8)
+    sa, sb = torch.zeros(5, 2), torch.zeros(2, 2)
+    with pytest.raises(rq.RmsqError) as e:
+        rq.fp8_block_matmul(a, sa, "fp8_group128_row", b, sb, stream=0)
+    assert e.value.status == rq.ERR_NO_DEVICE
+    with pytest.raises(rq.RmsqError) as e:
+        rq.fp8_block_matmul(a.view(torch.float8_e4m3fn), torch.zeros(2, 16, dtype=u8), "fp8_group128_col+ue8m0+tma", b, sb,
+                            torch.float16, stream=0)
+    assert e.value.status == rq.ERR_NO_DEVICE
+    for args in ((a, sa, "fp8_per_token", b, sb), (a, sa, "fp8_group64_row", b, sb), (a, sa, "fp8_group128_col", b, sb),
+                 (a, sa, "fp8_group128_row", b[:, :128], sb), (a, sa, "fp8_group128_row", b, sb[:1]),
+                 (a[:, ::2], sa, "fp8_group128_row", b[:, ::2], sb), (a, sa[:, :1], "fp8_group128_row", b, sb)):
+        with pytest.raises(ValueError):
+            rq.fp8_block_matmul(*args, stream=0)
+    for args in ((a.float(), sa, "fp8_group128_row", b, sb), (a, sa.double(), "fp8_group128_row", b, sb),
+                 (a, sa, "fp8_group128_row+ue8m0", b, sb), (a, sa, "fp8_group128_row", b, sb.half()),
+                 (a, sa, "fp8_group128_row", b, sb, torch.float32)):
+        with pytest.raises(TypeError):
+            rq.fp8_block_matmul(*args, stream=0)
 
 
 def _attn_args(**kw):
