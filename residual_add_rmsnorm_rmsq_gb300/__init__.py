@@ -8,6 +8,7 @@ instead of computing anything another way.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -36,6 +37,7 @@ MODES = {
 OPTIONS = {"e8m0": 0x10, "tma": 0x20, "ue8m0": 0x40}
 
 
+@functools.lru_cache(maxsize=None)
 def mode_code(mode: str) -> int:
     """The C quant_mode argument for a mode name with optional "+e8m0" / "+tma"."""
     base, *opts = mode.split("+")
@@ -84,6 +86,8 @@ _lib = None
 def load(path: str | None = None):
     """Load librmsq.so (built by ``residual_add_rmsnorm_rmsq_gb300._build.build()``)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -172,13 +176,21 @@ def query_sizes(mode: str, n_tokens: int, hidden: int) -> tuple[int, int]:
 
 
 def _p(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> ctypes.c_void_p:
+# The current stream's handle without building a Stream object for it (0.1
+# instead of 2.9 us a call on the Grace host); the public way where a torch
+# build lacks the function.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None and torch.cuda.is_initialized():
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def scales_like(mode: str, n_tokens: int, hidden: int, device) -> torch.Tensor | None:
@@ -377,8 +389,17 @@ def _check_tensors(named, dtypes) -> None:
             raise ValueError(f"{name} is on {t.device}, the others on {device}")
 
 
+def _fits(t: torch.Tensor, dtype: torch.dtype, device: int, shape: tuple) -> bool:
+    """The checks below in one go, for the path without an error."""
+    return t.dtype is dtype and t.get_device() == device and t.shape == shape and t.is_contiguous()
+
+
+def _is_current(device: int) -> bool:
+    return device >= 0 and device == torch.cuda.current_device()
+
+
 def _want_shape(name: str, t: torch.Tensor, *shape) -> None:
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -389,9 +410,10 @@ def _token_rows(name: str, t: torch.Tensor) -> int:
     if t.dim() != 3:
         raise ValueError(f"{name} must be [tokens, heads, head_dim]")
     n, h, d = t.shape
-    if (t.stride(2) != 1 and d > 1) or (t.stride(1) != d and h > 1):
+    per_token, per_head, per_element = t.stride()
+    if (per_element != 1 and d > 1) or (per_head != d and h > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(0) if n > 1 else h * d
+    return per_token if n > 1 else h * d
 
 
 _I32, _I64, _F32, _U8 = torch.int32, torch.int64, torch.float32, torch.uint8
@@ -417,23 +439,16 @@ def build_slot_map(context_lens: torch.Tensor, query_lens: torch.Tensor, block_t
     """
     L = load()
     R, width = block_table.shape
-    dev = block_table.device
-    given = {"context_lens": context_lens, "query_lens": query_lens, "block_table": block_table,
-             "free_pages": free_pages, "num_free": num_free, "slot_map": slot_map, "positions": positions,
-             "query_start": query_start, "seq_lens": seq_lens, "num_free_out": num_free_out, "status": status}
-    _check_tensors(given, _SLOT_TYPES)
-    if max_tokens < 0:
-        raise ValueError("max_tokens must be >= 0")
-    sizes = {"context_lens": (R,), "query_lens": (R,), "block_table": (R, width), "free_pages": (free_pages.numel(),),
-             "num_free": (1,), "slot_map": (max_tokens,), "positions": (max_tokens,), "query_start": (R + 1,),
-             "seq_lens": (R,), "num_free_out": (1,), "status": (1,)}
-    for name, t in given.items():
-        if t is not None:
-            _want_shape(name, t, *sizes[name])
+    dev, i = block_table.device, block_table.get_device()
+    if slot_map is None and positions is None and max_tokens > 0:
+        slot_map, positions = torch.empty(2 * max_tokens, dtype=_I64, device=dev).split_with_sizes((max_tokens, max_tokens))
+    if query_start is None and seq_lens is None and num_free_out is None and status is None:
+        query_start, seq_lens, num_free_out, status = torch.empty(2 * R + 3, dtype=_I32, device=dev).split_with_sizes(
+            (R + 1, R, 1, 1))
     if slot_map is None:
-        slot_map = torch.empty(max_tokens, dtype=_I64, device=dev)
+        slot_map = torch.empty(max(max_tokens, 0), dtype=_I64, device=dev)
     if positions is None:
-        positions = torch.empty(max_tokens, dtype=_I64, device=dev)
+        positions = torch.empty(max(max_tokens, 0), dtype=_I64, device=dev)
     if query_start is None:
         query_start = torch.empty(R + 1, dtype=_I32, device=dev)
     if seq_lens is None:
@@ -442,8 +457,23 @@ def build_slot_map(context_lens: torch.Tensor, query_lens: torch.Tensor, block_t
         num_free_out = torch.empty(1, dtype=_I32, device=dev)
     if status is None:
         status = torch.empty(1, dtype=_I32, device=dev)
+    per_r, one, per_t, capacity = (R,), (1,), (max_tokens,), free_pages.shape
+    if not (_is_current(i) and _fits(context_lens, _I32, i, per_r) and _fits(query_lens, _I32, i, per_r) and
+            _fits(block_table, _I32, i, (R, width)) and _fits(free_pages, _I32, i, capacity) and
+            _fits(num_free, _I32, i, one) and _fits(slot_map, _I64, i, per_t) and _fits(positions, _I64, i, per_t) and
+            _fits(query_start, _I32, i, (R + 1,)) and _fits(seq_lens, _I32, i, per_r) and
+            _fits(num_free_out, _I32, i, one) and _fits(status, _I32, i, one) and len(capacity) == 1):
+        given = {"context_lens": context_lens, "query_lens": query_lens, "block_table": block_table,
+                 "free_pages": free_pages, "num_free": num_free, "slot_map": slot_map, "positions": positions,
+                 "query_start": query_start, "seq_lens": seq_lens, "num_free_out": num_free_out, "status": status}
+        _check_tensors(given, _SLOT_TYPES)
+        sizes = {"context_lens": per_r, "query_lens": per_r, "block_table": (R, width),
+                 "free_pages": (free_pages.numel(),), "num_free": one, "slot_map": per_t, "positions": per_t,
+                 "query_start": (R + 1,), "seq_lens": per_r, "num_free_out": one, "status": one}
+        for name, t in given.items():
+            _want_shape(name, t, *sizes[name])
     st = L.rmsq_build_slot_map(_p(context_lens), _p(query_lens), _p(block_table), width, _p(free_pages),
-                               free_pages.numel(), _p(num_free), page_size, R, max_tokens, _p(slot_map), _p(positions),
+                               capacity[0], _p(num_free), page_size, R, max_tokens, _p(slot_map), _p(positions),
                                _p(query_start), _p(seq_lens), _p(num_free_out), _p(status), _stream(stream))
     if st:
         raise RmsqError(st, "rmsq_build_slot_map")
@@ -458,6 +488,12 @@ def kv_cache_shape(num_pages: int, num_kv_heads: int, head_dim: int, page_size: 
 def _check_cache(cache: torch.Tensor, num_kv_heads: int, head_dim: int, page_size: int) -> int:
     _want_shape("cache", cache, *kv_cache_shape(cache.shape[0], num_kv_heads, head_dim, page_size))
     return cache.shape[0]
+
+
+def _check_global_scales(*scales) -> None:
+    for t in scales:
+        if t.numel() != 1:
+            raise ValueError("a global scale is one element")
 
 
 def _act_types(t: torch.Tensor) -> torch.dtype:
@@ -478,13 +514,16 @@ def kv_cache_store_nvfp4(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tenso
     n, h, d = k.shape
     if v.shape != k.shape:
         raise ValueError("k and v must have one shape")
-    _check_tensors({"k": k, "v": v, "slot_map": slot_map, "k_global_scale": k_global_scale,
-                    "v_global_scale": v_global_scale, "cache": cache},
-                   {"k": dt, "v": dt, "slot_map": _I64, "k_global_scale": _F32, "v_global_scale": _F32, "cache": _U8})
-    _want_shape("slot_map", slot_map, n)
-    pages = _check_cache(cache, h, d, page_size)
-    if k_global_scale.numel() != 1 or v_global_scale.numel() != 1:
-        raise ValueError("a global scale is one element")
+    i, pages = cache.get_device(), cache.shape[0]
+    if not (_is_current(i) and _fits(cache, _U8, i, kv_cache_shape(pages, h, d, page_size)) and
+            _fits(slot_map, _I64, i, (n,)) and _fits(k_global_scale, _F32, i, (1,)) and
+            _fits(v_global_scale, _F32, i, (1,)) and k.get_device() == i and v.get_device() == i and v.dtype is dt):
+        _check_tensors({"k": k, "v": v, "slot_map": slot_map, "k_global_scale": k_global_scale,
+                        "v_global_scale": v_global_scale, "cache": cache},
+                       {"k": dt, "v": dt, "slot_map": _I64, "k_global_scale": _F32, "v_global_scale": _F32, "cache": _U8})
+        _want_shape("slot_map", slot_map, n)
+        _check_cache(cache, h, d, page_size)
+        _check_global_scales(k_global_scale, v_global_scale)
     st = L.rmsq_kv_cache_store_nvfp4(_p(k), ks, _p(v), vs, _p(slot_map), _p(k_global_scale), _p(v_global_scale),
                                      _p(cache), pages, page_size, n, h, d, DTYPES[dt], _stream(stream))
     if st:
@@ -503,21 +542,26 @@ def kv_cache_load_nvfp4(cache: torch.Tensor, slot_map: torch.Tensor, k_global_sc
     if cache.dim() != 4:
         raise ValueError("cache must be [pages, 2, kv heads, bytes of a tile]")
     n, h = slot_map.shape[0], cache.shape[2]
-    _check_tensors({"cache": cache, "slot_map": slot_map, "k_global_scale": k_global_scale,
-                    "v_global_scale": v_global_scale, "k_out": k_out, "v_out": v_out},
-                   {"cache": _U8, "slot_map": _I64, "k_global_scale": _F32, "v_global_scale": _F32, "k_out": dtype,
-                    "v_out": dtype})
-    _want_shape("slot_map", slot_map, n)
-    pages = _check_cache(cache, h, head_dim, page_size)
-    if k_global_scale.numel() != 1 or v_global_scale.numel() != 1:
-        raise ValueError("a global scale is one element")
+    shape = (n, h, head_dim)
     if k_out is None:
-        k_out = torch.empty(n, h, head_dim, dtype=dtype, device=cache.device)
+        k_out = torch.empty(shape, dtype=dtype, device=cache.device)
     if v_out is None:
-        v_out = torch.empty(n, h, head_dim, dtype=dtype, device=cache.device)
+        v_out = torch.empty(shape, dtype=dtype, device=cache.device)
     ks, vs = _token_rows("k_out", k_out), _token_rows("v_out", v_out)
-    if tuple(k_out.shape) != (n, h, head_dim) or tuple(v_out.shape) != (n, h, head_dim):
-        raise ValueError(f"outputs must have shape {(n, h, head_dim)}")
+    i, pages = cache.get_device(), cache.shape[0]
+    if not (_is_current(i) and _fits(cache, _U8, i, kv_cache_shape(pages, h, head_dim, page_size)) and
+            _fits(slot_map, _I64, i, (n,)) and _fits(k_global_scale, _F32, i, (1,)) and
+            _fits(v_global_scale, _F32, i, (1,)) and k_out.get_device() == i and v_out.get_device() == i and
+            k_out.dtype is dtype and v_out.dtype is dtype):
+        _check_tensors({"cache": cache, "slot_map": slot_map, "k_global_scale": k_global_scale,
+                        "v_global_scale": v_global_scale, "k_out": k_out, "v_out": v_out},
+                       {"cache": _U8, "slot_map": _I64, "k_global_scale": _F32, "v_global_scale": _F32, "k_out": dtype,
+                        "v_out": dtype})
+        _want_shape("slot_map", slot_map, n)
+        _check_cache(cache, h, head_dim, page_size)
+        _check_global_scales(k_global_scale, v_global_scale)
+    if k_out.shape != shape or v_out.shape != shape:
+        raise ValueError(f"outputs must have shape {shape}")
     st = L.rmsq_kv_cache_load_nvfp4(_p(cache), pages, page_size, _p(slot_map), _p(k_global_scale), _p(v_global_scale),
                                     _p(k_out), ks, _p(v_out), vs, n, h, head_dim, DTYPES[dtype], _stream(stream))
     if st:
@@ -553,31 +597,36 @@ def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: tor
         raise ValueError("cache must be [pages, 2, kv heads, bytes of a tile], block_table [requests, width]")
     kv, (R, width) = cache.shape[2], block_table.shape
     if out is None:
-        out = torch.empty(n, heads, d, dtype=dt, device=q.device)
+        out = torch.empty((n, heads, d), dtype=dt, device=q.device)
     if lse is None and return_lse:
-        lse = torch.empty(n, heads, dtype=_F32, device=q.device)
+        lse = torch.empty((n, heads), dtype=_F32, device=q.device)
     if workspace is None:
         workspace = torch.empty(paged_attention_workspace_bytes(n, R, heads, kv, d), dtype=_U8, device=q.device)
-    _check_tensors({"q": q, "cache": cache, "block_table": block_table, "query_start": query_start,
-                    "seq_lens": seq_lens, "k_global_scale": k_global_scale, "v_global_scale": v_global_scale,
-                    "out": out, "lse": lse, "workspace": workspace},
-                   {"q": dt, "cache": _U8, "block_table": _I32, "query_start": _I32, "seq_lens": _I32,
-                    "k_global_scale": _F32, "v_global_scale": _F32, "out": dt, "lse": _F32, "workspace": _U8})
-    pages = _check_cache(cache, kv, d, page_size)
-    _want_shape("block_table", block_table, R, width)
-    _want_shape("query_start", query_start, R + 1)
-    _want_shape("seq_lens", seq_lens, R)
-    _want_shape("out", out, n, heads, d)
-    if lse is not None:
-        _want_shape("lse", lse, n, heads)
-    _want_shape("workspace", workspace, workspace.numel())
-    if k_global_scale.numel() != 1 or v_global_scale.numel() != 1:
-        raise ValueError("a global scale is one element")
+    i, pages, size = q.get_device(), cache.shape[0], workspace.numel()
+    if not (_is_current(i) and _fits(cache, _U8, i, kv_cache_shape(pages, kv, d, page_size)) and
+            _fits(block_table, _I32, i, (R, width)) and _fits(query_start, _I32, i, (R + 1,)) and
+            _fits(seq_lens, _I32, i, (R,)) and _fits(k_global_scale, _F32, i, (1,)) and
+            _fits(v_global_scale, _F32, i, (1,)) and _fits(out, dt, i, (n, heads, d)) and
+            (lse is None or _fits(lse, _F32, i, (n, heads))) and _fits(workspace, _U8, i, (size,))):
+        _check_tensors({"q": q, "cache": cache, "block_table": block_table, "query_start": query_start,
+                        "seq_lens": seq_lens, "k_global_scale": k_global_scale, "v_global_scale": v_global_scale,
+                        "out": out, "lse": lse, "workspace": workspace},
+                       {"q": dt, "cache": _U8, "block_table": _I32, "query_start": _I32, "seq_lens": _I32,
+                        "k_global_scale": _F32, "v_global_scale": _F32, "out": dt, "lse": _F32, "workspace": _U8})
+        _check_cache(cache, kv, d, page_size)
+        _want_shape("block_table", block_table, R, width)
+        _want_shape("query_start", query_start, R + 1)
+        _want_shape("seq_lens", seq_lens, R)
+        _want_shape("out", out, n, heads, d)
+        if lse is not None:
+            _want_shape("lse", lse, n, heads)
+        _want_shape("workspace", workspace, size)
+        _check_global_scales(k_global_scale, v_global_scale)
     if softmax_scale is None:
         softmax_scale = d ** -0.5
     st = L.rmsq_paged_attention_nvfp4(_p(q), qs, _p(cache), pages, page_size, _p(block_table), width, _p(query_start),
                                       _p(seq_lens), _p(k_global_scale), _p(v_global_scale), softmax_scale, window, _p(out),
-                                      _p(lse), _p(workspace), workspace.numel(), n, R, heads, kv, d, DTYPES[dt],
+                                      _p(lse), _p(workspace), size, n, R, heads, kv, d, DTYPES[dt],
                                       _stream(stream))
     if st:
         raise RmsqError(st, "rmsq_paged_attention_nvfp4")
@@ -610,20 +659,24 @@ def fp8_block_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, mode: str, b
     (m, k), n = a_codes.shape, b_codes.shape[0]
     st_dtype = _U8 if code & OPTIONS["ue8m0"] else _F32
     if out is None:
-        out = torch.empty(m, n, dtype=dtype, device=a_codes.device)
-    _check_tensors({"a_codes": a_codes, "a_scales": a_scales, "b_codes": b_codes, "b_scales": b_scales, "out": out},
-                   {"a_codes": a_codes.dtype, "a_scales": st_dtype, "b_codes": b_codes.dtype, "b_scales": _F32,
-                    "out": dtype})
+        out = torch.empty((m, n), dtype=dtype, device=a_codes.device)
     if code & 15 == MODES["fp8_group128_row"]:
         shape = (m, k // 128)
     else:
         per16 = 16 if code & OPTIONS["ue8m0"] else 4
         shape = (k // 128, (m + per16 - 1) // per16 * per16 if code & OPTIONS["tma"] else m)
-    _want_shape("a_codes", a_codes, m, k)
-    _want_shape("b_codes", b_codes, n, k)
-    _want_shape("a_scales", a_scales, *shape)
-    _want_shape("b_scales", b_scales, (n + 127) // 128, k // 128)
-    _want_shape("out", out, m, n)
+    i, b_shape = a_codes.get_device(), ((n + 127) // 128, k // 128)
+    if not (_is_current(i) and a_codes.is_contiguous() and _fits(a_scales, st_dtype, i, shape) and
+            _fits(b_codes, b_codes.dtype, i, (n, k)) and _fits(b_scales, _F32, i, b_shape) and
+            _fits(out, dtype, i, (m, n))):
+        _check_tensors({"a_codes": a_codes, "a_scales": a_scales, "b_codes": b_codes, "b_scales": b_scales, "out": out},
+                       {"a_codes": a_codes.dtype, "a_scales": st_dtype, "b_codes": b_codes.dtype, "b_scales": _F32,
+                        "out": dtype})
+        _want_shape("a_codes", a_codes, m, k)
+        _want_shape("b_codes", b_codes, n, k)
+        _want_shape("a_scales", a_scales, *shape)
+        _want_shape("b_scales", b_scales, *b_shape)
+        _want_shape("out", out, m, n)
     st = L.rmsq_fp8_block_matmul(_p(a_codes), _p(a_scales), code, _p(b_codes), _p(b_scales), _p(out), m, n, k,
                                  DTYPES[dtype], _stream(stream))
     if st:

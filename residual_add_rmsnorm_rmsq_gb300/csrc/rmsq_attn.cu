@@ -9,6 +9,14 @@
 #include "rmsq_host.cuh"
 
 namespace rmsq {
+
+cudaError_t take_attn_fault(unsigned int* out) {
+    const unsigned int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_attn_fault, sizeof(unsigned int));
+    if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(g_attn_fault, &zero, sizeof(zero));
+    return e;
+}
+
 namespace {
 
 // Row blocks of 8: two (16 rows share a pass over the keys) where a request
@@ -27,15 +35,17 @@ cudaError_t launch_split(AttnArgs a, int64_t max_tiles, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const void* split = (const void*)&attn_split_kernel<E, D, NB>;
     const void* join = (const void*)&attn_join_kernel<E, D, NB>;
-    const int smem = (a.requests + 1) * 8;
-    if (smem > 12 * 1024) {   // beyond what the default 48 KB leave beside the static part
-        const int most = (RMSQ_MAX_REQUESTS + 1) * 8;
+    // the scanned tile counts, in steps of 1 KB (so that few launch shapes occur)
+    const int smem = ((a.requests + 1) * 8 + 1023) / 1024 * 1024;
+    if (smem > 8 * 1024) {   // beyond what the default 48 KB leave beside the static part
+        const int most = ((RMSQ_MAX_REQUESTS + 1) * 8 + 1023) / 1024 * 1024;
         e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e == cudaSuccess) e = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return e;
     }
-    int per_sm = 0;
-    e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, split, kAttnThreads, smem);
+    e = cudaFuncSetAttribute(split, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (e != cudaSuccess) return e;
+    const int per_sm = occupancy_blocks(split, kAttnThreads, smem, &e);
     if (e != cudaSuccess) return e;
     if (per_sm < 1) return cudaErrorInvalidConfiguration;
     int64_t workers = static_cast<int64_t>(per_sm) * sms;

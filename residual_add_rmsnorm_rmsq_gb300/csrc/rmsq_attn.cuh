@@ -19,8 +19,9 @@
 // 2^kPShift so that those down to 2^-23 of the maximum keep all their bits.
 //
 // Layout: contractions may take their index in any order, so every lane loads
-// the piece of the cache it needs straight into registers, 16 bytes at a time,
-// with no shared memory and no shuffle.  Lane (g, t) = (lane / 4, lane % 4):
+// the piece of the cache it needs in one access, with no shuffle.  Each warp
+// keeps the next steps in flight as bulk copies into a ring of its own.
+// Lane (g, t) = (lane / 4, lane % 4):
 //   K: dims t * D/4 .. of keys kappa(g) and kappa(g) + 8;
 //   V: dims g * D/8 .. of keys t, t + 4, t + 8, t + 12 (one scale block for
 //      D = 128), whose nibbles are interleaved pairwise so that one
@@ -65,6 +66,8 @@ struct AttnArgs {
     int page_shift, num_pages, window, workers;
     float scale_log2;       // softmax scale * log2(e)
 };
+
+static __device__ unsigned int g_attn_fault;   // a CTA gave up waiting for its copies
 
 // One request as the kernels see it: every value is clamped so that no
 // length or offset in device memory can lead outside the buffers.
@@ -200,53 +203,77 @@ struct KeyRegs {
     uint32_t k[2][KW], v[4][VW];
     uint32_t ks[2];     // KS bytes each
     uint32_t vs[4];     // VS bytes each
-    int base;           // first key; < 0: nothing here
 };
 
+// A step of a warp: 16 keys, copied as four contiguous pieces.
 template <int D>
-__device__ __forceinline__ void load_keys(KeyRegs<D>& x, const AttnArgs& a, int base, int page, int head, int g, int t) {
-    x.base = page < 0 ? -1 : base;
-    if (page < 0) return;
-    using K = KeyRegs<D>;
-    const int P = 1 << a.page_shift;
+struct Step {
+    static constexpr int codes = 16 * D / 2, scales = D;      // bytes, keys or values
+    static constexpr int bytes = 2 * (codes + scales);
+    // steps in flight per warp: about 9 KB
+    static constexpr int stages = D == 64 ? 8 : D == 128 ? 4 : 2;
+};
+
+// Starts the copies of the 16 keys from `in` of a page (one lane).
+template <int D>
+__device__ __forceinline__ void copy_step(unsigned char* dst, const AttnArgs& a, int in, int page, int head, uint64_t* bar,
+                                          uint64_t policy) {
+    using S = Step<D>;
     const int64_t tile = static_cast<int64_t>(D / 16 * 9) << a.page_shift;
     const uint8_t* kt = a.cache + (static_cast<int64_t>(page) * 2 * a.kv_heads + head) * tile;
     const uint8_t* vt = kt + a.kv_heads * tile;
-    const int in = base & (P - 1);
+    const int c = in * (D / 2), s = ((D / 2) << a.page_shift) + in * (D / 16);
+    mbar_arrive_expect_tx(bar, S::bytes);
+    bulk_g2s(dst, kt + c, S::codes, bar, policy);
+    bulk_g2s(dst + S::codes, kt + s, S::scales, bar, policy);
+    bulk_g2s(dst + S::codes + S::scales, vt + c, S::codes, bar, policy);
+    bulk_g2s(dst + 2 * S::codes + S::scales, vt + s, S::scales, bar, policy);
+}
+
+// The lane's share of a copied step.  Rows of K at a 64-byte (D = 128) stride
+// and 16 bytes a lane, rows of V 4 at a time and 8 bytes a lane: contiguous
+// over the warp, free of bank conflicts.
+template <int D>
+__device__ __forceinline__ void read_step(KeyRegs<D>& x, const unsigned char* st, int g, int t) {
+    using K = KeyRegs<D>;
+    using S = Step<D>;
     const int kappa = (g >> 1) + ((g & 1) << 2);
+    const unsigned char* ks = st + S::codes;
+    const unsigned char* v = ks + S::scales;
+    const unsigned char* vs = v + S::codes;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const uint8_t* p = kt + (in + kappa + 8 * i) * (D / 2) + t * (D / 8);
+        const unsigned char* p = st + (kappa + 8 * i) * (D / 2) + t * (D / 8);
         if constexpr (D == 64) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+            const uint2 u = *reinterpret_cast<const uint2*>(p);
             x.k[i][0] = u.x; x.k[i][1] = u.y;
         } else {
 #pragma unroll
             for (int j = 0; j < K::KW; j += 4) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + j / 4);
+                const uint4 u = reinterpret_cast<const uint4*>(p)[j / 4];
                 x.k[i][j] = u.x; x.k[i][j + 1] = u.y; x.k[i][j + 2] = u.z; x.k[i][j + 3] = u.w;
             }
         }
-        const uint8_t* s = kt + P * (D / 2) + (in + kappa + 8 * i) * (D / 16) + t * K::KS;
-        if constexpr (D == 64) x.ks[i] = __ldg(s);
-        else if constexpr (D == 128) x.ks[i] = __ldg(reinterpret_cast<const uint16_t*>(s));
-        else x.ks[i] = __ldg(reinterpret_cast<const uint32_t*>(s));
+        const unsigned char* s = ks + (kappa + 8 * i) * (D / 16) + t * K::KS;
+        if constexpr (D == 64) x.ks[i] = *s;
+        else if constexpr (D == 128) x.ks[i] = *reinterpret_cast<const uint16_t*>(s);
+        else x.ks[i] = *reinterpret_cast<const uint32_t*>(s);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint8_t* p = vt + (in + t + 4 * i) * (D / 2) + g * (D / 16);
+        const unsigned char* p = v + (t + 4 * i) * (D / 2) + g * (D / 16);
         if constexpr (D == 64) {
-            x.v[i][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+            x.v[i][0] = *reinterpret_cast<const uint32_t*>(p);
         } else if constexpr (D == 128) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+            const uint2 u = *reinterpret_cast<const uint2*>(p);
             x.v[i][0] = u.x; x.v[i][1] = u.y;
         } else {
-            const uint4 u = __ldg(reinterpret_cast<const uint4*>(p));
+            const uint4 u = *reinterpret_cast<const uint4*>(p);
             x.v[i][0] = u.x; x.v[i][1] = u.y; x.v[i][2] = u.z; x.v[i][3] = u.w;
         }
-        const uint8_t* s = vt + P * (D / 2) + (in + t + 4 * i) * (D / 16) + (D == 64 ? g / 2 : g * K::VS);
-        if constexpr (D == 256) x.vs[i] = __ldg(reinterpret_cast<const uint16_t*>(s));
-        else x.vs[i] = __ldg(s);
+        const unsigned char* s = vs + (t + 4 * i) * (D / 16) + (D == 64 ? g / 2 : g * K::VS);
+        if constexpr (D == 256) x.vs[i] = *reinterpret_cast<const uint16_t*>(s);
+        else x.vs[i] = *s;
     }
 }
 
@@ -265,7 +292,7 @@ struct WarpState {
 template <int D, int NB>
 __device__ __forceinline__ void attend16(WarpState<D, NB>& w, const KeyRegs<D>& x, const uint32_t (&qf)[D / 16][NB][2],
                                          const float (&fs)[NB][2], const int (&pos)[NB][2], const int (&lo)[NB][2],
-                                         bool full, int g) {
+                                         bool full, int base, int g) {
     using K = KeyRegs<D>;
     float s[NB][4];
 #pragma unroll
@@ -319,7 +346,7 @@ __device__ __forceinline__ void attend16(WarpState<D, NB>& w, const KeyRegs<D>& 
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[b][j] *= fs[b][j & 1];
     if (!full) {
-        const int key = x.base + (g >> 1) + ((g & 1) << 2);
+        const int key = base + (g >> 1) + ((g & 1) << 2);
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -405,6 +432,7 @@ __device__ __forceinline__ void attend16(WarpState<D, NB>& w, const KeyRegs<D>& 
     }
 }
 
+// Where the warps' states meet; it takes the place of the copied steps.
 template <int D, int NB>
 struct AttnSmem {
     float o[kAttnWarps][8 * NB][D + 4];
@@ -422,8 +450,16 @@ __device__ __forceinline__ void store_quad(void* out, int64_t at, float4 o, floa
 template <class E, int D, int NB>
 __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
     constexpr int ROWS = 8 * NB;
+    using S = Step<D>;
+    constexpr int kRing = kAttnWarps * S::stages * S::bytes, kJoin = sizeof(AttnSmem<D, NB>);
     extern __shared__ int64_t prefix[];
-    __shared__ __align__(16) AttnSmem<D, NB> sm;
+    __shared__ __align__(128) unsigned char mem[kRing > kJoin ? kRing : kJoin];
+    __shared__ __align__(8) uint64_t bars[kAttnWarps][S::stages];
+    AttnSmem<D, NB>& sm = *reinterpret_cast<AttnSmem<D, NB>*>(mem);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kAttnWarps * S::stages; ++i) mbar_init(&bars[0][0] + i, 1);
+        fence_mbar_init();
+    }
     allow_dependents();
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -433,6 +469,10 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
     int64_t x = blockIdx.x * run;
     const int64_t end = x + run < total ? x + run : total;
     const float k_gs = __ldg(a.k_gs), v_gs = __ldg(a.v_gs);
+    unsigned char* ring = mem + warp * S::stages * S::bytes;
+    const uint64_t policy = l2_policy_evict_first();
+    uint32_t parity = 0;    // bit s: parity of the next fill of stage s
+    bool ok = true;
 
     while (x < end) {
         Req rq;
@@ -507,29 +547,49 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w.o[i][b][j] = 0.0f;
 
-        // The warp's steps: 16 keys each, two per tile, loaded one step ahead.
+        // The warp's steps: 16 keys each, two per tile, copied S::stages - 1
+        // steps ahead; the page of a step is read one step before its copy.
+        const int steps = 2 * ntiles;
         const int first_key = (rq.tile0 + at.tile) * kAttnKeyTile + warp * 32;
         const int* row_table = a.table + static_cast<int64_t>(at.r) * a.width;
         auto key_of = [&](int j) { return first_key + (j >> 1) * kAttnKeyTile + (j & 1) * 16; };
         auto page_of = [&](int j) {
             const int k = key_of(j);
-            if (j >= 2 * ntiles || k > pos_max || k + 15 < lo_min) return -1;
+            if (j >= steps || k > pos_max || k + 15 < lo_min) return -1;
             const int p = __ldg(row_table + (k >> a.page_shift));
             return p < a.num_pages ? p : -1;
         };
-        KeyRegs<D> cur, nxt;
-        int p1 = page_of(1);
-        load_keys<D>(cur, a, key_of(0), page_of(0), at.head, g, t);
-        for (int j = 0; j < 2 * ntiles; ++j) {
-            const int p2 = page_of(j + 2);
-            load_keys<D>(nxt, a, key_of(j + 1), p1, at.head, g, t);
-            p1 = p2;
-            if (cur.base >= 0) {
-                const bool full = cur.base + 15 <= pos_min && cur.base >= lo_max;
-                attend16<D, NB>(w, cur, qf, fs, pos, lo, full, g);
+        uint32_t filled = 0;    // bit s: stage s holds a step
+        auto issue = [&](int j, int page) {
+            const int s = j % S::stages;
+            filled &= ~(1u << s);
+            if (page < 0 || !ok) return;
+            filled |= 1u << s;
+            if (lane == 0)
+                copy_step<D>(ring + s * S::bytes, a, key_of(j) & ((1 << a.page_shift) - 1), page, at.head, &bars[warp][s],
+                             policy);
+        };
+#pragma unroll
+        for (int j = 0; j < S::stages - 1; ++j) issue(j, page_of(j));
+        int page = page_of(S::stages - 1);
+        for (int j = 0; j < steps; ++j) {
+            issue(j + S::stages - 1, page);
+            page = page_of(j + S::stages);
+            const int s = j % S::stages;
+            if (filled >> s & 1u) {
+                ok = __all_sync(kFull, mbar_wait_bounded(&bars[warp][s], parity >> s & 1u)) && ok;
+                parity ^= 1u << s;
+                if (ok) {
+                    KeyRegs<D> key;
+                    read_step<D>(key, ring + s * S::bytes, g, t);
+                    const int base = key_of(j);
+                    attend16<D, NB>(w, key, qf, fs, pos, lo, base + 15 <= pos_min && base >= lo_max, base, g);
+                }
             }
-            cur = nxt;
+            __syncwarp();   // every lane has read the stage that the next copy overwrites
         }
+        if (!ok && lane == 0) atomicOr(&g_attn_fault, 1u);
+        __syncthreads();
 
         // Join the warps.
 #pragma unroll
@@ -590,6 +650,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
                 if (d == 0) *reinterpret_cast<float2*>(part + row * (D + 2) + D) = make_float2(top, l);
             }
         }
+        // the join's reads and writes come before the next copies into the same place
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncthreads();
         x += ntiles;
     }

@@ -122,16 +122,6 @@ const void* pick_kernel(int mode, bool res, bool pipe, int J) {
     }
 }
 
-// Occupancy of a pipelined instantiation for a given ring size, cached per
-// device.
-struct OccEntry {
-    int dev;
-    const void* fn;
-    int smem;
-    int threads;
-    int blocks;
-};
-
 // Shared-memory ring budget per CTA (two CTAs per SM).
 constexpr int kPipeSmemBudget = 110 * 1024;
 
@@ -182,27 +172,6 @@ inline cudaError_t set_smem_attributes(const void* fn) {
         e = cudaFuncSetAttribute(fn, cudaFuncAttributePreferredSharedMemoryCarveout,
                                  cudaSharedmemCarveoutMaxShared);
     return e;
-}
-
-// Resident CTAs per SM of `fn` at `threads` threads and `smem` dynamic
-// shared-memory bytes (cached per device and launch shape).
-inline int occupancy_blocks(const void* fn, int threads, int smem, cudaError_t* err) {
-    static std::mutex mu;
-    constexpr int kCache = 256;   // more than the launch shapes in use; beyond it, queried per call
-    static OccEntry cache[kCache];
-    static int used = 0;
-    int dev = 0;
-    *err = cudaGetDevice(&dev);
-    if (*err != cudaSuccess) return 0;
-    std::lock_guard<std::mutex> lock(mu);
-    for (int i = 0; i < used; ++i)
-        if (cache[i].dev == dev && cache[i].fn == fn && cache[i].smem == smem && cache[i].threads == threads)
-            return cache[i].blocks;
-    int blocks = 0;
-    *err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, fn, threads, smem);
-    if (*err != cudaSuccess) return 0;
-    if (used < kCache) cache[used++] = {dev, fn, smem, threads, blocks};
-    return blocks;
 }
 
 // The same for a pipelined kernel, whose shared-memory attributes are set

@@ -2,6 +2,7 @@
 #pragma once
 
 #include <atomic>
+#include <mutex>
 #include <cuda_runtime.h>
 
 #include "rmsq_launch.h"
@@ -39,6 +40,36 @@ inline int sm_count(cudaError_t* err) {
         cached[dev].store(v, std::memory_order_release);
     }
     return v;
+}
+
+// One cached occupancy.
+struct OccEntry {
+    int dev;
+    const void* fn;
+    int smem;
+    int threads;
+    int blocks;
+};
+
+// Resident CTAs per SM of `fn` at `threads` threads and `smem` dynamic
+// shared-memory bytes (cached per device and launch shape).
+inline int occupancy_blocks(const void* fn, int threads, int smem, cudaError_t* err) {
+    static std::mutex mu;
+    constexpr int kCache = 256;   // more than the launch shapes in use; beyond it, queried per call
+    static OccEntry cache[kCache];
+    static int used = 0;
+    int dev = 0;
+    *err = cudaGetDevice(&dev);
+    if (*err != cudaSuccess) return 0;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < used; ++i)
+        if (cache[i].dev == dev && cache[i].fn == fn && cache[i].smem == smem && cache[i].threads == threads)
+            return cache[i].blocks;
+    int blocks = 0;
+    *err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, fn, threads, smem);
+    if (*err != cudaSuccess) return 0;
+    if (used < kCache) cache[used++] = {dev, fn, smem, threads, blocks};
+    return blocks;
 }
 
 }  // namespace rmsq
