@@ -384,8 +384,8 @@ int rmsq_build_slot_map(const int32_t *context_lens, const int32_t *query_lens, 
  * [page_size, head_dim / 2] (E2M1, element 2j in the low nibble of byte j),
  * then the E4M3 scales of the 16-element blocks [page_size, head_dim / 16].
  * Slot s is token s % page_size of page s / page_size.  An element stands for
- * code * scale / global scale; a scale byte's sign is ignored and its NaN code
- * counts as 0.
+ * code * scale / global scale; the scale's NaN codes, which the store never
+ * writes, read as 448.
  *
  * rmsq_kv_cache_store_nvfp4 — quantises the key and value heads of n_tokens
  * tokens into the cache, bit for bit as RMSQ_NVFP4 does (rmsq_quant).

@@ -440,11 +440,6 @@ def build_slot_map(context_lens: torch.Tensor, query_lens: torch.Tensor, block_t
     L = load()
     R, width = block_table.shape
     dev, i = block_table.device, block_table.get_device()
-    if slot_map is None and positions is None and max_tokens > 0:
-        slot_map, positions = torch.empty(2 * max_tokens, dtype=_I64, device=dev).split_with_sizes((max_tokens, max_tokens))
-    if query_start is None and seq_lens is None and num_free_out is None and status is None:
-        query_start, seq_lens, num_free_out, status = torch.empty(2 * R + 3, dtype=_I32, device=dev).split_with_sizes(
-            (R + 1, R, 1, 1))
     if slot_map is None:
         slot_map = torch.empty(max(max_tokens, 0), dtype=_I64, device=dev)
     if positions is None:

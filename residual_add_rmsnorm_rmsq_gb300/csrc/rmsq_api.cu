@@ -615,15 +615,14 @@ int rmsq_take_fault_flags(uint32_t* flags) {
     if (!flags) return RMSQ_ERR_INVALID_ARG;
     const int st = check_device();
     if (st != RMSQ_OK) return st;
-    unsigned int a = 0, b = 0, c = 0, d = 0, m = 0, t = 0;
+    unsigned int a = 0, b = 0, c = 0, d = 0, m = 0;
     cudaError_t e = rmsq::take_pipe_fault_bf16(&a);
     if (e == cudaSuccess) e = rmsq::take_pipe_fault_fp16(&b);
     if (e == cudaSuccess) e = rmsq::take_pipe_fault_qk(&c);
     if (e == cudaSuccess) e = rmsq::take_pipe_fault_ar(&d);
     if (e == cudaSuccess) e = rmsq::take_mm_fault(&m);
-    if (e == cudaSuccess) e = rmsq::take_attn_fault(&t);
     if (e != cudaSuccess) return fail_cuda(e);
-    *flags = a | b | c | d | m | t;
+    *flags = a | b | c | d | m;
     return RMSQ_OK;
 }
 

@@ -10,13 +10,6 @@
 
 namespace rmsq {
 
-cudaError_t take_attn_fault(unsigned int* out) {
-    const unsigned int zero = 0;
-    cudaError_t e = cudaMemcpyFromSymbol(out, g_attn_fault, sizeof(unsigned int));
-    if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(g_attn_fault, &zero, sizeof(zero));
-    return e;
-}
-
 namespace {
 
 // Row blocks of 8: two (16 rows share a pass over the keys) where a request
@@ -36,14 +29,11 @@ cudaError_t launch_split(AttnArgs a, int64_t max_tiles, cudaStream_t stream) {
     const void* split = (const void*)&attn_split_kernel<E, D, NB>;
     const void* join = (const void*)&attn_join_kernel<E, D, NB>;
     // the scanned tile counts, in steps of 1 KB (so that few launch shapes occur)
-    const int smem = ((a.requests + 1) * 8 + 1023) / 1024 * 1024;
-    if (smem > 8 * 1024) {   // beyond what the default 48 KB leave beside the static part
-        const int most = ((RMSQ_MAX_REQUESTS + 1) * 8 + 1023) / 1024 * 1024;
-        e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-        if (e != cudaSuccess) return e;
-    }
-    e = cudaFuncSetAttribute(split, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    const int counts = ((a.requests + 1) * 8 + 1023) / 1024 * 1024, smem = kAttnMem<D, NB> + counts;
+    constexpr int kMostCounts = ((RMSQ_MAX_REQUESTS + 1) * 8 + 1023) / 1024 * 1024;
+    e = cudaFuncSetAttribute(split, cudaFuncAttributeMaxDynamicSharedMemorySize, kAttnMem<D, NB> + kMostCounts);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(split, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     if (e != cudaSuccess) return e;
     const int per_sm = occupancy_blocks(split, kAttnThreads, smem, &e);
     if (e != cudaSuccess) return e;
@@ -55,7 +45,10 @@ cudaError_t launch_split(AttnArgs a, int64_t max_tiles, cudaStream_t stream) {
     void* params[] = {&a};
     e = launch_kernel(split, dim3(a.workers), dim3(kAttnThreads), params, smem, stream);
     if (e != cudaSuccess) return e;
-    return launch_kernel(join, dim3(a.workers), dim3(kAttnThreads), params, smem, stream);
+    // few items: each is cut into many parts
+    const int64_t items = (static_cast<int64_t>(a.tokens) * a.group / (8 * NB) + a.requests) * a.kv_heads;
+    const unsigned shares = items * 8 <= workers ? kJoinShares : 1;
+    return launch_kernel(join, dim3(a.workers, shares), dim3(kJoinThreads), params, 0, stream);
 }
 
 template <class E>
@@ -85,7 +78,7 @@ size_t rmsq_paged_attention_workspace_bytes(int64_t n_tokens, int64_t num_reques
                                             int head_dim) {
     if (rmsq::attn_shape(n_tokens, num_requests, num_heads, num_kv_heads, head_dim) != RMSQ_OK) return 0;
     const int nb = rmsq::row_blocks(n_tokens, num_requests, num_heads / num_kv_heads, head_dim);
-    return static_cast<size_t>(rmsq::kAttnMaxWorkers) * 2 * rmsq::part_floats(head_dim, nb) * 4;
+    return static_cast<size_t>(rmsq::kAttnMaxWorkers) * (sizeof(rmsq::CutItem) + 2 * rmsq::part_floats(head_dim, nb) * 4);
 }
 
 int rmsq_paged_attention_nvfp4(const void* q, int64_t q_stride, const void* kv_cache, int64_t num_pages, int64_t page_size,
@@ -147,7 +140,8 @@ int rmsq_paged_attention_nvfp4(const void* q, int64_t q_stride, const void* kv_c
     a.v_gs = v_global_scale;
     a.out = out;
     a.lse = lse;
-    a.part = static_cast<float*>(workspace);
+    a.cut = static_cast<rmsq::CutItem*>(workspace);
+    a.part = reinterpret_cast<float*>(a.cut + rmsq::kAttnMaxWorkers);
     a.requests = static_cast<int>(num_requests);
     a.width = static_cast<int>(table_width);
     a.tokens = static_cast<int>(n_tokens);

@@ -20,7 +20,7 @@
 //
 // Layout: contractions may take their index in any order, so every lane loads
 // the piece of the cache it needs in one access, with no shuffle.  Each warp
-// keeps the next steps in flight as bulk copies into a ring of its own.
+// keeps the next steps in flight as asynchronous copies into a ring of its own.
 // Lane (g, t) = (lane / 4, lane % 4):
 //   K: dims t * D/4 .. of keys kappa(g) and kappa(g) + 8;
 //   V: dims g * D/8 .. of keys t, t + 4, t + 8, t + 12 (one scale block for
@@ -50,6 +50,15 @@ constexpr int kAttnMaxWorkers = 1216;           // CTAs of the split launch: 8 p
 constexpr float kPShift = 9.0f;                 // probabilities are scaled by 2^9 ...
 constexpr float kLazy = 6.0f;                   // ... and by up to 2^6 more while the maximum lags: < 2^16 in f16
 
+// What the join has to know of an item that starts in a run and goes past its
+// end: the runs it lies in, and its rows.
+struct CutItem {
+    int parts;      // 0: no such item
+    int slot;       // of its first part
+    int q0, qlen, qtile, head;
+    int unused[2];
+};
+
 struct AttnArgs {
     const void* q;
     int64_t q_stride;       // elements between tokens
@@ -61,13 +70,12 @@ struct AttnArgs {
     const float* v_gs;
     void* out;              // [tokens, heads, D]
     float* lse;             // [tokens, heads] or null
+    CutItem* cut;           // [workers]
     float* part;            // [workers][2][ROWS][D + 2]
     int requests, width, tokens, heads, kv_heads, group;
     int page_shift, num_pages, window, workers;
     float scale_log2;       // softmax scale * log2(e)
 };
-
-static __device__ unsigned int g_attn_fault;   // a CTA gave up waiting for its copies
 
 // One request as the kernels see it: every value is clamped so that no
 // length or offset in device memory can lead outside the buffers.
@@ -179,17 +187,12 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Four scale bytes with sign bits cleared and NaN codes (0x7f) turned to 0.
-__device__ __forceinline__ uint32_t clean_scales(uint32_t w) {
-    w &= 0x7f7f7f7fu;
-    const uint32_t nan = (w + 0x01010101u) & 0x80808080u;
-    return w & ~(nan - (nan >> 7));
-}
-
-// Two E4M3 codes (low half of w) as an f16 pair; every E4M3 value is exact.
+// Two E4M3 codes (low half of w) as an f16 pair; every E4M3 value is exact,
+// and the minimum with 448 keeps a number where the code is NaN.
 __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
     uint32_t r;
-    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t"
+        "min.f16x2 %0, %0, %2;\n\t}" : "=r"(r) : "r"(w), "r"(0x5f005f00u));
     return r;
 }
 
@@ -205,42 +208,51 @@ struct KeyRegs {
     uint32_t vs[4];     // VS bytes each
 };
 
-// A step of a warp: 16 keys, copied as four contiguous pieces.
+// A step of a warp: 32 keys, two halves of 16 that each lie on one page.
+// Shared memory of a half: K codes, K scales, V codes, V scales.
 template <int D>
 struct Step {
-    static constexpr int codes = 16 * D / 2, scales = D;      // bytes, keys or values
-    static constexpr int bytes = 2 * (codes + scales);
-    // steps in flight per warp: about 9 KB
-    static constexpr int stages = D == 64 ? 8 : D == 128 ? 4 : 2;
+    static constexpr int codes = 16 * D / 2, scales = D;      // bytes of a half, keys or values
+    static constexpr int half = 2 * (codes + scales);
+    static constexpr int stages = D == 64 ? 4 : 2;            // 9 or 18 KB in flight per warp
+    static constexpr int ring = stages * 2 * half;            // per warp
 };
 
-// Starts the copies of the 16 keys from `in` of a page (one lane).
-template <int D>
-__device__ __forceinline__ void copy_step(unsigned char* dst, const AttnArgs& a, int in, int page, int head, uint64_t* bar,
-                                          uint64_t policy) {
-    using S = Step<D>;
-    const int64_t tile = static_cast<int64_t>(D / 16 * 9) << a.page_shift;
-    const uint8_t* kt = a.cache + (static_cast<int64_t>(page) * 2 * a.kv_heads + head) * tile;
-    const uint8_t* vt = kt + a.kv_heads * tile;
-    const int c = in * (D / 2), s = ((D / 2) << a.page_shift) + in * (D / 16);
-    mbar_arrive_expect_tx(bar, S::bytes);
-    bulk_g2s(dst, kt + c, S::codes, bar, policy);
-    bulk_g2s(dst + S::codes, kt + s, S::scales, bar, policy);
-    bulk_g2s(dst + S::codes + S::scales, vt + c, S::codes, bar, policy);
-    bulk_g2s(dst + 2 * S::codes + S::scales, vt + s, S::scales, bar, policy);
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
-// The lane's share of a copied step.  Rows of K at a 64-byte (D = 128) stride
-// and 16 bytes a lane, rows of V 4 at a time and 8 bytes a lane: contiguous
-// over the warp, free of bank conflicts.
+// Starts the copies of a half from row `in` of a page: 16 lanes, lane l takes
+// every 16th 16-byte chunk.
 template <int D>
-__device__ __forceinline__ void read_step(KeyRegs<D>& x, const unsigned char* st, int g, int t) {
+__device__ __forceinline__ void copy_half(unsigned char* dst, const AttnArgs& a, int in, int page, int head, int l) {
+    using S = Step<D>;
+    const uint32_t tile = static_cast<uint32_t>(D / 16 * 9) << a.page_shift;
+    const uint8_t* kt = a.cache + (static_cast<int64_t>(page) * 2 * a.kv_heads + head) * tile;
+    const uint8_t* vt = kt + static_cast<int64_t>(a.kv_heads) * tile;
+    const uint32_t c = in * (D / 2) + l * 16, s = ((D / 2) << a.page_shift) + in * (D / 16);
+    unsigned char* d = dst + l * 16;
+#pragma unroll
+    for (int i = 0; i < S::codes / 256; ++i) copy16(d + i * 256, kt + c + i * 256);
+#pragma unroll
+    for (int i = 0; i < S::codes / 256; ++i) copy16(d + S::codes + S::scales + i * 256, vt + c + i * 256);
+    // the scales of both sides together: D / 16 chunks each
+#pragma unroll
+    for (int i = 0; i < (D + 127) / 128; ++i) {
+        const int j = l + 16 * i, side = j >= D / 16, k = j - side * (D / 16);
+        if (D >= 128 || l < D / 8)
+            copy16(dst + S::codes + side * (S::codes + S::scales) + k * 16, (side ? vt : kt) + s + k * 16);
+    }
+}
+
+// The lane's share of a half.  Rows of K at a 64-byte (D = 128) stride and 16
+// bytes a lane, rows of V 4 at a time and 8 bytes a lane: contiguous over the
+// warp, free of bank conflicts.
+template <int D>
+__device__ __forceinline__ void read_keys(KeyRegs<D>& x, const unsigned char* st, int g, int t) {
     using K = KeyRegs<D>;
     using S = Step<D>;
     const int kappa = (g >> 1) + ((g & 1) << 2);
-    const unsigned char* ks = st + S::codes;
-    const unsigned char* v = ks + S::scales;
-    const unsigned char* vs = v + S::codes;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const unsigned char* p = st + (kappa + 8 * i) * (D / 2) + t * (D / 8);
@@ -254,11 +266,18 @@ __device__ __forceinline__ void read_step(KeyRegs<D>& x, const unsigned char* st
                 x.k[i][j] = u.x; x.k[i][j + 1] = u.y; x.k[i][j + 2] = u.z; x.k[i][j + 3] = u.w;
             }
         }
-        const unsigned char* s = ks + (kappa + 8 * i) * (D / 16) + t * K::KS;
+        const unsigned char* s = st + S::codes + (kappa + 8 * i) * (D / 16) + t * K::KS;
         if constexpr (D == 64) x.ks[i] = *s;
         else if constexpr (D == 128) x.ks[i] = *reinterpret_cast<const uint16_t*>(s);
         else x.ks[i] = *reinterpret_cast<const uint32_t*>(s);
     }
+}
+
+template <int D>
+__device__ __forceinline__ void read_values(KeyRegs<D>& x, const unsigned char* st, int g, int t) {
+    using K = KeyRegs<D>;
+    using S = Step<D>;
+    const unsigned char* v = st + S::codes + S::scales;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const unsigned char* p = v + (t + 4 * i) * (D / 2) + g * (D / 16);
@@ -271,7 +290,7 @@ __device__ __forceinline__ void read_step(KeyRegs<D>& x, const unsigned char* st
             const uint4 u = *reinterpret_cast<const uint4*>(p);
             x.v[i][0] = u.x; x.v[i][1] = u.y; x.v[i][2] = u.z; x.v[i][3] = u.w;
         }
-        const unsigned char* s = vs + (t + 4 * i) * (D / 16) + (D == 64 ? g / 2 : g * K::VS);
+        const unsigned char* s = v + S::codes + (t + 4 * i) * (D / 16) + (D == 64 ? g / 2 : g * K::VS);
         if constexpr (D == 256) x.vs[i] = *reinterpret_cast<const uint16_t*>(s);
         else x.vs[i] = *s;
     }
@@ -280,49 +299,38 @@ __device__ __forceinline__ void read_step(KeyRegs<D>& x, const unsigned char* st
 // f16 pair (s, s) from half `hi` of an f16 pair.
 __device__ __forceinline__ uint32_t dup_half(uint32_t pair, int hi) { return __byte_perm(pair, 0, hi ? 0x3232 : 0x1010); }
 
-// A warp's running state over its keys for one item.
+// A warp's running state over its keys for one item.  The logits stay in the
+// units of the product; f turns them into units of log2, m is the maximum in
+// those, limit the raw logit above which it has to move.
 template <int D, int NB>
 struct WarpState {
     float o[D / 16][NB][4];
-    float m[NB][2], l[NB][2];
+    float m[NB][2], l[NB][2], limit[NB][2];
 };
 
-// One step: 16 keys.  pos / lo: last and first key each of the lane's columns
-// may see; `full`: every key of the step is inside for every row.
+// S^T of 16 keys: s[b][0..1] key kappa(g), rows 2t and 2t + 1; s[b][2..3] key + 8.
 template <int D, int NB>
-__device__ __forceinline__ void attend16(WarpState<D, NB>& w, const KeyRegs<D>& x, const uint32_t (&qf)[D / 16][NB][2],
-                                         const float (&fs)[NB][2], const int (&pos)[NB][2], const int (&lo)[NB][2],
-                                         bool full, int base, int g) {
+__device__ __forceinline__ void scores16(float (&s)[NB][4], const KeyRegs<D>& x, const uint32_t (&qf)[D / 16][NB][2]) {
     using K = KeyRegs<D>;
-    float s[NB][4];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[b][j] = 0.0f;
-    // scale bytes of both keys: D = 64: one each, 128: two each, 256: four each
-    uint32_t kscale[2][K::KS];      // duplicated f16 pair per block
+    // duplicated f16 pair of each block's scale; D = 64: one block per key, 128: two, 256: four
+    uint32_t sc[2][K::KS];
     if constexpr (D == 64) {
-        const uint32_t p = e4m3x2_f16x2(clean_scales(x.ks[0] | (x.ks[1] << 8)));
-        kscale[0][0] = dup_half(p, 0);
-        kscale[1][0] = dup_half(p, 1);
-    } else if constexpr (D == 128) {
-        const uint32_t c = clean_scales(x.ks[0] | (x.ks[1] << 16));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t p = e4m3x2_f16x2(c >> (16 * i));
-            kscale[i][0] = dup_half(p, 0);
-            kscale[i][1] = dup_half(p, 1);
-        }
+        const uint32_t p = e4m3x2_f16x2(x.ks[0] | (x.ks[1] << 8));
+        sc[0][0] = dup_half(p, 0);
+        sc[1][0] = dup_half(p, 1);
     } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t c = clean_scales(x.ks[i]);
-            const uint32_t p0 = e4m3x2_f16x2(c), p1 = e4m3x2_f16x2(c >> 16);
-            kscale[i][0] = dup_half(p0, 0);
-            kscale[i][1] = dup_half(p0, 1);
-            kscale[i][2] = dup_half(p1, 0);
-            kscale[i][3] = dup_half(p1, 1);
-        }
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < K::KS; j += 2) {
+                const uint32_t p = e4m3x2_f16x2(x.ks[i] >> (8 * j));
+                sc[i][j] = dup_half(p, 0);
+                sc[i][j + 1] = dup_half(p, 1);
+            }
     }
 #pragma unroll
     for (int j = 0; j < K::KW; ++j) {   // a word of codes: 8 dims, two k-steps
@@ -331,8 +339,8 @@ __device__ __forceinline__ void attend16(WarpState<D, NB>& w, const KeyRegs<D>& 
         e2m1x8_f16x2(x.k[1][j], k1);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            k0[i] = mul_f16x2(k0[i], kscale[0][j / 2]);
-            k1[i] = mul_f16x2(k1[i], kscale[1][j / 2]);
+            k0[i] = mul_f16x2(k0[i], sc[0][j / 2]);
+            k1[i] = mul_f16x2(k1[i], sc[1][j / 2]);
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -340,74 +348,19 @@ __device__ __forceinline__ void attend16(WarpState<D, NB>& w, const KeyRegs<D>& 
             mma_f16(s[b], k0[2], k1[2], k0[3], k1[3], qf[2 * j + 1][b][0], qf[2 * j + 1][b][1]);
         }
     }
-    // logits in units of log2; s[b][0..1]: key kappa(g), rows 2t, 2t+1; s[b][2..3]: key + 8
+}
+
+// O^T += V^T . P of 16 keys.
+template <int D, int NB>
+__device__ __forceinline__ void values16(WarpState<D, NB>& w, const KeyRegs<D>& x, const uint32_t (&pf)[NB][2]) {
+    using K = KeyRegs<D>;
+    // scales of the pairs (key t, key t + 4) and (t + 8, t + 12)
+    uint32_t sc[2][K::VS];
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[b][j] *= fs[b][j & 1];
-    if (!full) {
-        const int key = base + (g >> 1) + ((g & 1) << 2);
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int k = key + (j >> 1) * 8;
-                if (k > pos[b][j & 1] || k < lo[b][j & 1]) s[b][j] = -INFINITY;
-            }
-    }
-    // The maximum is moved only when some logit passes it by more than kLazy.
-    bool grow = false;
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) grow |= fmaxf(s[b][j], s[b][j + 2]) > w.m[b][j] + kLazy;
-    if (__any_sync(kFull, grow)) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float top = fmaxf(s[b][j], s[b][j + 2]);
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-                const float m = fmaxf(top, w.m[b][j]);
-                const float f = m == -INFINITY ? 1.0f : exp2_approx(w.m[b][j] - m);
-                w.m[b][j] = m;
-                w.l[b][j] *= f;
-#pragma unroll
-                for (int i = 0; i < D / 16; ++i) {
-                    w.o[i][b][j] *= f;
-                    w.o[i][b][j + 2] *= f;
-                }
-            }
-    }
-    uint32_t pf[NB][2];
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-        float p[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float m = w.m[b][j & 1];
-            p[j] = exp2_approx(s[b][j] - (m == -INFINITY ? 0.0f : m - kPShift));
-        }
-        w.l[b][0] += p[0] + p[2];
-        w.l[b][1] += p[1] + p[3];
-        pf[b][0] = transpose8x8(Fp16T::pack(p[0], p[1]));
-        pf[b][1] = transpose8x8(Fp16T::pack(p[2], p[3]));
-    }
-    // V: pair (key t, key t + 4) and (t + 8, t + 12)
-    uint32_t vscale[2][K::VS];
-    if constexpr (D == 256) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t c = clean_scales(__byte_perm(x.vs[2 * i], x.vs[2 * i + 1], 0x5140));
-            vscale[i][0] = e4m3x2_f16x2(c);
-            vscale[i][1] = e4m3x2_f16x2(c >> 16);
-        }
-    } else {
-        const uint32_t c = clean_scales(__byte_perm(x.vs[0], x.vs[1], 0x1140) |
-                                        (__byte_perm(x.vs[2], x.vs[3], 0x1140) << 16));
-        vscale[0][0] = e4m3x2_f16x2(c);
-        vscale[1][0] = e4m3x2_f16x2(c >> 16);
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t c = __byte_perm(x.vs[2 * i], x.vs[2 * i + 1], 0x5140);
+        sc[i][0] = e4m3x2_f16x2(c);
+        if constexpr (D == 256) sc[i][1] = e4m3x2_f16x2(c >> 16);
     }
 #pragma unroll
     for (int j = 0; j < K::VW; ++j) {   // 8 dims: four m-tiles
@@ -417,11 +370,11 @@ __device__ __forceinline__ void attend16(WarpState<D, NB>& w, const KeyRegs<D>& 
             const uint32_t A = x.v[2 * i][j], B = x.v[2 * i + 1][j];
             e2m1x8_f16x2((A & 0x0f0f0f0fu) | ((B << 4) & 0xf0f0f0f0u), even[i]);
             e2m1x8_f16x2(((A >> 4) & 0x0f0f0f0fu) | (B & 0xf0f0f0f0u), odd[i]);
-            const uint32_t sc = vscale[i][K::VS == 2 ? j / 2 : 0];
+            const uint32_t m = sc[i][K::VS == 2 ? j / 2 : 0];
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                even[i][c] = mul_f16x2(even[i][c], sc);
-                odd[i][c] = mul_f16x2(odd[i][c], sc);
+                even[i][c] = mul_f16x2(even[i][c], m);
+                odd[i][c] = mul_f16x2(odd[i][c], m);
             }
         }
 #pragma unroll
@@ -432,12 +385,97 @@ __device__ __forceinline__ void attend16(WarpState<D, NB>& w, const KeyRegs<D>& 
     }
 }
 
+// One step: 32 keys from `base`.  pos / lo: last and first key each of the
+// lane's columns may see; `full`: every key is inside for every row; bit i of
+// `have`: half i is there.
+template <int D, int NB>
+__device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned char* st, const uint32_t (&qf)[D / 16][NB][2],
+                                         const float (&f)[NB][2], const int (&pos)[NB][2], const int (&lo)[NB][2],
+                                         bool full, uint32_t have, int base, int g, int t) {
+    float s[2][NB][4];
+    KeyRegs<D> x[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        read_keys<D>(x[h], st + h * Step<D>::half, g, t);
+        scores16<D, NB>(s[h], x[h], qf);
+    }
+    if (!full) {
+        const int key = base + (g >> 1) + ((g & 1) << 2);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int k = key + 16 * h + (j >> 1) * 8;
+                    if (k > pos[b][j & 1] || k < lo[b][j & 1] || !(have >> h & 1u)) s[h][b][j] = -INFINITY;
+                }
+    }
+    // The maximum is moved only when some logit passes it by more than kLazy.
+    float top[NB][2];
+    bool grow = false;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            top[b][j] = fmaxf(fmaxf(s[0][b][j], s[0][b][j + 2]), fmaxf(s[1][b][j], s[1][b][j + 2]));
+            grow |= top[b][j] > w.limit[b][j];
+        }
+    if (__any_sync(kFull, grow)) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                float x = top[b][j];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+                const float m = fmaxf(x * f[b][j], w.m[b][j]);
+                const float r = m == -INFINITY ? 1.0f : exp2_approx(w.m[b][j] - m);
+                w.m[b][j] = m;
+                w.limit[b][j] = (m + kLazy) / f[b][j];
+                w.l[b][j] *= r;
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i) {
+                    w.o[i][b][j] *= r;
+                    w.o[i][b][j + 2] *= r;
+                }
+            }
+    }
+    uint32_t pf[2][NB][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        float shift[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) shift[j] = w.m[b][j] == -INFINITY ? 0.0f : kPShift - w.m[b][j];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float p[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[j] = exp2_approx(fmaf(s[h][b][j], f[b][j & 1], shift[j & 1]));
+            w.l[b][0] += p[0] + p[2];
+            w.l[b][1] += p[1] + p[3];
+            pf[h][b][0] = transpose8x8(Fp16T::pack(p[0], p[1]));
+            pf[h][b][1] = transpose8x8(Fp16T::pack(p[2], p[3]));
+        }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        read_values<D>(x[h], st + h * Step<D>::half, g, t);
+        values16<D, NB>(w, x[h], pf[h]);
+    }
+}
+
 // Where the warps' states meet; it takes the place of the copied steps.
 template <int D, int NB>
 struct AttnSmem {
     float o[kAttnWarps][8 * NB][D + 4];
     float m[kAttnWarps][8 * NB], l[kAttnWarps][8 * NB];
 };
+
+// Bytes of the ring, or of the join if that is more.
+template <int D, int NB>
+constexpr int kAttnMem = (kAttnWarps * Step<D>::ring > static_cast<int>(sizeof(AttnSmem<D, NB>))
+                              ? kAttnWarps * Step<D>::ring : static_cast<int>(sizeof(AttnSmem<D, NB>)) + 127) / 128 * 128;
 
 // Writes row `row` of an item: out = o / l / gs and the log-sum-exp.  A row
 // that sees no key gets zeros and -inf.
@@ -451,15 +489,9 @@ template <class E, int D, int NB>
 __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
     constexpr int ROWS = 8 * NB;
     using S = Step<D>;
-    constexpr int kRing = kAttnWarps * S::stages * S::bytes, kJoin = sizeof(AttnSmem<D, NB>);
-    extern __shared__ int64_t prefix[];
-    __shared__ __align__(128) unsigned char mem[kRing > kJoin ? kRing : kJoin];
-    __shared__ __align__(8) uint64_t bars[kAttnWarps][S::stages];
+    extern __shared__ __align__(128) unsigned char mem[];
     AttnSmem<D, NB>& sm = *reinterpret_cast<AttnSmem<D, NB>*>(mem);
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kAttnWarps * S::stages; ++i) mbar_init(&bars[0][0] + i, 1);
-        fence_mbar_init();
-    }
+    int64_t* prefix = reinterpret_cast<int64_t*>(mem + kAttnMem<D, NB>);
     allow_dependents();
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -469,10 +501,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
     int64_t x = blockIdx.x * run;
     const int64_t end = x + run < total ? x + run : total;
     const float k_gs = __ldg(a.k_gs), v_gs = __ldg(a.v_gs);
-    unsigned char* ring = mem + warp * S::stages * S::bytes;
-    const uint64_t policy = l2_policy_evict_first();
-    uint32_t parity = 0;    // bit s: parity of the next fill of stage s
-    bool ok = true;
+    CutItem cut = {};
+    unsigned char* ring = mem + warp * S::ring;
 
     while (x < end) {
         Req rq;
@@ -480,6 +510,37 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
         const int ntiles = static_cast<int>(min(static_cast<int64_t>(rq.ktiles - at.tile), end - x));
         const int rows = rq.qlen * a.group;      // of the request
         const int row0 = at.qtile * ROWS;
+
+        // Range of the tile's rows: last key any row sees, and the keys every row sees.
+        const int last_row = min(row0 + ROWS, rows) - 1;
+        const int pos_min = rq.seq - rq.qlen + row0 / a.group, pos_max = rq.seq - rq.qlen + last_row / a.group;
+        const int lo_min = a.window > 0 ? pos_min - a.window + 1 : 0, lo_max = a.window > 0 ? pos_max - a.window + 1 : 0;
+
+        // The warp's steps, one per tile, copied S::stages - 1 steps ahead; the
+        // page of a half is read one step before its copy.  Lanes 0-15 care
+        // for the first half of a step, lanes 16-31 for the second.
+        const int my_half = lane >> 4;
+        const int first_key = (rq.tile0 + at.tile) * kAttnKeyTile + warp * 32;
+        const int* row_table = a.table + static_cast<int64_t>(at.r) * a.width;
+        auto page_of = [&](int j) {
+            const int k = first_key + j * kAttnKeyTile + my_half * 16;
+            if (j >= ntiles || k > pos_max || k + 15 < lo_min) return -1;
+            const int p = __ldg(row_table + (k >> a.page_shift));
+            return p < a.num_pages ? p : -1;
+        };
+        uint32_t have = 0;      // bits 2s, 2s + 1: halves of stage s
+        auto issue = [&](int j, int s, int page) {
+            const uint32_t there = __ballot_sync(kFull, page >= 0);
+            have = (have & ~(3u << (2 * s))) | (((there & 1u) | (there >> 16 & 1u) << 1) << (2 * s));
+            if (page >= 0)
+                copy_half<D>(ring + (s * 2 + my_half) * S::half, a,
+                             (first_key + j * kAttnKeyTile + my_half * 16) & ((1 << a.page_shift) - 1), page, at.head,
+                             lane & 15);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+#pragma unroll
+        for (int j = 0; j < S::stages - 1; ++j) issue(j, j, page_of(j));
+        int page = page_of(S::stages - 1);
 
         // Query fragments: column n = g of block b is row row0 + 8 b + g.
         uint32_t qf[D / 16][NB][2];
@@ -521,23 +582,18 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                fs[b][j] = __shfl_sync(kFull, f, (2 * t + j) * 4);
+                fs[b][j] = fmaxf(__shfl_sync(kFull, f, (2 * t + j) * 4), 1.17549435e-38f);
                 const int col = row0 + 8 * b + 2 * t + j;
                 pos[b][j] = col < rows ? rq.seq - rq.qlen + col / a.group : -1;
                 lo[b][j] = a.window > 0 ? pos[b][j] - a.window + 1 : 0;
             }
         }
-        // Range of the tile's rows: last key any row sees, and the keys every row sees.
-        const int last_row = min(row0 + ROWS, rows) - 1;
-        const int pos_min = rq.seq - rq.qlen + row0 / a.group, pos_max = rq.seq - rq.qlen + last_row / a.group;
-        const int lo_min = a.window > 0 ? pos_min - a.window + 1 : 0, lo_max = a.window > 0 ? pos_max - a.window + 1 : 0;
-
         WarpState<D, NB> w;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                w.m[b][j] = -INFINITY;
+                w.m[b][j] = w.limit[b][j] = -INFINITY;
                 w.l[b][j] = 0.0f;
             }
 #pragma unroll
@@ -547,48 +603,21 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) w.o[i][b][j] = 0.0f;
 
-        // The warp's steps: 16 keys each, two per tile, copied S::stages - 1
-        // steps ahead; the page of a step is read one step before its copy.
-        const int steps = 2 * ntiles;
-        const int first_key = (rq.tile0 + at.tile) * kAttnKeyTile + warp * 32;
-        const int* row_table = a.table + static_cast<int64_t>(at.r) * a.width;
-        auto key_of = [&](int j) { return first_key + (j >> 1) * kAttnKeyTile + (j & 1) * 16; };
-        auto page_of = [&](int j) {
-            const int k = key_of(j);
-            if (j >= steps || k > pos_max || k + 15 < lo_min) return -1;
-            const int p = __ldg(row_table + (k >> a.page_shift));
-            return p < a.num_pages ? p : -1;
-        };
-        uint32_t filled = 0;    // bit s: stage s holds a step
-        auto issue = [&](int j, int page) {
-            const int s = j % S::stages;
-            filled &= ~(1u << s);
-            if (page < 0 || !ok) return;
-            filled |= 1u << s;
-            if (lane == 0)
-                copy_step<D>(ring + s * S::bytes, a, key_of(j) & ((1 << a.page_shift) - 1), page, at.head, &bars[warp][s],
-                             policy);
-        };
-#pragma unroll
-        for (int j = 0; j < S::stages - 1; ++j) issue(j, page_of(j));
-        int page = page_of(S::stages - 1);
-        for (int j = 0; j < steps; ++j) {
-            issue(j + S::stages - 1, page);
+        for (int j = 0; j < ntiles; ++j) {
+            issue(j + S::stages - 1, (j + S::stages - 1) % S::stages, page);
             page = page_of(j + S::stages);
+            asm volatile("cp.async.wait_group %0;" :: "n"(S::stages - 1) : "memory");
+            __syncwarp();   // every lane's copies of this step are there
             const int s = j % S::stages;
-            if (filled >> s & 1u) {
-                ok = __all_sync(kFull, mbar_wait_bounded(&bars[warp][s], parity >> s & 1u)) && ok;
-                parity ^= 1u << s;
-                if (ok) {
-                    KeyRegs<D> key;
-                    read_step<D>(key, ring + s * S::bytes, g, t);
-                    const int base = key_of(j);
-                    attend16<D, NB>(w, key, qf, fs, pos, lo, base + 15 <= pos_min && base >= lo_max, base, g);
-                }
+            const uint32_t here = have >> (2 * s) & 3u;
+            if (here) {
+                const int base = first_key + j * kAttnKeyTile;
+                attend32<D, NB>(w, ring + s * 2 * S::half, qf, fs, pos, lo,
+                                here == 3u && base + 31 <= pos_min && base >= lo_max, here, base, g, t);
             }
             __syncwarp();   // every lane has read the stage that the next copy overwrites
         }
-        if (!ok && lane == 0) atomicOr(&g_attn_fault, 1u);
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         __syncthreads();
 
         // Join the warps.
@@ -650,59 +679,93 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
                 if (d == 0) *reinterpret_cast<float2*>(part + row * (D + 2) + D) = make_float2(top, l);
             }
         }
-        // the join's reads and writes come before the next copies into the same place
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncthreads();
+        if (at.tile == 0 && ntiles < rq.ktiles)
+            cut = {static_cast<int>((at.item0 + rq.ktiles - 1) / run) - static_cast<int>(blockIdx.x) + 1,
+                   x == blockIdx.x * run ? 0 : 1, rq.q0, rq.qlen, at.qtile, at.head, {0, 0}};
         x += ntiles;
     }
+    if (tid == 0) a.cut[blockIdx.x] = cut;
 }
 
-// Joins the parts of the items that the runs cut: CTA b takes the item that
-// starts in run b and goes past its end.
+// Joins the parts of the items that the runs cut: CTA (b, y) takes the y-th
+// share of the rows of the item that starts in run b and goes past its end.
+// Four dims per thread; the threads that a share leaves over split its parts
+// and meet in shared memory (in order, so the result does not depend on
+// timing).  The loads of a round of four parts are independent: with one part
+// after the other an item of 15 parts cost 15 memory latencies, 10 us of a 90 us
+// launch.  One share (gridDim.y = 1) fits all the joins of a ragged batch on
+// the card at once; eight shares serve few, long items of many parts.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinShares = 8;
+
+struct Partial {
+    float4 o;
+    float m, l;
+};
+
+__device__ __forceinline__ Partial load_partial(const float* p, int d, int D) {
+    const float2 u = __ldcg(reinterpret_cast<const float2*>(p + d)), v = __ldcg(reinterpret_cast<const float2*>(p + d + 2));
+    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + D));
+    return {make_float4(u.x, u.y, v.x, v.y), ml.x, ml.y};
+}
+
+__device__ __forceinline__ void merge(Partial& a, const Partial& b) {
+    const float m = fmaxf(a.m, b.m);
+    const float f = a.m == -INFINITY ? 0.0f : exp2_approx(a.m - m), h = b.m == -INFINITY ? 0.0f : exp2_approx(b.m - m);
+    a.o.x = a.o.x * f + b.o.x * h;
+    a.o.y = a.o.y * f + b.o.y * h;
+    a.o.z = a.o.z * f + b.o.z * h;
+    a.o.w = a.o.w * f + b.o.w * h;
+    a.l = a.l * f + b.l * h;
+    a.m = m;
+}
+
 template <class E, int D, int NB>
-__global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a) {
     constexpr int ROWS = 8 * NB;
-    extern __shared__ int64_t prefix[];
+    __shared__ __align__(16) Partial met[kJoinThreads];
     allow_dependents();
     grid_dependency_wait();
-    scan_requests<ROWS>(a, prefix);
-    const int64_t total = prefix[a.requests] * a.kv_heads;
-    const int64_t run = run_length(total, a.workers);
-    const int64_t end = (blockIdx.x + 1) * run;
-    if (end >= total) return;
-    Req rq;
-    const Place at = locate<ROWS>(a, prefix, end - 1, rq);
-    const int64_t item_end = at.item0 + rq.ktiles;
-    if (item_end <= end || at.item0 < end - run) return;
-    const int w1 = static_cast<int>((item_end - 1) / run);
+    const int4* c = reinterpret_cast<const int4*>(a.cut + blockIdx.x);
+    const int4 c0 = __ldcg(c), c1 = __ldcg(c + 1);
+    const int parts = c0.x, first_slot = c0.y, head = c1.y;
+    if (parts == 0) return;
+    const Req rq = {c0.z, c0.w, 0, 0, 0, 0};
+    const int w0 = blockIdx.x;
     const float v_gs = __ldg(a.v_gs);
-    const int rows = rq.qlen * a.group, row0 = at.qtile * ROWS;
+    const int rows = rq.qlen * a.group, row0 = c1.x * ROWS;
     const int64_t slot = ROWS * (D + 2);
-    const float* first = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (at.item0 == end - run ? 0 : 1)) * slot;
-    for (int i = threadIdx.x; i < ROWS * (D / 4); i += kAttnThreads) {
-        const int row = i / (D / 4), d = i % (D / 4) * 4;
-        if (row0 + row >= rows) continue;
-        const float* p = first + row * (D + 2);
-        float top = p[D], l = p[D + 1];
-        const float2 u0 = *reinterpret_cast<const float2*>(p + d), u1 = *reinterpret_cast<const float2*>(p + d + 2);
-        float4 o = make_float4(u0.x, u0.y, u1.x, u1.y);
-        for (int w = blockIdx.x + 1; w <= w1; ++w) {
-            p = a.part + static_cast<int64_t>(w) * 2 * slot + row * (D + 2);
-            const float m = fmaxf(top, p[D]);
-            const float f0 = top == -INFINITY ? 0.0f : exp2_approx(top - m);
-            const float f1 = p[D] == -INFINITY ? 0.0f : exp2_approx(p[D] - m);
-            const float2 v0 = *reinterpret_cast<const float2*>(p + d), v1 = *reinterpret_cast<const float2*>(p + d + 2);
-            o.x = o.x * f0 + v0.x * f1;
-            o.y = o.y * f0 + v0.y * f1;
-            o.z = o.z * f0 + v1.x * f1;
-            o.w = o.w * f0 + v1.y * f1;
-            l = l * f0 + p[D + 1] * f1;
-            top = m;
+    const int quads = ROWS * (D / 4) / static_cast<int>(gridDim.y);      // of this share; a power of two
+    const int across = min(quads, kJoinThreads), split = kJoinThreads / across;
+    const int quad = threadIdx.x % across, group = threadIdx.x / across;
+    for (int q0 = 0; q0 < quads; q0 += across) {
+        const int at_quad = blockIdx.y * quads + q0 + quad, row = at_quad / (D / 4), d = at_quad % (D / 4) * 4;
+        Partial acc = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, 0.0f};
+        auto part = [&](int w) {
+            return a.part + (static_cast<int64_t>(w0 + w) * 2 + (w == 0 ? first_slot : 0)) * slot + row * (D + 2);
+        };
+        for (int w = group; w < parts; w += 4 * split) {
+            Partial p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                p[i] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, 0.0f};
+                if (w + i * split < parts) p[i] = load_partial(part(w + i * split), d, D);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) merge(acc, p[i]);
         }
-        const int64_t tok = rq.q0 + (row0 + row) / a.group;
-        const int64_t oh = tok * a.heads + at.head * a.group + (row0 + row) % a.group;
-        store_quad<E>(a.out, oh * D + d, o, l > 0.0f ? 1.0f / (l * v_gs) : (l == 0.0f ? 0.0f : l));
-        if (a.lse && d == 0) a.lse[oh] = l == 0.0f ? -INFINITY : (top + log2f(l) - kPShift) * 0.693147180559945309f;
+        met[threadIdx.x] = acc;
+        __syncthreads();
+        if (group == 0 && row0 + row < rows) {
+            for (int i = 1; i < split; ++i) merge(acc, met[i * across + quad]);
+            const int64_t tok = rq.q0 + (row0 + row) / a.group;
+            const int64_t oh = tok * a.heads + head * a.group + (row0 + row) % a.group;
+            const float l = acc.l;
+            store_quad<E>(a.out, oh * D + d, acc.o, l > 0.0f ? 1.0f / (l * v_gs) : (l == 0.0f ? 0.0f : l));
+            if (a.lse && d == 0) a.lse[oh] = l == 0.0f ? -INFINITY : (acc.m + log2f(l) - kPShift) * 0.693147180559945309f;
+        }
+        __syncthreads();
     }
 }
 

@@ -188,13 +188,16 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(SlotArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Store.  One thread per 16-element block: two 16-byte loads, the block's
-// largest magnitude, its E4M3 scale and 16 E2M1 codes with the same steps (and
-// so the same bits) as the RMSQ_NVFP4 quantisation of the row ops.  Bound by
-// HBM: 2 bytes read and 9/16 written per element.  Consecutive threads take
-// consecutive blocks of a token, so a warp reads 1 KB in one piece and writes
-// whole 32-byte sectors of codes; the eight scale bytes of a head are
-// adjacent bytes of one store.
+// Store and load.  One thread per 16-element block; a token's blocks (keys,
+// then values) take `lanes` lanes of a warp, a power of two up to 32, so that
+// neither a token nor a head is found by division, and a token with more
+// blocks several rounds.  Bound by HBM: 2 bytes of T and 9/16 of codes and
+// scales per element.  A warp reads (store) or writes (load) up to 1 KB of T in
+// one piece and whole 32-byte sectors of codes; the scale bytes of a head are
+// adjacent bytes of one access.
+//
+// The store takes the same steps as the RMSQ_NVFP4 quantisation of the row ops
+// and so gives the same bits.
 // ---------------------------------------------------------------------------
 struct CacheArgs {
     const uint4* k;            // source (store) / destination (load) of the keys
@@ -207,6 +210,7 @@ struct CacheArgs {
     int64_t slots_total;       // pages * page size
     int n, heads, blocks;      // tokens, kv heads, 16-element blocks per head
     int page_shift;
+    int lane_shift;            // log2 of the lanes per token
 };
 
 template <class E>
@@ -227,28 +231,49 @@ __device__ __forceinline__ int64_t tile_offset(const CacheArgs& a, int64_t page,
     return ((page * 2 + side) * a.heads + head) * tile;
 }
 
-template <class E>
+// The token of a thread and its first block; false beyond the last token.
+__device__ __forceinline__ bool cache_place(const CacheArgs& a, int& t, int& c) {
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    c = static_cast<int>(i) & ((1 << a.lane_shift) - 1);
+    const int64_t token = i >> a.lane_shift;
+    t = static_cast<int>(token);
+    return token < a.n;
+}
+
+// A block of a token: its place in the token's rows and in the cache.
+template <int B>
+struct BlockPlace {
+    int side, rest;      // keys or values; 16-element block within the token's heads
+    uint8_t *codes, *scale;
+    __device__ __forceinline__ BlockPlace(const CacheArgs& a, int c, int64_t slot) {
+        const int per_side = a.heads * B;
+        side = c >= per_side;
+        rest = c - side * per_side;
+        const int head = rest / B, blk = rest % B;      // B is a power of two
+        const int in_page = static_cast<int>(slot) & ((1 << a.page_shift) - 1);
+        uint8_t* tile = a.cache + tile_offset(a, slot >> a.page_shift, side, head);
+        codes = tile + (in_page * B + blk) * 8;
+        scale = tile + ((B * 8) << a.page_shift) + in_page * B + blk;
+    }
+};
+
+template <class E, int B>
 __global__ void __launch_bounds__(256) cache_store_kernel(CacheArgs a) {
     allow_dependents();
     grid_dependency_wait();
+    int t, c;
+    if (!cache_place(a, t, c)) return;
+    const int64_t slot = __ldg(reinterpret_cast<const long long*>(a.slots) + t);
+    if (slot < 0 || slot >= a.slots_total) return;
     const float gs[2] = {__ldg(a.k_gs), __ldg(a.v_gs)};
-    const int per_side = a.heads * a.blocks, per_token = 2 * per_side;
-    const int64_t total = static_cast<int64_t>(a.n) * per_token;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int t = static_cast<int>(i / per_token);
-        int rest = static_cast<int>(i - static_cast<int64_t>(t) * per_token);
-        const int64_t slot = __ldg(reinterpret_cast<const long long*>(a.slots) + t);
-        if (slot < 0 || slot >= a.slots_total) continue;
-        const int side = rest >= per_side;
-        rest -= side * per_side;
-        const int head = rest / a.blocks, blk = rest - head * a.blocks;
-        const uint4* src = (side ? a.v + t * a.v_stride : a.k + t * a.k_stride) + 2 * rest;
+    for (; c < 2 * a.heads * B; c += 1 << a.lane_shift) {
+        const BlockPlace<B> p(a, c, slot);
+        const uint4* src = (p.side ? a.v + t * a.v_stride : a.k + t * a.k_stride) + 2 * p.rest;
         const uint4 lo = ld_act(src), hi = ld_act(src + 1);
         float x[8], y[8];
         unpack16<E>(lo, hi, x, y);
         const float amax = max_abs8(max_abs8(0.0f, x), y);
-        const float g = gs[side];
+        const float g = p.side ? gs[1] : gs[0];
         const uint32_t sb = e4m3x2(__fmul_rn(__fdiv_rn(amax, 6.0f), g), 0.0f) & 0x7fu;
         const float r = sb == 0u ? 0.0f : __fdiv_rn(g, e4m3_value_nonneg(sb));
 #pragma unroll
@@ -256,46 +281,51 @@ __global__ void __launch_bounds__(256) cache_store_kernel(CacheArgs a) {
             x[j] = __fmul_rn(x[j], r);
             y[j] = __fmul_rn(y[j], r);
         }
-        const int64_t page = slot >> a.page_shift;
-        const int in_page = static_cast<int>(slot & ((1 << a.page_shift) - 1));
-        uint8_t* tile = a.cache + tile_offset(a, page, side, head);
-        *reinterpret_cast<uint2*>(tile + (in_page * a.blocks + blk) * 8) = make_uint2(e2m1x8(x), e2m1x8(y));
-        tile[((a.blocks * 8) << a.page_shift) + in_page * a.blocks + blk] = static_cast<uint8_t>(sb);
+        *reinterpret_cast<uint2*>(p.codes) = make_uint2(e2m1x8(x), e2m1x8(y));
+        *p.scale = static_cast<uint8_t>(sb);
     }
 }
 
-// Load: value = T((q * d) / gs), q * d exact in fp32; zero for a token whose
-// slot is outside the cache.  Same split as the store, bytes the other way.
-template <class E>
+// Load: value = T((q * d) / gs) with q * d exact in fp32; zero for a token
+// whose slot is outside the cache.  The correctly rounded quotient lies
+// between the products with the two ends of a bracket around 1 / gs (2^-18
+// wide, far above the roundings involved), and rounding to T is monotone, so
+// where both ends round to the same T that is the result; otherwise (about
+// one block in a thousand) the block is divided out.
+template <class E, int B>
 __global__ void __launch_bounds__(256) cache_load_kernel(CacheArgs a) {
     allow_dependents();
     grid_dependency_wait();
+    int t, c;
+    if (!cache_place(a, t, c)) return;
+    const int64_t slot = __ldg(reinterpret_cast<const long long*>(a.slots) + t);
+    const bool inside = slot >= 0 && slot < a.slots_total;
     const float gs[2] = {__ldg(a.k_gs), __ldg(a.v_gs)};
-    const int per_side = a.heads * a.blocks, per_token = 2 * per_side;
-    const int64_t total = static_cast<int64_t>(a.n) * per_token;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < total;
-         i += static_cast<int64_t>(gridDim.x) * 256) {
-        const int t = static_cast<int>(i / per_token);
-        int rest = static_cast<int>(i - static_cast<int64_t>(t) * per_token);
-        const int64_t slot = __ldg(reinterpret_cast<const long long*>(a.slots) + t);
-        const int side = rest >= per_side;
-        rest -= side * per_side;
-        uint4* dst = const_cast<uint4*>(side ? a.v + t * a.v_stride : a.k + t * a.k_stride) + 2 * rest;
+    const Fp8Recips rc[2] = {fp8_recips(gs[0]), fp8_recips(gs[1])};
+    for (; c < 2 * a.heads * B; c += 1 << a.lane_shift) {
+        const BlockPlace<B> p(a, c, inside ? slot : 0);
+        uint4* dst = const_cast<uint4*>(p.side ? a.v + t * a.v_stride : a.k + t * a.k_stride) + 2 * p.rest;
         uint32_t w[8] = {};
-        if (slot >= 0 && slot < a.slots_total) {
-            const int head = rest / a.blocks, blk = rest - head * a.blocks;
-            const int64_t page = slot >> a.page_shift;
-            const int in_page = static_cast<int>(slot & ((1 << a.page_shift) - 1));
-            const uint8_t* tile = a.cache + tile_offset(a, page, side, head);
-            const uint2 c = __ldg(reinterpret_cast<const uint2*>(tile + (in_page * a.blocks + blk) * 8));
-            const float d = nvfp4_scale_value(
-                __ldg(tile + ((a.blocks * 8) << a.page_shift) + in_page * a.blocks + blk));
-            const float g = gs[side];
+        if (inside) {
+            const uint2 q = __ldg(reinterpret_cast<const uint2*>(p.codes));
+            const float d = nvfp4_scale_value(__ldg(p.scale)), g = p.side ? gs[1] : gs[0];
+            const float dn = p.side ? rc[1].rdn : rc[0].rdn, up = p.side ? rc[1].rup : rc[0].rup;
+            // outside this range the bracket's ends would be subnormal or infinite
+            uint32_t pair[8], diff = !(g >= 7.8886091e-31f && g <= 1.2676506e30f);
+            e2m1x8_f16x2(q.x, *reinterpret_cast<uint32_t(*)[4]>(&pair[0]));
+            e2m1x8_f16x2(q.y, *reinterpret_cast<uint32_t(*)[4]>(&pair[4]));
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const uint32_t word = j < 4 ? c.x : c.y;
-                const uint32_t pair = e2m1x2_f16x2(word >> (8 * (j & 3)));
-                w[j] = E::pack(__fdiv_rn(__fmul_rn(Fp16T::lo(pair), d), g), __fdiv_rn(__fmul_rn(Fp16T::hi(pair), d), g));
+                const float2 v = mul2_rn(make_float2(Fp16T::lo(pair[j]), Fp16T::hi(pair[j])), make_float2(d, d));
+                const float2 lo = mul2_rn(v, make_float2(dn, dn)), hi = mul2_rn(v, make_float2(up, up));
+                w[j] = E::pack(lo.x, lo.y);
+                diff |= w[j] ^ E::pack(hi.x, hi.y);
+            }
+            if (diff) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    w[j] = E::pack(__fdiv_rn(__fmul_rn(Fp16T::lo(pair[j]), d), g),
+                                   __fdiv_rn(__fmul_rn(Fp16T::hi(pair[j]), d), g));
             }
         }
         st_stream(dst, make_uint4(w[0], w[1], w[2], w[3]));
@@ -359,13 +389,20 @@ CacheSpans cache_spans(const CacheArgs& a, const float* k_gs, const float* v_gs)
             {rmsq_abi::span(a.slots, static_cast<size_t>(a.n) * 8), rmsq_abi::span(k_gs, 4), rmsq_abi::span(v_gs, 4)}};
 }
 
-cudaError_t launch_cache(const void* fn, CacheArgs& a, cudaStream_t stream) {
-    cudaError_t e;
-    const int sms = sm_count(&e);
-    if (e != cudaSuccess) return e;
-    const int64_t threads = static_cast<int64_t>(a.n) * 2 * a.heads * a.blocks;
-    int64_t grid = (threads + 255) / 256;
-    if (grid > static_cast<int64_t>(sms) * 32) grid = static_cast<int64_t>(sms) * 32;
+cudaError_t launch_cache(bool store, bool fp16, CacheArgs& a, cudaStream_t stream) {
+    const void* fn;
+#define RMSQ_CACHE_KERNEL(B)                                                                                     \
+    (store ? (fp16 ? (const void*)&cache_store_kernel<Fp16T, B> : (const void*)&cache_store_kernel<Bf16T, B>)    \
+           : (fp16 ? (const void*)&cache_load_kernel<Fp16T, B> : (const void*)&cache_load_kernel<Bf16T, B>))
+    switch (a.blocks) {
+    case 4: fn = RMSQ_CACHE_KERNEL(4); break;
+    case 8: fn = RMSQ_CACHE_KERNEL(8); break;
+    default: fn = RMSQ_CACHE_KERNEL(16); break;
+    }
+#undef RMSQ_CACHE_KERNEL
+    a.lane_shift = 3;   // the smallest token: one head of 64, keys and values
+    while (a.lane_shift < 5 && (1 << a.lane_shift) < 2 * a.heads * a.blocks) ++a.lane_shift;
+    const int64_t grid = ((static_cast<int64_t>(a.n) << a.lane_shift) + 255) / 256;
     void* params[] = {&a};
     return launch_kernel(fn, dim3(static_cast<unsigned>(grid)), dim3(256), params, 0, stream);
 }
@@ -444,9 +481,7 @@ int rmsq_kv_cache_store_nvfp4(const void* k, int64_t k_stride, const void* v, in
         if (rmsq_abi::overlaps(s.cache, in)) return RMSQ_ERR_ALIAS;
     st = rmsq_abi::check_device();
     if (st != RMSQ_OK) return st;
-    const void* fn = dtype == RMSQ_BF16 ? (const void*)&rmsq::cache_store_kernel<rmsq::Bf16T>
-                                        : (const void*)&rmsq::cache_store_kernel<rmsq::Fp16T>;
-    const cudaError_t e = rmsq::launch_cache(fn, a, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = rmsq::launch_cache(true, dtype == RMSQ_FP16, a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? RMSQ_OK : rmsq_abi::fail_cuda(e);
 }
 
@@ -470,9 +505,7 @@ int rmsq_kv_cache_load_nvfp4(const void* kv_cache, int64_t num_pages, int64_t pa
     }
     st = rmsq_abi::check_device();
     if (st != RMSQ_OK) return st;
-    const void* fn = dtype == RMSQ_BF16 ? (const void*)&rmsq::cache_load_kernel<rmsq::Bf16T>
-                                        : (const void*)&rmsq::cache_load_kernel<rmsq::Fp16T>;
-    const cudaError_t e = rmsq::launch_cache(fn, a, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = rmsq::launch_cache(false, dtype == RMSQ_FP16, a, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? RMSQ_OK : rmsq_abi::fail_cuda(e);
 }
 

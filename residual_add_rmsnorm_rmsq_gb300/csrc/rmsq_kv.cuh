@@ -29,11 +29,12 @@ __device__ __forceinline__ void e2m1x8_f16x2(uint32_t w, uint32_t (&r)[4]) {
 }
 
 // Value of a stored block scale.  The store writes codes 0x00 .. 0x7e; the
-// sign bit is ignored and the NaN code counts as zero, so that a page nobody
-// has written yet cannot put a NaN into a sum.
+// NaN codes read as 448, so that a page nobody has written yet cannot put a
+// NaN into a sum.
 __device__ __forceinline__ float nvfp4_scale_value(uint32_t code) {
     const uint32_t c = code & 0x7fu;
-    return c == 0x7fu ? 0.0f : e4m3_value_nonneg(c);
+    const float v = e4m3_value_nonneg(c);
+    return c == 0x7fu ? 448.0f : (code & 0x80u) ? -v : v;
 }
 
 // Whether rows of `row` 16-byte chunks at a and b, both at the same stride,

@@ -12,12 +12,12 @@ E2M1 = np.array([0, 0.5, 1, 1.5, 2, 3, 4, 6, -0.0, -0.5, -1, -1.5, -2, -3, -4, -
 
 
 def e4m3_table() -> np.ndarray:
-    """Value of each scale byte: sign ignored, the NaN code 0."""
+    """Value of each scale byte; the NaN codes read as 448."""
     out = np.zeros(256)
     for c in range(256):
         e, m = (c >> 3) & 15, c & 7
         v = m * 2.0 ** -9 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7)
-        out[c] = 0.0 if (c & 127) == 127 else v
+        out[c] = 448.0 if (c & 127) == 127 else -v if c & 128 else v
     return out
 
 

@@ -48,7 +48,7 @@ def check(rq, c, *, window=0, scale=None, **kw):
     assert np.array_equal(np.isinf(s), empty) and (s[empty] < 0).all() and (o[empty] == 0).all()
     bad = np.abs(o - w_out) - tol
     assert bad.max(initial=0) <= 0, f"out off by up to {np.abs(o - w_out).max()}, {(bad > 0).sum()} beyond"
-    bad = np.abs(s - w_lse)[~empty] - tol_lse[~empty]
+    bad = np.abs(s[~empty] - w_lse[~empty]) - tol_lse[~empty]
     assert bad.max(initial=0) <= 0, f"lse beyond by {bad.max()}"
     return out, lse
 

@@ -144,11 +144,11 @@ def test_store_and_load(rmsq_gpu, dtype, n, h, D, page):
     assert torch.equal(k2, ko) and torch.equal(v2, vo)
 
 
-def test_load_reads_nan_scales_as_zero(rmsq_gpu):
+def test_load_reads_nan_scales_as_448(rmsq_gpu):
     cache = torch.full(rmsq_gpu.kv_cache_shape(1, 1, 64, 16), 0xff, dtype=torch.uint8, device="cuda")
     one = torch.ones(1, device="cuda")
     k, v = rmsq_gpu.kv_cache_load_nvfp4(cache, torch.arange(16, device="cuda"), one, one, 64, 16)
-    assert (k == 0).all() and (v == 0).all()
+    assert (k == -6 * 448).all() and (v == -6 * 448).all()
 
 
 def test_store_saturates_and_keeps_infinities_out_of_the_scales(rmsq_gpu):
