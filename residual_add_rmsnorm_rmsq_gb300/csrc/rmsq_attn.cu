@@ -6,9 +6,17 @@
 #include "rmsq.h"
 #include "rmsq_abi.h"
 #include "rmsq_attn.cuh"
+#include "rmsq_attn_prompt.cuh"
 #include "rmsq_host.cuh"
 
 namespace rmsq {
+
+cudaError_t take_prompt_fault(unsigned int* out) {
+    const unsigned int zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbol(out, g_prompt_fault, sizeof(unsigned int));
+    if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(g_prompt_fault, &zero, sizeof(zero));
+    return e;
+}
 
 namespace {
 
@@ -51,8 +59,32 @@ cudaError_t launch_split(AttnArgs a, int64_t max_tiles, cudaStream_t stream) {
     return launch_kernel(join, dim3(a.workers, shares), dim3(kJoinThreads), params, 0, stream);
 }
 
+template <class E, int D>
+cudaError_t launch_prompt(AttnArgs a, cudaStream_t stream) {
+    const void* fn = (const void*)&attn_prompt_kernel<E, D>;
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptTile<D>::smem);
+    if (e != cudaSuccess) return e;
+    // as many 256-row items as these sizes can hold; those without one return at once
+    const int64_t rows = static_cast<int64_t>(a.tokens) * a.group;
+    const int64_t few = rows / (a.most_rows + 1);
+    const int64_t items = rows / 256 + (few < a.requests ? few : a.requests);
+    void* params[] = {&a};
+    return launch_kernel(fn, dim3(static_cast<unsigned>(items * a.kv_heads)), dim3(kPromptThreads), params,
+                         PromptTile<D>::smem, stream);
+}
+
+// Requests of more than kPromptRows rows go to the prompt kernel, the others
+// to the split kernel, whichever they are: the lengths are the device's.  The
+// prompt kernel is launched where a request may have more than that on average.
 template <class E>
-cudaError_t launch_attn(const AttnArgs& a, int head_dim, int64_t max_tiles, cudaStream_t stream) {
+cudaError_t launch_attn(AttnArgs a, int head_dim, int64_t max_tiles, cudaStream_t stream) {
+    const bool prompt = head_dim <= 128 && static_cast<int64_t>(a.tokens) * a.group > static_cast<int64_t>(kPromptRows) * a.requests;
+    // (a single request is the prompt kernel's whatever its length)
+    a.most_rows = !prompt ? INT32_MAX : a.requests == 1 ? 0 : kPromptRows;
+    if (prompt) {
+        const cudaError_t e = head_dim == 64 ? launch_prompt<E, 64>(a, stream) : launch_prompt<E, 128>(a, stream);
+        if (e != cudaSuccess || a.requests == 1) return e;
+    }
     const int nb = row_blocks(a.tokens, a.requests, a.group, head_dim);
     switch (head_dim) {
     case 64: return nb == 2 ? launch_split<E, 64, 2>(a, max_tiles, stream) : launch_split<E, 64, 1>(a, max_tiles, stream);

@@ -47,6 +47,7 @@ constexpr int kAttnWarps = 4;
 constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kAttnKeyTile = kAttnWarps * 32;   // keys per CTA step: 32 per warp
 constexpr int kAttnMaxWorkers = 1216;           // CTAs of the split launch: 8 per SM of 152
+constexpr int kPromptRows = 64;                 // see launch_attn
 constexpr float kPShift = 9.0f;                 // probabilities are scaled by 2^9 ...
 constexpr float kLazy = 6.0f;                   // ... and by up to 2^6 more while the maximum lags: < 2^16 in f16
 
@@ -74,6 +75,7 @@ struct AttnArgs {
     float* part;            // [workers][2][ROWS][D + 2]
     int requests, width, tokens, heads, kv_heads, group;
     int page_shift, num_pages, window, workers;
+    int most_rows;          // rows of a request above which the split kernel leaves it to the prompt kernel
     float scale_log2;       // softmax scale * log2(e)
 };
 
@@ -92,7 +94,8 @@ __device__ __forceinline__ Req load_request(const AttnArgs& a, int r) {
     const int first = a.window > 0 ? max(x.seq - x.qlen - a.window + 1, 0) : 0;
     x.tile0 = min(first, max(x.seq - 1, 0)) / kAttnKeyTile;
     x.ktiles = max((x.seq + kAttnKeyTile - 1) / kAttnKeyTile - x.tile0, 1);
-    x.qtiles = static_cast<int>((static_cast<int64_t>(x.qlen) * a.group + ROWS - 1) / ROWS);
+    const int64_t rows = static_cast<int64_t>(x.qlen) * a.group;
+    x.qtiles = rows > a.most_rows ? 0 : static_cast<int>((rows + ROWS - 1) / ROWS);
     return x;
 }
 

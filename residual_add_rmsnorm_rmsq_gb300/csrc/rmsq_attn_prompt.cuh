@@ -1,0 +1,517 @@
+// Attention over the paged NVFP4 cache for many queries per request (prompts),
+// on the fifth-generation tensor cores.  The mathematics, the f16 operands and
+// the scaling of queries and probabilities are those of rmsq_attn.cuh.
+//
+// A CTA takes 256 rows (query token, head of the group) of a request and kv
+// head as two tiles of 128, and walks the keys 128 at a time:
+//   S = Q . K^T (128 x 128 x D)  ->  P = 2^(f S - m)  ->  O += P . V (128 x D x 128)
+// with S, P (f16, in S's place) and O in tensor memory, a thread per row in the
+// softmax.  While one tile is in its softmax the matrix unit works for the
+// other.  Four warps turn the cache's codes into f16 operand tiles in shared
+// memory, once for both tiles: a key per thread for K; 8 keys x D/8 dims per
+// thread for V, whose nibbles are interleaved pairwise so that eight keys of a
+// dim come out as one 16-byte piece of V^T, the layout the product wants.
+//
+// Bound by the matrix unit in the limit (4 D flop per row and key, 1024 clocks
+// per 128 x 128 tile at D = 128); the softmax takes about 2300 warp
+// instructions per tile and the conversion 1300 per two, which together leave
+// it no more than three quarters of the issue slots.
+//
+// Every wait is bounded, as in the matrix product.
+#pragma once
+
+#include "rmsq_attn.cuh"
+#include "rmsq_tc.cuh"
+
+namespace rmsq {
+
+static __device__ unsigned int g_prompt_fault;
+
+constexpr int kPromptThreads = 416;     // 8 softmax warps, 4 converting warps, the issuing warp
+
+template <int D>
+struct PromptTile {
+    static constexpr int q = 128 * D * 2, k = 128 * D * 2, v = 128 * D * 2;    // bytes of one operand tile
+    // one CTA per SM in any case: it takes all of tensor memory
+    static constexpr int smem = 1024 + (6 * q > 120 * 1024 ? 6 * q : 120 * 1024);
+};
+
+// Instruction descriptor: f16 x f16 -> fp32, both K-major, 128 x N.
+template <int N>
+constexpr uint32_t kF16Idesc = (1u << 4) | (static_cast<uint32_t>(N / 8) << 17) | ((128u / 16u) << 24);
+
+// D = A . B^T over `steps` steps of 16 along K; A and B in swizzled tiles whose
+// 64-element column blocks are a_block / b_block bytes apart.
+template <int N, int STEPS>
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, int a_block, uint64_t b, int b_block) {
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const uint64_t da = a + (i >> 2) * (a_block >> 4) + (i & 3) * 2, db = b + (i >> 2) * (b_block >> 4) + (i & 3) * 2;
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                     :: "r"(d), "l"(da), "l"(db), "r"(kF16Idesc<N>), "r"(i) : "memory");
+    }
+}
+
+// D (+)= A . B^T with A in tensor memory (8 columns per step).
+template <int N, int STEPS>
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, int b_block, bool add) {
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+        const uint64_t db = b + (i >> 2) * (b_block >> 4) + (i & 3) * 2;
+        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                     :: "r"(d), "r"(a + 8 * i), "l"(db), "r"(kF16Idesc<N>), "r"(i > 0 || add ? 1 : 0) : "memory");
+    }
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+                 "%14, %15, %16};"
+                 :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                    "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A converting thread's share of a 128-key tile, as it lies in the cache.
+template <int D>
+struct RawTile {
+    static constexpr int KW = D / 8;        // words of the thread's key
+    static constexpr int VW = D / 64;       // words of each of its 8 keys' values (D/8 dims)
+    uint32_t k[KW], ks[D / 64], v[8][VW], vs[8];
+};
+
+template <int D>
+__device__ __forceinline__ void load_tile(RawTile<D>& x, const AttnArgs& a, int key0, int kpage, int vpage, int head,
+                                          int tid, int octet, int unit) {
+    const int64_t tile = static_cast<int64_t>(D / 16 * 9) << a.page_shift;
+    const int mask = (1 << a.page_shift) - 1;
+    if (kpage >= 0) {
+        const uint8_t* t = a.cache + (static_cast<int64_t>(kpage) * 2 * a.kv_heads + head) * tile;
+        const int in = (key0 + tid) & mask;
+        const uint4* p = reinterpret_cast<const uint4*>(t + in * (D / 2));
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) {
+            const uint4 u = __ldg(p + j);
+            x.k[4 * j] = u.x; x.k[4 * j + 1] = u.y; x.k[4 * j + 2] = u.z; x.k[4 * j + 3] = u.w;
+        }
+        const uint32_t* s = reinterpret_cast<const uint32_t*>(t + ((D / 2) << a.page_shift) + in * (D / 16));
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) x.ks[j] = __ldg(s + j);
+    } else {
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j) x.k[j] = 0u;
+#pragma unroll
+        for (int j = 0; j < D / 64; ++j) x.ks[j] = 0u;
+    }
+    const uint8_t* t = a.cache + ((static_cast<int64_t>(max(vpage, 0)) * 2 + 1) * a.kv_heads + head) * tile;
+    const int in = (key0 + octet * 8) & mask;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        if (vpage >= 0) {
+            const uint8_t* p = t + (in + i) * (D / 2) + unit * (D / 16);
+            if constexpr (D == 128) {
+                const uint2 u = __ldg(reinterpret_cast<const uint2*>(p));
+                x.v[i][0] = u.x; x.v[i][1] = u.y;
+            } else {
+                x.v[i][0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+            }
+            x.vs[i] = __ldg(t + ((D / 2) << a.page_shift) + (in + i) * (D / 16) + unit * (D / 8) / 16);
+        } else {
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) x.v[i][j] = 0u;
+            x.vs[i] = 0u;
+        }
+    }
+}
+
+// K of the thread's key as a row of the operand tile.
+template <int D>
+__device__ __forceinline__ void write_keys(unsigned char* dst, const RawTile<D>& x, int row) {
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j) {
+        uint32_t lo[4], hi[4];
+        e2m1x8_f16x2(x.k[2 * j], lo);
+        e2m1x8_f16x2(x.k[2 * j + 1], hi);
+        const uint32_t s = dup_half(e4m3x2_f16x2(x.ks[j / 4] >> (8 * (j & 2))), j & 1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            lo[i] = mul_f16x2(lo[i], s);
+            hi[i] = mul_f16x2(hi[i], s);
+        }
+        unsigned char* r = dst + (j >> 2) * (128 * 128) + row * 128;
+        const int c = (j & 3) * 2;
+        *reinterpret_cast<uint4*>(r + ((c ^ (row & 7)) << 4)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        *reinterpret_cast<uint4*>(r + (((c + 1) ^ (row & 7)) << 4)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+    }
+}
+
+// V of the thread's 8 keys and D/8 dims as 16-byte pieces of V^T's rows.
+template <int D>
+__device__ __forceinline__ void write_values(unsigned char* dst, const RawTile<D>& x, int octet, int unit) {
+    uint32_t sc[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) sc[p] = e4m3x2_f16x2(x.vs[2 * p] | (x.vs[2 * p + 1] << 8));
+    unsigned char* base = dst + (octet >> 3) * (D * 128);
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+        uint32_t even[4][4], odd[4][4];
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+            const uint32_t A = x.v[2 * p][j], B = x.v[2 * p + 1][j];
+            e2m1x8_f16x2((A & 0x0f0f0f0fu) | ((B << 4) & 0xf0f0f0f0u), even[p]);
+            e2m1x8_f16x2(((A >> 4) & 0x0f0f0f0fu) | (B & 0xf0f0f0f0u), odd[p]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                even[p][c] = mul_f16x2(even[p][c], sc[p]);
+                odd[p][c] = mul_f16x2(odd[p][c], sc[p]);
+            }
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int row = unit * (D / 8) + 8 * j + 2 * c;
+            *reinterpret_cast<uint4*>(base + row * 128 + (((octet & 7) ^ (row & 7)) << 4)) =
+                make_uint4(even[0][c], even[1][c], even[2][c], even[3][c]);
+            *reinterpret_cast<uint4*>(base + (row + 1) * 128 + (((octet & 7) ^ ((row + 1) & 7)) << 4)) =
+                make_uint4(odd[0][c], odd[1][c], odd[2][c], odd[3][c]);
+        }
+    }
+}
+
+// Items (256-row tiles) of a request; requests of few rows are the split
+// kernel's.
+__device__ __forceinline__ int prompt_items(const AttnArgs& a, int r) {
+    const int q0 = min(max(__ldg(a.q_start + r), 0), a.tokens);
+    const int64_t rows = static_cast<int64_t>(min(max(__ldg(a.q_start + r + 1), q0), a.tokens) - q0) * a.group;
+    return rows > a.most_rows ? static_cast<int>((rows + 255) / 256) : 0;
+}
+
+template <class E, int D>
+__global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs a) {
+    using Tile = PromptTile<D>;
+    extern __shared__ unsigned char dyn[];
+    __shared__ __align__(8) uint64_t qfull[2], kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pready[2], ofull[2],
+        drained;
+    __shared__ __align__(16) uint32_t valid[4][4];  // which keys of a tile lie on a page, four tiles deep
+    __shared__ uint32_t tmem_base;
+    __shared__ int wsum[kPromptThreads / 32];
+    unsigned char* qs = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
+    unsigned char* ks = qs + 2 * Tile::q;
+    unsigned char* vs = ks + 2 * Tile::k;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&qfull[i], 4);
+            mbar_init(&kfull[i], 4);
+            mbar_init(&kempty[i], 1);
+            mbar_init(&vfull[i], 4);
+            mbar_init(&vempty[i], 1);
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pready[i], 4);
+            mbar_init(&ofull[i], 1);
+        }
+        mbar_init(&drained, 1);
+        fence_mbar_init();
+    }
+    grid_dependency_wait();
+
+    // The item of this CTA: tiles of a request from the last rows (most keys)
+    // to the first, kv heads innermost.  The scan borrows the key tiles' space.
+    int* prefix = reinterpret_cast<int*>(ks);
+    {
+        const int per = (a.requests + kPromptThreads - 1) / kPromptThreads;
+        const int r0 = min(tid * per, a.requests), r1 = min(r0 + per, a.requests);
+        int sum = 0;
+        for (int r = r0; r < r1; ++r) {
+            const int c = prompt_items(a, r);
+            prefix[r + 1] = c;
+            sum += c;
+        }
+        int inc = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(kFull, inc, o);
+            if (lane >= o) inc += u;
+        }
+        if (lane == 31) wsum[warp] = inc;
+        __syncthreads();
+        int run = inc - sum;
+        for (int w = 0; w < warp; ++w) run += wsum[w];
+        for (int r = r0; r < r1; ++r) {
+            run += prefix[r + 1];
+            prefix[r + 1] = run;
+        }
+        if (tid == 0) prefix[0] = 0;
+        __syncthreads();
+    }
+    const int item = prefix[a.requests] - 1 - static_cast<int>(blockIdx.x) / a.kv_heads;
+    const int head = blockIdx.x % a.kv_heads;
+    int req = 0;
+    if (item >= 0) {
+        int hi = a.requests;
+        while (hi - req > 1) {
+            const int mid = (req + hi) >> 1;
+            if (prefix[mid] <= item) req = mid;
+            else hi = mid;
+        }
+    }
+    const int row0 = item >= 0 ? (item - prefix[req]) * 256 : 0;
+    __syncthreads();    // the scan has been read: its space is the key tiles' now
+    if (item < 0) {
+        allow_dependents();
+        return;
+    }
+    if (warp == 12) tmem_alloc(&tmem_base, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    allow_dependents();
+    const uint32_t tmem = tmem_base;
+
+    const Req rq = load_request<8>(a, req);
+    const int rows = rq.qlen * a.group, first_pos = rq.seq - rq.qlen;
+    const int tiles = min(rows - row0, 256) > 128 ? 2 : 1;
+    const int last_pos = first_pos + (min(row0 + 256, rows) - 1) / a.group;
+    const int low_pos = first_pos + row0 / a.group;
+    const int low_key = a.window > 0 ? max(low_pos - a.window + 1, 0) : 0;
+    const int key_begin = low_key / 128 * 128;
+    const int steps = last_pos < key_begin ? 0 : (last_pos - key_begin) / 128 + 1;
+    bool ok = true;
+
+    if (warp == 12) {
+        if (lane == 0 && steps > 0) {
+            for (int i = 0; i < tiles && ok; ++i) ok = mbar_wait_bounded(&qfull[i], 0);
+            for (int n = 0; n <= steps && ok; ++n) {
+                const int s = n & 1, z = (n - 1) & 1;
+                if (n < steps) ok = mbar_wait_bounded(&kfull[s], (n >> 1) & 1);
+                if (n > 0) ok = ok && mbar_wait_bounded(&vfull[z], ((n - 1) >> 1) & 1);
+                for (int i = 0; i < tiles && ok; ++i) {
+                    if (n > 0) {
+                        ok = mbar_wait_bounded(&pready[i], (n - 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        mma_f16_ts<D, 8>(tmem + 256 + i * D, tmem + i * 128, tile_desc(vs + z * Tile::v), D * 128, n > 1);
+                        if (n == steps) mma_commit(&ofull[i]);
+                        if (i == tiles - 1) mma_commit(&vempty[z]);
+                    }
+                    if (n < steps) {
+                        tc_fence_after();
+                        mma_f16_ss<128, D / 16>(tmem + i * 128, tile_desc(qs + i * Tile::q), 128 * 128,
+                                                tile_desc(ks + s * Tile::k), 128 * 128);
+                        mma_commit(&sfull[i]);
+                    }
+                }
+                if (ok && n < steps) mma_commit(&kempty[s]);
+            }
+            if (!ok) {
+                mma_commit(&drained);
+                mbar_wait_bounded(&drained, 0);
+            }
+        }
+    } else if (warp >= 8) {
+        // Conversion: the codes of the next tile, and the pages of the one
+        // after it, are on their way while a tile is converted.
+        const int t = tid - 256, w = warp - 8;
+        const int octet = (w & 1) * 8 + (lane & 7), unit = (w >> 1) * 4 + (lane >> 3);
+        const int* table = a.table + static_cast<int64_t>(req) * a.width;
+        auto page_of = [&](int key) {
+            if (key > last_pos) return -1;
+            const int p = __ldg(table + (key >> a.page_shift));
+            return p < a.num_pages ? p : -1;
+        };
+        RawTile<D> cur, nxt;
+        int kp = page_of(key_begin + t), vp = page_of(key_begin + octet * 8);
+        load_tile<D>(cur, a, key_begin, kp, vp, head, t, octet, unit);
+        int kp1 = page_of(key_begin + 128 + t), vp1 = page_of(key_begin + 128 + octet * 8);
+        for (int n = 0; n < steps; ++n) {
+            const int key0 = key_begin + n * 128, s = n & 1;
+            load_tile<D>(nxt, a, key0 + 128, kp1, vp1, head, t, octet, unit);
+            const int kp2 = page_of(key0 + 256 + t), vp2 = page_of(key0 + 256 + octet * 8);
+            ok = warp_wait(&kempty[s], ((n >> 1) & 1) ^ 1);
+            if (!ok) break;
+            const uint32_t there = __ballot_sync(kFull, kp >= 0);
+            if (lane == 0) valid[n & 3][w] = there;
+            write_keys<D>(ks + s * Tile::k, cur, t);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&kfull[s]);
+            ok = warp_wait(&vempty[s], ((n >> 1) & 1) ^ 1);
+            if (!ok) break;
+            write_values<D>(vs + s * Tile::v, cur, octet, unit);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&vfull[s]);
+            cur = nxt;
+            kp = kp1;
+            kp1 = kp2;
+            vp1 = vp2;
+        }
+    } else {
+        const int i = warp >> 2, quad = warp & 3, local = quad * 32 + lane, row = row0 + i * 128 + local;
+        if (i < tiles) {
+            // The row's query: scaled into f16's range, into its operand row.
+            const int token = row / a.group, qh = head * a.group + row % a.group;
+            const bool live = row < rows;
+            uint32_t q[D / 2];
+#pragma unroll
+            for (int j = 0; j < D / 2; ++j) q[j] = 0u;
+            if (live) {
+                const uint4* p = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) +
+                                                                (rq.q0 + token) * a.q_stride + qh * D);
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) {
+                    const uint4 u = __ldg(p + j);
+                    q[4 * j] = u.x; q[4 * j + 1] = u.y; q[4 * j + 2] = u.z; q[4 * j + 3] = u.w;
+                }
+            }
+            float f = a.scale_log2 / __ldg(a.k_gs);
+            if constexpr (E::kBits87 == Bf16T::kBits87) {
+                float top = 0.0f;
+#pragma unroll
+                for (int j = 0; j < D / 2; ++j) top = max_abs3(top, E::lo(q[j]), E::hi(q[j]));
+                const int e = min(14 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 126);
+                const float up = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+                f *= __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+                for (int j = 0; j < D / 2; ++j) q[j] = Fp16T::pack(E::lo(q[j]) * up, E::hi(q[j]) * up);
+            }
+            f = fmaxf(f, 1.17549435e-38f);
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j)
+                *reinterpret_cast<uint4*>(qs + i * Tile::q + (j >> 3) * (128 * 128) + local * 128 +
+                                          (((j & 7) ^ (local & 7)) << 4)) =
+                    make_uint4(q[4 * j], q[4 * j + 1], q[4 * j + 2], q[4 * j + 3]);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&qfull[i]);
+
+            const int pos = live ? first_pos + token : -1, lo = a.window > 0 ? pos - a.window + 1 : 0;
+            const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
+            const uint32_t s_at = tmem + i * 128 + lanes, o_at = tmem + 256 + i * D + lanes;
+            float m = -INFINITY, l = 0.0f, limit = -INFINITY;
+            for (int n = 0; n < steps; ++n) {
+                const int key0 = key_begin + n * 128;
+                ok = warp_wait(&sfull[i], n & 1);
+                if (!ok) break;
+                tc_fence_after();
+                const uint4 have = *reinterpret_cast<const uint4*>(valid[n & 3]);
+                const uint32_t hv[4] = {have.x, have.y, have.z, have.w};
+                const bool whole = (have.x & have.y & have.z & have.w) == 0xffffffffu;
+                // keys this row may see, as bits, where not every row of the warp sees all of them
+                const bool full = __all_sync(kFull, whole && (!live || (key0 + 127 <= pos && key0 >= lo)));
+                uint32_t see[4];
+                if (!full) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int k = key0 + 32 * c;
+                        const int upto = min(max(pos - k + 1, 0), 32), from = min(max(lo - k, 0), 32);
+                        const uint32_t below = upto == 32 ? 0xffffffffu : (1u << upto) - 1u;
+                        const uint32_t above = from == 32 ? 0u : 0xffffffffu << from;
+                        see[c] = below & above & hv[c];
+                    }
+                }
+                float d[2][16];
+                float top = -INFINITY;
+                tmem_ld16(d[0], s_at);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    tmem_wait(d[c & 1]);
+                    if (c < 7) tmem_ld16(d[(c + 1) & 1], s_at + (c + 1) * 16);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        top = fmaxf(top, full || (see[c >> 1] >> ((c & 1) * 16 + j) & 1u) ? d[c & 1][j] : -INFINITY);
+                }
+                if (__any_sync(kFull, top > limit)) {
+                    // sfull of this step says that the previous P . V has
+                    // completed too: O may be rescaled here
+                    const float m1 = fmaxf(top * f, m);
+                    const float r = m1 == -INFINITY ? 1.0f : exp2_approx(m - m1);
+                    m = m1;
+                    limit = (m + kLazy) / f;
+                    l *= r;
+                    if (n > 0) {
+#pragma unroll
+                        for (int c = 0; c < D / 16; ++c) {
+                            float o[16];
+                            uint32_t u[16];
+                            tmem_ld16(o, o_at + c * 16);
+                            tmem_wait(o);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) u[j] = __float_as_uint(o[j] * r);
+                            tmem_st16(o_at + c * 16, u);
+                        }
+                    }
+                }
+                const float shift = m == -INFINITY ? 0.0f : kPShift - m;
+                const float2 f2 = make_float2(f, f), s2 = make_float2(shift, shift);
+                float2 sum = make_float2(0.0f, 0.0f);
+                uint32_t p[16];
+                tmem_ld16(d[0], s_at);
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    tmem_wait(d[c & 1]);
+                    if (c < 7) tmem_ld16(d[(c + 1) & 1], s_at + (c + 1) * 16);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float2 x = make_float2(d[c & 1][2 * j], d[c & 1][2 * j + 1]);
+                        if (!full) {
+                            const uint32_t bits = see[c >> 1] >> ((c & 1) * 16 + 2 * j);
+                            if (!(bits & 1u)) x.x = -INFINITY;
+                            if (!(bits & 2u)) x.y = -INFINITY;
+                        }
+                        x = fma2_rn(x, f2, s2);
+                        x.x = exp2_approx(x.x);
+                        x.y = exp2_approx(x.y);
+                        sum = add2_rn(sum, x);
+                        p[(c & 1) * 8 + j] = Fp16T::pack(x.x, x.y);
+                    }
+                    // columns 0 .. 16 c + 15 of S have been read: P's first
+                    // 8 c + 8 columns lie inside them
+                    if (c & 1) tmem_st16(s_at + (c >> 1) * 16, p);
+                }
+                l += sum.x + sum.y;
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pready[i]);
+            }
+            // O / l, in T
+            if (ok && steps > 0) {
+                ok = warp_wait(&ofull[i], 0);
+                tc_fence_after();
+            }
+            const float inv = l > 0.0f ? 1.0f / (l * __ldg(a.v_gs)) : (l == 0.0f ? 0.0f : l);
+            const int64_t oh = static_cast<int64_t>(rq.q0 + token) * a.heads + qh;
+            uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + oh * D);
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+                float o[16];
+                if (steps > 0) {
+                    tmem_ld16(o, o_at + c * 16);
+                    tmem_wait(o);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[j] = 0.0f;
+                }
+                if (live && ok) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        out[2 * c + h] = make_uint4(E::pack(o[8 * h] * inv, o[8 * h + 1] * inv),
+                                                    E::pack(o[8 * h + 2] * inv, o[8 * h + 3] * inv),
+                                                    E::pack(o[8 * h + 4] * inv, o[8 * h + 5] * inv),
+                                                    E::pack(o[8 * h + 6] * inv, o[8 * h + 7] * inv));
+                }
+            }
+            if (live && ok && a.lse) a.lse[oh] = l == 0.0f ? -INFINITY : (m + log2f(l) - kPShift) * 0.693147180559945309f;
+        }
+    }
+    if (!ok) atomicOr(&g_prompt_fault, 1u);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 12) tmem_free(tmem, 512);
+}
+
+}  // namespace rmsq

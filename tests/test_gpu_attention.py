@@ -72,9 +72,97 @@ def test_several_queries(rmsq_gpu, dtype, D, heads, kv, page, window):
     check(rmsq_gpu, c, window=window)
 
 
-@pytest.mark.parametrize("heads, kv", [(16, 1), (32, 4)])
-def test_prompt(rmsq_gpu, heads, kv):
-    check(rmsq_gpu, make([150, 1], [150, 201], heads, kv, 128, 16, "bf16", seed=5))
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("heads, kv, page, q_lens, seq", [
+    (1, 1, 16, [65], [65]),                        # one row more than the split kernel takes; a half tile
+    (1, 1, 64, [128, 129], [128, 300]),
+    (2, 2, 32, [257], [400]),                      # a tile and one row
+    (8, 1, 16, [150, 1, 40], [150, 201, 127]),     # prompts and a decode in one batch
+    (5, 1, 128, [60], [61]),                       # a group that does not divide the tile
+    (16, 1, 16, [33, 9], [256, 129]),
+    (6, 2, 256, [100, 90], [612, 90]),
+])
+def test_prompt(rmsq_gpu, dtype, D, heads, kv, page, q_lens, seq):
+    check(rmsq_gpu, make(q_lens, seq, heads, kv, D, page, dtype, seed=5 + D))
+    assert rmsq_gpu.take_fault_flags() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [1, 50, 128, 300])
+def test_prompt_with_a_window(rmsq_gpu, D, window):
+    check(rmsq_gpu, make([200, 70], [700, 70], 4, 2, D, 16, "bf16", seed=window), window=window)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_bad_pages_empty_rows_padding(rmsq_gpu, D):
+    """More queries than keys, pages outside the cache, garbage behind the
+    last key, rows of padding, extreme and flat queries."""
+    c = make([100, 80, 90], [60, 300, 0], 4, 2, D, 16, "bf16", seed=31, extra_rows=70)
+    c["table"][1, 2], c["table"][1, 7], c["table"][1, 18] = -1, len(c["cache"]), -(2**31)
+    codes, scales = ref.tiles(c["cache"], 16, D)
+    codes[c["table"][0, 3], :, :, 12:] = 0xff
+    scales[c["table"][0, 3], :, :, 12:] = 0xff
+    c["q"][130:140] = 0
+    c["q"][140:150] *= 1e3
+    c["q64"] = c["q"].double().numpy()
+    out = torch.full(c["q"].shape, 3.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full(c["q"].shape[:2], 5.0, device="cuda")
+    check(rmsq_gpu, c, out=out, lse=lse)
+    assert (out[270:] == 3).all() and (lse[270:] == 5).all()
+
+
+@pytest.mark.parametrize("rows", [1, 70, 300])
+def test_a_single_padded_request(rmsq_gpu, rows):
+    """A token buffer of 300 of which a single request fills some."""
+    check(rmsq_gpu, make([rows], [rows + 33], 2, 1, 64, 16, "fp16", extra_rows=300 - rows))
+
+
+def test_prompt_rising_logits(rmsq_gpu):
+    """The running maximum moves at every step, and differently per row."""
+    c = make([300], [1000], 4, 1, 64, 16, "fp16", seed=3)
+    codes, scales = ref.tiles(c["cache"], 16, 64)
+    codes[:, 0] = 0x22
+    for j in range(1000):
+        scales[c["table"][0, j // 16], 0, :, j % 16] = 0x10 + j // 10
+    c["q"], c["q64"] = ref.act(c["q64"] + np.linspace(-1, 1, 300)[:, None, None], torch.float16)
+    check(rmsq_gpu, c, scale=0.5)
+
+
+def test_prompt_infinite_and_nan_queries_stay_in_their_rows(rmsq_gpu):
+    c = make([100, 30], [150, 30], 4, 1, 128, 16, "bf16", seed=6)
+    good, good_lse = run(rmsq_gpu, c)
+    q = c["q"].clone()
+    q[10, 2, 5], q[99, 0, 0] = float("inf"), float("nan")
+    out, lse = run(rmsq_gpu, c, q=q.cuda())
+    hit = torch.zeros(130, 4, dtype=torch.bool)
+    hit[10, 2] = hit[99, 0] = True
+    assert torch.equal(out[~hit], good[~hit]) and torch.equal(lse[~hit], good_lse[~hit])
+    assert torch.isnan(out[99, 0]).all()
+
+
+def test_prompts_repeat_bit_for_bit_and_in_graphs(rmsq_gpu):
+    rq = rmsq_gpu
+    c = make([500, 3, 260], [900, 1000, 260], 8, 2, 128, 64, "bf16", seed=40)
+    a = run(rq, c)
+    for _ in range(3):
+        b = run(rq, c)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()  # noqa: E731
+    q, cache, table, seq = c["q"].cuda(), dev(c["cache"]), dev(c["table"]), dev(np.array(c["seq"], np.int32))
+    start = torch.tensor([0, 500, 503, 763], dtype=torch.int32, device="cuda")
+    g1, g2 = torch.tensor([c["k_gs"]], device="cuda"), torch.tensor([c["v_gs"]], device="cuda")
+    ws = torch.empty(rq.paged_attention_workspace_bytes(763, 3, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(763, 8, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rq.paged_attention_nvfp4(q, cache, table, start, seq, g1, g2, 64, out=out, lse=lse, workspace=ws)
+    graph.replay()
+    assert torch.equal(out, a[0]) and torch.equal(lse, a[1])
+    start.copy_(torch.tensor([0, 10, 700, 763]))        # other lengths, the same graph
+    graph.replay()
+    want = rq.paged_attention_nvfp4(q, cache, table, start, seq, g1, g2, 64, return_lse=True)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and rq.take_fault_flags() == 0
 
 
 def test_rows_without_keys(rmsq_gpu):
@@ -185,6 +273,12 @@ def test_lengths_outside_the_buffers_are_clamped(rmsq_gpu):
                                        dev(np.array(seq, np.int32)), one, one, 16, out=torch.zeros_like(c["q"]).cuda())
         torch.cuda.synchronize()
         assert out.shape == (3, 4, 64)
+    c = make([100, 100], [300, 300], 4, 2, 64, 16, "bf16")
+    for start, seq in (([0, 100, 200], [2**31 - 1, -5]), ([-9, 2**31 - 1, 150], [300, 300]), ([200, 100, 0], [300, 1])):
+        rq.paged_attention_nvfp4(c["q"].cuda(), dev(c["cache"]), dev(c["table"]), dev(np.array(start, np.int32)),
+                                 dev(np.array(seq, np.int32)), one, one, 16, out=torch.zeros_like(c["q"]).cuda())
+        torch.cuda.synchronize()
+    assert rq.take_fault_flags() == 0
 
 
 def test_most_requests(rmsq_gpu):
