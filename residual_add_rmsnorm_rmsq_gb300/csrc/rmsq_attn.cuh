@@ -528,11 +528,13 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
         auto page_of = [&](int j) {
             const int k = first_key + j * kAttnKeyTile + my_half * 16;
             if (j >= ntiles || k > pos_max || k + 15 < lo_min) return -1;
-            const int p = __ldg(row_table + (k >> a.page_shift));
-            return p < a.num_pages ? p : -1;
+            return __ldg(row_table + (k >> a.page_shift));
         };
         uint32_t have = 0;      // bits 2s, 2s + 1: halves of stage s
+        // (a page is compared with their number here and not where it is
+        // loaded: the warp would wait for the load there)
         auto issue = [&](int j, int s, int page) {
+            if (page >= a.num_pages) page = -1;
             const uint32_t there = __ballot_sync(kFull, page >= 0);
             have = (have & ~(3u << (2 * s))) | (((there & 1u) | (there >> 16 & 1u) << 1) << (2 * s));
             if (page >= 0)

@@ -27,7 +27,21 @@ namespace rmsq {
 
 static __device__ unsigned int g_prompt_fault;
 
-constexpr int kPromptThreads = 416;     // 8 softmax warps, 4 converting warps, the issuing warp
+// Four warpgroups: two for the softmax, one converting, one whose first warp
+// issues.  They are launched with 128 registers a thread and share them out
+// anew: 176 + 176 + 120 + 40 = 4 x 128.
+constexpr int kPromptThreads = 512;
+constexpr int kSoftmaxRegs = 176, kConvertRegs = 120, kIssueRegs = 40;
+static_assert(2 * kSoftmaxRegs + kConvertRegs + kIssueRegs == 4 * 128, "the shares are the launch's registers");
+
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
+}
 
 template <int D>
 struct PromptTile {
@@ -40,29 +54,31 @@ struct PromptTile {
 template <int N>
 constexpr uint32_t kF16Idesc = (1u << 4) | (static_cast<uint32_t>(N / 8) << 17) | ((128u / 16u) << 24);
 
-// D = A . B^T over `steps` steps of 16 along K; A and B in swizzled tiles whose
-// 64-element column blocks are a_block / b_block bytes apart.
-template <int N, int STEPS>
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, int a_block, uint64_t b, int b_block) {
+// D = A . B^T over STEPS steps of 16 along K; A and B in swizzled tiles (low
+// descriptor words) whose 64-element column blocks are A_BLOCK / B_BLOCK bytes
+// apart.
+template <int N, int STEPS, int A_BLOCK, int B_BLOCK>
+__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint32_t a, uint32_t b) {
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        const uint64_t da = a + (i >> 2) * (a_block >> 4) + (i & 3) * 2, db = b + (i >> 2) * (b_block >> 4) + (i & 3) * 2;
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                     :: "r"(d), "l"(da), "l"(db), "r"(kF16Idesc<N>), "r"(i) : "memory");
-    }
+    for (int i = 0; i < STEPS; ++i)
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
+                     :: "r"(d), "r"(a + (i >> 2) * (A_BLOCK >> 4) + (i & 3) * 2),
+                        "r"(b + (i >> 2) * (B_BLOCK >> 4) + (i & 3) * 2), "r"(kF16Idesc<N>), "r"(i), "n"(kTileDescHigh)
+                     : "memory");
 }
 
 // D (+)= A . B^T with A in tensor memory (8 columns per step).
-template <int N, int STEPS>
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, int b_block, bool add) {
+template <int N, int STEPS, int B_BLOCK>
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, bool add) {
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        const uint64_t db = b + (i >> 2) * (b_block >> 4) + (i & 3) * 2;
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                     :: "r"(d), "r"(a + 8 * i), "l"(db), "r"(kF16Idesc<N>), "r"(i > 0 || add ? 1 : 0) : "memory");
-    }
+    for (int i = 0; i < STEPS; ++i)
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
+                     :: "r"(d), "r"(a + 8 * i), "r"(b + (i >> 2) * (B_BLOCK >> 4) + (i & 3) * 2), "r"(kF16Idesc<N>),
+                        "r"(i > 0 || add ? 1 : 0), "n"(kTileDescHigh)
+                     : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
@@ -179,6 +195,64 @@ __device__ __forceinline__ void write_values(unsigned char* dst, const RawTile<D
     }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// A row's 128 logits.  They stay in registers from the maximum to the weights:
+// read from tensor memory twice, 16 at a time, the two passes waited out
+// sixteen load latencies per tile (260 us for the prompt step of 147 GFLOP).
+using Row = float[8][16];
+
+__device__ __forceinline__ void read_row(Row& d, uint32_t s_at) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c) tmem_ld16(d[c], s_at + c * 16);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) tmem_wait(d[c]);    // the first one waits for all
+}
+
+// Logits whose bit is not set in `see` to -inf.
+__device__ __forceinline__ void mask_row(Row& d, const uint32_t (&see)[4]) {
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (!(see[c >> 1] >> ((c & 1) * 16 + j) & 1u)) d[c][j] = -INFINITY;
+}
+
+__device__ __forceinline__ float row_max(const Row& d) {
+    float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top[j & 1] = max3(top[j & 1], d[c][2 * j], d[c][2 * j + 1]);
+    return fmaxf(top[0], top[1]);
+}
+
+// The row's weights 2^(f s + shift) in f16, in the place of its logits in
+// tensor memory; returns their sum.
+__device__ __forceinline__ float row_weights(const Row& d, uint32_t s_at, float f, float shift) {
+    const float2 f2 = make_float2(f, f), s2 = make_float2(shift, shift);
+    float2 sum[2] = {};
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t p[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            const float(&h)[16] = d[2 * c + (j >> 3)];
+            float2 x = fma2_rn(make_float2(h[2 * (j & 7)], h[2 * (j & 7) + 1]), f2, s2);
+            x.x = exp2_approx(x.x);
+            x.y = exp2_approx(x.y);
+            sum[j & 1] = add2_rn(sum[j & 1], x);
+            p[j] = Fp16T::pack(x.x, x.y);
+        }
+        tmem_st16(s_at + c * 16, p);
+    }
+    return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+}
+
 // Items (256-row tiles) of a request; requests of few rows are the split
 // kernel's.
 __device__ __forceinline__ int prompt_items(const AttnArgs& a, int r) {
@@ -279,53 +353,62 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
     const int steps = last_pos < key_begin ? 0 : (last_pos - key_begin) / 128 + 1;
     bool ok = true;
 
-    if (warp == 12) {
-        if (lane == 0 && steps > 0) {
-            for (int i = 0; i < tiles && ok; ++i) ok = mbar_wait_bounded(&qfull[i], 0);
+    if (warp >= 12) {
+        fewer_registers<kIssueRegs>();
+        if (warp == 12 && steps > 0) {
+            // The whole warp walks the loop, so that its addresses stay
+            // uniform; one lane issues.
+            const bool issuer = elect_one();
+            const uint32_t q_desc = tile_desc(smem_u32(qs)), k_desc = tile_desc(smem_u32(ks)), v_desc = tile_desc(smem_u32(vs));
+            for (int i = 0; i < tiles && ok; ++i) ok = mbar_wait(&qfull[i], 0);
             for (int n = 0; n <= steps && ok; ++n) {
-                const int s = n & 1, z = (n - 1) & 1;
-                if (n < steps) ok = mbar_wait_bounded(&kfull[s], (n >> 1) & 1);
-                if (n > 0) ok = ok && mbar_wait_bounded(&vfull[z], ((n - 1) >> 1) & 1);
-                for (int i = 0; i < tiles && ok; ++i) {
-                    if (n > 0) {
-                        ok = mbar_wait_bounded(&pready[i], (n - 1) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        mma_f16_ts<D, 8>(tmem + 256 + i * D, tmem + i * 128, tile_desc(vs + z * Tile::v), D * 128, n > 1);
-                        if (n == steps) mma_commit(&ofull[i]);
-                        if (i == tiles - 1) mma_commit(&vempty[z]);
-                    }
-                    if (n < steps) {
-                        tc_fence_after();
-                        mma_f16_ss<128, D / 16>(tmem + i * 128, tile_desc(qs + i * Tile::q), 128 * 128,
-                                                tile_desc(ks + s * Tile::k), 128 * 128);
-                        mma_commit(&sfull[i]);
+                const int s = n & 1, z = s ^ 1;
+                if (n < steps) ok = mbar_wait(&kfull[s], (n >> 1) & 1);
+                if (n > 0) ok = ok && mbar_wait(&vfull[z], ((n - 1) >> 1) & 1);
+                for (int i = 0; i < tiles; ++i) {
+                    if (n > 0) ok = ok && mbar_wait(&pready[i], (n - 1) & 1);
+                    ok = __all_sync(kFull, ok);
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (issuer) {
+                        if (n > 0) {
+                            mma_f16_ts<D, 8, D * 128>(tmem + 256 + i * D, tmem + i * 128, v_desc + z * (Tile::v >> 4), n > 1);
+                            if (n == steps) mma_commit(&ofull[i]);
+                            if (i == tiles - 1) mma_commit(&vempty[z]);
+                        }
+                        if (n < steps) {
+                            mma_f16_ss<128, D / 16, 128 * 128, 128 * 128>(tmem + i * 128, q_desc + i * (Tile::q >> 4),
+                                                                          k_desc + s * (Tile::k >> 4));
+                            mma_commit(&sfull[i]);
+                            if (i == tiles - 1) mma_commit(&kempty[s]);
+                        }
                     }
                 }
-                if (ok && n < steps) mma_commit(&kempty[s]);
             }
-            if (!ok) {
+            if (!ok && issuer) {
                 mma_commit(&drained);
-                mbar_wait_bounded(&drained, 0);
+                mbar_wait(&drained, 0);
             }
         }
     } else if (warp >= 8) {
+        fewer_registers<kConvertRegs>();
         // Conversion: the codes of the next tile, and the pages of the one
         // after it, are on their way while a tile is converted.
         const int t = tid - 256, w = warp - 8;
         const int octet = (w & 1) * 8 + (lane & 7), unit = (w >> 1) * 4 + (lane >> 3);
         const int* table = a.table + static_cast<int64_t>(req) * a.width;
-        auto page_of = [&](int key) {
-            if (key > last_pos) return -1;
-            const int p = __ldg(table + (key >> a.page_shift));
-            return p < a.num_pages ? p : -1;
-        };
+        // A page is compared with their number only when it is used: next to
+        // the load the comparison would make the warp wait for it every time.
+        auto page_of = [&](int key) { return key > last_pos ? -1 : __ldg(table + (key >> a.page_shift)); };
+        auto checked = [&](int p) { return p < a.num_pages ? p : -1; };
         RawTile<D> cur, nxt;
-        int kp = page_of(key_begin + t), vp = page_of(key_begin + octet * 8);
+        int kp = checked(page_of(key_begin + t)), vp = checked(page_of(key_begin + octet * 8));
         load_tile<D>(cur, a, key_begin, kp, vp, head, t, octet, unit);
         int kp1 = page_of(key_begin + 128 + t), vp1 = page_of(key_begin + 128 + octet * 8);
         for (int n = 0; n < steps; ++n) {
             const int key0 = key_begin + n * 128, s = n & 1;
+            kp1 = checked(kp1);
+            vp1 = checked(vp1);
             load_tile<D>(nxt, a, key0 + 128, kp1, vp1, head, t, octet, unit);
             const int kp2 = page_of(key0 + 256 + t), vp2 = page_of(key0 + 256 + octet * 8);
             ok = warp_wait(&kempty[s], ((n >> 1) & 1) ^ 1);
@@ -348,6 +431,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
             vp1 = vp2;
         }
     } else {
+        more_registers<kSoftmaxRegs>();
         const int i = warp >> 2, quad = warp & 3, local = quad * 32 + lane, row = row0 + i * 128 + local;
         if (i < tiles) {
             // The row's query: scaled into f16's range, into its operand row.
@@ -400,7 +484,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                 const bool whole = (have.x & have.y & have.z & have.w) == 0xffffffffu;
                 // keys this row may see, as bits, where not every row of the warp sees all of them
                 const bool full = __all_sync(kFull, whole && (!live || (key0 + 127 <= pos && key0 >= lo)));
-                uint32_t see[4];
+                uint32_t see[4] = {};
                 if (!full) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -411,17 +495,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                         see[c] = below & above & hv[c];
                     }
                 }
-                float d[2][16];
-                float top = -INFINITY;
-                tmem_ld16(d[0], s_at);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    tmem_wait(d[c & 1]);
-                    if (c < 7) tmem_ld16(d[(c + 1) & 1], s_at + (c + 1) * 16);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        top = fmaxf(top, full || (see[c >> 1] >> ((c & 1) * 16 + j) & 1u) ? d[c & 1][j] : -INFINITY);
-                }
+                Row d;
+                read_row(d, s_at);
+                if (!full) mask_row(d, see);
+                const float top = row_max(d);
                 if (__any_sync(kFull, top > limit)) {
                     // sfull of this step says that the previous P . V has
                     // completed too: O may be rescaled here
@@ -444,33 +521,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                     }
                 }
                 const float shift = m == -INFINITY ? 0.0f : kPShift - m;
-                const float2 f2 = make_float2(f, f), s2 = make_float2(shift, shift);
-                float2 sum = make_float2(0.0f, 0.0f);
-                uint32_t p[16];
-                tmem_ld16(d[0], s_at);
-#pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    tmem_wait(d[c & 1]);
-                    if (c < 7) tmem_ld16(d[(c + 1) & 1], s_at + (c + 1) * 16);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float2 x = make_float2(d[c & 1][2 * j], d[c & 1][2 * j + 1]);
-                        if (!full) {
-                            const uint32_t bits = see[c >> 1] >> ((c & 1) * 16 + 2 * j);
-                            if (!(bits & 1u)) x.x = -INFINITY;
-                            if (!(bits & 2u)) x.y = -INFINITY;
-                        }
-                        x = fma2_rn(x, f2, s2);
-                        x.x = exp2_approx(x.x);
-                        x.y = exp2_approx(x.y);
-                        sum = add2_rn(sum, x);
-                        p[(c & 1) * 8 + j] = Fp16T::pack(x.x, x.y);
-                    }
-                    // columns 0 .. 16 c + 15 of S have been read: P's first
-                    // 8 c + 8 columns lie inside them
-                    if (c & 1) tmem_st16(s_at + (c >> 1) * 16, p);
-                }
-                l += sum.x + sum.y;
+                l += row_weights(d, s_at, f, shift);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();

@@ -50,22 +50,26 @@ template <int N>
 constexpr uint32_t kMmIdesc = (1u << 4) | (static_cast<uint32_t>(N / 8) << 17) | ((128u / 16u) << 24);
 
 // One block of 128 along K: D = A . B^T as four K = 32 products.
-__device__ __forceinline__ void mma_block(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+__device__ __forceinline__ void mma_block(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-                     :: "r"(d), "l"(a + 2 * i), "l"(b + 2 * i), "r"(idesc), "r"(i) : "memory");
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+                     "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}"
+                     :: "r"(d), "r"(a + 2 * i), "r"(b + 2 * i), "r"(idesc), "r"(i), "n"(kTileDescHigh) : "memory");
     }
 }
 
-__device__ __forceinline__ float load_sa(const MmArgs& a, int row, int kb) {
+// A scale of a as it lies in memory, and its value.  The kernels load a block's
+// scales one block ahead and turn them into a factor only when it is their
+// turn: arithmetic on the loaded value next to the load would make the warp,
+// which issues in order, wait out the load's latency at every block.
+__device__ __forceinline__ uint32_t load_sa(const MmArgs& a, int row, int kb) {
     const int64_t i = row * a.sa_row + kb * a.sa_kb;
-    if (a.ue8m0) {
-        const uint32_t e = __ldg(static_cast<const uint8_t*>(a.sa) + i);
-        return __uint_as_float(e ? e << 23 : 0x00400000u);
-    }
-    return __ldg(static_cast<const float*>(a.sa) + i);
+    return a.ue8m0 ? __ldg(static_cast<const uint8_t*>(a.sa) + i) : __ldg(static_cast<const uint32_t*>(a.sa) + i);
+}
+__device__ __forceinline__ float sa_value(const MmArgs& a, uint32_t raw) {
+    return __uint_as_float(!a.ue8m0 ? raw : raw ? raw << 23 : 0x00400000u);
 }
 
 constexpr int kMmTile = 128 * 128;   // bytes of a 128-row operand tile
@@ -73,7 +77,7 @@ constexpr int kMmTile = 128 * 128;   // bytes of a 128-row operand tile
 // Waits (bounded) for the copies of the last `stages` of `issued` fills.
 __device__ __forceinline__ void drain_copies(uint64_t* full, int stages, int issued) {
     for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
-        mbar_wait_bounded(&full[i % stages], (i / stages) & 1);
+        mbar_wait(&full[i % stages], (i / stages) & 1);
 }
 
 // ---------------------------------------------------------------------------
@@ -143,7 +147,7 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 raster(i, mt, nt, tm, tn);
                 for (int kb = 0; kb < a.kb; ++kb, ++it) {
                     const int s = it % S;
-                    ok = mbar_wait_bounded(&empty[s], ((it / S) & 1) ^ 1);
+                    ok = mbar_wait(&empty[s], ((it / S) & 1) ^ 1);
                     if (!ok) break;
                     unsigned char* st = ring + s * Tile::stage_bytes;
                     mbar_arrive_expect_tx(&full[s], Tile::stage_bytes);
@@ -154,24 +158,37 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             if (!ok) drain_copies(full, S, it);
         }
     } else if (warp == 9) {
-        if (lane == 0) {
-            int it = 0;
-            for (int i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
-                for (int kb = 0; kb < a.kb; ++kb, ++it) {
-                    const int s = it % S, b = it & 1;
-                    ok = mbar_wait_bounded(&tempty[b], ((it >> 1) & 1) ^ 1) && mbar_wait_bounded(&full[s], (it / S) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const unsigned char* st = ring + s * Tile::stage_bytes;
-                    mma_block(tmem + b * BN, tile_desc(st), tile_desc(st + kMmTile), kMmIdesc<BN>);
+        // The whole warp walks the loop, so that its addresses stay uniform;
+        // one lane issues.
+        const bool issuer = elect_one();
+        const uint32_t ring_desc = tile_desc(smem_u32(ring));
+        int s = 0, b = 0;
+        uint32_t phase = 0, tphase = 1;     // parities of full[s] and tempty[b]
+        for (int i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+            for (int kb = 0; kb < a.kb; ++kb) {
+                ok = mbar_wait(&tempty[b], tphase) && mbar_wait(&full[s], phase);
+                if (!__all_sync(kFull, ok)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                if (issuer) {
+                    const uint32_t st = ring_desc + s * (Tile::stage_bytes >> 4);
+                    mma_block(tmem + b * BN, st, st + (kMmTile >> 4), kMmIdesc<BN>);
                     mma_commit(&empty[s]);
                     mma_commit(&tfull[b]);
                 }
+                if (++s == S) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+                b ^= 1;
+                if (b == 0) tphase ^= 1u;
             }
-            if (!ok) {
-                mma_commit(&drained);
-                mbar_wait_bounded(&drained, 0);
-            }
+        }
+        if (!ok && issuer) {
+            mma_commit(&drained);
+            mbar_wait(&drained, 0);
         }
     } else {
         const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
@@ -188,15 +205,21 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             float2 acc[HALF / 2];
 #pragma unroll
             for (int j = 0; j < HALF / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
-            float scale = live ? load_sa(a, m, 0) * __ldg(sb) : 0.0f;
+            uint32_t raw = live ? load_sa(a, m, 0) : 0u;
+            float block = __ldg(sb);
             for (int kb = 0; kb < a.kb; ++kb, ++it) {
                 const int b = it & 1;
-                float next = 0.0f;
-                if (live && kb + 1 < a.kb) next = load_sa(a, m, kb + 1) * __ldg(sb + kb + 1);
+                uint32_t next = 0u;
+                float next_block = 0.0f;
+                if (kb + 1 < a.kb) {
+                    if (live) next = load_sa(a, m, kb + 1);
+                    next_block = __ldg(sb + kb + 1);
+                }
                 ok = ok && warp_wait(&tfull[b], (it >> 1) & 1);
                 if (!ok) continue;
                 tc_fence_after();
                 const uint32_t addr = tmem + b * BN + wg * HALF + (static_cast<uint32_t>(quad * 32) << 16);
+                const float scale = sa_value(a, raw) * block;
                 const float2 s2 = make_float2(scale, scale);
                 float d[2][16];
                 tmem_ld16(d[0], addr);
@@ -214,7 +237,8 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     for (int j = 0; j < 8; ++j)
                         acc[c * 8 + j] = fma2_rn(make_float2(d[c & 1][2 * j], d[c & 1][2 * j + 1]), s2, acc[c * 8 + j]);
                 }
-                scale = next;
+                raw = next;
+                block = next_block;
             }
             // Round to T, through shared memory (swizzled as the tensor map
             // says) into 64-column stores; rows and columns beyond the matrix
@@ -305,7 +329,7 @@ mm_tokens_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             int kb = 0;
             for (; kb < nkb; ++kb) {
                 const int s = kb % stages;
-                ok = mbar_wait_bounded(&empty[s], ((kb / stages) & 1) ^ 1);
+                ok = mbar_wait(&empty[s], ((kb / stages) & 1) ^ 1);
                 if (!ok) break;
                 unsigned char* st = ring + s * Tile::stage_bytes;
                 mbar_arrive_expect_tx(&full[s], Tile::stage_bytes);
@@ -315,27 +339,38 @@ mm_tokens_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             if (!ok) drain_copies(full, stages, kb);
         }
     } else if (warp == 5) {
-        if (lane == 0) {
-            for (int kb = 0; kb < nkb; ++kb) {
-                const int s = kb % stages, b = kb & 1;
-                ok = mbar_wait_bounded(&tempty[b], ((kb >> 1) & 1) ^ 1) && mbar_wait_bounded(&full[s], (kb / stages) & 1);
-                if (!ok) break;
-                tc_fence_after();
-                const unsigned char* st = ring + s * Tile::stage_bytes;
-                mma_block(tmem + b * NT, tile_desc(st), tile_desc(st + kMmTile), kMmIdesc<NT>);
+        const bool issuer = elect_one();
+        const uint32_t ring_desc = tile_desc(smem_u32(ring));
+        int s = 0;
+        uint32_t phase = 0;
+        for (int kb = 0; kb < nkb; ++kb) {
+            const int b = kb & 1;
+            ok = mbar_wait(&tempty[b], ((kb >> 1) & 1) ^ 1) && mbar_wait(&full[s], phase);
+            if (!__all_sync(kFull, ok)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            if (issuer) {
+                const uint32_t st = ring_desc + s * (Tile::stage_bytes >> 4);
+                mma_block(tmem + b * NT, st, st + (kMmTile >> 4), kMmIdesc<NT>);
                 mma_commit(&empty[s]);
                 mma_commit(&tfull[b]);
             }
-            if (!ok) {
-                mma_commit(&drained);
-                mbar_wait_bounded(&drained, 0);
+            if (++s == stages) {
+                s = 0;
+                phase ^= 1u;
             }
+        }
+        if (!ok && issuer) {
+            mma_commit(&drained);
+            mbar_wait(&drained, 0);
         }
     } else {
         // sa * sb of the CTA's blocks, while the first tiles are on their way
         for (int i = tid; i < nkb * NT; i += 128) {
             const int kb = i / NT, m = m0 + i % NT;
-            scales[i] = m < a.m ? load_sa(a, m, kb0 + kb) * __ldg(a.sb + static_cast<int64_t>(tn) * a.kb + kb0 + kb) : 0.0f;
+            scales[i] = m < a.m ? sa_value(a, load_sa(a, m, kb0 + kb)) * __ldg(a.sb + static_cast<int64_t>(tn) * a.kb + kb0 + kb) : 0.0f;
         }
         named_sync(1, 128);
         float2 acc[NT / 2];

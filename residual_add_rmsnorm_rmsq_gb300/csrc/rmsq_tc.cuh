@@ -43,10 +43,10 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 }
 
 // Matrix descriptor of a K-major tile of 128-byte rows under the 128-byte
-// swizzle (1024-byte aligned): 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t tile_desc(const void* p) {
-    return static_cast<uint64_t>((smem_u32(p) >> 4) & 0x3fffu) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
+// swizzle (1024-byte aligned): 8-row groups 1024 bytes apart.  The low word
+// holds the address; a step along K or to another tile is an addition to it.
+constexpr uint32_t kTileDescHigh = 64u | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t tile_desc(uint32_t smem) { return ((smem >> 4) & 0x3fffu) | (1u << 16); }
 
 // Sixteen accumulator columns of the warp's 32 lanes.
 __device__ __forceinline__ void tmem_ld16(float (&r)[16], uint32_t addr) {
@@ -74,9 +74,32 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// mbar_wait_bounded for the roles of one kernel that wait for one another: a
+// loop of a few instructions whose clock is read only every 1024 polls, so
+// that a wait costs the issuing warp little more than its one poll.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+        if ((i & 1023u) == 0u) {
+            const uint64_t now = globaltimer_ns();
+            if (t0 == 0) t0 = now;
+            if (now - t0 > kWaitLimitNs || i > (1u << 24)) return false;
+        }
+    }
+    return true;
+}
+
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0u;
+}
+
 // The whole warp's answer to a bounded wait of each lane.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-    return __all_sync(kFull, mbar_wait_bounded(bar, parity));
+    return __all_sync(kFull, mbar_wait(bar, parity));
 }
 
 }  // namespace rmsq
