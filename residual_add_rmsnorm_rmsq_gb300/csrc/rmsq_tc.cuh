@@ -57,6 +57,17 @@ __device__ __forceinline__ void tmem_ld16(float (&r)[16], uint32_t addr) {
                  : "r"(addr));
 }
 
+// Thirty-two columns, as two groups of sixteen.
+__device__ __forceinline__ void tmem_ld32(float (&r)[16], float (&q)[16], uint32_t addr) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+                 "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+                 : "=f"(r[0]), "=f"(r[1]), "=f"(r[2]), "=f"(r[3]), "=f"(r[4]), "=f"(r[5]), "=f"(r[6]), "=f"(r[7]),
+                   "=f"(r[8]), "=f"(r[9]), "=f"(r[10]), "=f"(r[11]), "=f"(r[12]), "=f"(r[13]), "=f"(r[14]), "=f"(r[15]),
+                   "=f"(q[0]), "=f"(q[1]), "=f"(q[2]), "=f"(q[3]), "=f"(q[4]), "=f"(q[5]), "=f"(q[6]), "=f"(q[7]),
+                   "=f"(q[8]), "=f"(q[9]), "=f"(q[10]), "=f"(q[11]), "=f"(q[12]), "=f"(q[13]), "=f"(q[14]), "=f"(q[15])
+                 : "r"(addr));
+}
+
 // Waits for the thread's loads; the registers pass through it, so that no use
 // of them can be moved ahead of the wait.
 __device__ __forceinline__ void tmem_wait(float (&r)[16]) {
