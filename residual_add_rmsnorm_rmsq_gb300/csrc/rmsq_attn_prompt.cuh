@@ -36,15 +36,6 @@ constexpr int kPromptThreads = 512;
 constexpr int kSoftmaxRegs = 176, kConvertRegs = 120, kIssueRegs = 40;
 static_assert(2 * kSoftmaxRegs + kConvertRegs + kIssueRegs == 4 * 128, "the shares are the launch's registers");
 
-template <int N>
-__device__ __forceinline__ void more_registers() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
-}
-template <int N>
-__device__ __forceinline__ void fewer_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
-}
-
 template <int D>
 struct PromptTile {
     static constexpr int q = 128 * D * 2, k = 128 * D * 2, v = 128 * D * 2;    // bytes of one operand tile

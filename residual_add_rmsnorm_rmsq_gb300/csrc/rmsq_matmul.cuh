@@ -87,10 +87,16 @@ template <int BN>
 struct RowsTile {
     static constexpr int stage_bytes = kMmTile + BN * 128;
     static constexpr int stages = 196608 / stage_bytes;     // 4 (BN = 256), 6 (BN = 128)
+    static constexpr int buffers = 512 / BN;                // block sums in tensor memory
     static constexpr int staging = 128 * 128;               // 128 rows x 64 columns of T, per warpgroup
     static constexpr int smem = 1024 + stages * stage_bytes + 2 * staging;
 };
-constexpr int kRowsThreads = 320;   // 8 promoting warps, the copying warp, the issuing warp
+// Three warpgroups: two promoting, one whose first warp copies and whose second
+// issues.  Launched with 168 registers a thread, shared out as 224 + 224 + 56: a
+// promoting thread holds up to 128 running sums and 64 block sums.
+constexpr int kRowsThreads = 384;
+constexpr int kPromoteRegs = 224, kOtherRegs = 56;
+static_assert(2 * kPromoteRegs + kOtherRegs == 3 * 168, "the shares are the launch's registers");
 constexpr int kRasterRows = 16;     // row tiles per raster group
 
 // Tile `i` of the raster: groups of kRasterRows row tiles, columns outermost
@@ -107,9 +113,9 @@ __global__ void __launch_bounds__(kRowsThreads, 1)
 mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
                const __grid_constant__ CUtensorMap map_out, const MmArgs a) {
     using Tile = RowsTile<BN>;
-    constexpr int S = Tile::stages, HALF = BN / 2;
+    constexpr int S = Tile::stages, B = Tile::buffers, HALF = BN / 2;
     extern __shared__ unsigned char dyn[];
-    __shared__ __align__(8) uint64_t full[S], empty[S], tfull[2], tempty[2], drained;
+    __shared__ __align__(8) uint64_t full[S], empty[S], tfull[B], tempty[B], drained;
     __shared__ uint32_t tmem_base;
     unsigned char* ring = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
     unsigned char* staging = ring + S * Tile::stage_bytes;
@@ -119,7 +125,7 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < B; ++i) {
             mbar_init(&tfull[i], 1);
             mbar_init(&tempty[i], 8);
         }
@@ -140,6 +146,7 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     bool ok = true;
 
     if (warp == 8) {
+        fewer_registers<kOtherRegs>();
         if (lane == 0) {
             int it = 0;
             for (int i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
@@ -158,6 +165,7 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             if (!ok) drain_copies(full, S, it);
         }
     } else if (warp == 9) {
+        fewer_registers<kOtherRegs>();
         // The whole warp walks the loop, so that its addresses stay uniform;
         // one lane issues.
         const bool issuer = elect_one();
@@ -182,18 +190,24 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     s = 0;
                     phase ^= 1u;
                 }
-                b ^= 1;
-                if (b == 0) tphase ^= 1u;
+                if (++b == B) {
+                    b = 0;
+                    tphase ^= 1u;
+                }
             }
         }
         if (!ok && issuer) {
             mma_commit(&drained);
             mbar_wait(&drained, 0);
         }
+    } else if (warp > 9) {
+        fewer_registers<kOtherRegs>();
     } else {
+        more_registers<kPromoteRegs>();
         const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
         unsigned char* stage = staging + wg * Tile::staging;
-        int it = 0;
+        int b = 0;
+        uint32_t tphase = 0;
         // A warp whose wait ran out keeps walking the loop (the warpgroup's
         // barriers need every warp) without waiting or reading any more.
         for (int i = blockIdx.x; i < tiles; i += gridDim.x) {
@@ -207,35 +221,47 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             for (int j = 0; j < HALF / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
             uint32_t raw = live ? load_sa(a, m, 0) : 0u;
             float block = __ldg(sb);
-            for (int kb = 0; kb < a.kb; ++kb, ++it) {
-                const int b = it & 1;
+            for (int kb = 0; kb < a.kb; ++kb) {
                 uint32_t next = 0u;
                 float next_block = 0.0f;
                 if (kb + 1 < a.kb) {
                     if (live) next = load_sa(a, m, kb + 1);
                     next_block = __ldg(sb + kb + 1);
                 }
-                ok = ok && warp_wait(&tfull[b], (it >> 1) & 1);
+                ok = ok && warp_wait(&tfull[b], tphase);
+                const int buffer = b;
+                if (++b == B) {
+                    b = 0;
+                    tphase ^= 1u;
+                }
                 if (!ok) continue;
                 tc_fence_after();
-                const uint32_t addr = tmem + b * BN + wg * HALF + (static_cast<uint32_t>(quad * 32) << 16);
+                const uint32_t addr = tmem + buffer * BN + wg * HALF + (static_cast<uint32_t>(quad * 32) << 16);
+                // 64 block sums at a time: a load takes some 250 clocks to
+                // arrive and the matrix unit waits for the buffer meanwhile
+                // (16 at a time: 209 us for 8192 x 4096 x 7168)
+                float d[4][16];
+                tmem_ld32(d[0], d[1], addr);
+                tmem_ld32(d[2], d[3], addr + 32);
                 const float scale = sa_value(a, raw) * block;
                 const float2 s2 = make_float2(scale, scale);
-                float d[2][16];
-                tmem_ld16(d[0], addr);
 #pragma unroll
-                for (int c = 0; c < HALF / 16; ++c) {
-                    tmem_wait(d[c & 1]);
-                    if (c + 1 < HALF / 16) {
-                        tmem_ld16(d[(c + 1) & 1], addr + (c + 1) * 16);
-                    } else {   // the accumulator has been read: hand it back
+                for (int h = 0; h < HALF / 64; ++h) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) tmem_wait(d[c]);
+                    if (h + 1 == HALF / 64) {   // the block sums have been read: hand the buffer back
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&tempty[b]);
+                        if (lane == 0) mbar_arrive(&tempty[buffer]);
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        acc[c * 8 + j] = fma2_rn(make_float2(d[c & 1][2 * j], d[c & 1][2 * j + 1]), s2, acc[c * 8 + j]);
+                    for (int c = 0; c < 4; ++c) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            acc[h * 32 + c * 8 + j] = fma2_rn(make_float2(d[c][2 * j], d[c][2 * j + 1]), s2, acc[h * 32 + c * 8 + j]);
+                        if (h + 1 < HALF / 64 && (c & 1))
+                            tmem_ld32(d[c - 1], d[c], addr + (h + 1) * 64 + (c - 1) * 16);
+                    }
                 }
                 raw = next;
                 block = next_block;

@@ -113,4 +113,16 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
     return __all_sync(kFull, mbar_wait(bar, parity));
 }
 
+// Shares the registers of the launch out anew between warpgroups: the sum of
+// the shares must not exceed what the CTA was launched with, or the increase
+// waits forever.
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N));
+}
+
 }  // namespace rmsq
