@@ -1,4 +1,5 @@
 // FP8 block-scaled matrix product: argument checks, tensor maps, launches.
+#include <atomic>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -51,6 +52,51 @@ bool make_map(CUtensorMap* map, const void* p, bool codes, int64_t rows, int64_t
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// One launch in clusters of `size` CTAs along x.
+cudaError_t launch_cluster(const void* fn, dim3 grid, dim3 block, void** params, int smem, int size, cudaStream_t stream) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = programmatic_launch() ? 2 : 1;
+    return cudaLaunchKernelExC(&cfg, fn, params);
+}
+
+// Pairs of CTAs of `fn` that can run at once (cached per device): not more are
+// launched, since their tiles are dealt out in advance.
+int resident_pairs(const void* fn, int smem, std::atomic<int>* cached, cudaError_t* err) {
+    int dev = 0;
+    *err = cudaGetDevice(&dev);
+    if (*err != cudaSuccess || dev < 0 || dev >= 128) return 0;
+    int n = cached[dev].load(std::memory_order_acquire);
+    if (n > 0) return n;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kRowsThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    *err = cudaOccupancyMaxActiveClusters(&n, fn, &cfg);
+    if (*err == cudaSuccess && n < 1) *err = cudaErrorInvalidConfiguration;
+    if (*err != cudaSuccess) return 0;
+    cached[dev].store(n, std::memory_order_release);
+    return n;
+}
+
 struct MmCall {
     const void *a, *b;
     int64_t m, n, k;
@@ -58,20 +104,23 @@ struct MmCall {
 };
 
 template <class E, int BN>
-cudaError_t launch_rows(const MmCall& c, int sms, cudaStream_t stream) {
+cudaError_t launch_rows(const MmCall& c, cudaStream_t stream) {
     using Tile = RowsTile<BN>;
     const void* fn = (const void*)&mm_rows_kernel<E, BN>;
+    static std::atomic<int> cached[128];
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile::smem);
     if (e != cudaSuccess) return e;
+    const int64_t pairs = resident_pairs(fn, Tile::smem, cached, &e);
+    if (e != cudaSuccess) return e;
     CUtensorMap ma, mb, mo;
-    if (!make_map(&ma, c.a, true, c.m, c.k, 128) || !make_map(&mb, c.b, true, c.n, c.k, BN) ||
+    if (!make_map(&ma, c.a, true, c.m, c.k, 128) || !make_map(&mb, c.b, true, c.n, c.k, BN / 2) ||
         !make_map(&mo, c.args.out, false, c.m, c.n, 128))
         return cudaErrorInvalidValue;
-    const int64_t tiles = (c.m + 127) / 128 * ((c.n + BN - 1) / BN);
+    const int64_t tiles = (c.m + 255) / 256 * ((c.n + BN - 1) / BN);
     MmArgs args = c.args;
     void* params[] = {&ma, &mb, &mo, &args};
-    return launch_kernel(fn, dim3(static_cast<unsigned>(tiles < sms ? tiles : sms)), dim3(kRowsThreads), params, Tile::smem,
-                         stream);
+    return launch_cluster(fn, dim3(2 * static_cast<unsigned>(tiles < pairs ? tiles : pairs)), dim3(kRowsThreads), params,
+                          Tile::smem, 2, stream);
 }
 
 template <class E, int NT>
@@ -94,23 +143,10 @@ cudaError_t launch_tokens(const MmCall& c, int sms, cudaStream_t stream) {
     if (!make_map(&ma, c.a, true, c.m, c.k, NT) || !make_map(&mb, c.b, true, c.n, c.k, 128)) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTokSmem);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks * splits), static_cast<unsigned>(mt));
-    cfg.blockDim = dim3(kTokThreads);
-    cfg.dynamicSmemBytes = kTokSmem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = programmatic_launch() ? 2 : 1;
     MmArgs args = c.args;
     void* params[] = {&ma, &mb, &args, &splits, &stages};
-    return cudaLaunchKernelExC(&cfg, fn, params);
+    return launch_cluster(fn, dim3(static_cast<unsigned>(blocks * splits), static_cast<unsigned>(mt)), dim3(kTokThreads),
+                          params, kTokSmem, splits, stream);
 }
 
 template <class E>
@@ -118,9 +154,11 @@ cudaError_t launch_matmul(const MmCall& c, cudaStream_t stream) {
     cudaError_t e;
     const int sms = sm_count(&e);
     if (e != cudaSuccess) return e;
-    const int64_t mt = (c.m + 127) / 128;
-    if (c.m > 128 && mt * ((c.n + 255) / 256) >= sms) return launch_rows<E, 256>(c, sms, stream);
-    if (c.m > 128 && mt * ((c.n + 127) / 128) * 3 >= 2 * sms) return launch_rows<E, 128>(c, sms, stream);
+    // Row tiles while they occupy most of the pairs, the wider ones (fewer
+    // bytes per product) where those do.
+    const int64_t mt = (c.m + 255) / 256, pairs = sms / 2;
+    if (c.m > 128 && mt * ((c.n + 255) / 256) >= pairs) return launch_rows<E, 256>(c, stream);
+    if (c.m > 128 && mt * ((c.n + 127) / 128) * 3 >= 2 * pairs) return launch_rows<E, 128>(c, stream);
     if (c.m <= 16) return launch_tokens<E, 16>(c, sms, stream);
     if (c.m <= 32) return launch_tokens<E, 32>(c, sms, stream);
     if (c.m <= 64) return launch_tokens<E, 64>(c, sms, stream);

@@ -13,9 +13,15 @@
 // keeps each chain of matrix-unit additions at 128 terms.
 //
 // Two kernels:
-//  mm_rows_kernel    many rows.  Tile 128 rows x BN columns, accumulator lane =
-//                    row of a, so a thread owns one row: its scale is one
-//                    number per block.  Persistent, one CTA per SM.
+//  mm_rows_kernel    many rows.  Tile 256 rows x BN columns per pair of CTAs,
+//                    accumulator lane = row of a, so a thread owns one row: its
+//                    scale is one number per block.  Persistent, one CTA per SM.
+//                    Each CTA holds 128 rows of a and half the tile's rows of b,
+//                    and the matrix units of both read both halves: a CTA alone
+//                    with 128 x 256 fills and reads 96 KB of shared memory per
+//                    block of K, 768 clocks at 128 bytes a clock where its
+//                    products take 512 (measured: 1000; 206 us for 8192 x 4096 x
+//                    7168), a pair 64 KB per CTA.
 //  mm_tokens_kernel  few rows (decode).  Bound by the bytes of b, so b's 128
 //                    rows are the accumulator's lanes and the tokens its
 //                    16 .. 128 columns, and the blocks of K are split over a
@@ -45,9 +51,9 @@ struct MmArgs {
     bool ue8m0;
 };
 
-// Instruction descriptor: E4M3 x E4M3 -> fp32, both K-major, 128 x N.
-template <int N>
-constexpr uint32_t kMmIdesc = (1u << 4) | (static_cast<uint32_t>(N / 8) << 17) | ((128u / 16u) << 24);
+// Instruction descriptor: E4M3 x E4M3 -> fp32, both K-major, M x N.
+template <int M, int N>
+constexpr uint32_t kMmIdesc = (1u << 4) | (static_cast<uint32_t>(N / 8) << 17) | (static_cast<uint32_t>(M / 16) << 24);
 
 // One block of 128 along K: D = A . B^T as four K = 32 products.
 __device__ __forceinline__ void mma_block(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
@@ -56,6 +62,17 @@ __device__ __forceinline__ void mma_block(uint32_t d, uint32_t a, uint32_t b, ui
         asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
                      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n\t}"
+                     :: "r"(d), "r"(a + 2 * i), "r"(b + 2 * i), "r"(idesc), "r"(i), "n"(kTileDescHigh) : "memory");
+    }
+}
+
+// The same over a CTA pair: 128 rows of A in each, half the rows of B in each.
+__device__ __forceinline__ void mma_block_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                     "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
+                     "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], da, db, %3, p;\n\t}"
                      :: "r"(d), "r"(a + 2 * i), "r"(b + 2 * i), "r"(idesc), "r"(i), "n"(kTileDescHigh) : "memory");
     }
 }
@@ -85,8 +102,8 @@ __device__ __forceinline__ void drain_copies(uint64_t* full, int stages, int iss
 // ---------------------------------------------------------------------------
 template <int BN>
 struct RowsTile {
-    static constexpr int stage_bytes = kMmTile + BN * 128;
-    static constexpr int stages = 196608 / stage_bytes;     // 4 (BN = 256), 6 (BN = 128)
+    static constexpr int stage_bytes = kMmTile + BN / 2 * 128;      // of one CTA
+    static constexpr int stages = 196608 / stage_bytes;     // 6 (BN = 256), 8 (BN = 128)
     static constexpr int buffers = 512 / BN;                // block sums in tensor memory
     static constexpr int staging = 128 * 128;               // 128 rows x 64 columns of T, per warpgroup
     static constexpr int smem = 1024 + stages * stage_bytes + 2 * staging;
@@ -97,7 +114,7 @@ struct RowsTile {
 constexpr int kRowsThreads = 384;
 constexpr int kPromoteRegs = 224, kOtherRegs = 56;
 static_assert(2 * kPromoteRegs + kOtherRegs == 3 * 168, "the shares are the launch's registers");
-constexpr int kRasterRows = 16;     // row tiles per raster group
+constexpr int kRasterRows = 8;      // row tiles per raster group
 
 // Tile `i` of the raster: groups of kRasterRows row tiles, columns outermost
 // inside a group, so that the tiles in flight share rows and columns in L2.
@@ -127,78 +144,84 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         }
         for (int i = 0; i < B; ++i) {
             mbar_init(&tfull[i], 1);
-            mbar_init(&tempty[i], 8);
+            mbar_init(&tempty[i], 16);      // the promoting warps of both CTAs
         }
         mbar_init(&drained, 1);
         fence_mbar_init();
     }
+    const uint32_t rank = cluster_rank();
     // Tensor memory is taken only once the previous kernel of the stream has
     // ended, and the next one may start only after that: neither can hold
     // columns the other still waits for.
     grid_dependency_wait();
-    if (warp == 9) tmem_alloc(&tmem_base, 512);
+    if (warp == 9) tmem_alloc_pair(&tmem_base, 512);
     tc_fence_before();
-    __syncthreads();
+    cluster_sync();     // barriers and tensor memory of both CTAs are ready
     tc_fence_after();
     allow_dependents();
     const uint32_t tmem = tmem_base;
-    const int mt = (a.m + 127) / 128, nt = (a.n + BN - 1) / BN, tiles = mt * nt;
+    const int mt = (a.m + 255) / 256, nt = (a.n + BN - 1) / BN, tiles = mt * nt;
+    const int first = blockIdx.x >> 1, pairs = gridDim.x >> 1;
     bool ok = true;
 
     if (warp == 8) {
         fewer_registers<kOtherRegs>();
         if (lane == 0) {
             int it = 0;
-            for (int i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
+            for (int i = first; i < tiles && ok; i += pairs) {
                 int tm, tn;
                 raster(i, mt, nt, tm, tn);
                 for (int kb = 0; kb < a.kb; ++kb, ++it) {
                     const int s = it % S;
                     ok = mbar_wait(&empty[s], ((it / S) & 1) ^ 1);
                     if (!ok) break;
+                    // both CTAs' copies complete on the first one's barrier
                     unsigned char* st = ring + s * Tile::stage_bytes;
-                    mbar_arrive_expect_tx(&full[s], Tile::stage_bytes);
-                    tma_load_2d(st, &map_a, kb * 128, tm * 128, &full[s]);
-                    tma_load_2d(st + kMmTile, &map_b, kb * 128, tn * BN, &full[s]);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * Tile::stage_bytes);
+                    const uint32_t bar = map_to_rank(&full[s], 0);
+                    tma_load_2d_pair(st, &map_a, kb * 128, tm * 256 + rank * 128, bar);
+                    tma_load_2d_pair(st + kMmTile, &map_b, kb * 128, tn * BN + rank * (BN / 2), bar);
                 }
             }
-            if (!ok) drain_copies(full, S, it);
+            if (!ok && rank == 0) drain_copies(full, S, it);
         }
     } else if (warp == 9) {
         fewer_registers<kOtherRegs>();
         // The whole warp walks the loop, so that its addresses stay uniform;
-        // one lane issues.
-        const bool issuer = elect_one();
-        const uint32_t ring_desc = tile_desc(smem_u32(ring));
-        int s = 0, b = 0;
-        uint32_t phase = 0, tphase = 1;     // parities of full[s] and tempty[b]
-        for (int i = blockIdx.x; i < tiles && ok; i += gridDim.x) {
-            for (int kb = 0; kb < a.kb; ++kb) {
-                ok = mbar_wait(&tempty[b], tphase) && mbar_wait(&full[s], phase);
-                if (!__all_sync(kFull, ok)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                if (issuer) {
-                    const uint32_t st = ring_desc + s * (Tile::stage_bytes >> 4);
-                    mma_block(tmem + b * BN, st, st + (kMmTile >> 4), kMmIdesc<BN>);
-                    mma_commit(&empty[s]);
-                    mma_commit(&tfull[b]);
-                }
-                if (++s == S) {
-                    s = 0;
-                    phase ^= 1u;
-                }
-                if (++b == B) {
-                    b = 0;
-                    tphase ^= 1u;
+        // one lane of the first CTA issues for both.
+        if (rank == 0) {
+            const bool issuer = elect_one();
+            const uint32_t ring_desc = tile_desc(smem_u32(ring));
+            int s = 0, b = 0;
+            uint32_t phase = 0, tphase = 1;     // parities of full[s] and tempty[b]
+            for (int i = first; i < tiles && ok; i += pairs) {
+                for (int kb = 0; kb < a.kb; ++kb) {
+                    ok = mbar_wait(&tempty[b], tphase) && mbar_wait(&full[s], phase);
+                    if (!__all_sync(kFull, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (issuer) {
+                        const uint32_t st = ring_desc + s * (Tile::stage_bytes >> 4);
+                        mma_block_pair(tmem + b * BN, st, st + (kMmTile >> 4), kMmIdesc<256, BN>);
+                        mma_commit_pair(&empty[s]);
+                        mma_commit_pair(&tfull[b]);
+                    }
+                    if (++s == S) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                    if (++b == B) {
+                        b = 0;
+                        tphase ^= 1u;
+                    }
                 }
             }
-        }
-        if (!ok && issuer) {
-            mma_commit(&drained);
-            mbar_wait(&drained, 0);
+            if (!ok && issuer) {
+                mma_commit_pair(&drained);
+                mbar_wait(&drained, 0);
+            }
         }
     } else if (warp > 9) {
         fewer_registers<kOtherRegs>();
@@ -210,10 +233,10 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         uint32_t tphase = 0;
         // A warp whose wait ran out keeps walking the loop (the warpgroup's
         // barriers need every warp) without waiting or reading any more.
-        for (int i = blockIdx.x; i < tiles; i += gridDim.x) {
+        for (int i = first; i < tiles; i += pairs) {
             int tm, tn;
             raster(i, mt, nt, tm, tn);
-            const int m = tm * 128 + row, n0 = tn * BN + wg * HALF;
+            const int m_tile = tm * 256 + static_cast<int>(rank) * 128, m = m_tile + row, n0 = tn * BN + wg * HALF;
             const bool live = m < a.m;
             const float* sb = a.sb + static_cast<int64_t>(min(n0, a.n - 1) / 128) * a.kb;
             float2 acc[HALF / 2];
@@ -252,7 +275,7 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     if (h + 1 == HALF / 64) {   // the block sums have been read: hand the buffer back
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&tempty[buffer]);
+                        if (lane == 0) mbar_arrive_cluster(map_to_rank(&tempty[buffer], 0));
                     }
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
@@ -283,7 +306,7 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 named_sync(1 + wg, 128);
                 if (quad == 0 && lane == 0) {
-                    if (ok && n0 + h * 64 < a.n) tma_store_2d(&map_out, stage, n0 + h * 64, tm * 128);
+                    if (ok && n0 + h * 64 < a.n && m_tile < a.m) tma_store_2d(&map_out, stage, n0 + h * 64, m_tile);
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
             }
@@ -293,9 +316,9 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     if (!ok) atomicOr(&g_mm_fault, 1u);
     __syncwarp();
     tc_fence_before();
-    __syncthreads();
+    cluster_sync();     // nothing of either CTA reaches into the other any more
     tc_fence_after();
-    if (warp == 9) tmem_free(tmem, 512);
+    if (warp == 9) tmem_free_pair(tmem, 512);
 }
 
 // ---------------------------------------------------------------------------
@@ -379,7 +402,7 @@ mm_tokens_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constan
             tc_fence_after();
             if (issuer) {
                 const uint32_t st = ring_desc + s * (Tile::stage_bytes >> 4);
-                mma_block(tmem + b * NT, st, st + (kMmTile >> 4), kMmIdesc<NT>);
+                mma_block(tmem + b * NT, st, st + (kMmTile >> 4), kMmIdesc<128, NT>);
                 mma_commit(&empty[s]);
                 mma_commit(&tfull[b]);
             }
