@@ -196,7 +196,7 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             uint32_t phase = 0, tphase = 1;     // parities of full[s] and tempty[b]
             for (int i = first; i < tiles && ok; i += pairs) {
                 for (int kb = 0; kb < a.kb; ++kb) {
-                    ok = mbar_wait(&tempty[b], tphase) && mbar_wait(&full[s], phase);
+                    ok = mbar_wait(&full[s], phase) && mbar_wait(&tempty[b], tphase);
                     if (!__all_sync(kFull, ok)) {
                         ok = false;
                         break;
@@ -229,6 +229,10 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         more_registers<kPromoteRegs>();
         const int wg = warp >> 2, quad = warp & 3, row = quad * 32 + lane;
         unsigned char* stage = staging + wg * Tile::staging;
+        const int64_t sa_bytes = a.ue8m0 ? 1 : 4, sa_step = a.sa_kb * sa_bytes;
+        const uint32_t sa_shift = a.ue8m0 ? 23 : 0, sa_zero = a.ue8m0 ? 0x00400000u : 0u;
+        const uint32_t tmem_at = tmem + wg * HALF + (static_cast<uint32_t>(quad * 32) << 16),
+                       tempty_at = map_to_rank(tempty, 0);
         int b = 0;
         uint32_t tphase = 0;
         // A warp whose wait ran out keeps walking the loop (the warpgroup's
@@ -237,36 +241,39 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             int tm, tn;
             raster(i, mt, nt, tm, tn);
             const int m_tile = tm * 256 + static_cast<int>(rank) * 128, m = m_tile + row, n0 = tn * BN + wg * HALF;
-            const bool live = m < a.m;
             const float* sb = a.sb + static_cast<int64_t>(min(n0, a.n - 1) / 128) * a.kb;
             float2 acc[HALF / 2];
 #pragma unroll
             for (int j = 0; j < HALF / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
-            uint32_t raw = live ? load_sa(a, m, 0) : 0u;
+            // The scales of the next block are on their way while this one is
+            // promoted, into the registers that this one's have just left.
+            // (Rows behind the last hold zeros and are not stored; they take the
+            // first row's scales.)
+            const unsigned char* sa = static_cast<const unsigned char*>(a.sa) +
+                                      (m < a.m ? static_cast<int64_t>(m) * a.sa_row : 0) * sa_bytes;
+            uint32_t raw = a.ue8m0 ? __ldg(sa) : __ldg(reinterpret_cast<const uint32_t*>(sa));
             float block = __ldg(sb);
+#pragma unroll 1
             for (int kb = 0; kb < a.kb; ++kb) {
-                uint32_t next = 0u;
-                float next_block = 0.0f;
+                // (the byte of a UE8M0 scale is the exponent, 0 standing for 2^-127)
+                const float scale = __uint_as_float((raw << sa_shift) | (raw == 0u ? sa_zero : 0u)) * block;
                 if (kb + 1 < a.kb) {
-                    if (live) next = load_sa(a, m, kb + 1);
-                    next_block = __ldg(sb + kb + 1);
+                    sa += sa_step;
+                    ++sb;
+                    raw = a.ue8m0 ? __ldg(sa) : __ldg(reinterpret_cast<const uint32_t*>(sa));
+                    block = __ldg(sb);
                 }
                 ok = ok && warp_wait(&tfull[b], tphase);
-                const int buffer = b;
-                if (++b == B) {
-                    b = 0;
-                    tphase ^= 1u;
-                }
+                const uint32_t addr = tmem_at + b * BN, handed = tempty_at + b * 8;
+                b = (b + 1) & (B - 1);
+                tphase ^= b == 0 ? 1u : 0u;
                 if (!ok) continue;
                 tc_fence_after();
-                const uint32_t addr = tmem + buffer * BN + wg * HALF + (static_cast<uint32_t>(quad * 32) << 16);
                 // 64 block sums at a time: a load takes some 250 clocks to
                 // arrive and the matrix unit waits for the buffer meanwhile
-                // (16 at a time: 209 us for 8192 x 4096 x 7168)
                 float d[4][16];
                 tmem_ld32(d[0], d[1], addr);
                 tmem_ld32(d[2], d[3], addr + 32);
-                const float scale = sa_value(a, raw) * block;
                 const float2 s2 = make_float2(scale, scale);
 #pragma unroll
                 for (int h = 0; h < HALF / 64; ++h) {
@@ -275,19 +282,17 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     if (h + 1 == HALF / 64) {   // the block sums have been read: hand the buffer back
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(map_to_rank(&tempty[buffer], 0));
+                        if (lane == 0) mbar_arrive_cluster(handed);
                     }
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            acc[h * 32 + c * 8 + j] = fma2_rn(make_float2(d[c][2 * j], d[c][2 * j + 1]), s2, acc[h * 32 + c * 8 + j]);
+                        for (int q = 0; q < 8; ++q)
+                            acc[h * 32 + c * 8 + q] = fma2_rn(make_float2(d[c][2 * q], d[c][2 * q + 1]), s2, acc[h * 32 + c * 8 + q]);
                         if (h + 1 < HALF / 64 && (c & 1))
                             tmem_ld32(d[c - 1], d[c], addr + (h + 1) * 64 + (c - 1) * 16);
                     }
                 }
-                raw = next;
-                block = next_block;
             }
             // Round to T, through shared memory (swizzled as the tensor map
             // says) into 64-column stores; rows and columns beyond the matrix
