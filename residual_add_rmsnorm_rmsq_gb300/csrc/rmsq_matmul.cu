@@ -103,6 +103,14 @@ struct MmCall {
     MmArgs args;
 };
 
+// CTAs of a cluster that divide K: doubled while there are not more than two
+// CTAs per SM and each keeps two blocks.
+int token_splits(int64_t ctas, int64_t kb, int sms) {
+    int splits = 1;
+    while (splits < 8 && ctas * splits * 2 <= 2 * sms && kb >= splits * 4) splits *= 2;
+    return splits;
+}
+
 template <class E, int BN>
 cudaError_t launch_rows(const MmCall& c, cudaStream_t stream) {
     using Tile = RowsTile<BN>;
@@ -128,9 +136,7 @@ cudaError_t launch_tokens(const MmCall& c, int sms, cudaStream_t stream) {
     using Tile = TokTile<NT>;
     const void* fn = (const void*)&mm_tokens_kernel<E, NT>;
     const int64_t blocks = (c.n + 127) / 128, mt = (c.m + NT - 1) / NT, kb = c.k / 128;
-    // K split in two as long as the CTAs are not two per SM and each keeps two blocks
-    int splits = 1;
-    while (splits < 8 && blocks * mt * splits * 2 <= 2 * sms && kb >= splits * 4) splits *= 2;
+    int splits = token_splits(blocks * mt, kb, sms);
     const int64_t most_kb = (kb + splits - 1) / splits;
     int stages = static_cast<int>((kTokSmem - 1024 - most_kb * NT * 4) / Tile::stage_bytes);
     if (stages > Tile::max_stages) stages = Tile::max_stages;
@@ -154,11 +160,25 @@ cudaError_t launch_matmul(const MmCall& c, cudaStream_t stream) {
     cudaError_t e;
     const int sms = sm_count(&e);
     if (e != cudaSuccess) return e;
-    // Row tiles while they occupy most of the pairs, the wider ones (fewer
-    // bytes per product) where those do.
-    const int64_t mt = (c.m + 255) / 256, pairs = sms / 2;
-    if (c.m > 128 && mt * ((c.n + 255) / 256) >= pairs) return launch_rows<E, 256>(c, stream);
-    if (c.m > 128 && mt * ((c.n + 127) / 128) * 3 >= 2 * pairs) return launch_rows<E, 128>(c, stream);
+    // Up to 64 rows the tokens kernel, which reads b at 4.5 TB/s then.  Above,
+    // whichever of it and the two row tiles is expected sooner.  The estimates
+    // (us) are straight lines through what was measured at n = 2048 .. 14336,
+    // k = 2048 .. 7168 and m = 96 .. 2048: a round of 256 x 128 (256 x 256) tiles
+    // takes 0.27 (0.36) per block of K, a tokens CTA 0.85 per block of its part
+    // of K.  At 128 x 4096 x 4096 the tokens kernel takes 11.5 and the narrow row
+    // tiles 12.8, at 256 rows 14.9 and 13.0, at 128 x 7168 x 2048 10.7 and 8.9; at
+    // 768 x 4096 x 4096 the narrow tiles take 22.9 (two rounds), the wide ones
+    // 18.2, at 512 rows 13.4 and 17.7.
+    if (c.m > 64) {
+        const int64_t mt = (c.m + 255) / 256, pairs = sms / 2, kb = c.k / 128;
+        const int64_t narrow = (mt * ((c.n + 127) / 128) + pairs - 1) / pairs, wide = (mt * ((c.n + 255) / 256) + pairs - 1) / pairs;
+        const double us_narrow = 3.9 + 0.27 * static_cast<double>(narrow * kb), us_wide = 3.9 + 0.36 * static_cast<double>(wide * kb);
+        const int64_t ctas = (c.n + 127) / 128 * ((c.m + 127) / 128), splits = token_splits(ctas, kb, sms);
+        const int64_t rounds = (ctas * splits + 2 * sms - 1) / (2 * sms);
+        const double us_tokens = 8.0 + 0.85 * static_cast<double>((kb + splits - 1) / splits * rounds);
+        if (us_wide <= us_narrow && us_wide <= us_tokens) return launch_rows<E, 256>(c, stream);
+        if (us_narrow <= us_tokens) return launch_rows<E, 128>(c, stream);
+    }
     if (c.m <= 16) return launch_tokens<E, 16>(c, sms, stream);
     if (c.m <= 32) return launch_tokens<E, 32>(c, sms, stream);
     if (c.m <= 64) return launch_tokens<E, 64>(c, sms, stream);

@@ -84,6 +84,13 @@ def test_few_rows(rmsq_gpu, m, n, k, dtype):
     check(rmsq_gpu, m, n, k, "fp8_group128_row", dtype, seed=m)
 
 
+@pytest.mark.parametrize("m, n, k", [(100, 520, 7168), (128, 136, 4096), (200, 264, 7168), (65, 72, 7168)])
+def test_some_rows_long_k(rmsq_gpu, m, n, k):
+    """Few tiles and a long K, which a cluster divides: 128 tokens per CTA, one
+    and two token tiles."""
+    check(rmsq_gpu, m, n, k, "fp8_group128_col", "bf16", seed=m)
+
+
 @pytest.mark.parametrize("m, n, k", [
     (520, 2680, 256),      # 128-column tiles, ragged both ways
     (1100, 4360, 384),     # 256-column tiles, more than one per CTA
