@@ -185,10 +185,12 @@ def _p(t):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> int:
+def _stream(stream, device: int = -1) -> int:
+    """The handle of `stream`, or of the current one of `device` (of the
+    current device if that is not known)."""
     if stream is None:
         if _raw_stream is not None and torch.cuda.is_initialized():
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(device if device >= 0 else torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -443,15 +445,15 @@ def build_slot_map(context_lens: torch.Tensor, query_lens: torch.Tensor, block_t
     if slot_map is None:
         slot_map = torch.empty(max(max_tokens, 0), dtype=_I64, device=dev)
     if positions is None:
-        positions = torch.empty(max(max_tokens, 0), dtype=_I64, device=dev)
+        positions = torch.empty_like(slot_map)
     if query_start is None:
         query_start = torch.empty(R + 1, dtype=_I32, device=dev)
     if seq_lens is None:
-        seq_lens = torch.empty(R, dtype=_I32, device=dev)
+        seq_lens = torch.empty_like(context_lens)
     if num_free_out is None:
-        num_free_out = torch.empty(1, dtype=_I32, device=dev)
+        num_free_out = torch.empty_like(num_free)
     if status is None:
-        status = torch.empty(1, dtype=_I32, device=dev)
+        status = torch.empty_like(num_free)
     per_r, one, per_t, capacity = (R,), (1,), (max_tokens,), free_pages.shape
     if not (_is_current(i) and _fits(context_lens, _I32, i, per_r) and _fits(query_lens, _I32, i, per_r) and
             _fits(block_table, _I32, i, (R, width)) and _fits(free_pages, _I32, i, capacity) and
@@ -467,9 +469,10 @@ def build_slot_map(context_lens: torch.Tensor, query_lens: torch.Tensor, block_t
                  "query_start": (R + 1,), "seq_lens": per_r, "num_free_out": one, "status": one}
         for name, t in given.items():
             _want_shape(name, t, *sizes[name])
-    st = L.rmsq_build_slot_map(_p(context_lens), _p(query_lens), _p(block_table), width, _p(free_pages),
-                               capacity[0], _p(num_free), page_size, R, max_tokens, _p(slot_map), _p(positions),
-                               _p(query_start), _p(seq_lens), _p(num_free_out), _p(status), _stream(stream))
+    st = L.rmsq_build_slot_map(context_lens.data_ptr(), query_lens.data_ptr(), block_table.data_ptr(), width,
+                               free_pages.data_ptr(), capacity[0], num_free.data_ptr(), page_size, R, max_tokens,
+                               slot_map.data_ptr(), positions.data_ptr(), query_start.data_ptr(), seq_lens.data_ptr(),
+                               num_free_out.data_ptr(), status.data_ptr(), _stream(stream, i))
     if st:
         raise RmsqError(st, "rmsq_build_slot_map")
     return slot_map, positions, query_start, seq_lens, num_free_out, status
@@ -519,8 +522,9 @@ def kv_cache_store_nvfp4(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tenso
         _want_shape("slot_map", slot_map, n)
         _check_cache(cache, h, d, page_size)
         _check_global_scales(k_global_scale, v_global_scale)
-    st = L.rmsq_kv_cache_store_nvfp4(_p(k), ks, _p(v), vs, _p(slot_map), _p(k_global_scale), _p(v_global_scale),
-                                     _p(cache), pages, page_size, n, h, d, DTYPES[dt], _stream(stream))
+    st = L.rmsq_kv_cache_store_nvfp4(k.data_ptr(), ks, v.data_ptr(), vs, slot_map.data_ptr(), k_global_scale.data_ptr(),
+                                     v_global_scale.data_ptr(), cache.data_ptr(), pages, page_size, n, h, d, DTYPES[dt],
+                                     _stream(stream, i))
     if st:
         raise RmsqError(st, "rmsq_kv_cache_store_nvfp4")
 
@@ -538,11 +542,15 @@ def kv_cache_load_nvfp4(cache: torch.Tensor, slot_map: torch.Tensor, k_global_sc
         raise ValueError("cache must be [pages, 2, kv heads, bytes of a tile]")
     n, h = slot_map.shape[0], cache.shape[2]
     shape = (n, h, head_dim)
+    ks = vs = h * head_dim
     if k_out is None:
         k_out = torch.empty(shape, dtype=dtype, device=cache.device)
+    else:
+        ks = _token_rows("k_out", k_out)
     if v_out is None:
         v_out = torch.empty(shape, dtype=dtype, device=cache.device)
-    ks, vs = _token_rows("k_out", k_out), _token_rows("v_out", v_out)
+    else:
+        vs = _token_rows("v_out", v_out)
     i, pages = cache.get_device(), cache.shape[0]
     if not (_is_current(i) and _fits(cache, _U8, i, kv_cache_shape(pages, h, head_dim, page_size)) and
             _fits(slot_map, _I64, i, (n,)) and _fits(k_global_scale, _F32, i, (1,)) and
@@ -557,8 +565,9 @@ def kv_cache_load_nvfp4(cache: torch.Tensor, slot_map: torch.Tensor, k_global_sc
         _check_global_scales(k_global_scale, v_global_scale)
     if k_out.shape != shape or v_out.shape != shape:
         raise ValueError(f"outputs must have shape {shape}")
-    st = L.rmsq_kv_cache_load_nvfp4(_p(cache), pages, page_size, _p(slot_map), _p(k_global_scale), _p(v_global_scale),
-                                    _p(k_out), ks, _p(v_out), vs, n, h, head_dim, DTYPES[dtype], _stream(stream))
+    st = L.rmsq_kv_cache_load_nvfp4(cache.data_ptr(), pages, page_size, slot_map.data_ptr(), k_global_scale.data_ptr(),
+                                    v_global_scale.data_ptr(), k_out.data_ptr(), ks, v_out.data_ptr(), vs, n, h, head_dim,
+                                    DTYPES[dtype], _stream(stream, i))
     if st:
         raise RmsqError(st, "rmsq_kv_cache_load_nvfp4")
     return k_out, v_out
@@ -592,7 +601,7 @@ def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: tor
         raise ValueError("cache must be [pages, 2, kv heads, bytes of a tile], block_table [requests, width]")
     kv, (R, width) = cache.shape[2], block_table.shape
     if out is None:
-        out = torch.empty((n, heads, d), dtype=dt, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if lse is None and return_lse:
         lse = torch.empty((n, heads), dtype=_F32, device=q.device)
     if workspace is None:
@@ -619,10 +628,10 @@ def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: tor
         _check_global_scales(k_global_scale, v_global_scale)
     if softmax_scale is None:
         softmax_scale = d ** -0.5
-    st = L.rmsq_paged_attention_nvfp4(_p(q), qs, _p(cache), pages, page_size, _p(block_table), width, _p(query_start),
-                                      _p(seq_lens), _p(k_global_scale), _p(v_global_scale), softmax_scale, window, _p(out),
-                                      _p(lse), _p(workspace), size, n, R, heads, kv, d, DTYPES[dt],
-                                      _stream(stream))
+    st = L.rmsq_paged_attention_nvfp4(q.data_ptr(), qs, cache.data_ptr(), pages, page_size, block_table.data_ptr(), width,
+                                      query_start.data_ptr(), seq_lens.data_ptr(), k_global_scale.data_ptr(),
+                                      v_global_scale.data_ptr(), softmax_scale, window, out.data_ptr(), _p(lse),
+                                      workspace.data_ptr(), size, n, R, heads, kv, d, DTYPES[dt], _stream(stream, i))
     if st:
         raise RmsqError(st, "rmsq_paged_attention_nvfp4")
     return out if lse is None else (out, lse)
@@ -672,8 +681,8 @@ def fp8_block_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, mode: str, b
         _want_shape("a_scales", a_scales, *shape)
         _want_shape("b_scales", b_scales, *b_shape)
         _want_shape("out", out, m, n)
-    st = L.rmsq_fp8_block_matmul(_p(a_codes), _p(a_scales), code, _p(b_codes), _p(b_scales), _p(out), m, n, k,
-                                 DTYPES[dtype], _stream(stream))
+    st = L.rmsq_fp8_block_matmul(a_codes.data_ptr(), a_scales.data_ptr(), code, b_codes.data_ptr(), b_scales.data_ptr(),
+                                 out.data_ptr(), m, n, k, DTYPES[dtype], _stream(stream, i))
     if st:
         raise RmsqError(st, "rmsq_fp8_block_matmul")
     return out
