@@ -444,6 +444,12 @@ int rmsq_kv_cache_load_nvfp4(const void *kv_cache, int64_t num_pages, int64_t pa
  *                rmsq_paged_attention_workspace_bytes(...) bytes of scratch;
  *                contents on entry do not matter.  Two calls in flight at the
  *                same time must not share one.
+ *  variant       an rmsq_variant.  DIRECT: the kernel for few queries, which
+ *                divides the keys of each request over the device.  PIPELINED:
+ *                a tensor-core kernel for requests of more than 64 (query, head
+ *                of the group) pairs, DIRECT for the others (and for head_dim
+ *                256).  AUTO: whichever is expected sooner.  The two agree
+ *                within the rounding of their sums.
  * Sums, maxima and the log-sum-exp are fp32; probabilities are rounded to f16
  * before they meet the values.  Results are deterministic.  n_tokens *
  * num_heads below 2^31; 0 tokens or requests return RMSQ_OK without a launch.
@@ -455,7 +461,7 @@ int rmsq_paged_attention_nvfp4(const void *q, int64_t q_stride, const void *kv_c
                                const float *v_global_scale, float softmax_scale, int64_t window, void *out,
                                float *lse, void *workspace, size_t workspace_bytes, int64_t n_tokens,
                                int64_t num_requests, int num_heads, int num_kv_heads, int head_dim, int dtype,
-                               void *stream);
+                               void *stream, int variant);
 
 /* Bytes of workspace rmsq_paged_attention_nvfp4 needs (0 for arguments it
  * refuses). */

@@ -122,7 +122,7 @@ def load(path: str | None = None):
         L.rmsq_kv_cache_load_nvfp4.argtypes = [vp, i64, i64, vp, vp, vp, vp, i64, vp, i64, i64, ci, ci, ci, vp]
         L.rmsq_kv_cache_load_nvfp4.restype = ci
         L.rmsq_paged_attention_nvfp4.argtypes = [vp, i64, vp, i64, i64, vp, i64, vp, vp, vp, vp, f32, i64, vp, vp, vp,
-                                                 ctypes.c_size_t, i64, i64, ci, ci, ci, ci, vp]
+                                                 ctypes.c_size_t, i64, i64, ci, ci, ci, ci, vp, ci]
         L.rmsq_paged_attention_nvfp4.restype = ci
         L.rmsq_paged_attention_workspace_bytes.argtypes = [i64, i64, ci, ci, ci]
         L.rmsq_paged_attention_workspace_bytes.restype = ctypes.c_size_t
@@ -582,7 +582,7 @@ def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: tor
                           seq_lens: torch.Tensor, k_global_scale: torch.Tensor, v_global_scale: torch.Tensor,
                           page_size: int, softmax_scale: float | None = None, *, window: int = 0,
                           return_lse: bool = False, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
-                          workspace: torch.Tensor | None = None, stream=None):
+                          workspace: torch.Tensor | None = None, stream=None, variant: str = "auto"):
     """rmsq_paged_attention_nvfp4: causal attention of q [tokens, heads, D]
     (token stride free) over the paged NVFP4 cache.
 
@@ -590,9 +590,11 @@ def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: tor
     [R], the lengths with this step's tokens, which are in the cache already.
     softmax_scale: 1 / sqrt(D) by default; window > 0 limits a query to its
     last `window` keys.  Missing outputs and the workspace are allocated (rows
-    of q behind query_start[R] are not computed).  Returns out [tokens, heads,
-    D], or (out, lse [tokens, heads] fp32) with return_lse or a given lse.
+    of q behind query_start[R] are not computed).  variant: "auto", "direct"
+    (few queries) or "pipelined" (prompts).  Returns out [tokens, heads, D], or
+    (out, lse [tokens, heads] fp32) with return_lse or a given lse.
     """
+    vcode = _variant(variant)
     L = load()
     dt = _act_types(q)
     qs = _token_rows("q", q)
@@ -606,6 +608,8 @@ def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: tor
         lse = torch.empty((n, heads), dtype=_F32, device=q.device)
     if workspace is None:
         workspace = torch.empty(paged_attention_workspace_bytes(n, R, heads, kv, d), dtype=_U8, device=q.device)
+        if stream is not None and q.is_cuda:    # it is let go on return, perhaps before that stream is done with it
+            workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
     i, pages, size = q.get_device(), cache.shape[0], workspace.numel()
     if not (_is_current(i) and _fits(cache, _U8, i, kv_cache_shape(pages, kv, d, page_size)) and
             _fits(block_table, _I32, i, (R, width)) and _fits(query_start, _I32, i, (R + 1,)) and
@@ -631,7 +635,8 @@ def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: tor
     st = L.rmsq_paged_attention_nvfp4(q.data_ptr(), qs, cache.data_ptr(), pages, page_size, block_table.data_ptr(), width,
                                       query_start.data_ptr(), seq_lens.data_ptr(), k_global_scale.data_ptr(),
                                       v_global_scale.data_ptr(), softmax_scale, window, out.data_ptr(), _p(lse),
-                                      workspace.data_ptr(), size, n, R, heads, kv, d, DTYPES[dt], _stream(stream, i))
+                                      workspace.data_ptr(), size, n, R, heads, kv, d, DTYPES[dt], _stream(stream, i),
+                                      vcode)
     if st:
         raise RmsqError(st, "rmsq_paged_attention_nvfp4")
     return out if lse is None else (out, lse)

@@ -73,12 +73,29 @@ cudaError_t launch_prompt(AttnArgs a, cudaStream_t stream) {
                          PromptTile<D>::smem, stream);
 }
 
-// Requests of more than kPromptRows rows go to the prompt kernel, the others
-// to the split kernel, whichever they are: the lengths are the device's.  The
-// prompt kernel is launched where a request may have more than that on average.
+// Requests of more than kPromptRows rows go to the prompt kernel, the others to
+// the split kernel, whichever they are: the lengths are the device's.
+//
+// The prompt kernel is launched (AUTO) where it is expected sooner.  It gives a
+// CTA 256 rows and all their keys, about 1.25 us per 128 of them; the split
+// kernel gives its CTAs (three per SM) 16 rows and equal runs of keys, about 1.1
+// us per 128.  So few rows on a long context belong to the split kernel, although
+// it reads the keys once per 16 rows.  Both costs are proportional to the
+// length, which the host does not know.  Measured, split and prompt, D = 128: 8
+// queries of 16 x 8 heads on 100000 keys 126 and 633 us, 64 of 8 x 8 heads 594
+// and 966, 256 of them 1925 and 805; 8 requests of 50 queries (8 x 4 heads) on
+// 2000 keys 72 and 43; 4 of 200 (4 x 8) on 500 keys 72 and 24.
 template <class E>
-cudaError_t launch_attn(AttnArgs a, int head_dim, int64_t max_tiles, cudaStream_t stream) {
-    const bool prompt = head_dim <= 128 && static_cast<int64_t>(a.tokens) * a.group > static_cast<int64_t>(kPromptRows) * a.requests;
+cudaError_t launch_attn(AttnArgs a, int head_dim, int64_t max_tiles, int variant, cudaStream_t stream) {
+    cudaError_t err;
+    const int sms = sm_count(&err);
+    if (err != cudaSuccess) return err;
+    const int64_t rows = static_cast<int64_t>(a.tokens) * a.group;
+    const int64_t items = (rows / 256 + 1) * a.kv_heads;
+    const bool sooner = 1.1 * static_cast<double>(rows * a.kv_heads) / (16.0 * 3.0 * sms) > 1.25 * static_cast<double>((items + sms - 1) / sms);
+    // (no request can have more than kPromptRows rows if all together have not)
+    const bool prompt = head_dim <= 128 && rows > kPromptRows && variant != kVariantDirect &&
+                        (variant == kVariantPipelined || sooner);
     // (a single request is the prompt kernel's whatever its length)
     a.most_rows = !prompt ? INT32_MAX : a.requests == 1 ? 0 : kPromptRows;
     if (prompt) {
@@ -118,12 +135,14 @@ int rmsq_paged_attention_nvfp4(const void* q, int64_t q_stride, const void* kv_c
                                const int32_t* seq_lens, const float* k_global_scale, const float* v_global_scale,
                                float softmax_scale, int64_t window, void* out, float* lse, void* workspace,
                                size_t workspace_bytes, int64_t n_tokens, int64_t num_requests, int num_heads,
-                               int num_kv_heads, int head_dim, int dtype, void* stream) {
+                               int num_kv_heads, int head_dim, int dtype, void* stream, int variant) {
     using rmsq_abi::aligned;
     using rmsq_abi::overlaps;
     using rmsq_abi::Span;
     using rmsq_abi::span;
     if (dtype != RMSQ_BF16 && dtype != RMSQ_FP16) return RMSQ_ERR_INVALID_ARG;
+    if (variant != RMSQ_VARIANT_AUTO && variant != RMSQ_VARIANT_DIRECT && variant != RMSQ_VARIANT_PIPELINED)
+        return RMSQ_ERR_INVALID_ARG;
     int st = rmsq::attn_shape(n_tokens, num_requests, num_heads, num_kv_heads, head_dim);
     if (st != RMSQ_OK) return st;
     if (!std::isfinite(softmax_scale) || softmax_scale <= 0.0f || window < 0 || num_pages < 0 || table_width < 0)
@@ -190,8 +209,10 @@ int rmsq_paged_attention_nvfp4(const void* q, int64_t q_stride, const void* kv_c
     const int64_t qtiles = n_tokens * a.group / 8 + num_requests;
     const int64_t max_tiles = qtiles > kMaxTiles / ktiles / num_kv_heads ? kMaxTiles : qtiles * ktiles * num_kv_heads;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == RMSQ_BF16 ? rmsq::launch_attn<rmsq::Bf16T>(a, head_dim, max_tiles, s)
-                                             : rmsq::launch_attn<rmsq::Fp16T>(a, head_dim, max_tiles, s);
+    const int v = variant == RMSQ_VARIANT_DIRECT ? rmsq::kVariantDirect
+                  : variant == RMSQ_VARIANT_PIPELINED ? rmsq::kVariantPipelined : rmsq::kVariantAuto;
+    const cudaError_t e = dtype == RMSQ_BF16 ? rmsq::launch_attn<rmsq::Bf16T>(a, head_dim, max_tiles, v, s)
+                                             : rmsq::launch_attn<rmsq::Fp16T>(a, head_dim, max_tiles, v, s);
     return e == cudaSuccess ? RMSQ_OK : rmsq_abi::fail_cuda(e);
 }
 

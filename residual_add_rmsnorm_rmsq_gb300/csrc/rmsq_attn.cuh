@@ -30,9 +30,17 @@
 // kappa is the order of the keys that makes S^T's accumulator, transposed by
 // movmatrix, the second product's operand.
 //
-// Bound by HBM for long caches (9/16 byte per element, K and V): see the
-// table of measurements beside the launch.  Work is split evenly over the
-// CTAs whatever the lengths: the (request, row tile, kv head, 128-key tile)
+// Bound by HBM and, nearly as much, by issue for long caches (9/16 byte per
+// element, K and V): 128 requests of 2048 to 8192 keys, 8 heads on each of 4 kv
+// heads of 128, take 81 us for 390 MB (4.8 TB/s; 71 with the arithmetic left out,
+// 76 with the copies left out), 3 requests of up to 131071 keys on 8 kv heads 72
+// us for 357 MB.  About 300 warp instructions per 16 keys and kv head are left, 64
+// of them conversions of codes, 64 multiplications by scales, 16 products.
+// Measured and not kept: the codes loaded straight into registers a step ahead
+// (116 us), a ring of bulk copies on mbarriers (111), 16 keys per softmax step
+// (111), a third stage (84), registers capped for five CTAs per SM (86).
+//
+// Work is split evenly over the CTAs whatever the lengths: the (request, row tile, kv head, 128-key tile)
 // tiles form one sequence, cut into equal runs; a CTA writes the items its
 // run holds whole, and leaves (O, m, l) in the workspace for the two that its
 // ends may cut, which a second launch joins in order.
@@ -697,9 +705,10 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
 // share of the rows of the item that starts in run b and goes past its end.
 // Four dims per thread; the threads that a share leaves over split its parts
 // and meet in shared memory (in order, so the result does not depend on
-// timing).  The loads of a round of four parts are independent: with one part
-// after the other an item of 15 parts cost 15 memory latencies, 10 us of a 90 us
-// launch.  One share (gridDim.y = 1) fits all the joins of a ragged batch on
+// timing).  The split has written down which items those are; a join that
+// scanned the lengths again took 20 us for 3 long requests.  The loads of a
+// round of four parts are independent: with one part after the other an item of
+// 15 parts cost 15 memory latencies, 10 us of a 90 us launch.  One share (gridDim.y = 1) fits all the joins of a ragged batch on
 // the card at once; eight shares serve few, long items of many parts.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinShares = 8;

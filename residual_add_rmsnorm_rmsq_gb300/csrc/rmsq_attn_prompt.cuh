@@ -12,10 +12,18 @@
 // thread for V, whose nibbles are interleaved pairwise so that eight keys of a
 // dim come out as one 16-byte piece of V^T, the layout the product wants.
 //
-// Bound by the matrix unit in the limit (4 D flop per row and key, 1024 clocks
-// per 128 x 128 tile at D = 128); the softmax takes about 2300 warp
-// instructions per tile and the conversion 1300 per two, which together leave
-// it no more than three quarters of the issue slots.
+// Bound by the matrix unit in the limit (4 D flop per row and key; 16 products
+// of 72 clocks per tile and 128 keys at D = 128), and at present by the chain of
+// a tile: its products (1150 clocks), the hand-over (200), its softmax (2100: 520
+// to read the logits, 330 for the maximum, 1040 for the weights, the rest
+// hand-over) and the next products.  Two tiles hide half of that.  2478 and 2445
+// queries of 32 heads on contexts of 732 and 1574 keys: 212 us, 192 GFLOP (0.9
+// PFLOP/s; 48 % of the measured bf16 rate, 101 us).  Measured and not kept: one
+// issuing warp per tile (260 us, the two fall into step), the logits of 64 keys
+// in two buffers so that products run ahead (268: a product of 64 columns takes as
+// long as one of 128), weights handed over in halves (226), weights taken before
+// the maximum is known and again where it moves (231), logits read twice instead
+// of held (259).
 //
 // Every wait is bounded, as in the matrix product.
 #pragma once

@@ -17,17 +17,26 @@
 //                    accumulator lane = row of a, so a thread owns one row: its
 //                    scale is one number per block.  Persistent, one CTA per SM.
 //                    Each CTA holds 128 rows of a and half the tile's rows of b,
-//                    and the matrix units of both read both halves: a CTA alone
-//                    with 128 x 256 fills and reads 96 KB of shared memory per
-//                    block of K, 768 clocks at 128 bytes a clock where its
-//                    products take 512 (measured: 1000; 206 us for 8192 x 4096 x
-//                    7168), a pair 64 KB per CTA.
+//                    and the matrix units of both read both halves, so that a
+//                    CTA fills and reads 64 KB of shared memory per block of K
+//                    instead of 96.  8192 x 4096 x 7168: 167 us, 2.88 PFLOP/s.
+//                    Bound by the promotion: about 750 clocks per block of 256
+//                    columns (465 to read them from tensor memory beside the
+//                    products, 130 to add them, the rest hand-overs) where the
+//                    products take 512.  What it took: 236 us with 16 columns
+//                    read at a time, the scales multiplied next to their loads
+//                    and an issuing thread with long waits; 209 with compact
+//                    waits and descriptors; 206 with 64 columns at a time; 201 as
+//                    a pair; 167 with the next scales loaded into the registers
+//                    they are used from (a move of a loaded value waits for it).
 //  mm_tokens_kernel  few rows (decode).  Bound by the bytes of b, so b's 128
 //                    rows are the accumulator's lanes and the tokens its
 //                    16 .. 128 columns, and the blocks of K are split over a
 //                    cluster of up to eight CTAs to occupy the card; the
 //                    partial sums are joined through distributed shared memory,
-//                    in a fixed order.
+//                    in a fixed order.  33 x 4096 x 14336: 13.0 us, 4.6 TB/s of
+//                    b; 1 x 4096 x 4096: 5.3 us, half of it launch and the filling
+//                    of the ring.
 //
 // Both: one thread keeps a ring of operand tiles in flight (tensor-map copies,
 // 128-byte swizzle), one thread issues the products, the other warps promote.

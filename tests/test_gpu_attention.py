@@ -27,6 +27,9 @@ def make(q_lens, seq_lens, heads, kv, D, page, dtype, *, seed=0, extra_rows=0, s
             "heads": heads, "kv": kv, "dtype": dtype, "k_gs": np.float32(611.3), "v_gs": np.float32(57.9)}
 
 
+VARIANTS = ("direct", "pipelined")
+
+
 def run(rq, c, *, window=0, scale=None, stream=None, **kw):
     dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
     start = np.concatenate([[0], np.cumsum(c["q_lens"])]).astype(np.int32)
@@ -62,16 +65,18 @@ def test_decode(rmsq_gpu, dtype, D, page, heads, kv):
     check(rmsq_gpu, make([1] * len(seq), seq, heads, kv, D, page, dtype, seed=D + heads))
 
 
+@pytest.mark.parametrize("variant", VARIANTS)
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("D, heads, kv, page", [(64, 8, 1, 16), (128, 8, 2, 64), (128, 3, 1, 16), (256, 4, 2, 32)])
 @pytest.mark.parametrize("window", [0, 1, 16, 100])
-def test_several_queries(rmsq_gpu, dtype, D, heads, kv, page, window):
+def test_several_queries(rmsq_gpu, dtype, D, heads, kv, page, window, variant):
     """Speculative tokens and prompts of odd lengths, with and without a
     window; a request without queries, one that is nothing but queries."""
     c = make([4, 1, 0, 33, 130], [77, 300, 20, 33, 391], heads, kv, D, page, dtype, seed=window)
-    check(rmsq_gpu, c, window=window)
+    check(rmsq_gpu, c, window=window, variant=variant)
 
 
+@pytest.mark.parametrize("variant", VARIANTS)
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("heads, kv, page, q_lens, seq", [
@@ -83,19 +88,27 @@ def test_several_queries(rmsq_gpu, dtype, D, heads, kv, page, window):
     (16, 1, 16, [33, 9], [256, 129]),
     (6, 2, 256, [100, 90], [612, 90]),
 ])
-def test_prompt(rmsq_gpu, dtype, D, heads, kv, page, q_lens, seq):
-    check(rmsq_gpu, make(q_lens, seq, heads, kv, D, page, dtype, seed=5 + D))
+def test_prompt(rmsq_gpu, dtype, D, heads, kv, page, q_lens, seq, variant):
+    check(rmsq_gpu, make(q_lens, seq, heads, kv, D, page, dtype, seed=5 + D), variant=variant)
     assert rmsq_gpu.take_fault_flags() == 0
 
 
+@pytest.mark.parametrize("variant", VARIANTS)
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("window", [1, 50, 128, 300])
-def test_prompt_with_a_window(rmsq_gpu, D, window):
-    check(rmsq_gpu, make([200, 70], [700, 70], 4, 2, D, 16, "bf16", seed=window), window=window)
+def test_prompt_with_a_window(rmsq_gpu, D, window, variant):
+    check(rmsq_gpu, make([200, 70], [700, 70], 4, 2, D, 16, "bf16", seed=window), window=window, variant=variant)
 
 
+def test_prompts_of_the_automatic_choice(rmsq_gpu):
+    """Enough rows for the prompt kernel to be chosen, a decode beside them."""
+    check(rmsq_gpu, make([700, 1, 300], [700, 900, 420], 32, 2, 64, 16, "bf16", seed=70))
+    assert rmsq_gpu.take_fault_flags() == 0
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
 @pytest.mark.parametrize("D", [64, 128])
-def test_prompt_bad_pages_empty_rows_padding(rmsq_gpu, D):
+def test_prompt_bad_pages_empty_rows_padding(rmsq_gpu, D, variant):
     """More queries than keys, pages outside the cache, garbage behind the
     last key, rows of padding, extreme and flat queries."""
     c = make([100, 80, 90], [60, 300, 0], 4, 2, D, 16, "bf16", seed=31, extra_rows=70)
@@ -108,17 +121,19 @@ def test_prompt_bad_pages_empty_rows_padding(rmsq_gpu, D):
     c["q64"] = c["q"].double().numpy()
     out = torch.full(c["q"].shape, 3.0, dtype=torch.bfloat16, device="cuda")
     lse = torch.full(c["q"].shape[:2], 5.0, device="cuda")
-    check(rmsq_gpu, c, out=out, lse=lse)
+    check(rmsq_gpu, c, out=out, lse=lse, variant=variant)
     assert (out[270:] == 3).all() and (lse[270:] == 5).all()
 
 
+@pytest.mark.parametrize("variant", VARIANTS)
 @pytest.mark.parametrize("rows", [1, 70, 300])
-def test_a_single_padded_request(rmsq_gpu, rows):
+def test_a_single_padded_request(rmsq_gpu, rows, variant):
     """A token buffer of 300 of which a single request fills some."""
-    check(rmsq_gpu, make([rows], [rows + 33], 2, 1, 64, 16, "fp16", extra_rows=300 - rows))
+    check(rmsq_gpu, make([rows], [rows + 33], 2, 1, 64, 16, "fp16", extra_rows=300 - rows), variant=variant)
 
 
-def test_prompt_rising_logits(rmsq_gpu):
+@pytest.mark.parametrize("variant", VARIANTS)
+def test_prompt_rising_logits(rmsq_gpu, variant):
     """The running maximum moves at every step, and differently per row."""
     c = make([300], [1000], 4, 1, 64, 16, "fp16", seed=3)
     codes, scales = ref.tiles(c["cache"], 16, 64)
@@ -126,27 +141,29 @@ def test_prompt_rising_logits(rmsq_gpu):
     for j in range(1000):
         scales[c["table"][0, j // 16], 0, :, j % 16] = 0x10 + j // 10
     c["q"], c["q64"] = ref.act(c["q64"] + np.linspace(-1, 1, 300)[:, None, None], torch.float16)
-    check(rmsq_gpu, c, scale=0.5)
+    check(rmsq_gpu, c, scale=0.5, variant=variant)
 
 
-def test_prompt_infinite_and_nan_queries_stay_in_their_rows(rmsq_gpu):
+@pytest.mark.parametrize("variant", VARIANTS)
+def test_prompt_infinite_and_nan_queries_stay_in_their_rows(rmsq_gpu, variant):
     c = make([100, 30], [150, 30], 4, 1, 128, 16, "bf16", seed=6)
-    good, good_lse = run(rmsq_gpu, c)
+    good, good_lse = run(rmsq_gpu, c, variant=variant)
     q = c["q"].clone()
     q[10, 2, 5], q[99, 0, 0] = float("inf"), float("nan")
-    out, lse = run(rmsq_gpu, c, q=q.cuda())
+    out, lse = run(rmsq_gpu, c, q=q.cuda(), variant=variant)
     hit = torch.zeros(130, 4, dtype=torch.bool)
     hit[10, 2] = hit[99, 0] = True
     assert torch.equal(out[~hit], good[~hit]) and torch.equal(lse[~hit], good_lse[~hit])
     assert torch.isnan(out[99, 0]).all()
 
 
-def test_prompts_repeat_bit_for_bit_and_in_graphs(rmsq_gpu):
+@pytest.mark.parametrize("variant", VARIANTS)
+def test_prompts_repeat_bit_for_bit_and_in_graphs(rmsq_gpu, variant):
     rq = rmsq_gpu
     c = make([500, 3, 260], [900, 1000, 260], 8, 2, 128, 64, "bf16", seed=40)
-    a = run(rq, c)
+    a = run(rq, c, variant=variant)
     for _ in range(3):
-        b = run(rq, c)
+        b = run(rq, c, variant=variant)
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     dev = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()  # noqa: E731
     q, cache, table, seq = c["q"].cuda(), dev(c["cache"]), dev(c["table"]), dev(np.array(c["seq"], np.int32))
@@ -156,12 +173,13 @@ def test_prompts_repeat_bit_for_bit_and_in_graphs(rmsq_gpu):
     out, lse = torch.empty_like(q), torch.empty(763, 8, device="cuda")
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        rq.paged_attention_nvfp4(q, cache, table, start, seq, g1, g2, 64, out=out, lse=lse, workspace=ws)
+        rq.paged_attention_nvfp4(q, cache, table, start, seq, g1, g2, 64, out=out, lse=lse, workspace=ws,
+                                 variant=variant)
     graph.replay()
     assert torch.equal(out, a[0]) and torch.equal(lse, a[1])
     start.copy_(torch.tensor([0, 10, 700, 763]))        # other lengths, the same graph
     graph.replay()
-    want = rq.paged_attention_nvfp4(q, cache, table, start, seq, g1, g2, 64, return_lse=True)
+    want = rq.paged_attention_nvfp4(q, cache, table, start, seq, g1, g2, 64, return_lse=True, variant=variant)
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and rq.take_fault_flags() == 0
 
 
@@ -276,7 +294,8 @@ def test_lengths_outside_the_buffers_are_clamped(rmsq_gpu):
     c = make([100, 100], [300, 300], 4, 2, 64, 16, "bf16")
     for start, seq in (([0, 100, 200], [2**31 - 1, -5]), ([-9, 2**31 - 1, 150], [300, 300]), ([200, 100, 0], [300, 1])):
         rq.paged_attention_nvfp4(c["q"].cuda(), dev(c["cache"]), dev(c["table"]), dev(np.array(start, np.int32)),
-                                 dev(np.array(seq, np.int32)), one, one, 16, out=torch.zeros_like(c["q"]).cuda())
+                                 dev(np.array(seq, np.int32)), one, one, 16, out=torch.zeros_like(c["q"]).cuda(),
+                                 variant="pipelined")
         torch.cuda.synchronize()
     assert rq.take_fault_flags() == 0
 
@@ -361,3 +380,25 @@ def test_a_decode_loop_of_the_operators_together(rmsq_gpu):
         assert (np.abs(out[:n].double().cpu().numpy() - w_out) <= tol).all()
         assert (np.abs(lse[:n].double().cpu().numpy() - w_lse) <= tol_lse).all()
         ctx = seq
+
+
+def test_a_workspace_of_its_own_on_another_stream(rmsq_gpu):
+    """Without a given workspace a call on a side stream keeps its own until
+    that stream is done, whatever the current stream allocates meanwhile."""
+    c = make([1] * 16, [2000] * 16, 32, 8, 128, 16, "bf16", seed=50)
+    want = run(rmsq_gpu, c)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(8):
+        got.append(run(rmsq_gpu, c, stream=s))
+        torch.full((30 << 20,), 0xff, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for g in got:
+        assert torch.equal(g[0], want[0]) and torch.equal(g[1], want[1])
+
+
+def test_cpu_tensors_are_refused(rmsq_gpu):
+    c = make([1], [20], 4, 2, 64, 16, "bf16")
+    with pytest.raises(ValueError):
+        run(rmsq_gpu, c, q=c["q"])

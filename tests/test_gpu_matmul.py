@@ -96,6 +96,7 @@ def test_some_rows_long_k(rmsq_gpu, m, n, k):
     (1100, 4360, 384),     # 256-column tiles, more than one per CTA
     (2049, 2568, 128),     # one block of K, one row in the last tile
     (129, 20000, 128),     # two row tiles
+    (300, 8, 256),         # fewer columns than a tile has
 ])
 @pytest.mark.parametrize("mode", ["fp8_group128_col+tma", "fp8_group128_row+ue8m0"])
 def test_many_rows(rmsq_gpu, m, n, k, mode):

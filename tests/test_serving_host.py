@@ -94,9 +94,9 @@ def test_load_outputs_must_not_overlap(L):
 
 
 def attn(L, q=A[0], qs=1024, cache=A[1], pages=10, page=16, table=A[2], width=8, start=A[3], seq=A[4], kg=A[5], vg=A[6],
-         scale=0.1, window=0, out=A[7], lse=A[8], ws=A[9], wsb=1 << 27, T=4, R=3, h=8, kv=2, d=128, dt=0):
+         scale=0.1, window=0, out=A[7], lse=A[8], ws=A[9], wsb=1 << 27, T=4, R=3, h=8, kv=2, d=128, dt=0, var=0):
     return L.rmsq_paged_attention_nvfp4(vp(q), qs, vp(cache), pages, page, vp(table), width, vp(start), vp(seq), vp(kg),
-                                        vp(vg), scale, window, vp(out), vp(lse), vp(ws), wsb, T, R, h, kv, d, dt, None)
+                                        vp(vg), scale, window, vp(out), vp(lse), vp(ws), wsb, T, R, h, kv, d, dt, None, var)
 
 
 def test_attention_refusals(L):
@@ -106,7 +106,8 @@ def test_attention_refusals(L):
     assert attn(L, lse=A[12] + 2) == rq.ERR_ALIGNMENT and attn(L, qs=1028) == rq.ERR_ALIGNMENT
     nan, inf = float("nan"), float("inf")
     for kw in ({"dt": 2}, {"T": -1}, {"R": -1}, {"h": 0}, {"kv": 0}, {"scale": 0.0}, {"scale": -1.0}, {"scale": nan},
-               {"scale": inf}, {"window": -1}, {"qs": 1016}, {"pages": -1}, {"width": -1}, {"wsb": 100}):
+               {"scale": inf}, {"window": -1}, {"qs": 1016}, {"pages": -1}, {"width": -1}, {"wsb": 100}, {"var": 3},
+               {"var": -1}):
         assert attn(L, **kw) == rq.ERR_INVALID_ARG, kw
     for kw in ({"kv": 3}, {"d": 80}, {"d": 512}, {"page": 8}, {"R": rq.MAX_REQUESTS + 1}, {"T": 1 << 28},
                {"h": 8192, "kv": 8192}, {"width": 1 << 27}):
@@ -190,7 +191,7 @@ def test_binding_refusals(L):
     for kw in ({"q": z(4, 8, 256).bfloat16()[..., ::2]}, {"q": z(4, 128).bfloat16()}, {"page_size": 32},
                {"cache": z(10, 2, 2, 1151, dtype=u8)}, {"cache": z(10, 2, 2, 2304, dtype=u8)[..., ::2]},
                {"query_start": z(3, dtype=I32)}, {"seq_lens": z(4, dtype=I32)}, {"block_table": z(3, dtype=I32)},
-               {"k_global_scale": torch.ones(2)}, {"out": z(5, 8, 128).bfloat16()}, {"lse": z(4, 9)}):
+               {"k_global_scale": torch.ones(2)}, {"out": z(5, 8, 128).bfloat16()}, {"lse": z(4, 9)}, {"variant": "fast"}):
         with pytest.raises(ValueError):
             rq.paged_attention_nvfp4(**_attn_args(**kw))
     k = z(4, 2, 128).bfloat16()
