@@ -402,3 +402,67 @@ def test_cpu_tensors_are_refused(rmsq_gpu):
     c = make([1], [20], 4, 2, 64, 16, "bf16")
     with pytest.raises(ValueError):
         run(rmsq_gpu, c, q=c["q"])
+
+
+def test_an_attention_block_from_norm_to_output_projection(rmsq_gpu):
+    """The operators as a decoder layer uses them, two steps captured in one
+    graph and replayed: norm + quant, FP8 projection, QK-norm + RoPE, store,
+    attention, quant, FP8 projection.  The graph's results are those of the
+    calls made one by one, and each attention that of float64 over its cache."""
+    rq = rmsq_gpu
+    import rmsq_inputs as ri
+    R, nq, nkv, D, H, page, cap = 4, 8, 2, 64, 512, 16, 40
+    torch.manual_seed(2)
+    E4M3 = torch.float8_e4m3fn
+    w_qkv, w_o = (torch.randn(*s, device="cuda").to(E4M3) for s in (((nq + 2 * nkv) * D, H), (H, nq * D)))
+    s_qkv, s_o = torch.rand(6, 4, device="cuda") * 0.05, torch.rand(4, 4, device="cuda") * 0.05
+    cos_sin = torch.from_numpy(ri.rope_table(256, D)).cuda()
+    wn, wh = torch.ones(H, device="cuda").bfloat16(), torch.ones(D, device="cuda").bfloat16()
+    gs = torch.tensor([2688 / 8.0], device="cuda")
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    steps = [i32([30, 5, 1, 17]), i32([1, 1, 1, 1])]
+    tokens = [60, 6]                                       # buffers, with padding rows
+    xs = [torch.randn(t, H, device="cuda").bfloat16() for t in tokens]
+    free, first_left = torch.randperm(cap, device="cuda").int(), i32([cap])
+    ws = torch.empty(rq.paged_attention_workspace_bytes(60, R, nq, nkv, D), dtype=torch.uint8, device="cuda")
+
+    def layer(table, cache):
+        outs, ctx, left = [], i32_zero.clone(), first_left
+        for new, n, x in zip(steps, tokens, xs):
+            slots, pos, start, seq, left, status = rq.build_slot_map(ctx, new, table, free, left, page, n)
+            q8, s8, r = rq.fused_add_rmsnorm_quant(x, x, wn, 1e-6, "fp8_group128_col+tma")
+            qkv = rq.fp8_block_matmul(q8, s8, "fp8_group128_col+tma", w_qkv, s_qkv)
+            rq.qk_norm_rope(qkv, pos, cos_sin, wh, wh, 1e-6, nq, nkv, D)
+            heads = qkv.unflatten(1, (nq + 2 * nkv, D))
+            rq.kv_cache_store_nvfp4(heads[:, nq: nq + nkv], heads[:, nq + nkv:], slots, gs, gs, cache, page)
+            o = torch.zeros(n, nq, D, device="cuda", dtype=torch.bfloat16)
+            rq.paged_attention_nvfp4(heads[:, :nq], cache, table, start, seq, gs, gs, page, out=o, workspace=ws)
+            o8, so = rq.quant(o.flatten(1), "fp8_group128_row")
+            y = rq.fp8_block_matmul(o8, so, "fp8_group128_row", w_o, s_o)
+            outs.append((heads, o, y, status, seq, table.clone(), cache.clone()))
+            ctx = seq
+        return outs
+
+    i32_zero = i32([0] * R)
+    new_table = lambda: torch.full((R, 8), -1, dtype=torch.int32, device="cuda")  # noqa: E731
+    new_cache = lambda: torch.zeros(rq.kv_cache_shape(cap, nkv, D, page), dtype=torch.uint8, device="cuda")  # noqa: E731
+    plain = layer(new_table(), new_cache())
+    table, cache = new_table(), new_cache()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        graphed = layer(table, cache)
+    for _ in range(2):
+        table.fill_(-1)
+        g.replay()
+        torch.cuda.synchronize()
+        for a, b, new in zip(plain, graphed, steps):
+            n = int(new.sum())
+            assert b[3].item() == 0 and torch.equal(a[4], b[4]) and torch.equal(a[5], b[5])
+            assert torch.equal(a[1][:n], b[1][:n]) and torch.equal(a[2][:n], b[2][:n])
+    for (heads, o, y, _, seq, table, cache), new in zip(plain, steps):
+        n = int(new.sum())
+        w_out, _, tol, _ = ref.attention(heads[:n, :nq].double().cpu().numpy(), cache.cpu().numpy(), table.cpu().numpy(),
+                                         new.tolist(), seq.tolist(), gs.item(), gs.item(), page, D ** -0.5, 0,
+                                         torch.finfo(torch.bfloat16).eps)
+        assert (np.abs(o[:n].double().cpu().numpy() - w_out) <= tol).all()
+    assert rq.take_fault_flags() == 0
