@@ -264,14 +264,6 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
             float block = __ldg(sb);
 #pragma unroll 1
             for (int kb = 0; kb < a.kb; ++kb) {
-                // (the byte of a UE8M0 scale is the exponent, 0 standing for 2^-127)
-                const float scale = __uint_as_float((raw << sa_shift) | (raw == 0u ? sa_zero : 0u)) * block;
-                if (kb + 1 < a.kb) {
-                    sa += sa_step;
-                    ++sb;
-                    raw = a.ue8m0 ? __ldg(sa) : __ldg(reinterpret_cast<const uint32_t*>(sa));
-                    block = __ldg(sb);
-                }
                 ok = ok && warp_wait(&tfull[b], tphase);
                 const uint32_t addr = tmem_at + b * BN, handed = tempty_at + b * 8;
                 b = (b + 1) & (B - 1);
@@ -283,6 +275,15 @@ mm_rows_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                 float d[4][16];
                 tmem_ld32(d[0], d[1], addr);
                 tmem_ld32(d[2], d[3], addr + 32);
+                // meanwhile the factor of this block, and the next one's loads
+                // (the byte of a UE8M0 scale is the exponent, 0 standing for 2^-127)
+                const float scale = __uint_as_float((raw << sa_shift) | (raw == 0u ? sa_zero : 0u)) * block;
+                if (kb + 1 < a.kb) {
+                    sa += sa_step;
+                    ++sb;
+                    raw = a.ue8m0 ? __ldg(sa) : __ldg(reinterpret_cast<const uint32_t*>(sa));
+                    block = __ldg(sb);
+                }
                 const float2 s2 = make_float2(scale, scale);
 #pragma unroll
                 for (int h = 0; h < HALF / 64; ++h) {
