@@ -488,8 +488,7 @@ template <int D, int NB>
 constexpr int kAttnMem = (kAttnWarps * Step<D>::ring > static_cast<int>(sizeof(AttnSmem<D, NB>))
                               ? kAttnWarps * Step<D>::ring : static_cast<int>(sizeof(AttnSmem<D, NB>)) + 127) / 128 * 128;
 
-// Writes row `row` of an item: out = o / l / gs and the log-sum-exp.  A row
-// that sees no key gets zeros and -inf.
+// Four dims of an output row, times the row's factor.
 template <class E>
 __device__ __forceinline__ void store_quad(void* out, int64_t at, float4 o, float inv) {
     reinterpret_cast<uint2*>(out)[at / 4] =

@@ -11,16 +11,8 @@
 
 namespace rmsq {
 
-// The two E2M1 codes in the low byte of w as an f16 pair, low nibble first
-// (every E2M1 value is exact in f16).
-__device__ __forceinline__ uint32_t e2m1x2_f16x2(uint32_t w) {
-    uint32_t r;
-    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}"
-        : "=r"(r) : "r"(w));
-    return r;
-}
-
-// The eight E2M1 codes of w as four f16 pairs: pair j holds byte j.
+// The eight E2M1 codes of w as four f16 pairs: pair j holds byte j, its low
+// nibble first (every E2M1 value is exact in f16).
 __device__ __forceinline__ void e2m1x8_f16x2(uint32_t w, uint32_t (&r)[4]) {
     asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
         "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
