@@ -41,6 +41,7 @@ static __device__ unsigned int g_prompt_fault;
 // warps issue.  They are launched with 128 registers a thread and share them out
 // anew: 176 + 176 + 120 + 40 = 4 x 128.
 constexpr int kPromptThreads = 512;
+constexpr int kSoftmaxGroups = 2;
 constexpr int kSoftmaxRegs = 176, kConvertRegs = 120, kIssueRegs = 40;
 static_assert(2 * kSoftmaxRegs + kConvertRegs + kIssueRegs == 4 * 128, "the shares are the launch's registers");
 
@@ -100,13 +101,11 @@ struct RawTile {
 };
 
 template <int D>
-__device__ __forceinline__ void load_tile(RawTile<D>& x, const AttnArgs& a, int key0, int kpage, int vpage, int head,
-                                          int tid, int octet, int unit) {
+__device__ __forceinline__ void load_keys(RawTile<D>& x, const AttnArgs& a, int key, int kpage, int head) {
     const int64_t tile = static_cast<int64_t>(D / 16 * 9) << a.page_shift;
-    const int mask = (1 << a.page_shift) - 1;
     if (kpage >= 0) {
         const uint8_t* t = a.cache + (static_cast<int64_t>(kpage) * 2 * a.kv_heads + head) * tile;
-        const int in = (key0 + tid) & mask;
+        const int in = key & ((1 << a.page_shift) - 1);
         const uint4* p = reinterpret_cast<const uint4*>(t + in * (D / 2));
 #pragma unroll
         for (int j = 0; j < D / 32; ++j) {
@@ -122,8 +121,13 @@ __device__ __forceinline__ void load_tile(RawTile<D>& x, const AttnArgs& a, int 
 #pragma unroll
         for (int j = 0; j < D / 64; ++j) x.ks[j] = 0u;
     }
+}
+
+template <int D>
+__device__ __forceinline__ void load_values(RawTile<D>& x, const AttnArgs& a, int key, int vpage, int head, int unit) {
+    const int64_t tile = static_cast<int64_t>(D / 16 * 9) << a.page_shift;
     const uint8_t* t = a.cache + ((static_cast<int64_t>(max(vpage, 0)) * 2 + 1) * a.kv_heads + head) * tile;
-    const int in = (key0 + octet * 8) & mask;
+    const int in = key & ((1 << a.page_shift) - 1);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         if (vpage >= 0) {
@@ -411,43 +415,45 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
         }
     } else if (warp >= 8) {
         fewer_registers<kConvertRegs>();
-        // Conversion: the codes of the next tile, and the pages of the one
-        // after it, are on their way while a tile is converted.
-        const int t = tid - 256, w = warp - 8;
+        // Conversion.  The codes of the next tile are loaded into the registers
+        // that this one's have just left, the pages a tile before that.
+        const int t = tid - 128 * kSoftmaxGroups, w = warp - 4 * kSoftmaxGroups;
         const int octet = (w & 1) * 8 + (lane & 7), unit = (w >> 1) * 4 + (lane >> 3);
         const int* table = a.table + static_cast<int64_t>(req) * a.width;
         // A page is compared with their number only when it is used: next to
         // the load the comparison would make the warp wait for it every time.
         auto page_of = [&](int key) { return key > last_pos ? -1 : __ldg(table + (key >> a.page_shift)); };
         auto checked = [&](int p) { return p < a.num_pages ? p : -1; };
-        RawTile<D> cur, nxt;
-        int kp = checked(page_of(key_begin + t)), vp = checked(page_of(key_begin + octet * 8));
-        load_tile<D>(cur, a, key_begin, kp, vp, head, t, octet, unit);
-        int kp1 = page_of(key_begin + 128 + t), vp1 = page_of(key_begin + 128 + octet * 8);
+        RawTile<D> raw;
+        int kkey = key_begin + t, vkey = key_begin + octet * 8;
+        bool here = checked(page_of(kkey)) >= 0;
+        load_keys<D>(raw, a, kkey, checked(page_of(kkey)), head);
+        load_values<D>(raw, a, vkey, checked(page_of(vkey)), head, unit);
+        int kp = page_of(kkey + 128), vp = page_of(vkey + 128);
         for (int n = 0; n < steps; ++n) {
-            const int key0 = key_begin + n * 128, s = n & 1;
-            kp1 = checked(kp1);
-            vp1 = checked(vp1);
-            load_tile<D>(nxt, a, key0 + 128, kp1, vp1, head, t, octet, unit);
-            const int kp2 = page_of(key0 + 256 + t), vp2 = page_of(key0 + 256 + octet * 8);
+            const int s = n & 1;
+            kkey += 128;
+            vkey += 128;
             ok = warp_wait(&kempty[s], ((n >> 1) & 1) ^ 1);
             if (!ok) break;
-            const uint32_t there = __ballot_sync(kFull, kp >= 0);
+            const uint32_t there = __ballot_sync(kFull, here);
             if (lane == 0) valid[n & 3][w] = there;
-            write_keys<D>(ks + s * Tile::k, cur, t);
+            write_keys<D>(ks + s * Tile::k, raw, t);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&kfull[s]);
+            kp = checked(kp);
+            here = kp >= 0;
+            load_keys<D>(raw, a, kkey, kp, head);
+            kp = page_of(kkey + 128);
             ok = warp_wait(&vempty[s], ((n >> 1) & 1) ^ 1);
             if (!ok) break;
-            write_values<D>(vs + s * Tile::v, cur, octet, unit);
+            write_values<D>(vs + s * Tile::v, raw, octet, unit);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&vfull[s]);
-            cur = nxt;
-            kp = kp1;
-            kp1 = kp2;
-            vp1 = vp2;
+            load_values<D>(raw, a, vkey, checked(vp), head, unit);
+            vp = page_of(vkey + 128);
         }
     } else {
         more_registers<kSoftmaxRegs>();
