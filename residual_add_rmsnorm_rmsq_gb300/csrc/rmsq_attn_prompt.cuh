@@ -17,13 +17,14 @@
 // a tile: its products (1150 clocks), the hand-over (200), its softmax (2100: 520
 // to read the logits, 330 for the maximum, 1040 for the weights, the rest
 // hand-over) and the next products.  Two tiles hide half of that.  2478 and 2445
-// queries of 32 heads on contexts of 732 and 1574 keys: 212 us, 192 GFLOP (0.9
-// PFLOP/s; 48 % of the measured bf16 rate, 101 us).  Measured and not kept: one
-// issuing warp per tile (260 us, the two fall into step), the logits of 64 keys
+// queries of 32 heads on contexts of 732 and 1574 keys: 203 us, 192 GFLOP (0.95
+// PFLOP/s; half the measured bf16 rate, 101 us).  Measured and not kept (against
+// 212 to 215 us): two threads per row (326: 88 registers a thread spill), one
+// issuing warp per tile (260, the two fall into step), the logits of 64 keys
 // in two buffers so that products run ahead (268: a product of 64 columns takes as
 // long as one of 128), weights handed over in halves (226), weights taken before
 // the maximum is known and again where it moves (231), logits read twice instead
-// of held (259).
+// of held (259), the next tile's codes in registers of their own (215, spilling).
 //
 // Every wait is bounded, as in the matrix product.
 #pragma once
