@@ -466,3 +466,19 @@ def test_an_attention_block_from_norm_to_output_projection(rmsq_gpu):
                                          torch.finfo(torch.bfloat16).eps)
         assert (np.abs(o[:n].double().cpu().numpy() - w_out) <= tol).all()
     assert rq.take_fault_flags() == 0
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+def test_many_short_requests_of_many_heads(rmsq_gpu, variant):
+    """A thousand requests of 0 to 4 queries, 32 heads on one: rows on both
+    sides of the prompt kernel's limit, lengths around a page."""
+    rng = np.random.default_rng(60)
+    q_lens = [int(x) for x in rng.integers(0, 5, 1000)]
+    seq = [q + int(x) for q, x in zip(q_lens, rng.integers(0, 20, 1000))]
+    check(rmsq_gpu, make(q_lens, seq, 32, 1, 64, 16, "bf16", seed=61), variant=variant)
+    assert rmsq_gpu.take_fault_flags() == 0
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+def test_one_query_of_128_heads(rmsq_gpu, variant):
+    check(rmsq_gpu, make([1, 1], [700, 129], 128, 1, 128, 64, "fp16", seed=62), variant=variant)

@@ -120,6 +120,23 @@ def test_zero_rows_and_nan_codes(rmsq_gpu):
     assert torch.equal(got[keep], out[keep])
 
 
+@pytest.mark.parametrize("m", [3, 300])
+def test_extreme_scales(rmsq_gpu, m):
+    """Zero and smallest scales, exact powers of two: a row's result is its
+    integer sum times them."""
+    rq = rmsq_gpu
+    a = torch.full((m, 256), 0x38, dtype=torch.uint8, device="cuda")          # 1.0
+    b = torch.full((136, 256), 0x38, dtype=torch.uint8, device="cuda")
+    sb = torch.full((2, 2), 2.0 ** 40, device="cuda")
+    sa = torch.full((m, 2), 127 - 40, dtype=torch.uint8, device="cuda")      # 2^-40
+    sa[0], sa[1, 0] = 0, 0                                                   # 2^-127: lost beside the other block
+    got = rq.fp8_block_matmul(a, sa, "fp8_group128_row+ue8m0", b, sb).float()
+    assert (got[2:] == 256).all() and (got[1] == 128).all()
+    assert (got[0] == 256 * 2.0 ** (40 - 127)).all()
+    got = rq.fp8_block_matmul(a, torch.zeros(m, 2, device="cuda"), "fp8_group128_row", b, sb)
+    assert (got == 0).all()
+
+
 def test_fp16_overflows_to_infinity(rmsq_gpu):
     a = torch.full((2, 128), 0x7e, dtype=torch.uint8, device="cuda")
     one = torch.ones(2, 1, device="cuda")
