@@ -427,7 +427,8 @@ int rmsq_kv_cache_load_nvfp4(const void *kv_cache, int64_t num_pages, int64_t pa
  *   out = sum_j softmax_j(softmax_scale * q.k_j) v_j,
  *   lse = ln sum_j exp(softmax_scale * q.k_j).
  * A query that sees no key (an empty request, p < 0) gets zeros and -inf.
- * A key on a page outside [0, num_pages) is left out.
+ * A key on a page outside [0, num_pages) is left out.  A NaN among a query
+ * head's elements gives NaN in its out and lse, and nowhere else.
  *  q             device, T[n_tokens, num_heads, head_dim], tokens q_stride
  *                elements apart (a multiple of 8), 16-byte aligned.
  *  kv_cache, num_pages, page_size, head_dim, global scales: as above.
@@ -464,7 +465,8 @@ int rmsq_paged_attention_nvfp4(const void *q, int64_t q_stride, const void *kv_c
                                void *stream, int variant);
 
 /* Bytes of workspace rmsq_paged_attention_nvfp4 needs (0 for arguments it
- * refuses). */
+ * refuses; else the same for every number of tokens and requests, 10 to 20
+ * MB: one workspace serves the calls of a program that follow one another). */
 size_t rmsq_paged_attention_workspace_bytes(int64_t n_tokens, int64_t num_requests, int num_heads,
                                             int num_kv_heads, int head_dim);
 

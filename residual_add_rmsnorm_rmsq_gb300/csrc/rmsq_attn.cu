@@ -126,7 +126,8 @@ extern "C" {
 size_t rmsq_paged_attention_workspace_bytes(int64_t n_tokens, int64_t num_requests, int num_heads, int num_kv_heads,
                                             int head_dim) {
     if (rmsq::attn_shape(n_tokens, num_requests, num_heads, num_kv_heads, head_dim) != RMSQ_OK) return 0;
-    const int nb = rmsq::row_blocks(n_tokens, num_requests, num_heads / num_kv_heads, head_dim);
+    // for the most row blocks of any call, so that a workspace serves every smaller one
+    const int nb = head_dim <= 128 ? 2 : 1;
     return static_cast<size_t>(rmsq::kAttnMaxWorkers) * (sizeof(rmsq::CutItem) + 2 * rmsq::part_floats(head_dim, nb) * 4);
 }
 

@@ -676,7 +676,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
                 const float4 u = *reinterpret_cast<const float4*>(&sm.o[k][row][d]);
                 o.x += u.x; o.y += u.y; o.z += u.z; o.w += u.w;
                 const float mk = sm.m[k][row];
-                l += mk == -INFINITY ? 0.0f : sm.l[k][row] * exp2_approx(mk - top);
+                // (without a maximum the sum is 0, or NaN where the logits are)
+                l += mk == -INFINITY ? sm.l[k][row] : sm.l[k][row] * exp2_approx(mk - top);
             }
             if (whole) {
                 if (row0 + row < rows) {

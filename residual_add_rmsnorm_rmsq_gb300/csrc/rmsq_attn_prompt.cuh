@@ -328,7 +328,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
         if (tid == 0) prefix[0] = 0;
         __syncthreads();
     }
-    const int item = prefix[a.requests] - 1 - static_cast<int>(blockIdx.x) / a.kv_heads;
+    int item = prefix[a.requests] - 1 - static_cast<int>(blockIdx.x) / a.kv_heads;
     const int head = blockIdx.x % a.kv_heads;
     int req = 0;
     if (item >= 0) {
@@ -338,6 +338,8 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
             if (prefix[mid] <= item) req = mid;
             else hi = mid;
         }
+        // (starts that do not ascend can add up to more items than an int holds)
+        if (item < prefix[req] || item >= prefix[req + 1]) item = -1;
     }
     const int row0 = item >= 0 ? (item - prefix[req]) * 256 : 0;
     __syncthreads();    // the scan has been read: its space is the key tiles' now

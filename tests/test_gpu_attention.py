@@ -482,3 +482,42 @@ def test_many_short_requests_of_many_heads(rmsq_gpu, variant):
 @pytest.mark.parametrize("variant", VARIANTS)
 def test_one_query_of_128_heads(rmsq_gpu, variant):
     check(rmsq_gpu, make([1, 1], [700, 129], 128, 1, 128, 64, "fp16", seed=62), variant=variant)
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("q_lens, seq", [([1, 1, 1], [40, 1, 5000]), ([30, 1, 20], [30, 200, 900])])
+def test_a_nan_in_a_query_head_stays_there(rmsq_gpu, dtype, q_lens, seq, variant):
+    """NaN in out and lse of that query head, alone or joined from parts; the
+    others get what they get without it; a query without keys stays empty."""
+    c = make(q_lens, seq, 8, 2, 128, 16, dtype, seed=63)
+    want, want_lse = check(rmsq_gpu, c, variant=variant)
+    hit = [(0, 3), (sum(q_lens) - 1, 0), (q_lens[0], 7)]
+    for t, h in hit:
+        c["q"][t, h, 77] = float("nan")
+    out, lse = run(rmsq_gpu, c, variant=variant)
+    bad = torch.zeros(out.shape[:2], dtype=torch.bool, device="cuda")
+    for t, h in hit:
+        bad[t, h] = True
+    assert out[bad].isnan().all() and lse[bad].isnan().all()
+    assert torch.equal(out[~bad], want[~bad]) and torch.equal(lse[~bad], want_lse[~bad])
+    c["seq"] = [0] * len(seq)
+    out, lse = run(rmsq_gpu, c, variant=variant)
+    assert (out == 0).all() and (lse == float("-inf")).all()
+
+
+def test_query_starts_that_do_not_ascend(rmsq_gpu):
+    """Nothing outside the buffers is read or written, and requests in order
+    keep their results."""
+    rq = rmsq_gpu
+    c = make([100, 50, 30], [200, 90, 30], 8, 1, 64, 16, "bf16", seed=64)
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    gs = torch.tensor([c["k_gs"]], device="cuda")
+    around = torch.full((3, 180, 8, 64), 7.0, device="cuda", dtype=torch.bfloat16)
+    for variant in VARIANTS:
+        for starts in ([0, 180, 0, 180], [-5, 100, 90, 1000], [180, 0, 180, 0], [0, 2**31 - 1, -2**31, 50]):
+            rq.paged_attention_nvfp4(c["q"].cuda(), dev(c["cache"]), dev(c["table"]), dev(np.array(starts, np.int64).astype(np.int32)),
+                                     dev(np.array(c["seq"], np.int32)), gs, gs, 16, out=around[1], variant=variant)
+            torch.cuda.synchronize()
+    assert (around[0] == 7).all() and (around[2] == 7).all() and around[1].isfinite().all()
+    assert rq.take_fault_flags() == 0

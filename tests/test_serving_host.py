@@ -124,6 +124,13 @@ def test_attention_workspace_size(L):
     assert rq.paged_attention_workspace_bytes(8, 8, 8, 1, 100) == 0
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_workspace_of_the_largest_step_serves_the_smaller(L, D):
+    most = rq.paged_attention_workspace_bytes(256, 256, 8, 4, D)
+    for tokens, requests in ((256, 1), (256, 4), (200, 255), (1, 1)):
+        assert rq.paged_attention_workspace_bytes(tokens, requests, 8, 4, D) <= most
+
+
 def matmul(L, a=A[0], sa=A[1], mode=2, b=A[2], sb=A[3], out=A[4], m=4, n=256, k=512, dt=0):
     return L.rmsq_fp8_block_matmul(vp(a), vp(sa), mode, vp(b), vp(sb), vp(out), m, n, k, dt, None)
 
