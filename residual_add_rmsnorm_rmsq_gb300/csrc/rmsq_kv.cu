@@ -1,6 +1,7 @@
 // Paged key / value cache: slot maps from request lengths, and the NVFP4
 // cache's store and load.
 #include <cstdint>
+#include <type_traits>
 #include <cuda_runtime.h>
 
 #include "rmsq.h"
@@ -191,12 +192,16 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(SlotArgs a) {
 // Store and load.  One thread per 16-element block; a token's blocks (keys,
 // then values) take `lanes` lanes of a warp, a power of two up to 32, so that
 // neither a token nor a head is found by division, and a token with more
-// blocks several rounds.  Bound by HBM: 2 bytes of T and 9/16 of codes and
-// scales per element; 16001 tokens of 4 + 4 heads of 128 take 18.5 us stored and
-// loaded, 84 MB (4.5 TB/s; 40 us with a 64-bit division per block to find its
-// place and sixteen divisions to decode it).  A warp reads (store) or writes
-// (load) up to 1 KB of T in one piece and whole 32-byte sectors of codes; the
-// scale bytes of a head are adjacent bytes of one access.
+// blocks several rounds, two at a time with their loads together (256 tokens of
+// 8 + 8 heads of 128 3.0 us stored and 2.8 loaded; 3.4 and 3.1 with one after the
+// other, where the second round's loads waited for the first's arithmetic).
+// Bound by HBM: 2 bytes of T and 9/16 of codes and scales per element; 16001
+// tokens of 4 + 4 heads of 128, 42 MB each way, take 9.3 us stored (4.5 TB/s)
+// and 12.1 loaded into buffers larger than L2 (3.5 TB/s, about half of the issue
+// slots).  What it took for both together: 40 us with a 64-bit division
+// per block to find its place and sixteen divisions to decode it.  A warp reads
+// (store) or writes (load) up to 1 KB of T in one piece and whole 32-byte
+// sectors of codes; the scale bytes of a head are adjacent bytes of one access.
 //
 // The store takes the same steps as the RMSQ_NVFP4 quantisation of the row ops
 // and so gives the same bits.
@@ -259,8 +264,10 @@ struct BlockPlace {
     }
 };
 
+// (bf16 at 48 registers, five CTAs per SM: 9.3 us instead of 10.1 for 16001
+// tokens; fp16 would spill there, 10.4 instead of 9.9)
 template <class E, int B>
-__global__ void __launch_bounds__(256) cache_store_kernel(CacheArgs a) {
+__global__ void __launch_bounds__(256, std::is_same<E, Bf16T>::value ? 5 : 4) cache_store_kernel(CacheArgs a) {
     allow_dependents();
     grid_dependency_wait();
     int t, c;
@@ -268,23 +275,37 @@ __global__ void __launch_bounds__(256) cache_store_kernel(CacheArgs a) {
     const int64_t slot = __ldg(reinterpret_cast<const long long*>(a.slots) + t);
     if (slot < 0 || slot >= a.slots_total) return;
     const float gs[2] = {__ldg(a.k_gs), __ldg(a.v_gs)};
-    for (; c < 2 * a.heads * B; c += 1 << a.lane_shift) {
-        const BlockPlace<B> p(a, c, slot);
-        const uint4* src = (p.side ? a.v + t * a.v_stride : a.k + t * a.k_stride) + 2 * p.rest;
-        const uint4 lo = ld_act(src), hi = ld_act(src + 1);
-        float x[8], y[8];
-        unpack16<E>(lo, hi, x, y);
-        const float amax = max_abs8(max_abs8(0.0f, x), y);
-        const float g = p.side ? gs[1] : gs[0];
-        const uint32_t sb = e4m3x2(__fmul_rn(__fdiv_rn(amax, 6.0f), g), 0.0f) & 0x7fu;
-        const float r = sb == 0u ? 0.0f : __fdiv_rn(g, e4m3_value_nonneg(sb));
+    const int blocks = 2 * a.heads * B, step = 1 << a.lane_shift;
+    for (; c < blocks; c += 2 * step) {
+        // two blocks' loads before either's arithmetic
+        uint4 in[2][2];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            x[j] = __fmul_rn(x[j], r);
-            y[j] = __fmul_rn(y[j], r);
+        for (int i = 0; i < 2; ++i) {
+            if (c + i * step < blocks) {
+                const BlockPlace<B> p(a, c + i * step, slot);
+                const uint4* src = (p.side ? a.v + t * a.v_stride : a.k + t * a.k_stride) + 2 * p.rest;
+                in[i][0] = ld_act(src);
+                in[i][1] = ld_act(src + 1);
+            }
         }
-        *reinterpret_cast<uint2*>(p.codes) = make_uint2(e2m1x8(x), e2m1x8(y));
-        *p.scale = static_cast<uint8_t>(sb);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (c + i * step >= blocks) break;
+            const BlockPlace<B> p(a, c + i * step, slot);
+            float x[8], y[8];
+            unpack16<E>(in[i][0], in[i][1], x, y);
+            const float amax = max_abs8(max_abs8(0.0f, x), y);
+            const float g = p.side ? gs[1] : gs[0];
+            const uint32_t sb = e4m3x2(__fmul_rn(__fdiv_rn(amax, 6.0f), g), 0.0f) & 0x7fu;
+            const float r = sb == 0u ? 0.0f : __fdiv_rn(g, e4m3_value_nonneg(sb));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                x[j] = __fmul_rn(x[j], r);
+                y[j] = __fmul_rn(y[j], r);
+            }
+            *reinterpret_cast<uint2*>(p.codes) = make_uint2(e2m1x8(x), e2m1x8(y));
+            *p.scale = static_cast<uint8_t>(sb);
+        }
     }
 }
 
@@ -295,7 +316,7 @@ __global__ void __launch_bounds__(256) cache_store_kernel(CacheArgs a) {
 // where both ends round to the same T that is the result; otherwise (about
 // one block in a thousand) the block is divided out.
 template <class E, int B>
-__global__ void __launch_bounds__(256) cache_load_kernel(CacheArgs a) {
+__global__ void __launch_bounds__(256, 4) cache_load_kernel(CacheArgs a) {
     allow_dependents();
     grid_dependency_wait();
     int t, c;
@@ -304,18 +325,32 @@ __global__ void __launch_bounds__(256) cache_load_kernel(CacheArgs a) {
     const bool inside = slot >= 0 && slot < a.slots_total;
     const float gs[2] = {__ldg(a.k_gs), __ldg(a.v_gs)};
     const Fp8Recips rc[2] = {fp8_recips(gs[0]), fp8_recips(gs[1])};
-    for (; c < 2 * a.heads * B; c += 1 << a.lane_shift) {
-        const BlockPlace<B> p(a, c, inside ? slot : 0);
-        uint4* dst = const_cast<uint4*>(p.side ? a.v + t * a.v_stride : a.k + t * a.k_stride) + 2 * p.rest;
-        uint32_t w[8] = {};
-        if (inside) {
-            const uint2 q = __ldg(reinterpret_cast<const uint2*>(p.codes));
-            const float d = nvfp4_scale_value(__ldg(p.scale)), g = p.side ? gs[1] : gs[0];
-            const float dn = p.side ? rc[1].rdn : rc[0].rdn, up = p.side ? rc[1].rup : rc[0].rup;
+    const int blocks = 2 * a.heads * B, step = 1 << a.lane_shift;
+    for (; c < blocks; c += 2 * step) {
+        // two blocks' loads before either's arithmetic
+        uint2 codes[2];
+        uint32_t scale[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            codes[i] = make_uint2(0u, 0u);
+            scale[i] = 0u;
+            if (inside && c + i * step < blocks) {
+                const BlockPlace<B> p(a, c + i * step, slot);
+                codes[i] = __ldg(reinterpret_cast<const uint2*>(p.codes));
+                scale[i] = __ldg(p.scale);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (c + i * step >= blocks) break;
+            const int side = c + i * step >= a.heads * B, rest = c + i * step - side * a.heads * B;
+            uint4* dst = const_cast<uint4*>(side ? a.v + t * a.v_stride : a.k + t * a.k_stride) + 2 * rest;
+            const float d = nvfp4_scale_value(scale[i]), g = side ? gs[1] : gs[0];
+            const float dn = side ? rc[1].rdn : rc[0].rdn, up = side ? rc[1].rup : rc[0].rup;
             // outside this range the bracket's ends would be subnormal or infinite
-            uint32_t pair[8], diff = !(g >= 7.8886091e-31f && g <= 1.2676506e30f);
-            e2m1x8_f16x2(q.x, *reinterpret_cast<uint32_t(*)[4]>(&pair[0]));
-            e2m1x8_f16x2(q.y, *reinterpret_cast<uint32_t(*)[4]>(&pair[4]));
+            uint32_t w[8], pair[8], diff = !(g >= 7.8886091e-31f && g <= 1.2676506e30f);
+            e2m1x8_f16x2(codes[i].x, *reinterpret_cast<uint32_t(*)[4]>(&pair[0]));
+            e2m1x8_f16x2(codes[i].y, *reinterpret_cast<uint32_t(*)[4]>(&pair[4]));
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float2 v = mul2_rn(make_float2(Fp16T::lo(pair[j]), Fp16T::hi(pair[j])), make_float2(d, d));
@@ -329,9 +364,13 @@ __global__ void __launch_bounds__(256) cache_load_kernel(CacheArgs a) {
                     w[j] = E::pack(__fdiv_rn(__fmul_rn(Fp16T::lo(pair[j]), d), g),
                                    __fdiv_rn(__fmul_rn(Fp16T::hi(pair[j]), d), g));
             }
+            if (!inside) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = 0u;
+            }
+            st_stream(dst, make_uint4(w[0], w[1], w[2], w[3]));
+            st_stream(dst + 1, make_uint4(w[4], w[5], w[6], w[7]));
         }
-        st_stream(dst, make_uint4(w[0], w[1], w[2], w[3]));
-        st_stream(dst + 1, make_uint4(w[4], w[5], w[6], w[7]));
     }
 }
 
