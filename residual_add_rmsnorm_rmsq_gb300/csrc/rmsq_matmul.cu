@@ -39,13 +39,14 @@ EncodeTiled encoder() {
     return fn;
 }
 
-// A row-major [rows, cols] matrix in boxes of box_rows x 128 bytes, swizzled.
-bool make_map(CUtensorMap* map, const void* p, bool codes, int64_t rows, int64_t cols, int box_rows) {
+// A row-major [rows, cols] matrix, rows `pitch` elements apart, in boxes of
+// box_rows x 128 bytes, swizzled.
+bool make_map(CUtensorMap* map, const void* p, bool codes, int64_t rows, int64_t cols, int64_t pitch, int box_rows) {
     const EncodeTiled enc = encoder();
     if (!enc) return false;
     const int elem = codes ? 1 : 2;
     const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * elem};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * elem};
     const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), static_cast<cuuint32_t>(box_rows)}, one[2] = {1, 1};
     return enc(map, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(p), dims,
                strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -111,8 +112,9 @@ int token_splits(int64_t ctas, int64_t kb, int sms) {
     return splits;
 }
 
+// Columns n0 .. n0 + n - 1 (n0 a multiple of 128) by the kernel for many rows.
 template <class E, int BN>
-cudaError_t launch_rows(const MmCall& c, cudaStream_t stream) {
+cudaError_t launch_rows(const MmCall& c, int64_t n0, int64_t n, cudaStream_t stream) {
     using Tile = RowsTile<BN>;
     const void* fn = (const void*)&mm_rows_kernel<E, BN>;
     static std::atomic<int> cached[128];
@@ -121,11 +123,15 @@ cudaError_t launch_rows(const MmCall& c, cudaStream_t stream) {
     const int64_t pairs = resident_pairs(fn, Tile::smem, cached, &e);
     if (e != cudaSuccess) return e;
     CUtensorMap ma, mb, mo;
-    if (!make_map(&ma, c.a, true, c.m, c.k, 128) || !make_map(&mb, c.b, true, c.n, c.k, BN / 2) ||
-        !make_map(&mo, c.args.out, false, c.m, c.n, 128))
-        return cudaErrorInvalidValue;
-    const int64_t tiles = (c.m + 255) / 256 * ((c.n + BN - 1) / BN);
     MmArgs args = c.args;
+    args.sb += n0 / 128 * args.kb;
+    args.out = static_cast<uint16_t*>(args.out) + n0;
+    args.n = static_cast<int>(n);
+    if (!make_map(&ma, c.a, true, c.m, c.k, c.k, 128) ||
+        !make_map(&mb, static_cast<const uint8_t*>(c.b) + n0 * c.k, true, n, c.k, c.k, BN / 2) ||
+        !make_map(&mo, args.out, false, c.m, n, c.n, 128))
+        return cudaErrorInvalidValue;
+    const int64_t tiles = (c.m + 255) / 256 * ((n + BN - 1) / BN);
     void* params[] = {&ma, &mb, &mo, &args};
     return launch_cluster(fn, dim3(2 * static_cast<unsigned>(tiles < pairs ? tiles : pairs)), dim3(kRowsThreads), params,
                           Tile::smem, 2, stream);
@@ -146,7 +152,7 @@ cudaError_t launch_tokens(const MmCall& c, int sms, cudaStream_t stream) {
     }
     if (stages < 2) return cudaErrorInvalidConfiguration;
     CUtensorMap ma, mb;
-    if (!make_map(&ma, c.a, true, c.m, c.k, NT) || !make_map(&mb, c.b, true, c.n, c.k, 128)) return cudaErrorInvalidValue;
+    if (!make_map(&ma, c.a, true, c.m, c.k, c.k, NT) || !make_map(&mb, c.b, true, c.n, c.k, c.k, 128)) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kTokSmem);
     if (e != cudaSuccess) return e;
     MmArgs args = c.args;
@@ -176,8 +182,22 @@ cudaError_t launch_matmul(const MmCall& c, cudaStream_t stream) {
         const int64_t ctas = (c.n + 127) / 128 * ((c.m + 127) / 128), splits = token_splits(ctas, kb, sms);
         const int64_t rounds = (ctas * splits + 2 * sms - 1) / (2 * sms);
         const double us_tokens = 8.0 + 0.85 * static_cast<double>((kb + splits - 1) / splits * rounds);
-        if (us_wide <= us_narrow && us_wide <= us_tokens) return launch_rows<E, 256>(c, stream);
-        if (us_narrow <= us_tokens) return launch_rows<E, 128>(c, stream);
+        // Or full rounds of wide tiles and, in a second launch (3 us: it waits for
+        // the first one's last tile), narrow ones for the columns left over: 300 x
+        // 10240 x 8192 takes 51.5 us so and 55.6 in two wide rounds, 768 x 7168 x
+        // 7168 46.8 and 49.2; at k = 4096 the second launch costs what it saves.
+        const int64_t full = wide > 1 ? (wide - 1) * pairs / mt * 256 : 0;
+        if (full > 0 && full < c.n) {
+            const int64_t last = (mt * ((c.n - full + 127) / 128) + pairs - 1) / pairs;
+            const int64_t first = (mt * (full / 256) + pairs - 1) / pairs;
+            const double us_both = 6.9 + (0.36 * static_cast<double>(first) + 0.27 * static_cast<double>(last)) * static_cast<double>(kb);
+            if (us_both < us_wide && us_both < us_narrow && us_both < us_tokens) {
+                e = launch_rows<E, 256>(c, 0, full, stream);
+                return e == cudaSuccess ? launch_rows<E, 128>(c, full, c.n - full, stream) : e;
+            }
+        }
+        if (us_wide <= us_narrow && us_wide <= us_tokens) return launch_rows<E, 256>(c, 0, c.n, stream);
+        if (us_narrow <= us_tokens) return launch_rows<E, 128>(c, 0, c.n, stream);
     }
     if (c.m <= 16) return launch_tokens<E, 16>(c, sms, stream);
     if (c.m <= 32) return launch_tokens<E, 32>(c, sms, stream);

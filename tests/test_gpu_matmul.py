@@ -197,3 +197,32 @@ def test_float8_tensors_and_outputs_of_the_fused_ops(rmsq_gpu):
     o = rq.fp8_block_matmul(q2, s2, "fp8_group128_row", *down)
     y, A = want(q2, s2, down)
     assert ((o.double().cpu() - y).abs() <= y.abs() * 2.0 ** -8 + A * 2.0 ** -23 * 200).all()
+
+
+@pytest.mark.parametrize("mode, dtype", [("fp8_group128_col+tma", "bf16"), ("fp8_group128_row+ue8m0", "fp16")])
+@pytest.mark.parametrize("m, n", [(257, 9800), (600, 6912)])
+def test_full_rounds_and_the_columns_left_over(rmsq_gpu, m, n, mode, dtype):
+    """A little more than a round of wide tiles with a long K: the columns
+    behind the full round go to narrow tiles of a second launch."""
+    check(rmsq_gpu, m, n, 5120, mode, dtype, seed=m)
+
+
+def test_both_launches_in_a_graph_follow_their_inputs(rmsq_gpu):
+    rq = rmsq_gpu
+    a, _, given, b, sb = make(257, 9800, 5120, "fp8_group128_row")
+    x, s, w, t = [torch.from_numpy(v).cuda() for v in (a, given, b, sb)]
+    out = torch.empty(257, 9800, dtype=torch.bfloat16, device="cuda")
+    rq.fp8_block_matmul(x, s, "fp8_group128_row", w, t, out=out)
+    want = out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        rq.fp8_block_matmul(x, s, "fp8_group128_row", w, t, out=out)
+        y = out.flip(0).contiguous()
+        x.copy_(x.flip(0))
+        s.copy_(s.flip(0))
+    for _ in range(4):
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(y, want.flip(0))
+        want = want.flip(0)
+    assert rq.take_fault_flags() == 0
