@@ -465,7 +465,7 @@ int rmsq_paged_attention_nvfp4(const void *q, int64_t q_stride, const void *kv_c
                                void *stream, int variant);
 
 /* Bytes of workspace rmsq_paged_attention_nvfp4 needs (0 for arguments it
- * refuses; else the same for every number of tokens and requests, 10 to 20
+ * refuses; else the same for every number of tokens and requests, 10 to 21
  * MB: one workspace serves the calls of a program that follow one another). */
 size_t rmsq_paged_attention_workspace_bytes(int64_t n_tokens, int64_t num_requests, int num_heads,
                                             int num_kv_heads, int head_dim);

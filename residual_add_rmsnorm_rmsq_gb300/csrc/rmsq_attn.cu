@@ -27,7 +27,7 @@ int row_blocks(int64_t tokens, int64_t requests, int group, int head_dim) {
     return head_dim <= 128 && tokens * group > 8 * requests ? 2 : 1;
 }
 
-size_t part_floats(int head_dim, int nb) { return static_cast<size_t>(8) * nb * (head_dim + 2); }
+size_t part_floats(int head_dim, int nb) { return static_cast<size_t>(8) * nb * (head_dim + 4); }    // kPartRow
 
 template <class E, int D, int NB>
 cudaError_t launch_split(AttnArgs a, int64_t max_tiles, cudaStream_t stream) {

@@ -18,6 +18,13 @@
 // rounded to f16 (11 bits; 8 would be as many as a bf16 output has), scaled by
 // 2^kPShift so that those down to 2^-23 of the maximum keep all their bits.
 //
+// Maxima are kept as logits and not as logits times f (the factor that turns
+// them into powers of two): the product's rounding, half a unit of its last
+// place, would be an error of the exponent, and from 2^24 on it takes weights
+// out of f16's range.  A weight is 2^(f s + (9 - f t)) while the maximum f t is
+// at most 2^10, where the bracket is off by 2^-14 at most, and 2^(f (s - t) + 9)
+// beyond, exact where it matters: the largest logit's weight is 2^9 always.
+//
 // Layout: contractions may take their index in any order, so every lane loads
 // the piece of the cache it needs in one access, with no shuffle.  Each warp
 // keeps the next steps in flight as asynchronous copies into a ring of its own.
@@ -58,6 +65,7 @@ constexpr int kAttnMaxWorkers = 1216;           // CTAs of the split launch: 8 p
 constexpr int kPromptRows = 64;                 // see launch_attn
 constexpr float kPShift = 9.0f;                 // probabilities are scaled by 2^9 ...
 constexpr float kLazy = 6.0f;                   // ... and by up to 2^6 more while the maximum lags: < 2^16 in f16
+constexpr float kFar = 1024.0f;                 // maximum (in powers of two) from which it is subtracted first
 
 // What the join has to know of an item that starts in a run and goes past its
 // end: the runs it lies in, and its rows.
@@ -80,12 +88,17 @@ struct AttnArgs {
     void* out;              // [tokens, heads, D]
     float* lse;             // [tokens, heads] or null
     CutItem* cut;           // [workers]
-    float* part;            // [workers][2][ROWS][D + 2]
+    float* part;            // [workers][2][ROWS][kPartRow<D>]
     int requests, width, tokens, heads, kv_heads, group;
     int page_shift, num_pages, window, workers;
     int most_rows;          // rows of a request above which the split kernel leaves it to the prompt kernel
     float scale_log2;       // softmax scale * log2(e)
 };
+
+// A row of a part in the workspace: D sums, the maximum, the sum of the weights,
+// the row's factor.
+template <int D>
+constexpr int kPartRow = D + 4;
 
 // One request as the kernels see it: every value is clamped so that no
 // length or offset in device memory can lead outside the buffers.
@@ -310,13 +323,28 @@ __device__ __forceinline__ void read_values(KeyRegs<D>& x, const unsigned char* 
 // f16 pair (s, s) from half `hi` of an f16 pair.
 __device__ __forceinline__ uint32_t dup_half(uint32_t pair, int hi) { return __byte_perm(pair, 0, hi ? 0x3232 : 0x1010); }
 
-// A warp's running state over its keys for one item.  The logits stay in the
-// units of the product; f turns them into units of log2, m is the maximum in
-// those, limit the raw logit above which it has to move.
+// The factor of a row's logits, kept within the normal numbers: zero or infinite,
+// it would turn differences of logits into NaN.
+__device__ __forceinline__ float clamp_factor(float f) { return fminf(fmaxf(f, 1.17549435e-38f), 3.40282347e38f); }
+
+// The logit above which a maximum of t has to move.  Rounded down: half a unit of
+// t's last place can be more than kLazy.
+__device__ __forceinline__ float lag_limit(float t, float f) { return t == -INFINITY ? t : __fadd_rd(t, kLazy / f); }
+
+// What the exponents of a row with maximum m are shifted by, and whether m is
+// so far out that it is to be subtracted from the logits instead.
+__device__ __forceinline__ float weight_shift(float m, float f) { return m == -INFINITY ? 0.0f : fmaf(-m, f, kPShift); }
+__device__ __forceinline__ bool is_far(float shift) { return !(fabsf(shift) <= kFar); }
+
+// A warp's running state over its keys for one item.  The logits and their
+// maximum m stay in the units of the product; f turns them into units of log2;
+// limit is the logit above which the maximum has to move; far: some row's
+// maximum is beyond kFar.
 template <int D, int NB>
 struct WarpState {
     float o[D / 16][NB][4];
     float m[NB][2], l[NB][2], limit[NB][2];
+    bool far;
 };
 
 // S^T of 16 keys: s[b][0..1] key kappa(g), rows 2t and 2t + 1; s[b][2..3] key + 8.
@@ -433,6 +461,7 @@ __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned cha
             grow |= top[b][j] > w.limit[b][j];
         }
     if (__any_sync(kFull, grow)) {
+        bool far = false;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -440,10 +469,11 @@ __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned cha
                 float x = top[b][j];
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
-                const float m = fmaxf(x * f[b][j], w.m[b][j]);
-                const float r = m == -INFINITY ? 1.0f : exp2_approx(w.m[b][j] - m);
+                const float m = fmaxf(x, w.m[b][j]);
+                const float r = m == -INFINITY ? 1.0f : exp2_approx((w.m[b][j] - m) * f[b][j]);
                 w.m[b][j] = m;
-                w.limit[b][j] = (m + kLazy) / f[b][j];
+                w.limit[b][j] = lag_limit(m, f[b][j]);
+                far |= is_far(weight_shift(m, f[b][j]));
                 w.l[b][j] *= r;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
@@ -451,18 +481,36 @@ __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned cha
                     w.o[i][b][j + 2] *= r;
                 }
             }
+        w.far = __any_sync(kFull, far);
+    }
+    float shift[NB][2];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) shift[b][j] = weight_shift(w.m[b][j], f[b][j]);
+    if (w.far) {    // the rows that are (the others as ever, whatever shares their warp)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const bool far = is_far(shift[b][j]);
+                const float m = far ? w.m[b][j] : 0.0f;
+                if (far) shift[b][j] = kPShift;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    s[h][b][j] -= m;
+                    s[h][b][j + 2] -= m;
+                }
+            }
     }
     uint32_t pf[2][NB][2];
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-        float shift[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) shift[j] = w.m[b][j] == -INFINITY ? 0.0f : kPShift - w.m[b][j];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float p[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) p[j] = exp2_approx(fmaf(s[h][b][j], f[b][j & 1], shift[j & 1]));
+            for (int j = 0; j < 4; ++j) p[j] = exp2_approx(fmaf(s[h][b][j], f[b][j & 1], shift[b][j & 1]));
             w.l[b][0] += p[0] + p[2];
             w.l[b][1] += p[1] + p[3];
             pf[h][b][0] = transpose8x8(Fp16T::pack(p[0], p[1]));
@@ -481,6 +529,7 @@ template <int D, int NB>
 struct AttnSmem {
     float o[kAttnWarps][8 * NB][D + 4];
     float m[kAttnWarps][8 * NB], l[kAttnWarps][8 * NB];
+    float f[8 * NB];
 };
 
 // Bytes of the ring, or of the join if that is more.
@@ -493,6 +542,11 @@ template <class E>
 __device__ __forceinline__ void store_quad(void* out, int64_t at, float4 o, float inv) {
     reinterpret_cast<uint2*>(out)[at / 4] =
         make_uint2(E::pack(o.x * inv, o.y * inv), E::pack(o.z * inv, o.w * inv));
+}
+
+// ln of the sum of the weights: l of them relative to the maximum m, times 2^kPShift.
+__device__ __forceinline__ float row_lse(float m, float l, float f) {
+    return l == 0.0f ? -INFINITY : fmaf(m, f, log2f(l) - kPShift) * 0.693147180559945309f;
 }
 
 template <class E, int D, int NB>
@@ -594,13 +648,14 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                fs[b][j] = fmaxf(__shfl_sync(kFull, f, (2 * t + j) * 4), 1.17549435e-38f);
+                fs[b][j] = clamp_factor(__shfl_sync(kFull, f, (2 * t + j) * 4));
                 const int col = row0 + 8 * b + 2 * t + j;
                 pos[b][j] = col < rows ? rq.seq - rq.qlen + col / a.group : -1;
                 lo[b][j] = a.window > 0 ? pos[b][j] - a.window + 1 : 0;
             }
         }
         WarpState<D, NB> w;
+        w.far = false;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -643,6 +698,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
                 if (g == 0) {
                     sm.m[warp][8 * b + 2 * t + j] = w.m[b][j];
                     sm.l[warp][8 * b + 2 * t + j] = l;
+                    if (warp == 0) sm.f[8 * b + 2 * t + j] = fs[b][j];
                 }
             }
         __syncthreads();
@@ -654,7 +710,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
                 float top = sm.m[0][row];
 #pragma unroll
                 for (int i = 1; i < kAttnWarps; ++i) top = fmaxf(top, sm.m[i][row]);
-                const float f = w.m[b][j] == -INFINITY ? 0.0f : exp2_approx(w.m[b][j] - top);
+                const float f = w.m[b][j] == -INFINITY ? 0.0f : exp2_approx((w.m[b][j] - top) * fs[b][j]);
                 float* dst = &sm.o[warp][row][g * (D / 8)];
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
@@ -664,9 +720,10 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
             }
         __syncthreads();
         const bool whole = at.tile == 0 && ntiles == rq.ktiles;
-        float* part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (x == blockIdx.x * run ? 0 : 1)) * ROWS * (D + 2);
+        float* part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (x == blockIdx.x * run ? 0 : 1)) * ROWS * kPartRow<D>;
         for (int i = tid; i < ROWS * (D / 4); i += kAttnThreads) {
             const int row = i / (D / 4), d = i % (D / 4) * 4;
+            const float f = sm.f[row];
             float top = sm.m[0][row], l = 0.0f;
 #pragma unroll
             for (int k = 1; k < kAttnWarps; ++k) top = fmaxf(top, sm.m[k][row]);
@@ -677,19 +734,18 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
                 o.x += u.x; o.y += u.y; o.z += u.z; o.w += u.w;
                 const float mk = sm.m[k][row];
                 // (without a maximum the sum is 0, or NaN where the logits are)
-                l += mk == -INFINITY ? sm.l[k][row] : sm.l[k][row] * exp2_approx(mk - top);
+                l += mk == -INFINITY ? sm.l[k][row] : sm.l[k][row] * exp2_approx((mk - top) * f);
             }
             if (whole) {
                 if (row0 + row < rows) {
                     const int64_t tok = rq.q0 + (row0 + row) / a.group;
                     const int64_t oh = tok * a.heads + at.head * a.group + (row0 + row) % a.group;
                     store_quad<E>(a.out, oh * D + d, o, l > 0.0f ? 1.0f / (l * v_gs) : (l == 0.0f ? 0.0f : l));
-                    if (a.lse && d == 0) a.lse[oh] = l == 0.0f ? -INFINITY : (top + log2f(l) - kPShift) * 0.693147180559945309f;
+                    if (a.lse && d == 0) a.lse[oh] = row_lse(top, l, f);
                 }
             } else {
-                *reinterpret_cast<float2*>(part + row * (D + 2) + d) = make_float2(o.x, o.y);
-                *reinterpret_cast<float2*>(part + row * (D + 2) + d + 2) = make_float2(o.z, o.w);
-                if (d == 0) *reinterpret_cast<float2*>(part + row * (D + 2) + D) = make_float2(top, l);
+                *reinterpret_cast<float4*>(part + row * kPartRow<D> + d) = o;
+                if (d == 0) *reinterpret_cast<float4*>(part + row * kPartRow<D> + D) = make_float4(top, l, f, 0.0f);
             }
         }
         __syncthreads();
@@ -718,15 +774,17 @@ struct Partial {
     float m, l;
 };
 
-__device__ __forceinline__ Partial load_partial(const float* p, int d, int D) {
-    const float2 u = __ldcg(reinterpret_cast<const float2*>(p + d)), v = __ldcg(reinterpret_cast<const float2*>(p + d + 2));
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + D));
-    return {make_float4(u.x, u.y, v.x, v.y), ml.x, ml.y};
+// The parts of a row have one factor, `factor`.
+__device__ __forceinline__ Partial load_partial(const float* p, int d, int D, float& factor) {
+    const float4 o = __ldcg(reinterpret_cast<const float4*>(p + d)), ml = __ldcg(reinterpret_cast<const float4*>(p + D));
+    factor = ml.z;
+    return {o, ml.x, ml.y};
 }
 
-__device__ __forceinline__ void merge(Partial& a, const Partial& b) {
+__device__ __forceinline__ void merge(Partial& a, const Partial& b, float factor) {
     const float m = fmaxf(a.m, b.m);
-    const float f = a.m == -INFINITY ? 0.0f : exp2_approx(a.m - m), h = b.m == -INFINITY ? 0.0f : exp2_approx(b.m - m);
+    const float f = a.m == -INFINITY ? 0.0f : exp2_approx((a.m - m) * factor);
+    const float h = b.m == -INFINITY ? 0.0f : exp2_approx((b.m - m) * factor);
     a.o.x = a.o.x * f + b.o.x * h;
     a.o.y = a.o.y * f + b.o.y * h;
     a.o.z = a.o.z * f + b.o.z * h;
@@ -749,7 +807,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a) {
     const int w0 = blockIdx.x;
     const float v_gs = __ldg(a.v_gs);
     const int rows = rq.qlen * a.group, row0 = c1.x * ROWS;
-    const int64_t slot = ROWS * (D + 2);
+    const int64_t slot = ROWS * kPartRow<D>;
     const int quads = ROWS * (D / 4) / static_cast<int>(gridDim.y);      // of this share; a power of two
     const int across = min(quads, kJoinThreads), split = kJoinThreads / across;
     const int quad = threadIdx.x % across, group = threadIdx.x / across;
@@ -757,27 +815,28 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a) {
         const int at_quad = blockIdx.y * quads + q0 + quad, row = at_quad / (D / 4), d = at_quad % (D / 4) * 4;
         Partial acc = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, 0.0f};
         auto part = [&](int w) {
-            return a.part + (static_cast<int64_t>(w0 + w) * 2 + (w == 0 ? first_slot : 0)) * slot + row * (D + 2);
+            return a.part + (static_cast<int64_t>(w0 + w) * 2 + (w == 0 ? first_slot : 0)) * slot + row * kPartRow<D>;
         };
+        float factor = 0.0f;
         for (int w = group; w < parts; w += 4 * split) {
             Partial p[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 p[i] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, 0.0f};
-                if (w + i * split < parts) p[i] = load_partial(part(w + i * split), d, D);
+                if (w + i * split < parts) p[i] = load_partial(part(w + i * split), d, D, factor);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) merge(acc, p[i]);
+            for (int i = 0; i < 4; ++i) merge(acc, p[i], factor);
         }
         met[threadIdx.x] = acc;
         __syncthreads();
         if (group == 0 && row0 + row < rows) {
-            for (int i = 1; i < split; ++i) merge(acc, met[i * across + quad]);
+            for (int i = 1; i < split; ++i) merge(acc, met[i * across + quad], factor);
             const int64_t tok = rq.q0 + (row0 + row) / a.group;
             const int64_t oh = tok * a.heads + head * a.group + (row0 + row) % a.group;
             const float l = acc.l;
             store_quad<E>(a.out, oh * D + d, acc.o, l > 0.0f ? 1.0f / (l * v_gs) : (l == 0.0f ? 0.0f : l));
-            if (a.lse && d == 0) a.lse[oh] = l == 0.0f ? -INFINITY : (acc.m + log2f(l) - kPShift) * 0.693147180559945309f;
+            if (a.lse && d == 0) a.lse[oh] = row_lse(acc.m, l, factor);
         }
         __syncthreads();
     }

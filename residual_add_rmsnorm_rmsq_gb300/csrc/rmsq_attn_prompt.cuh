@@ -4,7 +4,7 @@
 //
 // A CTA takes 256 rows (query token, head of the group) of a request and kv
 // head as two tiles of 128, and walks the keys 128 at a time:
-//   S = Q . K^T (128 x 128 x D)  ->  P = 2^(f S - m)  ->  O += P . V (128 x D x 128)
+//   S = Q . K^T (128 x 128 x D)  ->  P = 2^(f (S - m))  ->  O += P . V (128 x D x 128)
 // with S, P (f16, in S's place) and O in tensor memory, a thread per row in the
 // softmax.  While one tile is in its softmax the matrix unit works for the
 // other.  Four warps turn the cache's codes into f16 operand tiles in shared
@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
 #pragma unroll
                 for (int j = 0; j < D / 2; ++j) q[j] = Fp16T::pack(E::lo(q[j]) * up, E::hi(q[j]) * up);
             }
-            f = fmaxf(f, 1.17549435e-38f);
+            f = clamp_factor(f);
 #pragma unroll
             for (int j = 0; j < D / 8; ++j)
                 *reinterpret_cast<uint4*>(qs + i * Tile::q + (j >> 3) * (128 * 128) + local * 128 +
@@ -535,10 +535,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                 if (__any_sync(kFull, top > limit)) {
                     // sfull of this step says that the previous P . V has
                     // completed too: O may be rescaled here
-                    const float m1 = fmaxf(top * f, m);
-                    const float r = m1 == -INFINITY ? 1.0f : exp2_approx(m - m1);
+                    const float m1 = fmaxf(top, m);
+                    const float r = m1 == -INFINITY ? 1.0f : exp2_approx((m - m1) * f);
                     m = m1;
-                    limit = (m + kLazy) / f;
+                    limit = lag_limit(m, f);
                     l *= r;
                     if (n > 0) {
 #pragma unroll
@@ -553,7 +553,15 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                         }
                     }
                 }
-                const float shift = m == -INFINITY ? 0.0f : kPShift - m;
+                float shift = weight_shift(m, f);
+                if (__any_sync(kFull, is_far(shift))) {     // the rows that are; the others subtract zero
+                    const float t = is_far(shift) ? m : 0.0f;
+                    if (is_far(shift)) shift = kPShift;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) d[c][j] -= t;
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) l += weigh_half(d, h, s_at, f, shift);
                 tmem_st_wait();
@@ -588,7 +596,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                                                     E::pack(o[8 * h + 6] * inv, o[8 * h + 7] * inv));
                 }
             }
-            if (live && ok && a.lse) a.lse[oh] = l == 0.0f ? -INFINITY : (m + log2f(l) - kPShift) * 0.693147180559945309f;
+            if (live && ok && a.lse) a.lse[oh] = row_lse(m, l, f);
         }
     }
     if (!ok) atomicOr(&g_prompt_fault, 1u);

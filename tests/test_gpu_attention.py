@@ -521,3 +521,86 @@ def test_query_starts_that_do_not_ascend(rmsq_gpu):
             torch.cuda.synchronize()
     assert (around[0] == 7).all() and (around[2] == 7).all() and around[1].isfinite().all()
     assert rq.take_fault_flags() == 0
+
+
+def make_exact_logits(dtype, D, q_lens, seq, *, order, seed):
+    """Keys that are c_j in every dimension and queries that are +-2^i in every
+    one, i spread over the type's range: every product and every partial sum
+    has at most 6 + log2(D) bits, so the logits are exact in fp32 and lie from
+    below 1 to 2^35 (fp16) or 2^120 (bf16) in units of log2.  c_j takes steps of at
+    least 1/15, ascending, descending or mixed along the sequence."""
+    c = make(q_lens, seq, 4, 2, D, 16, dtype, seed=seed)
+    c["k_gs"] = np.float32(1.0)
+    codes, scales = ref.tiles(c["cache"], 16, D)
+    codes[:, 0] = 0x22                                    # every element 1.0
+    steps = np.arange(0x18, 0x7f)                         # 2^-4 .. 448, eight steps an octave
+    rng = np.random.default_rng(seed)
+    for r, n in enumerate(seq):
+        pick = np.sort(rng.integers(0, len(steps), n))
+        pick = {"up": pick, "down": pick[::-1], "mixed": rng.permutation(pick)}[order]
+        for j in range(n):
+            scales[c["table"][r, j // 16], 0, :, j % 16] = steps[pick[j]]
+    top = {"fp16": 15, "bf16": 100}[dtype]
+    T = sum(q_lens)
+    i = np.rint(np.linspace(-8, top, T * 4)).reshape(T, 4, 1)
+    sign = np.where(rng.integers(0, 2, (T, 4, 1)) == 0, -1.0, 1.0)
+    c["q"], c["q64"] = ref.act(np.broadcast_to(sign * 2.0 ** i, (T, 4, D)), DT[dtype])
+    return c
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("dtype, D", [("fp16", 64), ("fp16", 128), ("bf16", 64), ("bf16", 128), ("fp16", 256)])
+@pytest.mark.parametrize("order", ["up", "down", "mixed"])
+@pytest.mark.parametrize("q_lens, seq", [([1] * 24, [300 + 16 * r for r in range(24)]), ([130, 70], [130, 900]),
+                                         ([3], [9000])])
+def test_large_logits(rmsq_gpu, dtype, D, order, q_lens, seq, variant):
+    """Finite inputs whose logits are far beyond 2^24: the largest one's weight
+    is 1, whatever their magnitude, and lse is finite.
+
+    The logits are exact here, so that beside the roundings of
+    tests/_serve_ref.py (output, f16 weights, sums) there are: the factor that
+    turns logits into powers of two, off by three roundings (2^-22 relative),
+    which changes a weight e^-g by g e^-g 2^-22 < 2^-23; the subtraction of the
+    maximum, which for maxima up to 2^10 may round by 2^-14 and again where the
+    maximum has moved since (2 ln2 2^-14 < 2^-13), and the exponential (2^-21).
+    lse: its own roundings (2^-22 relative), 2^-13 and the sums."""
+    c = make_exact_logits(dtype, D, q_lens, seq, order=order, seed=D)
+    out, lse = run(rmsq_gpu, c, variant=variant)
+    eps = torch.finfo(DT[dtype]).eps
+    w_out, w_lse, _, _ = ref.attention(c["q64"], c["cache"], c["table"], q_lens, seq, 1.0, float(c["v_gs"]), 16, D ** -0.5,
+                                       0, eps)
+    most = max(np.abs(ref.values(*ref.tiles(c["cache"], 16, D), float(c["v_gs"]))[:, 1]).max(), 0.0)
+    n = max(seq)
+    tol = eps / 2 * np.abs(w_out) + most * (2.0 ** -11 + 2.0 ** -12 + 2 * n * 2.0 ** -23 + n * 2.0 ** -34)
+    tol_lse = 2.0 ** -21 * np.abs(w_lse) + 2.0 ** -12 + n * 2.0 ** -23
+    o, s = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.isfinite(o).all() and np.isfinite(s).all()
+    assert (np.abs(o - w_out) <= tol).all(), np.abs(o - w_out).max()
+    assert (np.abs(s - w_lse) <= tol_lse).all(), (np.abs(s - w_lse) / tol_lse).max()
+    assert (np.abs(w_lse) > 2.0 ** 13).any()
+    assert rmsq_gpu.take_fault_flags() == 0
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("dtype, q", [("fp16", 6e4), ("fp16", -6e4), ("bf16", 1e20), ("bf16", -1e38)])
+@pytest.mark.parametrize("rows", [1, 9, 90])
+def test_one_dominant_key(rmsq_gpu, dtype, q, rows, variant):
+    """Every element of the dominant key at its largest and the others at
+    random: out is that key's value, off by its own rounding and the weight's
+    (which is 2^9 exactly) alone; lse its logit (bf16 queries of 1e38: beyond
+    fp32, +inf)."""
+    c = make([rows], [400], 8, 1, 128, 16, dtype, seed=65)
+    c["k_gs"] = np.float32(2.0)
+    codes, scales = ref.tiles(c["cache"], 16, 128)
+    codes[c["table"][0, 7], 0, :, 5], scales[c["table"][0, 7], 0, :, 5] = 0x77 if q > 0 else 0xff, 0x7e   # key 117
+    c["q"], c["q64"] = ref.act(np.full((rows, 8, 128), q), DT[dtype])
+    out, lse = run(rmsq_gpu, c, variant=variant)
+    eps = torch.finfo(DT[dtype]).eps
+    w_out, w_lse, _, _ = ref.attention(c["q64"], c["cache"], c["table"], [rows], [400], 2.0, float(c["v_gs"]), 16,
+                                       128 ** -0.5, 0, eps)
+    o, s = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert (np.abs(o - w_out) <= np.abs(w_out) * (eps / 2 + 2.0 ** -21)).all(), np.abs(o - w_out).max()
+    if abs(q) < 1e30:
+        assert (np.abs(s - w_lse) <= np.abs(w_lse) * (130 + 8) * 2.0 ** -23).all()
+    else:
+        assert (s == np.inf).all()
