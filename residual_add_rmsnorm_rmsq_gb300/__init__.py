@@ -4,9 +4,18 @@ Argument marshalling only: every step of the op runs in the library's CUDA
 kernels.  torch is used for device memory and streams.  The names follow the C
 ABI in ``include/rmsq.h``; if the built library is missing this module raises
 instead of computing anything another way.
+
+``stream`` (a torch stream or a raw handle; None: the current one) is where a
+call launches.  As with any work on a side stream, ordering it after the
+producers of its inputs and before the consumers of its outputs is the
+caller's.  What a call allocates itself, its missing outputs and its workspace,
+comes from the launching stream's memory, and the outputs are kept until the
+stream that was current at the call is done with them too: neither can meet
+memory that work on the other stream still uses.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import os
@@ -195,23 +204,58 @@ def _stream(stream, device: int = -1) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _on(stream):
+    """A context in which `stream` is the current one; None where it is already."""
+    if stream is None or not torch.cuda.is_initialized():
+        return None
+    if not hasattr(stream, "cuda_stream"):      # a handle; 0 and 1 are the default stream
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) > 1 else torch.cuda.default_stream()
+    if stream.cuda_stream == torch.cuda.current_stream(stream.device).cuda_stream:
+        return None
+    return torch.cuda.stream(stream)
+
+
+def _empty_on(stream, *size, **kwargs) -> torch.Tensor:
+    """torch.empty for a launch on `stream`: from that stream's memory.  The
+    current stream's may have been let go while work there still uses it (the
+    workspace of the call before, say), and nothing orders the launch after
+    that work.  The current stream may read the result, so the memory is kept
+    until it is done too."""
+    on = _on(stream)
+    if on is None:
+        return torch.empty(*size, **kwargs)
+    with on:
+        t = torch.empty(*size, **kwargs)
+    if t.is_cuda:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _empty_for(stream):
+    return torch.empty if stream is None else functools.partial(_empty_on, stream)
+
+
 def scales_like(mode: str, n_tokens: int, hidden: int, device) -> torch.Tensor | None:
     """An output tensor of the right shape and dtype for the scales of ``mode``
     (column-major with "+tma": [hidden/G, n_tokens rounded up to 16 bytes of
     scales]; uint8 with "+ue8m0")."""
+    return _scales_like(mode, n_tokens, hidden, device, torch.empty)
+
+
+def _scales_like(mode, n_tokens, hidden, device, empty):
     base, *opts = mode.split("+")
     if base == "fp8_static":
         return None
     if base == "nvfp4":
-        return torch.empty(n_tokens, hidden // 16, dtype=torch.uint8, device=device)
+        return empty(n_tokens, hidden // 16, dtype=torch.uint8, device=device)
     dt = torch.uint8 if "ue8m0" in opts else torch.float32
     if base == "fp8_per_token":
-        return torch.empty(n_tokens, dtype=dt, device=device)
+        return empty(n_tokens, dtype=dt, device=device)
     G = 128 if "128" in base else 64
     per16 = 16 if "ue8m0" in opts else 4
     cols = (n_tokens + per16 - 1) // per16 * per16 if "tma" in opts else n_tokens
     shape = (hidden // G, cols) if base.endswith("_col") else (n_tokens, hidden // G)
-    return torch.empty(shape, dtype=dt, device=device)
+    return empty(shape, dtype=dt, device=device)
 
 
 def fused_add_rmsnorm_quant(x: torch.Tensor, residual: torch.Tensor | None, weight: torch.Tensor,
@@ -230,7 +274,7 @@ def fused_add_rmsnorm_quant(x: torch.Tensor, residual: torch.Tensor | None, weig
     Returns (q, scales, residual_out).
     """
     vcode = _variant(variant)
-    L = load()
+    L, empty = load(), _empty_for(stream)
     n, H = x.shape
     if x.dtype not in DTYPES:
         raise TypeError(f"unsupported activation dtype {x.dtype}")
@@ -238,11 +282,12 @@ def fused_add_rmsnorm_quant(x: torch.Tensor, residual: torch.Tensor | None, weig
         if t is not None and not t.is_contiguous():
             raise ValueError("all tensors must be contiguous")
     if out_q is None:
-        out_q = torch.empty(n, H // 2 if mode == "nvfp4" else H, dtype=torch.uint8, device=x.device)
+        width = H // 2 if mode == "nvfp4" else H
+        out_q = empty(n, width, dtype=torch.uint8, device=x.device)
     if out_scales is None:
-        out_scales = scales_like(mode, n, H, x.device)
+        out_scales = _scales_like(mode, n, H, x.device, empty)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(residual)
+        residual_out = empty(residual.shape, dtype=residual.dtype, device=residual.device)
     st = L.rmsq_fused_add_rmsnorm_quant_ex(_p(x), _p(residual), _p(weight), ctypes.c_float(eps),
                                            mode_code(mode), _p(scale_in), _p(out_q), _p(out_scales),
                                            _p(residual_out), n, H, DTYPES[x.dtype], _stream(stream),
@@ -262,7 +307,7 @@ def allreduce_add_rmsnorm_quant(partials, residual: torch.Tensor | None, weight:
     """rmsq_allreduce_add_rmsnorm_quant: ``partials`` is a sequence of [n, H]
     tensors, one per rank (each readable by the current device), summed in
     rank order; then the fused op on the sum.  Returns (q, scales, residual_out)."""
-    L = load()
+    L, empty = load(), _empty_for(stream)
     parts = list(partials)
     if not 1 <= len(parts) <= MAX_ALLREDUCE_RANKS:
         raise ValueError(f"1 to {MAX_ALLREDUCE_RANKS} partial tensors")
@@ -277,11 +322,12 @@ def allreduce_add_rmsnorm_quant(partials, residual: torch.Tensor | None, weight:
         if t is not None and not t.is_contiguous():
             raise ValueError("all tensors must be contiguous")
     if out_q is None:
-        out_q = torch.empty(n, H // 2 if mode == "nvfp4" else H, dtype=torch.uint8, device=x.device)
+        width = H // 2 if mode == "nvfp4" else H
+        out_q = empty(n, width, dtype=torch.uint8, device=x.device)
     if out_scales is None:
-        out_scales = scales_like(mode, n, H, x.device)
+        out_scales = _scales_like(mode, n, H, x.device, empty)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(residual)
+        residual_out = empty(residual.shape, dtype=residual.dtype, device=residual.device)
     arr = (ctypes.c_void_p * len(parts))(*[t.data_ptr() for t in parts])
     st = L.rmsq_allreduce_add_rmsnorm_quant(arr, len(parts), _p(residual), _p(weight), ctypes.c_float(eps),
                                             mode_code(mode), _p(scale_in), _p(out_q), _p(out_scales),
@@ -307,7 +353,7 @@ def fused_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None, weight: to
                       y_out: torch.Tensor | None = None, residual_out: torch.Tensor | None = None, stream=None):
     """rmsq_fused_add_rmsnorm: the norm alone, y in the activation type.
     Returns (y, residual_out)."""
-    L = load()
+    L, empty = load(), _empty_for(stream)
     n, H = x.shape
     if x.dtype not in DTYPES:
         raise TypeError(f"unsupported activation dtype {x.dtype}")
@@ -315,9 +361,9 @@ def fused_add_rmsnorm(x: torch.Tensor, residual: torch.Tensor | None, weight: to
         if t is not None and not t.is_contiguous():
             raise ValueError("all tensors must be contiguous")
     if y_out is None:
-        y_out = torch.empty_like(x)
+        y_out = empty(x.shape, dtype=x.dtype, device=x.device)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(residual)
+        residual_out = empty(residual.shape, dtype=residual.dtype, device=residual.device)
     st = L.rmsq_fused_add_rmsnorm(_p(x), _p(residual), _p(weight), ctypes.c_float(eps), _p(y_out), _p(residual_out),
                                   n, H, DTYPES[x.dtype], _stream(stream))
     if st:
@@ -329,7 +375,7 @@ def quant(y: torch.Tensor, mode: str, scale_in: torch.Tensor | None = None, *, o
           out_scales: torch.Tensor | None = None, stream=None):
     """rmsq_quant: the quantisation of a [n, H] activation-type tensor.
     Returns (q, scales)."""
-    L = load()
+    L, empty = load(), _empty_for(stream)
     n, H = y.shape
     if y.dtype not in DTYPES:
         raise TypeError(f"unsupported activation dtype {y.dtype}")
@@ -337,9 +383,10 @@ def quant(y: torch.Tensor, mode: str, scale_in: torch.Tensor | None = None, *, o
         if t is not None and not t.is_contiguous():
             raise ValueError("all tensors must be contiguous")
     if out_q is None:
-        out_q = torch.empty(n, H // 2 if mode == "nvfp4" else H, dtype=torch.uint8, device=y.device)
+        width = H // 2 if mode == "nvfp4" else H
+        out_q = empty(n, width, dtype=torch.uint8, device=y.device)
     if out_scales is None:
-        out_scales = scales_like(mode, n, H, y.device)
+        out_scales = _scales_like(mode, n, H, y.device, empty)
     st = L.rmsq_quant(_p(y), mode_code(mode), _p(scale_in), _p(out_q), _p(out_scales), n, H, DTYPES[y.dtype],
                       _stream(stream))
     if st:
@@ -439,21 +486,21 @@ def build_slot_map(context_lens: torch.Tensor, query_lens: torch.Tensor, block_t
     [max_tokens], query_start [R + 1], seq_lens [R], num_free_out [1],
     status [1]); status holds SLOT_* bits, 0 when the pages were assigned.
     """
-    L = load()
+    L, empty = load(), _empty_for(stream)
     R, width = block_table.shape
     dev, i = block_table.device, block_table.get_device()
     if slot_map is None:
-        slot_map = torch.empty(max(max_tokens, 0), dtype=_I64, device=dev)
+        slot_map = empty(max(max_tokens, 0), dtype=_I64, device=dev)
     if positions is None:
-        positions = torch.empty_like(slot_map)
+        positions = empty(max(max_tokens, 0), dtype=_I64, device=dev)
     if query_start is None:
-        query_start = torch.empty(R + 1, dtype=_I32, device=dev)
+        query_start = empty(R + 1, dtype=_I32, device=dev)
     if seq_lens is None:
-        seq_lens = torch.empty_like(context_lens)
+        seq_lens = empty(R, dtype=_I32, device=dev)
     if num_free_out is None:
-        num_free_out = torch.empty_like(num_free)
+        num_free_out = empty(1, dtype=_I32, device=dev)
     if status is None:
-        status = torch.empty_like(num_free)
+        status = empty(1, dtype=_I32, device=dev)
     per_r, one, per_t, capacity = (R,), (1,), (max_tokens,), free_pages.shape
     if not (_is_current(i) and _fits(context_lens, _I32, i, per_r) and _fits(query_lens, _I32, i, per_r) and
             _fits(block_table, _I32, i, (R, width)) and _fits(free_pages, _I32, i, capacity) and
@@ -535,7 +582,7 @@ def kv_cache_load_nvfp4(cache: torch.Tensor, slot_map: torch.Tensor, k_global_sc
     """rmsq_kv_cache_load_nvfp4: the tokens at slot_map (int64 [n]) as two
     [n, kv heads, D] tensors of `dtype`; zeros for a slot outside the cache.
     Missing outputs are allocated.  Returns (k, v)."""
-    L = load()
+    L, empty = load(), _empty_for(stream)
     if dtype not in DTYPES:
         raise TypeError(f"unsupported activation dtype {dtype}")
     if cache.dim() != 4:
@@ -544,11 +591,11 @@ def kv_cache_load_nvfp4(cache: torch.Tensor, slot_map: torch.Tensor, k_global_sc
     shape = (n, h, head_dim)
     ks = vs = h * head_dim
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=cache.device)
+        k_out = empty(shape, dtype=dtype, device=cache.device)
     else:
         ks = _token_rows("k_out", k_out)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=cache.device)
+        v_out = empty(shape, dtype=dtype, device=cache.device)
     else:
         vs = _token_rows("v_out", v_out)
     i, pages = cache.get_device(), cache.shape[0]
@@ -595,7 +642,7 @@ def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: tor
     (out, lse [tokens, heads] fp32) with return_lse or a given lse.
     """
     vcode = _variant(variant)
-    L = load()
+    L, empty = load(), _empty_for(stream)
     dt = _act_types(q)
     qs = _token_rows("q", q)
     n, heads, d = q.shape
@@ -603,13 +650,12 @@ def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: tor
         raise ValueError("cache must be [pages, 2, kv heads, bytes of a tile], block_table [requests, width]")
     kv, (R, width) = cache.shape[2], block_table.shape
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = empty(q.shape, dtype=dt, device=q.device)
     if lse is None and return_lse:
-        lse = torch.empty((n, heads), dtype=_F32, device=q.device)
+        lse = empty((n, heads), dtype=_F32, device=q.device)
     if workspace is None:
-        workspace = torch.empty(paged_attention_workspace_bytes(n, R, heads, kv, d), dtype=_U8, device=q.device)
-        if stream is not None and q.is_cuda:    # it is let go on return, perhaps before that stream is done with it
-            workspace.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+        size = paged_attention_workspace_bytes(n, R, heads, kv, d)
+        workspace = empty(size, dtype=_U8, device=q.device)
     i, pages, size = q.get_device(), cache.shape[0], workspace.numel()
     if not (_is_current(i) and _fits(cache, _U8, i, kv_cache_shape(pages, kv, d, page_size)) and
             _fits(block_table, _I32, i, (R, width)) and _fits(query_start, _I32, i, (R + 1,)) and
@@ -655,7 +701,7 @@ def fp8_block_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, mode: str, b
     options); b_codes [n, k] (uint8 or float8_e4m3fn) with b_scales fp32
     [ceil(n / 128), k / 128].  out is bf16 or fp16, allocated if missing.
     """
-    L = load()
+    L, empty = load(), _empty_for(stream)
     if dtype not in DTYPES:
         raise TypeError(f"unsupported activation dtype {dtype}")
     if a_codes.dtype not in _CODE_TYPES or b_codes.dtype not in _CODE_TYPES:
@@ -668,7 +714,7 @@ def fp8_block_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, mode: str, b
     (m, k), n = a_codes.shape, b_codes.shape[0]
     st_dtype = _U8 if code & OPTIONS["ue8m0"] else _F32
     if out is None:
-        out = torch.empty((m, n), dtype=dtype, device=a_codes.device)
+        out = empty((m, n), dtype=dtype, device=a_codes.device)
     if code & 15 == MODES["fp8_group128_row"]:
         shape = (m, k // 128)
     else:
@@ -698,7 +744,7 @@ def silu_mul_quant(gate_up: torch.Tensor, mode: str, scale_in: torch.Tensor | No
     """rmsq_silu_mul_quant on torch CUDA tensors: gate_up [n, 2d] (gate | up),
     scale_in a one-element fp32 device tensor (FP8 static scale / NVFP4 global
     scale).  Missing outputs are allocated.  Returns (q, scales)."""
-    L = load()
+    L, empty = load(), _empty_for(stream)
     n, d2 = gate_up.shape
     if gate_up.dtype not in DTYPES:
         raise TypeError(f"unsupported activation dtype {gate_up.dtype}")
@@ -709,9 +755,10 @@ def silu_mul_quant(gate_up: torch.Tensor, mode: str, scale_in: torch.Tensor | No
         if t is not None and not t.is_contiguous():
             raise ValueError("all tensors must be contiguous")
     if out_q is None:
-        out_q = torch.empty(n, d // 2 if mode == "nvfp4" else d, dtype=torch.uint8, device=gate_up.device)
+        width = d // 2 if mode == "nvfp4" else d
+        out_q = empty(n, width, dtype=torch.uint8, device=gate_up.device)
     if out_scales is None:
-        out_scales = scales_like(mode, n, d, gate_up.device)
+        out_scales = _scales_like(mode, n, d, gate_up.device, empty)
     st = L.rmsq_silu_mul_quant(_p(gate_up), mode_code(mode), _p(scale_in), _p(out_q), _p(out_scales), n, d,
                                DTYPES[gate_up.dtype], _stream(stream))
     if st:
@@ -735,7 +782,7 @@ def fused_add_rmsnorm_nvfp4_dynamic(x: torch.Tensor, residual: torch.Tensor | No
     gs = 2688 / amax(all y) computed on the device.  Missing outputs and the
     workspace are allocated.  Returns (q, block_scales, global_scale, residual_out)."""
     vcode = _variant(variant)
-    L = load()
+    L, empty = load(), _empty_for(stream)
     n, H = x.shape
     if x.dtype not in DTYPES:
         raise TypeError(f"unsupported activation dtype {x.dtype}")
@@ -744,16 +791,16 @@ def fused_add_rmsnorm_nvfp4_dynamic(x: torch.Tensor, residual: torch.Tensor | No
             raise ValueError("all tensors must be contiguous")
     dev = x.device
     if out_q is None:
-        out_q = torch.empty(n, H // 2, dtype=torch.uint8, device=dev)
+        out_q = empty(n, H // 2, dtype=torch.uint8, device=dev)
     if out_scales is None:
-        out_scales = torch.empty(n, H // 16, dtype=torch.uint8, device=dev)
+        out_scales = empty(n, H // 16, dtype=torch.uint8, device=dev)
     if out_global_scale is None:
-        out_global_scale = torch.empty(1, dtype=torch.float32, device=dev)
+        out_global_scale = empty(1, dtype=torch.float32, device=dev)
     if residual is not None and residual_out is None:
-        residual_out = torch.empty_like(residual)
+        residual_out = empty(residual.shape, dtype=residual.dtype, device=residual.device)
     ws_bytes = nvfp4_dynamic_workspace_bytes(n)
     if workspace is None:
-        workspace = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
+        workspace = empty(max(ws_bytes, 16), dtype=torch.uint8, device=dev)
     st = L.rmsq_fused_add_rmsnorm_nvfp4_dynamic(
         _p(x), _p(residual), _p(weight), ctypes.c_float(eps), _p(out_q), _p(out_scales),
         _p(out_global_scale), _p(residual_out), _p(workspace),
@@ -805,10 +852,11 @@ def take_fault_flags() -> int:
 def debug_activation(kind: str, values: torch.Tensor, up: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The library's e^x ("exp"; "exp_mid": the steps used for |x| <= 87),
     silu ("silu") or silu(g) * u ("silu_mul") on fp32 CUDA tensors, elementwise."""
-    L = load()
-    v = values.contiguous().float()
-    u = None if up is None else up.contiguous().float()
-    out = torch.empty(v.shape, dtype=torch.float32, device=v.device)
+    L, empty = load(), _empty_for(stream)
+    with _on(stream) or contextlib.nullcontext():
+        v = values.contiguous().float()
+        u = None if up is None else up.contiguous().float()
+    out = empty(v.shape, dtype=torch.float32, device=v.device)
     st = L.rmsq_debug_activation({"exp": 0, "silu": 1, "silu_mul": 2, "exp_mid": 3}[kind], _p(v), _p(u), _p(out), v.numel(),
                                  _stream(stream))
     if st:
@@ -828,9 +876,10 @@ def debug_bounded_wait(limit_ns: int) -> int:
 def debug_convert(kind: str, values: torch.Tensor, stream=None) -> torch.Tensor:
     """The library's E4M3 ("e4m3") or E2M1 ("e2m1", low nibble) conversion of a
     fp32 CUDA tensor."""
-    L = load()
-    v = values.contiguous().float()
-    out = torch.empty(v.shape, dtype=torch.uint8, device=v.device)
+    L, empty = load(), _empty_for(stream)
+    with _on(stream) or contextlib.nullcontext():
+        v = values.contiguous().float()
+    out = empty(v.shape, dtype=torch.uint8, device=v.device)
     st = L.rmsq_debug_convert({"e4m3": 0, "e2m1": 1}[kind], _p(v), _p(out), v.numel(), _stream(stream))
     if st:
         raise RmsqError(st, "rmsq_debug_convert")

@@ -39,3 +39,45 @@ def test_streams_of_all_kernels_at_once(rmsq_gpu):
         for g in gs:
             assert torch.equal(w, g)
     assert rq.take_fault_flags() == 0
+
+
+def test_calls_on_the_current_and_on_another_stream_in_turn(rmsq_gpu):
+    """Calls that allocate their own workspace and outputs, in turn on the
+    current stream and on others, next to memory that the current stream has let
+    go while its work is still to come: all give what one call alone gives, and
+    results that are read on the current stream and let go at once stay whole
+    until then."""
+    rq = rmsq_gpu
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    c = attn.make([1] * 16, [3000] * 16, 32, 8, 128, 16, "bf16", seed=51)
+    start = dev(np.arange(17, dtype=np.int32))
+    g1, g2 = torch.tensor([c["k_gs"]], device="cuda"), torch.tensor([c["v_gs"]], device="cuda")
+    args = [c["q"].cuda(), dev(c["cache"]), dev(c["table"]), start, dev(np.array(c["seq"], np.int32)), g1, g2, 16]
+    slots = torch.arange(256, device="cuda")
+    a, _, given, b, sb = mm.make(33, 2048, 1024, "fp8_group128_row", seed=3)
+    ops = [dev(x) for x in (a, given, b, sb)]
+    x, w = torch.randn(256, 2048, device="cuda").bfloat16(), torch.ones(2048, device="cuda").bfloat16()
+    calls = [lambda s: rq.paged_attention_nvfp4(*args, return_lse=True, stream=s),
+             lambda s: rq.kv_cache_load_nvfp4(args[1], slots, g1, g2, 128, 16, stream=s),
+             lambda s: (rq.fp8_block_matmul(ops[0], ops[1], "fp8_group128_row", ops[2], ops[3], stream=s),),
+             lambda s: rq.fused_add_rmsnorm_nvfp4_dynamic(x, x, w, 1e-6, stream=s)]
+    want = [[t.clone() for t in f(None)] for f in calls]
+    torch.cuda.synchronize()
+    here = torch.cuda.current_stream()
+    side, handle = torch.cuda.Stream(), torch.cuda.Stream()
+    wrong = torch.zeros(1, dtype=torch.int64, device="cuda")
+    torch.cuda.synchronize()
+    for turn in range(40):
+        torch.cuda._sleep(100_000)          # what follows on the current stream is late
+        for size in (1 << 16, 1 << 20, 21 << 20):
+            torch.full((size,), 0xff, dtype=torch.uint8, device="cuda")     # let go before it is filled
+        for f, ts in zip(calls, want):
+            for s in ((side, None), (handle.cuda_stream, None), (None, side))[turn % 3]:
+                got = f(s)
+                if s is not None:
+                    here.wait_stream(side if s is side else handle)
+                for g, t in zip(got, ts):
+                    wrong += (g.view(torch.uint8) != t.view(torch.uint8)).any()
+                del got, g
+    torch.cuda.synchronize()
+    assert wrong.item() == 0 and rq.take_fault_flags() == 0

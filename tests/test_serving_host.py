@@ -225,3 +225,72 @@ def test_binding_refusals(L):
     with pytest.raises(rq.RmsqError) as e:
         rq.build_slot_map(i(3), i(3), i(3, 4), i(9), i(1), 24, 8, stream=0)
     assert e.value.status == rq.ERR_UNSUPPORTED_SHAPE
+
+
+class _FakeStream:
+    device = None
+
+    def __init__(self, handle):
+        self.cuda_stream = handle
+
+
+def _binding_calls():
+    """Every binding that allocates, with none of its outputs given."""
+    z, u8 = torch.zeros, torch.uint8
+    i = lambda *s: z(*s, dtype=I32)  # noqa: E731
+    x, w, gs = z(4, 128).bfloat16(), z(128).bfloat16(), torch.ones(1)
+    cache = z(rq.kv_cache_shape(10, 2, 128, 16), dtype=u8)
+    args = _attn_args()
+    args.pop("stream")
+    return {
+        "fused_add_rmsnorm_quant": lambda s: rq.fused_add_rmsnorm_quant(x, x, w, 1e-6, "fp8_per_token", stream=s),
+        "allreduce_add_rmsnorm_quant": lambda s: rq.allreduce_add_rmsnorm_quant([x, x], x, w, 1e-6, "fp8_per_token", stream=s),
+        "fused_add_rmsnorm": lambda s: rq.fused_add_rmsnorm(x, x, w, 1e-6, stream=s),
+        "quant": lambda s: rq.quant(x, "fp8_per_token", stream=s),
+        "silu_mul_quant": lambda s: rq.silu_mul_quant(x, "fp8_group64_row", stream=s),
+        "fused_add_rmsnorm_nvfp4_dynamic": lambda s: rq.fused_add_rmsnorm_nvfp4_dynamic(x, x, w, 1e-6, stream=s),
+        "build_slot_map": lambda s: rq.build_slot_map(i(3), i(3), i(3, 4), i(9), i(1), 16, 8, stream=s),
+        "kv_cache_load_nvfp4": lambda s: rq.kv_cache_load_nvfp4(cache, torch.arange(4), gs, gs, 128, 16, stream=s),
+        "paged_attention_nvfp4": lambda s: rq.paged_attention_nvfp4(**args, return_lse=True, stream=s),
+        "fp8_block_matmul": lambda s: rq.fp8_block_matmul(z(5, 256, dtype=u8), z(5, 2), "fp8_group128_row",
+                                                          z(200, 256, dtype=u8), z(2, 2), stream=s),
+        "debug_activation": lambda s: rq.debug_activation("silu_mul", z(4), z(4), s),
+        "debug_convert": lambda s: rq.debug_convert("e4m3", z(4), s),
+    }
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="a fake of the streams")
+@pytest.mark.parametrize("name", sorted(_binding_calls()))
+def test_what_a_call_allocates_comes_from_the_launching_stream(monkeypatch, name):
+    """With a stream that is not the current one, every output and workspace a
+    binding allocates is taken while that stream is current; with the current
+    one, nothing is switched."""
+    import contextlib
+    call = _binding_calls()[name]
+    here, side = _FakeStream(0x100), _FakeStream(0x200)
+    current, taken = [here], []
+
+    @contextlib.contextmanager
+    def switched(s):
+        current.append(s)
+        yield
+        current.pop()
+
+    class Lib:
+        def __getattr__(self, fn):
+            return lambda *a: 64 if fn.endswith("workspace_bytes") else taken.append((fn, a)) or 0
+
+    monkeypatch.setattr(rq, "_lib", Lib())
+    monkeypatch.setattr(rq, "_raw_stream", None)
+    monkeypatch.setattr(torch.cuda, "is_initialized", lambda: True)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: current[-1])
+    monkeypatch.setattr(torch.cuda, "stream", switched)
+    for make in ("empty", "empty_like"):
+        plain = getattr(torch, make)
+        monkeypatch.setattr(torch, make, lambda *a, f=plain, **k: taken.append(("empty", current[-1])) or f(*a, **k))
+    for given, owner in ((side, side), (here, here), (None, here)):
+        taken.clear()
+        call(given)
+        made = [s for what, s in taken if what == "empty"]
+        assert made and all(s is owner for s in made), name
+        assert taken[-1][0].startswith("rmsq_") and current == [here]
