@@ -581,6 +581,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
             for (int c = 0; c < D / 16; ++c) {
                 float o[16];
                 if (steps > 0) {
+                    __syncwarp();   // the lanes come from the stores below, which not all of them make
                     tmem_ld16(o, o_at + c * 16);
                     tmem_wait(o);
                 } else {

@@ -77,7 +77,10 @@ __device__ __forceinline__ void tmem_wait(float (&r)[16]) {
                  :: "memory");
 }
 
+// Barriers that a warp has to reach as one: its lanes are gathered here, whatever
+// branch or loop they come from.
 __device__ __forceinline__ void named_sync(int id, int threads) {
+    __syncwarp();
     asm volatile("bar.sync %0, %1;" :: "r"(id), "r"(threads) : "memory");
 }
 
@@ -127,6 +130,7 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
 }
 
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();       // as in named_sync
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 

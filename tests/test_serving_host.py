@@ -294,3 +294,23 @@ def test_what_a_call_allocates_comes_from_the_launching_stream(monkeypatch, name
         made = [s for what, s in taken if what == "empty"]
         assert made and all(s is owner for s in made), name
         assert taken[-1][0].startswith("rmsq_") and current == [here]
+
+
+def _function(source, name):
+    at = source.index(f" {name}(")
+    return source[at: source.index("\n}", at)]
+
+
+def test_barriers_that_want_a_whole_warp_gather_it():
+    """bar.sync and barrier.cluster...aligned are undefined for a warp that
+    arrives in pieces, and their callers come from loops whose lanes leave at
+    different turns (b's last block of columns, a few scales)."""
+    import os
+    csrc = os.path.join(os.path.dirname(rq.__file__), "csrc")
+    tc = open(os.path.join(csrc, "rmsq_tc.cuh")).read()
+    for name, barrier in (("named_sync", "bar.sync"), ("cluster_sync", "barrier.cluster.arrive")):
+        body = _function(tc, name)
+        assert body.index("__syncwarp();") < body.index(barrier), name
+    sources = {f: open(os.path.join(csrc, f)).read() for f in os.listdir(csrc) if f.endswith((".cu", ".cuh"))}
+    assert [f for f, s in sources.items() if "barrier.cluster" in s] == ["rmsq_tc.cuh"]
+    assert sum(s.count('"bar.sync') for s in sources.values()) == 1
