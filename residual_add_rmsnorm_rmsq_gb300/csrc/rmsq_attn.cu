@@ -113,7 +113,7 @@ cudaError_t launch_attn(AttnArgs a, int head_dim, int64_t max_tiles, int variant
 int attn_shape(int64_t tokens, int64_t requests, int heads, int kv_heads, int head_dim) {
     if (tokens < 0 || requests < 0 || heads <= 0 || kv_heads <= 0) return RMSQ_ERR_INVALID_ARG;
     if (heads % kv_heads != 0 || heads > 4096 || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
-        requests > RMSQ_MAX_REQUESTS || tokens * heads > INT32_MAX)
+        requests > RMSQ_MAX_REQUESTS || tokens > INT32_MAX / heads)
         return RMSQ_ERR_UNSUPPORTED_SHAPE;
     return RMSQ_OK;
 }

@@ -314,3 +314,9 @@ def test_barriers_that_want_a_whole_warp_gather_it():
     sources = {f: open(os.path.join(csrc, f)).read() for f in os.listdir(csrc) if f.endswith((".cu", ".cuh"))}
     assert [f for f, s in sources.items() if "barrier.cluster" in s] == ["rmsq_tc.cuh"]
     assert sum(s.count('"bar.sync') for s in sources.values()) == 1
+
+
+@pytest.mark.parametrize("T, h", [(1 << 60, 16), (1 << 61, 8), ((1 << 63) - 1, 2), (1 << 58, 64)])
+def test_attention_sizes_whose_product_wraps_are_refused(L, T, h):
+    assert attn(L, T=T, h=h, kv=1, qs=1 << 16) == rq.ERR_UNSUPPORTED_SHAPE
+    assert rq.paged_attention_workspace_bytes(T, 3, h, 1, 128) == 0
