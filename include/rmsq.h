@@ -464,6 +464,18 @@ int rmsq_paged_attention_nvfp4(const void *q, int64_t q_stride, const void *kv_c
                                int64_t num_requests, int num_heads, int num_kv_heads, int head_dim, int dtype,
                                void *stream, int variant);
 
+/* rmsq_paged_attention_nvfp4 told the most queries any request has: max_query
+ * (0: not known).  It is for AUTO's choice alone, which cannot see the lengths:
+ * with it no step without a prompt pays for the kernel of prompts.  A request
+ * that is longer all the same gets its result too. */
+int rmsq_paged_attention_nvfp4_ex(const void *q, int64_t q_stride, const void *kv_cache, int64_t num_pages,
+                                  int64_t page_size, const int32_t *block_table, int64_t table_width,
+                                  const int32_t *query_start, const int32_t *seq_lens, const float *k_global_scale,
+                                  const float *v_global_scale, float softmax_scale, int64_t window, void *out,
+                                  float *lse, void *workspace, size_t workspace_bytes, int64_t n_tokens,
+                                  int64_t num_requests, int num_heads, int num_kv_heads, int head_dim, int dtype,
+                                  void *stream, int variant, int64_t max_query);
+
 /* Bytes of workspace rmsq_paged_attention_nvfp4 needs (0 for arguments it
  * refuses; else the same for every number of tokens and requests, 10 to 21
  * MB: one workspace serves the calls of a program that follow one another). */

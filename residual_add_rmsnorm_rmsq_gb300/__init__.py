@@ -73,7 +73,8 @@ EXPORTS = ("rmsq_fused_add_rmsnorm_quant", "rmsq_fused_add_rmsnorm_quant_ex",
            "rmsq_fused_add_rmsnorm", "rmsq_quant", "rmsq_qk_norm_rope", "rmsq_qk_norm_rope_ex",
            "rmsq_allreduce_add_rmsnorm_quant",
            "rmsq_build_slot_map", "rmsq_kv_cache_store_nvfp4", "rmsq_kv_cache_load_nvfp4",
-           "rmsq_paged_attention_nvfp4", "rmsq_paged_attention_workspace_bytes", "rmsq_fp8_block_matmul",
+           "rmsq_paged_attention_nvfp4", "rmsq_paged_attention_nvfp4_ex", "rmsq_paged_attention_workspace_bytes",
+           "rmsq_fp8_block_matmul",
            "rmsq_set_pipeline_config", "rmsq_set_programmatic_launch", "rmsq_take_fault_flags",
            "rmsq_query_sizes", "rmsq_query_launch", "rmsq_debug_convert", "rmsq_debug_activation", "rmsq_debug_bounded_wait",
            "rmsq_status_string", "rmsq_last_cuda_error", "rmsq_version")
@@ -133,6 +134,8 @@ def load(path: str | None = None):
         L.rmsq_paged_attention_nvfp4.argtypes = [vp, i64, vp, i64, i64, vp, i64, vp, vp, vp, vp, f32, i64, vp, vp, vp,
                                                  ctypes.c_size_t, i64, i64, ci, ci, ci, ci, vp, ci]
         L.rmsq_paged_attention_nvfp4.restype = ci
+        L.rmsq_paged_attention_nvfp4_ex.argtypes = L.rmsq_paged_attention_nvfp4.argtypes + [i64]
+        L.rmsq_paged_attention_nvfp4_ex.restype = ci
         L.rmsq_paged_attention_workspace_bytes.argtypes = [i64, i64, ci, ci, ci]
         L.rmsq_paged_attention_workspace_bytes.restype = ctypes.c_size_t
         L.rmsq_fp8_block_matmul.argtypes = [vp, vp, ci, vp, vp, vp, i64, i64, i64, ci, vp]
@@ -629,8 +632,9 @@ def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: tor
                           seq_lens: torch.Tensor, k_global_scale: torch.Tensor, v_global_scale: torch.Tensor,
                           page_size: int, softmax_scale: float | None = None, *, window: int = 0,
                           return_lse: bool = False, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
-                          workspace: torch.Tensor | None = None, stream=None, variant: str = "auto"):
-    """rmsq_paged_attention_nvfp4: causal attention of q [tokens, heads, D]
+                          workspace: torch.Tensor | None = None, stream=None, variant: str = "auto",
+                          max_query: int = 0):
+    """rmsq_paged_attention_nvfp4_ex: causal attention of q [tokens, heads, D]
     (token stride free) over the paged NVFP4 cache.
 
     block_table: int32 [R, width]; query_start: int32 [R + 1]; seq_lens: int32
@@ -638,7 +642,8 @@ def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: tor
     softmax_scale: 1 / sqrt(D) by default; window > 0 limits a query to its
     last `window` keys.  Missing outputs and the workspace are allocated (rows
     of q behind query_start[R] are not computed).  variant: "auto", "direct"
-    (few queries) or "pipelined" (prompts).  Returns out [tokens, heads, D], or
+    (few queries) or "pipelined" (prompts).  max_query: the most queries any
+    request has, if that is known; it lets "auto" choose better.  Returns out [tokens, heads, D], or
     (out, lse [tokens, heads] fp32) with return_lse or a given lse.
     """
     vcode = _variant(variant)
@@ -678,11 +683,11 @@ def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: tor
         _check_global_scales(k_global_scale, v_global_scale)
     if softmax_scale is None:
         softmax_scale = d ** -0.5
-    st = L.rmsq_paged_attention_nvfp4(q.data_ptr(), qs, cache.data_ptr(), pages, page_size, block_table.data_ptr(), width,
-                                      query_start.data_ptr(), seq_lens.data_ptr(), k_global_scale.data_ptr(),
-                                      v_global_scale.data_ptr(), softmax_scale, window, out.data_ptr(), _p(lse),
-                                      workspace.data_ptr(), size, n, R, heads, kv, d, DTYPES[dt], _stream(stream, i),
-                                      vcode)
+    st = L.rmsq_paged_attention_nvfp4_ex(q.data_ptr(), qs, cache.data_ptr(), pages, page_size, block_table.data_ptr(), width,
+                                         query_start.data_ptr(), seq_lens.data_ptr(), k_global_scale.data_ptr(),
+                                         v_global_scale.data_ptr(), softmax_scale, window, out.data_ptr(), _p(lse),
+                                         workspace.data_ptr(), size, n, R, heads, kv, d, DTYPES[dt], _stream(stream, i),
+                                         vcode, max_query)
     if st:
         raise RmsqError(st, "rmsq_paged_attention_nvfp4")
     return out if lse is None else (out, lse)

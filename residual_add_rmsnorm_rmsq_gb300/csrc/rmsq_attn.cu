@@ -85,16 +85,27 @@ cudaError_t launch_prompt(AttnArgs a, cudaStream_t stream) {
 // queries of 16 x 8 heads on 100000 keys 126 and 633 us, 64 of 8 x 8 heads 594
 // and 966, 256 of them 1925 and 805; 8 requests of 50 queries (8 x 4 heads) on
 // 2000 keys 72 and 43; 4 of 200 (4 x 8) on 500 keys 72 and 24.
+//
+// It is not launched where no request can be its: the caller's bound on the
+// queries of a request says so, or, without one, that there are no more than one
+// token per request and the rows of one prompt (requests without queries count
+// as having one: only the time is lost if a longer one is among them).  Its
+// empty CTAs are not free: 260 and 1000 decodes of 4 x 8 heads on 1000 keys took
+// 77 and 261 us behind them, 73 and 253 without, 1000 requests of four queries
+// on 200 keys 273 and 243.
 template <class E>
-cudaError_t launch_attn(AttnArgs a, int head_dim, int64_t max_tiles, int variant, cudaStream_t stream) {
+cudaError_t launch_attn(AttnArgs a, int head_dim, int64_t max_query, int64_t max_tiles, int variant, cudaStream_t stream) {
     cudaError_t err;
     const int sms = sm_count(&err);
     if (err != cudaSuccess) return err;
-    const int64_t rows = static_cast<int64_t>(a.tokens) * a.group;
+    const int64_t tokens = max_query > 0 && max_query < a.tokens / a.requests ? max_query * a.requests : a.tokens;
+    const int64_t rows = tokens * a.group;
     const int64_t items = (rows / 256 + 1) * a.kv_heads;
     const bool sooner = 1.1 * static_cast<double>(rows * a.kv_heads) / (16.0 * 3.0 * sms) > 1.25 * static_cast<double>((items + sms - 1) / sms);
-    // (no request can have more than kPromptRows rows if all together have not)
-    const bool prompt = head_dim <= 128 && rows > kPromptRows && variant != kVariantDirect &&
+    const int64_t rest = a.tokens >= a.requests ? a.tokens - a.requests + 1 : 1;    // left for one request
+    const int64_t longest = max_query > 0 ? (max_query < a.tokens ? max_query : a.tokens)
+                            : variant == kVariantPipelined ? a.tokens : rest;
+    const bool prompt = head_dim <= 128 && longest * a.group > kPromptRows && variant != kVariantDirect &&
                         (variant == kVariantPipelined || sooner);
     // (a single request is the prompt kernel's whatever its length)
     a.most_rows = !prompt ? INT32_MAX : a.requests == 1 ? 0 : kPromptRows;
@@ -137,6 +148,19 @@ int rmsq_paged_attention_nvfp4(const void* q, int64_t q_stride, const void* kv_c
                                float softmax_scale, int64_t window, void* out, float* lse, void* workspace,
                                size_t workspace_bytes, int64_t n_tokens, int64_t num_requests, int num_heads,
                                int num_kv_heads, int head_dim, int dtype, void* stream, int variant) {
+    return rmsq_paged_attention_nvfp4_ex(q, q_stride, kv_cache, num_pages, page_size, block_table, table_width, query_start,
+                                         seq_lens, k_global_scale, v_global_scale, softmax_scale, window, out, lse, workspace,
+                                         workspace_bytes, n_tokens, num_requests, num_heads, num_kv_heads, head_dim, dtype,
+                                         stream, variant, 0);
+}
+
+int rmsq_paged_attention_nvfp4_ex(const void* q, int64_t q_stride, const void* kv_cache, int64_t num_pages,
+                                  int64_t page_size, const int32_t* block_table, int64_t table_width,
+                                  const int32_t* query_start, const int32_t* seq_lens, const float* k_global_scale,
+                                  const float* v_global_scale, float softmax_scale, int64_t window, void* out, float* lse,
+                                  void* workspace, size_t workspace_bytes, int64_t n_tokens, int64_t num_requests,
+                                  int num_heads, int num_kv_heads, int head_dim, int dtype, void* stream, int variant,
+                                  int64_t max_query) {
     using rmsq_abi::aligned;
     using rmsq_abi::overlaps;
     using rmsq_abi::Span;
@@ -146,7 +170,8 @@ int rmsq_paged_attention_nvfp4(const void* q, int64_t q_stride, const void* kv_c
         return RMSQ_ERR_INVALID_ARG;
     int st = rmsq::attn_shape(n_tokens, num_requests, num_heads, num_kv_heads, head_dim);
     if (st != RMSQ_OK) return st;
-    if (!std::isfinite(softmax_scale) || softmax_scale <= 0.0f || window < 0 || num_pages < 0 || table_width < 0)
+    if (!std::isfinite(softmax_scale) || softmax_scale <= 0.0f || window < 0 || num_pages < 0 || table_width < 0 ||
+        max_query < 0)
         return RMSQ_ERR_INVALID_ARG;
     int shift = -1;
     for (int s = 4; s <= 8; ++s)
@@ -212,8 +237,8 @@ int rmsq_paged_attention_nvfp4(const void* q, int64_t q_stride, const void* kv_c
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int v = variant == RMSQ_VARIANT_DIRECT ? rmsq::kVariantDirect
                   : variant == RMSQ_VARIANT_PIPELINED ? rmsq::kVariantPipelined : rmsq::kVariantAuto;
-    const cudaError_t e = dtype == RMSQ_BF16 ? rmsq::launch_attn<rmsq::Bf16T>(a, head_dim, max_tiles, v, s)
-                                             : rmsq::launch_attn<rmsq::Fp16T>(a, head_dim, max_tiles, v, s);
+    const cudaError_t e = dtype == RMSQ_BF16 ? rmsq::launch_attn<rmsq::Bf16T>(a, head_dim, max_query, max_tiles, v, s)
+                                             : rmsq::launch_attn<rmsq::Fp16T>(a, head_dim, max_query, max_tiles, v, s);
     return e == cudaSuccess ? RMSQ_OK : rmsq_abi::fail_cuda(e);
 }
 

@@ -604,3 +604,44 @@ def test_one_dominant_key(rmsq_gpu, dtype, q, rows, variant):
         assert (np.abs(s - w_lse) <= np.abs(w_lse) * (130 + 8) * 2.0 ** -23).all()
     else:
         assert (s == np.inf).all()
+
+
+def launches(rq, c, **kw):
+    """Kernels that a call launches: the nodes of its graph."""
+    import ctypes
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    start = np.concatenate([[0], np.cumsum(c["q_lens"])]).astype(np.int32)
+    one = torch.ones(1, device="cuda")
+    args = [c["q"].cuda(), dev(c["cache"]), dev(c["table"]), dev(start), dev(np.array(c["seq"], np.int32)), one, one, c["page"]]
+    rq.paged_attention_nvfp4(*args, **kw)
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        rq.paged_attention_nvfp4(*args, **kw)
+    n = ctypes.c_size_t()
+    assert ctypes.CDLL("libcudart.so.13").cudaGraphGetNodes(ctypes.c_void_p(graph.raw_cuda_graph()), None,
+                                                            ctypes.byref(n)) == 0
+    return n.value
+
+
+def test_the_automatic_choice_launches_what_the_step_needs(rmsq_gpu):
+    """A large decode batch has no use for the kernel of prompts (beside the
+    split and its join); with a bound on the queries neither has a batch of
+    speculative tokens."""
+    def count(q_lens, seq, **kw):
+        return launches(rmsq_gpu, make(q_lens, seq, 32, 8, 64, 16, "bf16", seed=70), **kw)
+
+    assert count([1] * 300, [40] * 300) == 2
+    assert count([1] * 290 + [0] * 10, [40] * 300) == 2
+    assert count([4] * 100, [40] * 100, max_query=4) == 2
+    assert count([1] * 40 + [400], [40] * 40 + [400]) == 3
+    assert count([1] * 40 + [400], [40] * 40 + [400], max_query=400) == 3
+    assert count([400], [400]) == 1
+
+
+@pytest.mark.parametrize("max_query", [1, 30, 400, 10**9])
+@pytest.mark.parametrize("q_lens, seq", [([1] * 40, [60] * 40), ([1, 400, 30], [50, 450, 30]), ([300], [300])])
+def test_a_bound_on_the_queries_changes_no_result(rmsq_gpu, q_lens, seq, max_query):
+    """Right, too high and too low."""
+    for variant in ("auto", "pipelined"):
+        check(rmsq_gpu, make(q_lens, seq, 8, 2, 64, 16, "bf16", seed=71), max_query=max_query, variant=variant)
+    assert rmsq_gpu.take_fault_flags() == 0

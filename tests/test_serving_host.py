@@ -320,3 +320,19 @@ def test_barriers_that_want_a_whole_warp_gather_it():
 def test_attention_sizes_whose_product_wraps_are_refused(L, T, h):
     assert attn(L, T=T, h=h, kv=1, qs=1 << 16) == rq.ERR_UNSUPPORTED_SHAPE
     assert rq.paged_attention_workspace_bytes(T, 3, h, 1, 128) == 0
+
+
+def test_attention_with_a_bound_on_the_queries(L):
+    def call(T=4, R=3, max_query=0, out=A[7]):
+        return L.rmsq_paged_attention_nvfp4_ex(vp(A[0]), 1024, vp(A[1]), 10, 16, vp(A[2]), 8, vp(A[3]), vp(A[4]), vp(A[5]),
+                                               vp(A[6]), 0.1, 0, vp(out), vp(A[8]), vp(A[9]), 1 << 27, T, R, 8, 2, 128, 0,
+                                               None, 0, max_query)
+    assert call(max_query=-1) == rq.ERR_INVALID_ARG
+    assert call(out=A[0], max_query=3) == rq.ERR_ALIAS
+    assert call(T=0, max_query=1) == rq.OK
+    if not torch.cuda.is_available():       # fake addresses
+        for q in (0, 1, 4, 1 << 40):
+            assert call(max_query=q) in NO_GPU
+        with pytest.raises(rq.RmsqError) as e:
+            rq.paged_attention_nvfp4(**_attn_args(max_query=-3))
+        assert e.value.status == rq.ERR_INVALID_ARG
