@@ -22,9 +22,15 @@ namespace {
 
 // Row blocks of 8: two (16 rows share a pass over the keys) where a request
 // has more than 8 rows on average; one for D = 256, whose accumulators for 16
-// rows would not fit the registers.
-int row_blocks(int64_t tokens, int64_t requests, int group, int head_dim) {
-    return head_dim <= 128 && tokens * group > 8 * requests ? 2 : 1;
+// rows would not fit the registers.  Beside the prompt kernel the average says
+// nothing about the requests that are left, and they are taken for decodes of
+// one token: one block for a group of up to 8.  The other mistake is the
+// smaller one: 127 decodes of 8 x 4 heads on 2000 keys beside a prompt of 300
+// tokens take 58 us with one block and 78 with two (on 8000 keys beside 2000
+// tokens 225 and 273), but 250 requests of four queries of 4 x 8 heads on 1000
+// keys 139 and 132.
+int row_blocks(int64_t tokens, int64_t requests, int group, int head_dim, bool beside_prompts) {
+    return head_dim <= 128 && (beside_prompts ? group > 8 : tokens * group > 8 * requests) ? 2 : 1;
 }
 
 size_t part_floats(int head_dim, int nb) { return static_cast<size_t>(8) * nb * (head_dim + 4); }    // kPartRow
@@ -113,7 +119,7 @@ cudaError_t launch_attn(AttnArgs a, int head_dim, int64_t max_query, int64_t max
         const cudaError_t e = head_dim == 64 ? launch_prompt<E, 64>(a, stream) : launch_prompt<E, 128>(a, stream);
         if (e != cudaSuccess || a.requests == 1) return e;
     }
-    const int nb = row_blocks(a.tokens, a.requests, a.group, head_dim);
+    const int nb = row_blocks(a.tokens, a.requests, a.group, head_dim, prompt);
     switch (head_dim) {
     case 64: return nb == 2 ? launch_split<E, 64, 2>(a, max_tiles, stream) : launch_split<E, 64, 1>(a, max_tiles, stream);
     case 128: return nb == 2 ? launch_split<E, 128, 2>(a, max_tiles, stream) : launch_split<E, 128, 1>(a, max_tiles, stream);

@@ -645,3 +645,16 @@ def test_a_bound_on_the_queries_changes_no_result(rmsq_gpu, q_lens, seq, max_que
     for variant in ("auto", "pipelined"):
         check(rmsq_gpu, make(q_lens, seq, 8, 2, 64, 16, "bf16", seed=71), max_query=max_query, variant=variant)
     assert rmsq_gpu.take_fault_flags() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("heads, kv", [(8, 1), (8, 8), (16, 1), (32, 2), (12, 1)])
+def test_decodes_beside_a_prompt(rmsq_gpu, dtype, D, heads, kv):
+    """One batch for both kernels: groups on both sides of a row block, a few
+    requests of several queries among the decodes, lengths around a tile."""
+    q_lens = [1] * 20 + [300] + [1, 3, 0, 4, 1, 60] + [1] * 5
+    seq = [10 * i + 1 for i in range(20)] + [420] + [128, 3, 50, 129, 500, 64] + [257, 1, 16, 300, 0]
+    for variant in ("auto", "pipelined"):
+        check(rmsq_gpu, make(q_lens, seq, heads, kv, D, 16, dtype, seed=72), variant=variant)
+    assert rmsq_gpu.take_fault_flags() == 0
