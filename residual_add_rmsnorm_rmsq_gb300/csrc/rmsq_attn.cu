@@ -79,18 +79,29 @@ cudaError_t launch_prompt(AttnArgs a, cudaStream_t stream) {
                          PromptTile<D>::smem, stream);
 }
 
+// What the kernels take for 128 keys, in us: the split kernel for 48 (row, kv
+// head) per SM, the prompt kernel for a CTA's 256 rows on every SM.  Measured on
+// 20000 to 100000 keys: 1.92 to 2.07 and 1.80 to 1.92 (D = 128), 1.16 to 1.27 and
+// 1.44 to 1.52 (64).
+struct Cost {
+    double split, prompt;
+};
+Cost cost_of(int head_dim) { return head_dim <= 64 ? Cost{1.21, 1.48} : Cost{1.97, 1.86}; }
+
 // Requests of more than kPromptRows rows go to the prompt kernel, the others to
 // the split kernel, whichever they are: the lengths are the device's.
 //
 // The prompt kernel is launched (AUTO) where it is expected sooner.  It gives a
-// CTA 256 rows and all their keys, about 1.25 us per 128 of them; the split
-// kernel gives its CTAs (three per SM) 16 rows and equal runs of keys, about 1.1
-// us per 128.  So few rows on a long context belong to the split kernel, although
-// it reads the keys once per 16 rows.  Both costs are proportional to the
-// length, which the host does not know.  Measured, split and prompt, D = 128: 8
-// queries of 16 x 8 heads on 100000 keys 126 and 633 us, 64 of 8 x 8 heads 594
-// and 966, 256 of them 1925 and 805; 8 requests of 50 queries (8 x 4 heads) on
-// 2000 keys 72 and 43; 4 of 200 (4 x 8) on 500 keys 72 and 24.
+// CTA 256 rows and all their keys; the split kernel gives equal runs of keys, for
+// 16 rows at a time, to the CTAs of the whole card.  So few rows on a long context
+// belong to the split kernel, although it reads the keys once per 16 rows.  Both
+// costs are proportional to the length, which the host does not know, so that
+// what decides is the rows.  Measured with one request of 8 x 8 heads of 128 and
+// 20000 keys, split and prompt: 88 queries 250 and 300 us, 104 292 and 301, 112
+// 313 and 300, 128 355 and 301 (on 2000 keys already 96 queries 49 and 42); heads
+// of 64, 128 queries: 218 and 237.  8 queries of 16 x 8 heads on 50000 keys 124
+// and 675; 8 requests of 50 queries (8 x 4 heads) on 2000 82 and 46; 4 of 200 (4 x
+// 8) on 500 66 and 23.
 //
 // It is not launched where no request can be its: the caller's bound on the
 // queries of a request says so, or, without one, that there are no more than one
@@ -107,7 +118,9 @@ cudaError_t launch_attn(AttnArgs a, int head_dim, int64_t max_query, int64_t max
     const int64_t tokens = max_query > 0 && max_query < a.tokens / a.requests ? max_query * a.requests : a.tokens;
     const int64_t rows = tokens * a.group;
     const int64_t items = (rows / 256 + 1) * a.kv_heads;
-    const bool sooner = 1.1 * static_cast<double>(rows * a.kv_heads) / (16.0 * 3.0 * sms) > 1.25 * static_cast<double>((items + sms - 1) / sms);
+    const Cost cost = cost_of(head_dim);
+    const bool sooner = cost.split * static_cast<double>(rows * a.kv_heads) / (48.0 * sms) >
+                        cost.prompt * static_cast<double>((items + sms - 1) / sms);
     const int64_t rest = a.tokens >= a.requests ? a.tokens - a.requests + 1 : 1;    // left for one request
     const int64_t longest = max_query > 0 ? (max_query < a.tokens ? max_query : a.tokens)
                             : variant == kVariantPipelined ? a.tokens : rest;
