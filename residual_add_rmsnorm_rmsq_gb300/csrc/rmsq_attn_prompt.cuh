@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
             const int pos = live ? first_pos + token : -1, lo = a.window > 0 ? pos - a.window + 1 : 0;
             const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
             const uint32_t s_at = tmem + i * 128 + lanes, o_at = tmem + 256 + i * D + lanes;
-            float m = -INFINITY, l = 0.0f, limit = -INFINITY;
+            float m = -INFINITY, l = 0.0f, limit = -INFINITY, shift = 0.0f;
             for (int n = 0; n < steps; ++n) {
                 const int key0 = key_begin + n * 128;
                 ok = warp_wait(&sfull[i], n & 1);
@@ -535,10 +535,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                 if (__any_sync(kFull, top > limit)) {
                     // sfull of this step says that the previous P . V has
                     // completed too: O may be rescaled here
-                    const float m1 = fmaxf(top, m);
+                    const float m1 = top > limit ? fmaxf(top, m) : m;   // whatever shares the warp
                     const float r = m1 == -INFINITY ? 1.0f : exp2_approx((m - m1) * f);
                     m = m1;
                     limit = lag_limit(m, f);
+                    shift = weight_shift(m, f);
                     l *= r;
                     if (n > 0) {
 #pragma unroll
@@ -552,15 +553,20 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                             tmem_st16(o_at + c * 16, u);
                         }
                     }
-                }
-                float shift = weight_shift(m, f);
-                if (__any_sync(kFull, is_far(shift))) {     // the rows that are; the others subtract zero
-                    const float t = is_far(shift) ? m : 0.0f;
-                    if (is_far(shift)) shift = kPShift;
+                    // A row that is far out comes here at every step (its limit
+                    // is passed by any logit); the others subtract zero.
+                    if (__any_sync(kFull, is_far(shift))) {
+                        const bool own = is_far(shift);
+                        const float t = own ? m : 0.0f;
+                        if (own) {
+                            shift = kPShift;
+                            limit = -INFINITY;
+                        }
 #pragma unroll
-                    for (int c = 0; c < 8; ++c)
+                        for (int c = 0; c < 8; ++c)
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) d[c][j] -= t;
+                            for (int j = 0; j < 16; ++j) d[c][j] -= t;
+                    }
                 }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) l += weigh_half(d, h, s_at, f, shift);
