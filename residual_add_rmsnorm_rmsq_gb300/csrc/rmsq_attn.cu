@@ -27,8 +27,9 @@ namespace {
 // one token: one block for a group of up to 8.  The other mistake is the
 // smaller one: 127 decodes of 8 x 4 heads on 2000 keys beside a prompt of 300
 // tokens take 58 us with one block and 78 with two (on 8000 keys beside 2000
-// tokens 225 and 273), but 250 requests of four queries of 4 x 8 heads on 1000
-// keys 139 and 132.
+// tokens 225 and 273; one of 4 x 8 heads on 4000 keys beside 1500 70 and 79), but
+// 250 requests of four queries of 4 x 8 heads on 1000 keys 139 and 132, and two
+// prompts alone 3 us more, for the larger empty launch.
 int row_blocks(int64_t tokens, int64_t requests, int group, int head_dim, bool beside_prompts) {
     return head_dim <= 128 && (beside_prompts ? group > 8 : tokens * group > 8 * requests) ? 2 : 1;
 }
@@ -88,8 +89,9 @@ struct Cost {
 };
 Cost cost_of(int head_dim) { return head_dim <= 64 ? Cost{1.21, 1.48} : Cost{1.97, 1.86}; }
 
-// Requests of more than kPromptRows rows go to the prompt kernel, the others to
-// the split kernel, whichever they are: the lengths are the device's.
+// Requests of more than kPromptRows rows go to the prompt kernel (AUTO: if they
+// are worth it there, see prompt_takes), the others to the split kernel, whichever
+// they are: the lengths are the device's.
 //
 // The prompt kernel is launched (AUTO) where it is expected sooner.  It gives a
 // CTA 256 rows and all their keys; the split kernel gives equal runs of keys, for
@@ -128,6 +130,8 @@ cudaError_t launch_attn(AttnArgs a, int head_dim, int64_t max_query, int64_t max
                         (variant == kVariantPipelined || sooner);
     // (a single request is the prompt kernel's whatever its length)
     a.most_rows = !prompt ? INT32_MAX : a.requests == 1 ? 0 : kPromptRows;
+    if (prompt && variant == kVariantAuto && a.requests > 1)
+        a.share = static_cast<int64_t>(cost.prompt / cost.split * 48.0 * sms / a.kv_heads) + 1;
     if (prompt) {
         const cudaError_t e = head_dim == 64 ? launch_prompt<E, 64>(a, stream) : launch_prompt<E, 128>(a, stream);
         if (e != cudaSuccess || a.requests == 1) return e;

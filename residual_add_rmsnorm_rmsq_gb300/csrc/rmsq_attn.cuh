@@ -91,7 +91,8 @@ struct AttnArgs {
     float* part;            // [workers][2][ROWS][kPartRow<D>]
     int requests, width, tokens, heads, kv_heads, group;
     int page_shift, num_pages, window, workers;
-    int most_rows;          // rows of a request above which the split kernel leaves it to the prompt kernel
+    int most_rows;          // rows of a request above which it may be the prompt kernel's, see prompt_takes
+    int64_t share;          // 0, or what rows times requests have to reach for that
     float scale_log2;       // softmax scale * log2(e)
 };
 
@@ -103,10 +104,22 @@ constexpr int kPartRow = D + 4;
 // One request as the kernels see it: every value is clamped so that no
 // length or offset in device memory can lead outside the buffers.
 struct Req {
-    int q0, qlen, seq, tile0, ktiles, qtiles;
+    int q0, qlen, seq, tile0, ktiles;
 };
 
-template <int ROWS>
+// Which kernel takes a request.  The prompt kernel walks all its keys in one
+// CTA, the split kernel divides them over the card; the time of both is
+// proportional to the length.  So a request of few rows is better with the split
+// kernel unless there are enough others of its length beside it to fill the card
+// with prompt CTAs: rows * n >= share, n the requests of more than most_rows rows
+// whose keys are at least half as many (the same power of two and up).  Both
+// kernels count n themselves, from the same lengths.  128 decodes of 8 x 8 heads
+// on 2000 keys beside 9 queries on 100000: 1332 us with the prompt kernel for the
+// 9, 234 with the split kernel for all.
+__device__ __forceinline__ bool prompt_takes(const AttnArgs& a, int64_t rows, int ktiles, const int* longer) {
+    return rows > a.most_rows && (a.share == 0 || rows * longer[31 - __clz(ktiles)] >= a.share);
+}
+
 __device__ __forceinline__ Req load_request(const AttnArgs& a, int r) {
     Req x;
     x.q0 = min(max(__ldg(a.q_start + r), 0), a.tokens);
@@ -115,23 +128,39 @@ __device__ __forceinline__ Req load_request(const AttnArgs& a, int r) {
     const int first = a.window > 0 ? max(x.seq - x.qlen - a.window + 1, 0) : 0;
     x.tile0 = min(first, max(x.seq - 1, 0)) / kAttnKeyTile;
     x.ktiles = max((x.seq + kAttnKeyTile - 1) / kAttnKeyTile - x.tile0, 1);
-    const int64_t rows = static_cast<int64_t>(x.qlen) * a.group;
-    x.qtiles = rows > a.most_rows ? 0 : static_cast<int>((rows + ROWS - 1) / ROWS);
     return x;
 }
 
-// prefix[r] = tiles (per kv head) of the requests before r, prefix[requests]
-// = all, in shared memory.  Ends with a barrier.
-template <int ROWS>
-__device__ __forceinline__ void scan_requests(const AttnArgs& a, int64_t* prefix) {
-    __shared__ int64_t wsum[kAttnWarps];
+// prefix[r] = count(rows, key tiles, the prompt kernel's or not) summed over the
+// requests before r, prefix[requests] over all, in shared memory.  Ends with a
+// barrier.  (Compact on purpose: it is cold code at the start of every CTA.)
+template <int THREADS, class Count>
+__device__ __forceinline__ void scan_requests(const AttnArgs& a, int64_t* prefix, Count count) {
+    __shared__ int64_t wsum[THREADS / 32];
+    __shared__ int longer[32];      // candidates of 2^i key tiles and more
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (a.requests + kAttnThreads - 1) / kAttnThreads;
+    const int per = (a.requests + THREADS - 1) / THREADS;
     const int r0 = min(tid * per, a.requests), r1 = min(r0 + per, a.requests);
-    int64_t sum = 0;
+    if (a.share != 0) {
+        if (tid < 32) longer[tid] = 0;
+        __syncthreads();
+    }
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) {
-        const Req x = load_request<ROWS>(a, r);
-        const int64_t c = static_cast<int64_t>(x.qtiles) * x.ktiles;
+        const Req x = load_request(a, r);
+        const int rows = x.qlen * a.group;
+        prefix[r + 1] = static_cast<int64_t>(rows) << 32 | x.ktiles;
+        if (a.share != 0 && rows > a.most_rows)
+#pragma unroll 1
+            for (int i = 31 - __clz(x.ktiles); i >= 0; --i) atomicAdd(longer + i, 1);
+    }
+    if (a.share != 0) __syncthreads();
+    int64_t sum = 0;
+#pragma unroll 1
+    for (int r = r0; r < r1; ++r) {
+        const int64_t rows = prefix[r + 1] >> 32;
+        const int ktiles = static_cast<int>(prefix[r + 1]);
+        const int64_t c = count(rows, ktiles, prompt_takes(a, rows, ktiles, longer));
         prefix[r + 1] = c;
         sum += c;
     }
@@ -144,10 +173,11 @@ __device__ __forceinline__ void scan_requests(const AttnArgs& a, int64_t* prefix
     if (lane == 31) wsum[warp] = inc;
     __syncthreads();
     int64_t run = inc - sum;
+#pragma unroll 1
     for (int w = 0; w < warp; ++w) run += wsum[w];
+#pragma unroll 1
     for (int r = r0; r < r1; ++r) {
-        const int64_t c = prefix[r + 1];
-        run += c;
+        run += prefix[r + 1];
         prefix[r + 1] = run;
     }
     if (tid == 0) prefix[0] = 0;
@@ -160,7 +190,6 @@ struct Place {
     int64_t item0;              // first tile of the item in the sequence
 };
 
-template <int ROWS>
 __device__ __forceinline__ Place locate(const AttnArgs& a, const int64_t* prefix, int64_t x, Req& req) {
     int lo = 0, hi = a.requests;
     while (hi - lo > 1) {
@@ -168,7 +197,7 @@ __device__ __forceinline__ Place locate(const AttnArgs& a, const int64_t* prefix
         if (prefix[mid] * a.kv_heads <= x) lo = mid;
         else hi = mid;
     }
-    req = load_request<ROWS>(a, lo);
+    req = load_request(a, lo);
     const int64_t rest = x - prefix[lo] * a.kv_heads;
     const int64_t item = rest / req.ktiles;
     Place p;
@@ -559,7 +588,9 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
     allow_dependents();
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    scan_requests<ROWS>(a, prefix);
+    scan_requests<kAttnThreads>(a, prefix, [](int64_t r, int ktiles, bool taken) {
+        return taken ? 0 : (r + ROWS - 1) / ROWS * ktiles;
+    });
     const int64_t total = prefix[a.requests] * a.kv_heads;
     const int64_t run = run_length(total, a.workers);
     int64_t x = blockIdx.x * run;
@@ -570,7 +601,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
 
     while (x < end) {
         Req rq;
-        const Place at = locate<ROWS>(a, prefix, x, rq);
+        const Place at = locate(a, prefix, x, rq);
         const int ntiles = static_cast<int>(min(static_cast<int64_t>(rq.ktiles - at.tile), end - x));
         const int rows = rq.qlen * a.group;      // of the request
         const int row0 = at.qtile * ROWS;
@@ -803,7 +834,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a) {
     const int4 c0 = __ldcg(c), c1 = __ldcg(c + 1);
     const int parts = c0.x, first_slot = c0.y, head = c1.y;
     if (parts == 0) return;
-    const Req rq = {c0.z, c0.w, 0, 0, 0, 0};
+    const Req rq = {c0.z, c0.w, 0, 0, 0};
     const int w0 = blockIdx.x;
     const float v_gs = __ldg(a.v_gs);
     const int rows = rq.qlen * a.group, row0 = c1.x * ROWS;

@@ -51,6 +51,7 @@ struct PromptTile {
     static constexpr int q = 128 * D * 2, k = 128 * D * 2, v = 128 * D * 2;    // bytes of one operand tile
     // one CTA per SM in any case: it takes all of tensor memory
     static constexpr int smem = 1024 + (6 * q > 120 * 1024 ? 6 * q : 120 * 1024);
+    static_assert(smem - 1024 - 2 * q >= (RMSQ_MAX_REQUESTS + 1) * 8, "the scan fits behind the queries");
 };
 
 // Instruction descriptor: f16 x f16 -> fp32, both K-major, 128 x N.
@@ -262,12 +263,50 @@ __device__ __forceinline__ float weigh_half(const Row& d, int h, uint32_t s_at, 
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
-// Items (256-row tiles) of a request; requests of few rows are the split
-// kernel's.
-__device__ __forceinline__ int prompt_items(const AttnArgs& a, int r) {
-    const int q0 = min(max(__ldg(a.q_start + r), 0), a.tokens);
-    const int64_t rows = static_cast<int64_t>(min(max(__ldg(a.q_start + r + 1), q0), a.tokens) - q0) * a.group;
-    return rows > a.most_rows ? static_cast<int>((rows + 255) / 256) : 0;
+// The CTA's item, counted from its request's first one, and the request; -1 if
+// there are not that many.  Up to 32 requests every warp finds it for itself, a
+// lane per request; more are scanned in `scratch` (the key and value tiles' space,
+// which is theirs on return).
+__device__ __forceinline__ int64_t find_item(const AttnArgs& a, int64_t* scratch, int& req) {
+    const int skip = static_cast<int>(blockIdx.x) / a.kv_heads;
+    if (a.requests <= 32) {
+        const int lane = threadIdx.x & 31;
+        int rows = 0, own = 0, n = 0;
+        if (lane < a.requests) {
+            const Req x = load_request(a, lane);
+            rows = x.qlen * a.group;
+            own = 31 - __clz(x.ktiles);
+        }
+        const bool open = rows > a.most_rows;
+        const uint32_t all = __ballot_sync(kFull, open);
+        if (a.share != 0)
+#pragma unroll 1
+            for (uint32_t rest = all; rest != 0; rest &= rest - 1) n += __shfl_sync(kFull, own, __ffs(rest) - 1) >= own;
+        const int items = open && (a.share == 0 || static_cast<int64_t>(rows) * n >= a.share) ? (rows + 255) >> 8 : 0;
+        int inc = items;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(kFull, inc, o);
+            if (lane >= o) inc += u;
+        }
+        const int item = __shfl_sync(kFull, inc, 31) - 1 - skip;
+        if (item < 0) return -1;
+        req = __ffs(__ballot_sync(kFull, inc > item)) - 1;
+        return item - __shfl_sync(kFull, inc - items, req);
+    }
+    scan_requests<kPromptThreads>(a, scratch, [](int64_t r, int, bool taken) { return taken ? (r + 255) / 256 : 0; });
+    int64_t item = scratch[a.requests] - 1 - skip;
+    if (item >= 0) {
+        int hi = a.requests;
+        while (hi - req > 1) {
+            const int mid = (req + hi) >> 1;
+            if (scratch[mid] <= item) req = mid;
+            else hi = mid;
+        }
+        item -= scratch[req];
+    }
+    __syncthreads();    // the scan has been read
+    return item < 0 ? -1 : item;
 }
 
 template <class E, int D>
@@ -278,7 +317,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
         ofull[2], drained;
     __shared__ __align__(16) uint32_t valid[4][4];  // which keys of a tile lie on a page, four tiles deep
     __shared__ uint32_t tmem_base;
-    __shared__ int wsum[kPromptThreads / 32];
     unsigned char* qs = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
     unsigned char* ks = qs + 2 * Tile::q;
     unsigned char* vs = ks + 2 * Tile::k;
@@ -300,49 +338,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
     grid_dependency_wait();
 
     // The item of this CTA: tiles of a request from the last rows (most keys)
-    // to the first, kv heads innermost.  The scan borrows the key tiles' space.
-    int* prefix = reinterpret_cast<int*>(ks);
-    {
-        const int per = (a.requests + kPromptThreads - 1) / kPromptThreads;
-        const int r0 = min(tid * per, a.requests), r1 = min(r0 + per, a.requests);
-        int sum = 0;
-        for (int r = r0; r < r1; ++r) {
-            const int c = prompt_items(a, r);
-            prefix[r + 1] = c;
-            sum += c;
-        }
-        int inc = sum;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(kFull, inc, o);
-            if (lane >= o) inc += u;
-        }
-        if (lane == 31) wsum[warp] = inc;
-        __syncthreads();
-        int run = inc - sum;
-        for (int w = 0; w < warp; ++w) run += wsum[w];
-        for (int r = r0; r < r1; ++r) {
-            run += prefix[r + 1];
-            prefix[r + 1] = run;
-        }
-        if (tid == 0) prefix[0] = 0;
-        __syncthreads();
-    }
-    int item = prefix[a.requests] - 1 - static_cast<int>(blockIdx.x) / a.kv_heads;
+    // to the first, kv heads innermost.
     const int head = blockIdx.x % a.kv_heads;
     int req = 0;
-    if (item >= 0) {
-        int hi = a.requests;
-        while (hi - req > 1) {
-            const int mid = (req + hi) >> 1;
-            if (prefix[mid] <= item) req = mid;
-            else hi = mid;
-        }
-        // (starts that do not ascend can add up to more items than an int holds)
-        if (item < prefix[req] || item >= prefix[req + 1]) item = -1;
-    }
-    const int row0 = item >= 0 ? (item - prefix[req]) * 256 : 0;
-    __syncthreads();    // the scan has been read: its space is the key tiles' now
+    const int64_t item = find_item(a, reinterpret_cast<int64_t*>(ks), req);
+    const int row0 = static_cast<int>(item) * 256;
     if (item < 0) {
         allow_dependents();
         return;
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
     allow_dependents();
     const uint32_t tmem = tmem_base;
 
-    const Req rq = load_request<8>(a, req);
+    const Req rq = load_request(a, req);
     const int rows = rq.qlen * a.group, first_pos = rq.seq - rq.qlen;
     const int tiles = min(rows - row0, 256) > 128 ? 2 : 1;
     const int last_pos = first_pos + (min(row0 + 256, rows) - 1) / a.group;

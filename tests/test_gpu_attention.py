@@ -658,3 +658,48 @@ def test_decodes_beside_a_prompt(rmsq_gpu, dtype, D, heads, kv):
     for variant in ("auto", "pipelined"):
         check(rmsq_gpu, make(q_lens, seq, heads, kv, D, 16, dtype, seed=72), variant=variant)
     assert rmsq_gpu.take_fault_flags() == 0
+
+
+@pytest.mark.parametrize("window", [0, 200])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_lens, seq", [
+    ([1] * 12 + [40] + [300] + [1], [30] * 12 + [5000] + [300] + [700]),   # few rows on a long context beside a prompt
+    ([20] * 24, [20 + 40 * i for i in range(24)]),                         # enough of them for the card, of all lengths
+    ([0, 17, 300, 0, 90, 33, 16], [0, 2500, 300, 40, 1000, 20, 900]),      # on both sides of the rule, empty requests
+])
+def test_requests_shared_out_between_the_kernels(rmsq_gpu, q_lens, seq, D, window):
+    """Every request is exactly one kernel's, whatever the lengths beside it."""
+    c = make(q_lens, seq, 16, 4, D, 16, "bf16", seed=73)
+    out = torch.full(c["q"].shape, 3.0, dtype=torch.bfloat16, device="cuda")
+    check(rmsq_gpu, c, window=window, out=out)
+    assert rmsq_gpu.take_fault_flags() == 0
+
+
+def test_few_rows_on_a_long_context_beside_decodes_stay_divided(rmsq_gpu):
+    """The automatic choice takes no longer than twice the kernel that divides
+    the keys (the other one walks them in a few CTAs: five times)."""
+    rq = rmsq_gpu
+    q_lens, seq, heads, kv, D, page = [1] * 128 + [9], [2000] * 128 + [100000], 64, 8, 128, 64
+    pages = 1600
+    table = torch.randint(0, pages, (129, 1563), device="cuda").int()
+    cache = torch.randint(0, 0x40, rq.kv_cache_shape(pages, kv, D, page), device="cuda").to(torch.uint8)
+    q = torch.randn(137, heads, D, device="cuda").bfloat16()
+    start = torch.tensor([0] + q_lens, device="cuda").cumsum(0).int()
+    seqs, one = torch.tensor(seq, device="cuda").int(), torch.ones(1, device="cuda")
+    ws = torch.empty(rq.paged_attention_workspace_bytes(137, 129, heads, kv, D), dtype=torch.uint8, device="cuda")
+
+    def us(variant):
+        call = lambda: rq.paged_attention_nvfp4(q, cache, table, start, seqs, one, one, page, workspace=ws, variant=variant)  # noqa: E731
+        call()
+        times = []
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            for _ in range(4):
+                call()
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b) * 250)
+        return min(times)
+
+    assert us("auto") < 2 * us("direct")
