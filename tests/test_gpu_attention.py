@@ -666,10 +666,12 @@ def test_decodes_beside_a_prompt(rmsq_gpu, dtype, D, heads, kv):
     ([1] * 12 + [40] + [300] + [1], [30] * 12 + [5000] + [300] + [700]),   # few rows on a long context beside a prompt
     ([20] * 24, [20 + 40 * i for i in range(24)]),                         # enough of them for the card, of all lengths
     ([0, 17, 300, 0, 90, 33, 16], [0, 2500, 300, 40, 1000, 20, 900]),      # on both sides of the rule, empty requests
+    ([1] * 33 + [0, 20, 300, 17, 17, 17, 9], [i + 1 for i in range(33)] + [0, 1500, 310, 17, 140, 600, 3000]),  # more than 32
 ])
 def test_requests_shared_out_between_the_kernels(rmsq_gpu, q_lens, seq, D, window):
     """Every request is exactly one kernel's, whatever the lengths beside it."""
-    c = make(q_lens, seq, 16, 4, D, 16, "bf16", seed=73)
+    c = make(q_lens, seq, 32, 8, D, 16, "bf16", seed=73)
+    assert launches(rmsq_gpu, c, window=window) == 3        # both kernels and the join
     out = torch.full(c["q"].shape, 3.0, dtype=torch.bfloat16, device="cuda")
     check(rmsq_gpu, c, window=window, out=out)
     assert rmsq_gpu.take_fault_flags() == 0
@@ -703,3 +705,37 @@ def test_few_rows_on_a_long_context_beside_decodes_stay_divided(rmsq_gpu):
         return min(times)
 
     assert us("auto") < 2 * us("direct")
+
+
+def test_a_replayed_graph_follows_requests_that_change_hands(rmsq_gpu):
+    """Lengths in device memory move requests from one kernel to the other
+    between replays of one graph, with the workspace the call took itself."""
+    rq = rmsq_gpu
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    c = make([340, 30, 30], [340, 2000, 60], 32, 8, 64, 16, "bf16", seed=74)
+    assert launches(rq, c) == 3
+    q, cache, table = c["q"].cuda(), dev(c["cache"]), dev(c["table"])
+    # rows of every request on pages of the longest one
+    table[:] = table[1]
+    c["table"] = table.cpu().numpy()
+    start, seq = torch.zeros(4, dtype=torch.int32, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    g1, g2 = torch.tensor([c["k_gs"]], device="cuda"), torch.tensor([c["v_gs"]], device="cuda")
+    out, lse = torch.empty_like(q), torch.empty(400, 32, device="cuda")
+    call = lambda: rq.paged_attention_nvfp4(q, cache, table, start, seq, g1, g2, 16, out=out, lse=lse)  # noqa: E731
+    call()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for q_lens, lens in (([340, 30, 30], [340, 2000, 60]), ([20, 360, 20], [2000, 360, 20]), ([1, 1, 1], [7, 1999, 64]),
+                         ([100, 100, 100], [1900, 100, 150]), ([0, 0, 400], [5, 0, 400])):
+        start.copy_(torch.tensor([0] + list(np.cumsum(q_lens)), dtype=torch.int32))
+        seq.copy_(torch.tensor(lens, dtype=torch.int32))
+        out.fill_(3.0)
+        graph.replay()
+        got, got_lse, n = out.clone(), lse.clone(), sum(q_lens)
+        call()
+        assert torch.equal(got, out) and torch.equal(got_lse[:n], lse[:n]) and (got[n:] == 3).all()
+        w_out, w_lse, tol, tol_lse = ref.attention(c["q64"][:n], c["cache"], c["table"], q_lens, lens, float(c["k_gs"]),
+                                                   float(c["v_gs"]), 16, 64 ** -0.5, 0, torch.finfo(torch.bfloat16).eps)
+        assert (np.abs(got[:n].double().cpu().numpy() - w_out) <= tol).all()
+    assert rq.take_fault_flags() == 0

@@ -81,3 +81,32 @@ def test_calls_on_the_current_and_on_another_stream_in_turn(rmsq_gpu):
                 del got, g
     torch.cuda.synchronize()
     assert wrong.item() == 0 and rq.take_fault_flags() == 0
+
+
+def test_a_call_on_a_forked_stream_of_a_capture(rmsq_gpu):
+    """Inside a capture a call on a second stream takes its workspace and
+    outputs from the graph's memory, and replays give what the call gives."""
+    rq = rmsq_gpu
+    dev = lambda a: torch.from_numpy(np.ascontiguousarray(a)).cuda()  # noqa: E731
+    c = attn.make([1] * 8, [900] * 8, 16, 4, 128, 16, "bf16", seed=52)
+    start = dev(np.arange(9, dtype=np.int32))
+    g1, g2 = torch.tensor([c["k_gs"]], device="cuda"), torch.tensor([c["v_gs"]], device="cuda")
+    args = [c["q"].cuda(), dev(c["cache"]), dev(c["table"]), start, dev(np.array(c["seq"], np.int32)), g1, g2, 16]
+    want = rq.paged_attention_nvfp4(*args)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        first = rq.paged_attention_nvfp4(*args, stream=side)
+        other = rq.paged_attention_nvfp4(*args)
+        here.wait_stream(side)
+        total = first.float() + other.float()
+        del first, other
+    junk = [torch.full((1 << 20,), 0xff, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    for _ in range(3):
+        graph.replay()
+        assert torch.equal(total, 2 * want.float())
+    del junk
+    assert rq.take_fault_flags() == 0
