@@ -449,12 +449,16 @@ int rmsq_kv_cache_load_nvfp4(const void *kv_cache, int64_t num_pages, int64_t pa
  *                divides the keys of each request over the device.  PIPELINED:
  *                a tensor-core kernel for requests of more than 64 (query, head
  *                of the group) pairs, DIRECT for the others (and for head_dim
- *                256).  AUTO: whichever is expected sooner.  The two agree
- *                within the rounding of their sums.
- * Sums, maxima and the log-sum-exp are fp32; probabilities are rounded to f16
- * before they meet the values.  Results are deterministic.  n_tokens *
- * num_heads below 2^31; 0 tokens or requests return RMSQ_OK without a launch.
- * No output may overlap an input.  Asynchronous on `stream`.
+ *                256).  AUTO: whichever is expected sooner, for each request
+ *                by its own length and those beside it.  The two agree within
+ *                the rounding of their sums.
+ * Sums, maxima and the log-sum-exp are fp32, and logits may have any magnitude
+ * that fp32 has; probabilities are rounded to f16 before they meet the values
+ * (fp16 outputs are off by 2.9e-4 instead of 2.1e-4 on long contexts; bf16
+ * outputs hide it).  Results are deterministic.  n_tokens * num_heads below 2^31;
+ * 0 tokens or requests return RMSQ_OK without a launch.  No output may overlap an
+ * input.  Asynchronous on `stream`; a launch that gives up waiting shows in
+ * rmsq_take_fault_flags.
  */
 int rmsq_paged_attention_nvfp4(const void *q, int64_t q_stride, const void *kv_cache, int64_t num_pages,
                                int64_t page_size, const int32_t *block_table, int64_t table_width,
@@ -575,8 +579,10 @@ int rmsq_silu_mul_quant(const void *gate_up, int quant_mode, const float *scale_
  *  n            > 0, a multiple of 8;  k > 0, a multiple of 128, at most
  *               RMSQ_ACT_MAX_D (else RMSQ_ERR_UNSUPPORTED_SHAPE).
  * The 128 products of a block are summed by the tensor cores in fp32, the
- * blocks in fp32 registers; out is rounded once.  Deterministic.  NaN codes
- * give NaN in their row or column.  Asynchronous on `stream`.
+ * blocks in fp32 registers, times sa * sb, which is formed first, in fp32; out
+ * is rounded once.  Deterministic.  NaN codes give NaN in their row or column.
+ * Asynchronous on `stream`; a launch that gives up waiting shows in
+ * rmsq_take_fault_flags.
  */
 int rmsq_fp8_block_matmul(const void *a_codes, const void *a_scales, int quant_mode, const void *b_codes,
                           const float *b_scales, void *out, int64_t m, int64_t n, int64_t k, int dtype,
@@ -613,9 +619,11 @@ int rmsq_set_programmatic_launch(int enable);
 
 /*
  * rmsq_take_fault_flags — reads and clears, on the current device, the flag a
- * pipelined launch (norm or QK-norm + RoPE) or a matrix product sets if it ever gives up
- * waiting (after 100 ms) for its own shared-memory copies; the outputs of
- * such a launch are incomplete.
+ * pipelined launch (norm, QK-norm + RoPE, all-reduce), a matrix product
+ * (rmsq_fp8_block_matmul) or the attention's kernel of prompts sets if it ever
+ * gives up waiting (after 100 ms) for its own shared-memory copies, its matrix
+ * instructions or its other warps; the outputs of such a launch are incomplete,
+ * although the call that launched it has returned RMSQ_OK.
  * *flags = 0 when no launch gave up.  Synchronous with respect to the device:
  * call it after the launches of interest have completed.
  */

@@ -643,7 +643,8 @@ def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: tor
     last `window` keys.  Missing outputs and the workspace are allocated (rows
     of q behind query_start[R] are not computed).  variant: "auto", "direct"
     (few queries) or "pipelined" (prompts).  max_query: the most queries any
-    request has, if that is known; it lets "auto" choose better.  Returns out [tokens, heads, D], or
+    request has, if that is known; it lets "auto" choose better.  A launch that
+    gives up waiting shows in take_fault_flags.  Returns out [tokens, heads, D], or
     (out, lse [tokens, heads] fp32) with return_lse or a given lse.
     """
     vcode = _variant(variant)
@@ -704,7 +705,8 @@ def fp8_block_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, mode: str, b
     a_codes [m, k] and a_scales as fused_add_rmsnorm_quant or silu_mul_quant
     return them for `mode` ("fp8_group128_row" / "fp8_group128_col" with their
     options); b_codes [n, k] (uint8 or float8_e4m3fn) with b_scales fp32
-    [ceil(n / 128), k / 128].  out is bf16 or fp16, allocated if missing.
+    [ceil(n / 128), k / 128].  out is bf16 or fp16, allocated if missing.  A
+    launch that gives up waiting shows in take_fault_flags.
     """
     L, empty = load(), _empty_for(stream)
     if dtype not in DTYPES:
@@ -846,7 +848,9 @@ def set_programmatic_launch(enable: bool) -> None:
 
 
 def take_fault_flags() -> int:
-    """Read and clear the pipelined kernels' give-up flag (0 = none)."""
+    """Read and clear the flag of launches that gave up waiting (0 = none): the
+    pipelined kernels, the FP8 matrix product and the attention of prompts.  The
+    outputs of such a launch are incomplete."""
     f = ctypes.c_uint32()
     st = load().rmsq_take_fault_flags(ctypes.byref(f))
     if st:

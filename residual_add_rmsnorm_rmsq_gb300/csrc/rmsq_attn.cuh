@@ -16,7 +16,10 @@
 // by a power of two per row into f16's range, exact unless an element is
 // 2^-28 of the row's largest (then off by 2^-39 of it).  Probabilities are
 // rounded to f16 (11 bits; 8 would be as many as a bf16 output has), scaled by
-// 2^kPShift so that those down to 2^-23 of the maximum keep all their bits.
+// 2^kPShift so that those down to 2^-23 of the maximum keep all their bits.  With
+// 32-bit weights the relative error of fp16 outputs is 2.1e-4 and with these
+// 2.9e-4 (3 requests of up to 131071 keys, against 64 bits); bf16 outputs hide it
+// (1.7e-3 both ways).  The matrix unit's next wider type would halve its rate.
 //
 // Maxima are kept as logits and not as logits times f (the factor that turns
 // them into powers of two): the product's rounding, half a unit of its last
@@ -40,17 +43,17 @@
 // Bound by HBM and, nearly as much, by issue for long caches (9/16 byte per
 // element, K and V): 128 requests of 2048 to 8192 keys, 8 heads on each of 4 kv
 // heads of 128, take 81 us for 390 MB (4.8 TB/s; 71 with the arithmetic left out,
-// 76 with the copies left out), 3 requests of up to 131071 keys on 8 kv heads 72
+// 76 with the copies left out), 3 requests of up to 131071 keys on 8 kv heads 73
 // us for 357 MB.  About 300 warp instructions per 16 keys and kv head are left, 64
 // of them conversions of codes, 64 multiplications by scales, 16 products.
 // Measured and not kept: the codes loaded straight into registers a step ahead
 // (116 us), a ring of bulk copies on mbarriers (111), 16 keys per softmax step
 // (111), a third stage (84), registers capped for five CTAs per SM (86).
 //
-// Work is split evenly over the CTAs whatever the lengths: the (request, row tile, kv head, 128-key tile)
-// tiles form one sequence, cut into equal runs; a CTA writes the items its
-// run holds whole, and leaves (O, m, l) in the workspace for the two that its
-// ends may cut, which a second launch joins in order.
+// Work is split evenly over the CTAs whatever the lengths: the (request, row
+// tile, kv head, 128-key tile) tiles form one sequence, cut into equal runs; a CTA
+// writes the items its run holds whole, and leaves (O, m, l, f) in the workspace
+// for the two that its ends may cut, which a second launch joins in order.
 #pragma once
 
 #include "rmsq_device.cuh"

@@ -13,12 +13,19 @@
 // dim come out as one 16-byte piece of V^T, the layout the product wants.
 //
 // Bound by the matrix unit in the limit (4 D flop per row and key; 16 products
-// of 72 clocks per tile and 128 keys at D = 128), and at present by the chain of
-// a tile: its products (1150 clocks), the hand-over (200), its softmax (2100: 520
-// to read the logits, 330 for the maximum, 1040 for the weights, the rest
-// hand-over) and the next products.  Two tiles hide half of that.  2478 and 2445
-// queries of 32 heads on contexts of 732 and 1574 keys: 203 us, 192 GFLOP (0.95
-// PFLOP/s; half the measured bf16 rate, 101 us).  Measured and not kept (against
+// of 72 clocks per tile and 128 keys at D = 128), and at present by two things.
+// One is the chain of a tile: its products (1150 clocks), the hand-over (200), its
+// softmax (2100: 520 to read the logits, 330 for the maximum, 1040 for the
+// weights, the rest hand-over) and the next products; two tiles hide half of
+// that.  128 keys take 1.80 to 1.92 us on contexts of 20000 to 100000.  The other
+// is what lies outside it: a CTA has all of tensor memory, so the next one's
+// request, queries and first conversion, and the last one's output, overlap with
+// nothing (8 to 10 us a CTA: 128 queries of 8 x 8 heads take 12 us on 128 keys and
+// 74 on 4000).  2478 and 2445 queries of 32 heads on contexts of 732 and 1574
+// keys: 204 us, 192 GFLOP (0.94 PFLOP/s; half the measured bf16 rate, 101 us), of
+// which the 80 steps of an SM are 147 and the starts and ends of its 4.1 CTAs and
+// the last round the rest.  Heads of 64: 2000 queries of 32 heads on 4000 keys 88
+// us, of 128 115.  Measured and not kept (against
 // 212 to 215 us): two threads per row (326: 88 registers a thread spill), one
 // issuing warp per tile (260, the two fall into step), the logits of 64 keys
 // in two buffers so that products run ahead (268: a product of 64 columns takes as
