@@ -110,3 +110,19 @@ def test_a_call_on_a_forked_stream_of_a_capture(rmsq_gpu):
         assert torch.equal(total, 2 * want.float())
     del junk
     assert rq.take_fault_flags() == 0
+
+
+@pytest.mark.parametrize("handle", [0, 1])
+def test_the_default_stream_by_its_handle(rmsq_gpu, handle):
+    """Given as a raw handle while another stream is current, the default stream
+    is a launching stream like any other."""
+    rq = rmsq_gpu
+    x = torch.randn(300, 1024, device="cuda").bfloat16()
+    want = [t.clone() for t in rq.quant(x, "fp8_group128_row")]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        for _ in range(10):
+            torch.full((300, 1024), 0xff, dtype=torch.uint8, device="cuda")
+            got = rq.quant(x, "fp8_group128_row", stream=handle)
+            torch.cuda.current_stream().wait_stream(torch.cuda.default_stream())
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
