@@ -40,7 +40,11 @@
  * (rmsq_build_slot_map), a paged key / value cache in NVFP4
  * (rmsq_kv_cache_store_nvfp4, rmsq_kv_cache_load_nvfp4) and causal attention
  * over it (rmsq_paged_attention_nvfp4); and the FP8 matrix product that
- * consumes the group-128 modes' outputs (rmsq_fp8_block_matmul).
+ * consumes the group-128 modes' outputs (rmsq_fp8_block_matmul).  For models of
+ * images and video, and for caches in 8 bits, the same block has QK-norm + RoPE
+ * with three positions per token (rmsq_qk_norm_mrope), a paged FP8 cache with a
+ * power-of-two scale per 16 tokens and head (rmsq_kv_cache_store_fp8,
+ * rmsq_kv_cache_load_fp8) and attention over it (rmsq_paged_attention_fp8).
  *
  * Conventions for every entry point:
  *   - Pointers marked "device" must be addressable by the current CUDA device
@@ -331,7 +335,40 @@ int rmsq_qk_norm_rope_ex(void *qkv, const int64_t *positions, const float *cos_s
                          int64_t n_tokens, int num_q_heads, int num_kv_heads, int head_dim, int is_neox,
                          int dtype, void *stream, int variant);
 
-/* Most requests of rmsq_build_slot_map and rmsq_paged_attention_nvfp4. */
+/*
+ * rmsq_qk_norm_mrope — rmsq_qk_norm_rope_ex with three positions per token
+ * (time, height, width: images and video in the text), the norm optional and
+ * the result in place or in a buffer of its own.
+ *  qkv            as there; read only if out is given.
+ *  out            device, T[n_tokens, (num_q_heads + num_kv_heads) head_dim],
+ *                 16-byte aligned: the q heads, then the k heads; overlapping no
+ *                 input.  NULL: in place on qkv.
+ *  positions      device, int64[3, n_tokens], 8-byte aligned: the times, the
+ *                 heights, the widths.  A token with one of its three outside
+ *                 [0, max_positions) is left unchanged (its row of out is not
+ *                 written).
+ *  cos_sin_cache  as there.  Angle i takes its cos and sin from the row of its
+ *                 axis's position.
+ *  q_weight, k_weight  as there, or both NULL: no norm, the heads are rotated
+ *                 only (eps is then not used).
+ *  section_t, section_h, section_w  number of angles of each axis, together
+ *                 head_dim / 2.
+ *  interleaved    0: the first section_t angles are the time's, the next
+ *                 section_h the height's, the others the width's.  1: angles 1,
+ *                 4, 7, .. (section_h of them) are the height's, 2, 5, 8, ..
+ *                 (section_w) the width's, all others the time's; they have to
+ *                 exist, 3 section_h - 1 and 3 section_w at most head_dim / 2.
+ * The arithmetic is that of rmsq_qk_norm_rope: three equal positions give its
+ * bits.  Both variants give the same bits.  Sections that do not add up, or do
+ * not fit, are RMSQ_ERR_INVALID_ARG.
+ */
+int rmsq_qk_norm_mrope(void *qkv, void *out, const int64_t *positions, const float *cos_sin_cache,
+                       int64_t max_positions, const void *q_weight, const void *k_weight, float eps,
+                       int64_t n_tokens, int num_q_heads, int num_kv_heads, int head_dim, int section_t,
+                       int section_h, int section_w, int interleaved, int is_neox, int dtype, void *stream,
+                       int variant);
+
+/* Most requests of rmsq_build_slot_map and of the attention over a paged cache. */
 #define RMSQ_MAX_REQUESTS 8192
 
 /* Bits of rmsq_build_slot_map's status. */
@@ -485,6 +522,46 @@ int rmsq_paged_attention_nvfp4_ex(const void *q, int64_t q_stride, const void *k
  * MB: one workspace serves the calls of a program that follow one another). */
 size_t rmsq_paged_attention_workspace_bytes(int64_t n_tokens, int64_t num_requests, int num_heads,
                                             int num_kv_heads, int head_dim);
+
+/*
+ * The paged FP8 cache: codes, device, u8 (E4M3) [num_pages, 2, num_kv_heads,
+ * page_size, head_dim], 16-byte aligned, keys at index 0 and values at index 1
+ * of the second axis; and scales, device, u8 [num_pages, 2, num_kv_heads,
+ * page_size / 16], one for each block of 16 tokens and head: byte b stands for
+ * 2^(b - 127) (bytes are read as if they were at least 1 and at most 187, 2^60).
+ * Slot s is token s % page_size of page s / page_size; an element stands for
+ * code * scale.
+ *
+ * rmsq_kv_cache_store_fp8 — quantises the key and value heads of n_tokens tokens
+ * into the cache.  For each block of 16 slots and head that receives tokens, with
+ * amax their largest finite magnitude,
+ *   s = 2^ceil(log2 max(amax / 448, 1e-12))       (at most 2^60)
+ * as RMSQ_QUANT_E8M0 has it; if the block's first slot is not among those
+ * received the block is one that is partly filled, and s is at least the scale it
+ * has.  Codes are e4m3(x / s).  The block's other slots keep their values: if the
+ * scale has grown their codes are rounded to it (exact unless they become
+ * subnormal).  Magnitudes above 448 * 2^60 saturate.  An element that is not
+ * finite is stored as NaN, and so are then all key codes of that token and head,
+ * so that every query that attends to the token gives NaN, and no other.
+ * rmsq_kv_cache_load_fp8 — reads tokens back: T(code * scale), rounded once.
+ *  k, v, their strides, head_dim, page_size, n_tokens: as for the NVFP4 cache.
+ *  slot_map      device, int64[n_tokens].  A token whose slot lies outside
+ *                [0, num_pages * page_size) is skipped by the store and read as
+ *                zeros by the load.  Of the store's, those of one block of 16
+ *                have to be consecutive entries and ascend, as
+ *                rmsq_build_slot_map writes them; what a block holds after a
+ *                call where they do not is not specified (other blocks are not
+ *                concerned).  The load takes any slots.
+ * Deterministic.  No output may overlap an input; the load's k and v rows may
+ * interleave in one buffer.  Asynchronous on `stream`.
+ */
+int rmsq_kv_cache_store_fp8(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                            const int64_t *slot_map, void *cache, uint8_t *scales, int64_t num_pages,
+                            int64_t page_size, int64_t n_tokens, int num_kv_heads, int head_dim, int dtype,
+                            void *stream);
+int rmsq_kv_cache_load_fp8(const void *cache, const uint8_t *scales, int64_t num_pages, int64_t page_size,
+                           const int64_t *slot_map, void *k, int64_t k_stride, void *v, int64_t v_stride,
+                           int64_t n_tokens, int num_kv_heads, int head_dim, int dtype, void *stream);
 
 /* Most ranks rmsq_allreduce_add_rmsnorm_quant sums. */
 #define RMSQ_MAX_ALLREDUCE_RANKS 8

@@ -71,9 +71,11 @@ EXPORTS = ("rmsq_fused_add_rmsnorm_quant", "rmsq_fused_add_rmsnorm_quant_ex",
            "rmsq_fused_add_rmsnorm_nvfp4_dynamic", "rmsq_nvfp4_dynamic_workspace_bytes",
            "rmsq_fused_add_rmsnorm_nvfp4_dynamic_noalloc", "rmsq_silu_mul_quant",
            "rmsq_fused_add_rmsnorm", "rmsq_quant", "rmsq_qk_norm_rope", "rmsq_qk_norm_rope_ex",
+           "rmsq_qk_norm_mrope",
            "rmsq_allreduce_add_rmsnorm_quant",
            "rmsq_build_slot_map", "rmsq_kv_cache_store_nvfp4", "rmsq_kv_cache_load_nvfp4",
            "rmsq_paged_attention_nvfp4", "rmsq_paged_attention_nvfp4_ex", "rmsq_paged_attention_workspace_bytes",
+           "rmsq_kv_cache_store_fp8", "rmsq_kv_cache_load_fp8",
            "rmsq_fp8_block_matmul",
            "rmsq_set_pipeline_config", "rmsq_set_programmatic_launch", "rmsq_take_fault_flags",
            "rmsq_query_sizes", "rmsq_query_launch", "rmsq_debug_convert", "rmsq_debug_activation", "rmsq_debug_bounded_wait",
@@ -122,6 +124,8 @@ def load(path: str | None = None):
         L.rmsq_qk_norm_rope.restype = ci
         L.rmsq_qk_norm_rope_ex.argtypes = [vp, vp, vp, i64, vp, vp, f32, i64, ci, ci, ci, ci, ci, vp, ci]
         L.rmsq_qk_norm_rope_ex.restype = ci
+        L.rmsq_qk_norm_mrope.argtypes = [vp, vp, vp, vp, i64, vp, vp, f32, i64, ci, ci, ci, ci, ci, ci, ci, ci, ci, vp, ci]
+        L.rmsq_qk_norm_mrope.restype = ci
         L.rmsq_allreduce_add_rmsnorm_quant.argtypes = [ctypes.POINTER(vp), ci, vp, vp, f32, ci, vp, vp, vp, vp,
                                                        i64, i64, ci, vp]
         L.rmsq_allreduce_add_rmsnorm_quant.restype = ci
@@ -131,6 +135,10 @@ def load(path: str | None = None):
         L.rmsq_kv_cache_store_nvfp4.restype = ci
         L.rmsq_kv_cache_load_nvfp4.argtypes = [vp, i64, i64, vp, vp, vp, vp, i64, vp, i64, i64, ci, ci, ci, vp]
         L.rmsq_kv_cache_load_nvfp4.restype = ci
+        L.rmsq_kv_cache_store_fp8.argtypes = [vp, i64, vp, i64, vp, vp, vp, i64, i64, i64, ci, ci, ci, vp]
+        L.rmsq_kv_cache_store_fp8.restype = ci
+        L.rmsq_kv_cache_load_fp8.argtypes = [vp, vp, i64, i64, vp, vp, i64, vp, i64, i64, ci, ci, ci, vp]
+        L.rmsq_kv_cache_load_fp8.restype = ci
         L.rmsq_paged_attention_nvfp4.argtypes = [vp, i64, vp, i64, i64, vp, i64, vp, vp, vp, vp, f32, i64, vp, vp, vp,
                                                  ctypes.c_size_t, i64, i64, ci, ci, ci, ci, vp, ci]
         L.rmsq_paged_attention_nvfp4.restype = ci
@@ -468,6 +476,46 @@ def _token_rows(name: str, t: torch.Tensor) -> int:
     return per_token if n > 1 else h * d
 
 
+def qk_norm_mrope(qkv: torch.Tensor, positions: torch.Tensor, cos_sin_cache: torch.Tensor,
+                  q_weight: torch.Tensor | None, k_weight: torch.Tensor | None, eps: float, num_q_heads: int,
+                  num_kv_heads: int, head_dim: int, sections, is_neox: bool = True, *, interleaved: bool = False,
+                  out: torch.Tensor | None = None, stream=None, variant: str = "auto") -> torch.Tensor:
+    """rmsq_qk_norm_mrope: QK-norm + RoPE with three positions per token.
+
+    qkv [n, (q heads + 2 kv heads) D]; positions int64 [3, n] (time, height,
+    width); sections: the number of angles of each axis, together D / 2, one
+    after the other or (interleaved) alternating.  q_weight and k_weight None:
+    no norm.  In place on qkv, or with `out` [n, (q heads + kv heads) D] there.
+    Returns where the heads are.  variant "auto", "direct" or "pipelined"
+    (bit-identical results).
+    """
+    vcode = _variant(variant)
+    L = load()
+    dt = _act_types(qkv)
+    t, h, w = (int(s) for s in sections)
+    n = qkv.shape[0]
+    width = (num_q_heads + 2 * num_kv_heads) * head_dim
+    i = qkv.get_device()
+    given = {"qkv": qkv, "positions": positions, "cos_sin_cache": cos_sin_cache, "q_weight": q_weight,
+             "k_weight": k_weight, "out": out}
+    _check_tensors(given, {"qkv": dt, "positions": _I64, "cos_sin_cache": _F32, "q_weight": dt, "k_weight": dt, "out": dt})
+    _want_shape("qkv", qkv, n, width)
+    _want_shape("positions", positions, 3, n)
+    _want_shape("cos_sin_cache", cos_sin_cache, cos_sin_cache.shape[0], head_dim)
+    for name, t_ in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t_ is not None:
+            _want_shape(name, t_, head_dim)
+    if out is not None:
+        _want_shape("out", out, n, width - num_kv_heads * head_dim)
+    st = L.rmsq_qk_norm_mrope(qkv.data_ptr(), _p(out), positions.data_ptr(), cos_sin_cache.data_ptr(),
+                              cos_sin_cache.shape[0], _p(q_weight), _p(k_weight), eps, n, num_q_heads, num_kv_heads,
+                              head_dim, t, h, w, 1 if interleaved else 0, 1 if is_neox else 0, DTYPES[dt],
+                              _stream(stream, i), vcode)
+    if st:
+        raise RmsqError(st, "rmsq_qk_norm_mrope")
+    return qkv if out is None else out
+
+
 _I32, _I64, _F32, _U8 = torch.int32, torch.int64, torch.float32, torch.uint8
 _SLOT_TYPES = {"context_lens": _I32, "query_lens": _I32, "block_table": _I32, "free_pages": _I32, "num_free": _I32,
                "slot_map": _I64, "positions": _I64, "query_start": _I32, "seq_lens": _I32, "num_free_out": _I32,
@@ -623,6 +671,94 @@ def kv_cache_load_nvfp4(cache: torch.Tensor, slot_map: torch.Tensor, k_global_sc
     return k_out, v_out
 
 
+_CODE_TYPES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def kv_cache_shapes_fp8(num_pages: int, num_kv_heads: int, head_dim: int, page_size: int) -> tuple[tuple, tuple]:
+    """Shapes of the two tensors that hold a paged FP8 cache: the codes (uint8 or
+    float8_e4m3fn) and the uint8 scales of its blocks of 16 tokens."""
+    return (num_pages, 2, num_kv_heads, page_size, head_dim), (num_pages, 2, num_kv_heads, page_size // 16)
+
+
+def _cache_fp8(cache: torch.Tensor, scales: torch.Tensor) -> tuple[int, int, int, int]:
+    """(pages, kv heads, page size, head dim) of a paged FP8 cache, whose two
+    tensors have to fit each other."""
+    if cache.dtype not in _CODE_TYPES:
+        raise TypeError("cache must be uint8 or float8_e4m3fn")
+    if cache.dim() != 5 or cache.shape[1] != 2:
+        raise ValueError("cache must be [pages, 2, kv heads, page size, head_dim]")
+    pages, _, h, page, d = cache.shape
+    _want_shape("cache", cache, pages, 2, h, page, d)
+    if scales.dtype is not _U8:
+        raise TypeError(f"scales must be torch.uint8, got {scales.dtype}")
+    _want_shape("scales", scales, pages, 2, h, page // 16)
+    return pages, h, page, d
+
+
+def kv_cache_store_fp8(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor, cache: torch.Tensor,
+                       scales: torch.Tensor, *, stream=None) -> None:
+    """rmsq_kv_cache_store_fp8: k, v [n, kv heads, D] (token stride free, so
+    slices of a qkv buffer serve) quantised into `cache` and `scales`
+    (kv_cache_shapes_fp8) at slot_map (int64 [n], as build_slot_map writes it:
+    the slots of a block of 16 stand together and ascend); a slot outside the
+    cache skips its token."""
+    L = load()
+    dt = _act_types(k)
+    ks, vs = _token_rows("k", k), _token_rows("v", v)
+    n, h, d = k.shape
+    if v.shape != k.shape:
+        raise ValueError("k and v must have one shape")
+    pages, heads, page, dim = _cache_fp8(cache, scales)
+    if (heads, dim) != (h, d):
+        raise ValueError(f"the cache has {heads} heads of {dim}, k has {h} of {d}")
+    i = cache.get_device()
+    if not (_is_current(i) and scales.get_device() == i and _fits(slot_map, _I64, i, (n,)) and k.get_device() == i and
+            v.get_device() == i and v.dtype is dt):
+        _check_tensors({"k": k, "v": v, "slot_map": slot_map, "cache": cache, "scales": scales},
+                       {"k": dt, "v": dt, "slot_map": _I64, "cache": cache.dtype, "scales": _U8})
+        _want_shape("slot_map", slot_map, n)
+    st = L.rmsq_kv_cache_store_fp8(k.data_ptr(), ks, v.data_ptr(), vs, slot_map.data_ptr(), cache.data_ptr(),
+                                   scales.data_ptr(), pages, page, n, h, d, DTYPES[dt], _stream(stream, i))
+    if st:
+        raise RmsqError(st, "rmsq_kv_cache_store_fp8")
+
+
+def kv_cache_load_fp8(cache: torch.Tensor, scales: torch.Tensor, slot_map: torch.Tensor,
+                      dtype: torch.dtype = torch.bfloat16, *, k_out: torch.Tensor | None = None,
+                      v_out: torch.Tensor | None = None, stream=None):
+    """rmsq_kv_cache_load_fp8: the tokens at slot_map (int64 [n]) as two
+    [n, kv heads, D] tensors of `dtype`; zeros for a slot outside the cache.
+    Missing outputs are allocated.  Returns (k, v)."""
+    L, empty = load(), _empty_for(stream)
+    if dtype not in DTYPES:
+        raise TypeError(f"unsupported activation dtype {dtype}")
+    pages, h, page, d = _cache_fp8(cache, scales)
+    n = slot_map.shape[0]
+    shape = (n, h, d)
+    ks = vs = h * d
+    if k_out is None:
+        k_out = empty(shape, dtype=dtype, device=cache.device)
+    else:
+        ks = _token_rows("k_out", k_out)
+    if v_out is None:
+        v_out = empty(shape, dtype=dtype, device=cache.device)
+    else:
+        vs = _token_rows("v_out", v_out)
+    i = cache.get_device()
+    if not (_is_current(i) and scales.get_device() == i and _fits(slot_map, _I64, i, (n,)) and k_out.get_device() == i and
+            v_out.get_device() == i and k_out.dtype is dtype and v_out.dtype is dtype):
+        _check_tensors({"cache": cache, "scales": scales, "slot_map": slot_map, "k_out": k_out, "v_out": v_out},
+                       {"cache": cache.dtype, "scales": _U8, "slot_map": _I64, "k_out": dtype, "v_out": dtype})
+        _want_shape("slot_map", slot_map, n)
+    if k_out.shape != shape or v_out.shape != shape:
+        raise ValueError(f"outputs must have shape {shape}")
+    st = L.rmsq_kv_cache_load_fp8(cache.data_ptr(), scales.data_ptr(), pages, page, slot_map.data_ptr(), k_out.data_ptr(),
+                                  ks, v_out.data_ptr(), vs, n, h, d, DTYPES[dtype], _stream(stream, i))
+    if st:
+        raise RmsqError(st, "rmsq_kv_cache_load_fp8")
+    return k_out, v_out
+
+
 def paged_attention_workspace_bytes(n_tokens: int, num_requests: int, num_heads: int, num_kv_heads: int,
                                     head_dim: int) -> int:
     return load().rmsq_paged_attention_workspace_bytes(n_tokens, num_requests, num_heads, num_kv_heads, head_dim)
@@ -692,9 +828,6 @@ def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: tor
     if st:
         raise RmsqError(st, "rmsq_paged_attention_nvfp4")
     return out if lse is None else (out, lse)
-
-
-_CODE_TYPES = (torch.uint8, torch.float8_e4m3fn)
 
 
 def fp8_block_matmul(a_codes: torch.Tensor, a_scales: torch.Tensor, mode: str, b_codes: torch.Tensor,

@@ -4,7 +4,7 @@
 
 namespace rmsq {
 cudaError_t launch_qk_norm_rope(const QkLaunch& l, cudaStream_t stream) {
-    QkArgs a;
+    QkArgs a = {};
     a.qkv = static_cast<uint32_t*>(l.qkv);
     a.pos = l.positions;
     a.cs = l.cos_sin;
@@ -16,8 +16,8 @@ cudaError_t launch_qk_norm_rope(const QkLaunch& l, cudaStream_t stream) {
     a.n = l.n;
     a.nq = l.nq;
     a.nkv = l.nkv;
-    return l.fp16 ? launch_qk<Fp16T>(a, l.head_dim, l.neox, l.variant, stream)
-                  : launch_qk<Bf16T>(a, l.head_dim, l.neox, l.variant, stream);
+    return l.fp16 ? launch_qk<Fp16T, kOneAxis>(a, l.head_dim, l.neox, l.variant, stream)
+                  : launch_qk<Bf16T, kOneAxis>(a, l.head_dim, l.neox, l.variant, stream);
 }
 cudaError_t take_pipe_fault_qk(unsigned int* out) { return take_pipe_fault(out); }
 }  // namespace rmsq

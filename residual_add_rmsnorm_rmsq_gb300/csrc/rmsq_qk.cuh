@@ -20,15 +20,33 @@
 // position; every product and sum is rounded separately and the result is
 // rounded once to the activation type.  v heads are not touched; a token
 // whose position is outside [0, max_pos) is left unchanged.
+//
+// With three positions per token (time, height, width; AXES below) every angle
+// belongs to an axis and takes its cos / sin from that axis's row.  Bound by
+// HBM like the one-axis form: the rows come from L2.  The pipelined kernel
+// copies the three rows beside the heads, and a lane keeps the places of its
+// angles in registers for all tokens, so that a token costs no selection: two
+// 16-byte reads each of cos and sin where every aligned group of four angles
+// has one axis (sections that are multiples of four), eight 4-byte ones
+// otherwise (axes that alternate).
 #pragma once
+
+#include <type_traits>
 
 #include "rmsq_dispatch.cuh"
 
 namespace rmsq {
 
+// How a token's angles find their rows of the cos / sin table.
+constexpr int kOneAxis = 0;     // one position per token
+constexpr int kQuadAxes = 1;    // three; angles 4i .. 4i + 3 share an axis
+constexpr int kAnyAxes = 2;     // three; any assignment
+template <int AXES>
+constexpr int kQkRows = AXES == kOneAxis ? 1 : 3;
+
 struct QkArgs {
     uint32_t* qkv;            // [n, (nq + 2 nkv) D] T, as 32-bit words
-    const int64_t* pos;       // [n]
+    const int64_t* pos;       // [n], with three axes [3, n]
     const float* cs;          // [max_pos, D]: cos (D/2), sin (D/2)
     int64_t max_pos;
     const uint32_t* qw;       // [D] T
@@ -36,7 +54,17 @@ struct QkArgs {
     float eps;
     float inv_d;              // 1 / D (exact: D is a power of two)
     int n, nq, nkv;
+    // With three axes only:
+    uint32_t* out;            // destination of the heads (qkv in place)
+    int64_t out_words;        // words between its tokens
+    uint32_t axis_h[4], axis_w[4];   // bit i: angle i is the height's / the width's
 };
+
+// Axis of an angle.
+__device__ __forceinline__ int qk_axis(const QkArgs& a, int angle) {
+    return static_cast<int>(a.axis_h[angle >> 5] >> (angle & 31) & 1u) +
+           2 * static_cast<int>(a.axis_w[angle >> 5] >> (angle & 31) & 1u);
+}
 
 // A lane holds 16 elements of its head (two blocks of 8); a head takes D / 16
 // lanes (4, 8 or 16), so one warp works on 32 * 16 / D heads of a token
@@ -67,13 +95,30 @@ struct CsRegs {
 template <int D, bool NEOX>
 struct CsSmem {
     const float* row;   // the token's cos / sin row
-    int g;
+    const int (&lane)[1];   // the lane within its head
     __device__ __forceinline__ float4 cos4(int q) const {
-        return *reinterpret_cast<const float4*>(row + qk_angle<D, NEOX>(g, q));
+        return *reinterpret_cast<const float4*>(row + qk_angle<D, NEOX>(lane[0], q));
     }
     __device__ __forceinline__ float4 sin4(int q) const {
-        return *reinterpret_cast<const float4*>(row + D / 2 + qk_angle<D, NEOX>(g, q));
+        return *reinterpret_cast<const float4*>(row + D / 2 + qk_angle<D, NEOX>(lane[0], q));
     }
+};
+
+// The same from three rows in shared memory, one behind the other: the lane's
+// angles at word offsets `off` of the cosines (the sines D / 2 further on).
+template <int D, int AXES>
+struct CsSmemAxes {
+    static constexpr int N = AXES == kQuadAxes ? 2 : 8;
+    const float* rows;
+    const int (&off)[N];
+    __device__ __forceinline__ float4 at(const float* p, int q) const {
+        if constexpr (AXES == kQuadAxes)
+            return *reinterpret_cast<const float4*>(p + off[q]);
+        else
+            return make_float4(p[off[4 * q]], p[off[4 * q + 1]], p[off[4 * q + 2]], p[off[4 * q + 3]]);
+    }
+    __device__ __forceinline__ float4 cos4(int q) const { return at(rows, q); }
+    __device__ __forceinline__ float4 sin4(int q) const { return at(rows + D / 2, q); }
 };
 
 __device__ __forceinline__ float f4_at(const float4& v, int i) {
@@ -83,10 +128,10 @@ __device__ __forceinline__ float f4_at(const float4& v, int i) {
 // One head group's arithmetic, shared by both kernels.  xw / ww: the lane's
 // elements and weights as T pairs (words 0..3 the low block, 4..7 the high
 // block); `cs` gives its angles.  Returns the rotated, normed elements in the
-// same layout.
+// same layout.  Without `norm` (and with weights of one) they are rotated only.
 template <class E, int D, bool NEOX, class CS>
 __device__ __forceinline__ void qk_head_math(const uint32_t (&xw)[8], const uint32_t (&ww)[8], const CS& cs,
-                                             float eps, float inv_d, uint32_t (&ow)[8]) {
+                                             float eps, float inv_d, uint32_t (&ow)[8], bool norm = true) {
     constexpr int LPH = D / kQkEpl;
     float x[16];   // x[0..7] the low block, x[8..15] the high block
 #pragma unroll
@@ -113,7 +158,7 @@ __device__ __forceinline__ void qk_head_math(const uint32_t (&xw)[8], const uint
     const float sum = __fadd_rn(h.x, h.y);   // low half + high half
     // 1 / sqrt(...) as two correctly rounded steps (the reciprocal's value is
     // the IEEE division 1 / s)
-    const float inv = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sum, inv_d), eps)));
+    const float inv = norm ? __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sum, inv_d), eps))) : 1.0f;
     // y = (x * inv) * w, two elements an instruction (products only: nothing
     // to contract)
     float y[16];
@@ -172,7 +217,7 @@ __device__ __forceinline__ void unpack2(const uint4& a, const uint4& b, uint32_t
 // Warp kernel (few tokens): each warp takes one head group of one token,
 // loads straight into registers, computes and stores; warps stride over the
 // n * (head groups per token) work items.
-template <class E, int D, bool NEOX>
+template <class E, int D, bool NEOX, int AXES>
 __global__ void __launch_bounds__(256, RMSQ_QK_MIN_BLOCKS) qk_norm_rope_kernel(const QkArgs a) {
     constexpr int LPH = D / kQkEpl;             // lanes per head
     constexpr int HPW = 32 / LPH;               // heads per warp
@@ -188,29 +233,63 @@ __global__ void __launch_bounds__(256, RMSQ_QK_MIN_BLOCKS) qk_norm_rope_kernel(c
     for (int w = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); w < total; w += step) {
         const int t = w / chunks;
         const int hd = (w - t * chunks) * HPW + r;
-        const int64_t p = __ldg(a.pos + t);
-        if (p < 0 || p >= a.max_pos) continue;   // the same for the whole warp
+        int64_t p[kQkRows<AXES>];
+        bool inside = true;
+#pragma unroll
+        for (int i = 0; i < kQkRows<AXES>; ++i) {
+            p[i] = __ldg(a.pos + static_cast<int64_t>(i) * a.n + t);
+            inside = inside && p[i] >= 0 && p[i] < a.max_pos;
+        }
+        if (!inside) continue;   // the same for the whole warp
         const bool live = hd < heads;
         // loads first: the head's elements, its weight, the token's cos / sin
         uint32_t xw[8] = {}, ww[8] = {};
         uint32_t* hp = a.qkv + (int64_t)t * width_words + hd * (D / 2);
+        const uint32_t* wp = hd < a.nq ? a.qw : a.kw;
+        const bool norm = AXES == kOneAxis || a.qw != nullptr;
         if (live) {
-            const uint32_t* wp = hd < a.nq ? a.qw : a.kw;
             unpack2(ld_act(reinterpret_cast<const uint4*>(hp + qk_block_word<D>(g, 0))),
                     ld_act(reinterpret_cast<const uint4*>(hp + qk_block_word<D>(g, 1))), xw);
-            unpack2(__ldg(reinterpret_cast<const uint4*>(wp + qk_block_word<D>(g, 0))),
-                    __ldg(reinterpret_cast<const uint4*>(wp + qk_block_word<D>(g, 1))), ww);
+            if (norm)
+                unpack2(__ldg(reinterpret_cast<const uint4*>(wp + qk_block_word<D>(g, 0))),
+                        __ldg(reinterpret_cast<const uint4*>(wp + qk_block_word<D>(g, 1))), ww);
         }
-        const float* row = a.cs + p * D;
-        const float4 cv[2] = {__ldg(reinterpret_cast<const float4*>(row + qk_angle<D, NEOX>(g, 0))),
-                              __ldg(reinterpret_cast<const float4*>(row + qk_angle<D, NEOX>(g, 1)))};
-        const float4 sv[2] = {__ldg(reinterpret_cast<const float4*>(row + D / 2 + qk_angle<D, NEOX>(g, 0))),
-                              __ldg(reinterpret_cast<const float4*>(row + D / 2 + qk_angle<D, NEOX>(g, 1)))};
+        if (!norm) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ww[i] = E::pack(1.0f, 1.0f);
+        }
+        float4 cv[2], sv[2];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int angle = qk_angle<D, NEOX>(g, q);
+            if constexpr (AXES == kAnyAxes) {
+                float c[4], sn[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int axis = qk_axis(a, angle + i);
+                    const float* row = a.cs + (axis == 0 ? p[0] : axis == 1 ? p[1] : p[2]) * D + angle + i;
+                    c[i] = __ldg(row);
+                    sn[i] = __ldg(row + D / 2);
+                }
+                cv[q] = make_float4(c[0], c[1], c[2], c[3]);
+                sv[q] = make_float4(sn[0], sn[1], sn[2], sn[3]);
+            } else {
+                int64_t at = p[0];
+                if constexpr (AXES == kQuadAxes) {
+                    const int axis = qk_axis(a, angle);
+                    at = axis == 0 ? p[0] : axis == 1 ? p[1] : p[2];
+                }
+                const float* row = a.cs + at * D + angle;
+                cv[q] = __ldg(reinterpret_cast<const float4*>(row));
+                sv[q] = __ldg(reinterpret_cast<const float4*>(row + D / 2));
+            }
+        }
         uint32_t ow[8];
-        qk_head_math<E, D, NEOX>(xw, ww, CsRegs{cv, sv}, a.eps, a.inv_d, ow);
+        qk_head_math<E, D, NEOX>(xw, ww, CsRegs{cv, sv}, a.eps, a.inv_d, ow, norm);
         if (live) {
-            st_stream(reinterpret_cast<uint4*>(hp + qk_block_word<D>(g, 0)), make_uint4(ow[0], ow[1], ow[2], ow[3]));
-            st_stream(reinterpret_cast<uint4*>(hp + qk_block_word<D>(g, 1)), make_uint4(ow[4], ow[5], ow[6], ow[7]));
+            uint32_t* op = AXES == kOneAxis ? hp : a.out + t * a.out_words + hd * (D / 2);
+            st_stream(reinterpret_cast<uint4*>(op + qk_block_word<D>(g, 0)), make_uint4(ow[0], ow[1], ow[2], ow[3]));
+            st_stream(reinterpret_cast<uint4*>(op + qk_block_word<D>(g, 1)), make_uint4(ow[4], ow[5], ow[6], ow[7]));
         }
     }
 }
@@ -241,8 +320,8 @@ constexpr int kQkPipeMaxThreads = 512;
 #endif
 static_assert(RMSQ_QK_PIPE_MAXNREG <= 64, "a 512-thread CTA must fit the SM's registers");
 
-template <class E, int D, bool NEOX>
-__global__ void __maxnreg__(RMSQ_QK_PIPE_MAXNREG)
+template <class E, int D, bool NEOX, int AXES>
+__global__ void __maxnreg__(AXES == kOneAxis ? RMSQ_QK_PIPE_MAXNREG : 64)
     qk_pipe_kernel(const QkArgs a, const int stages, const uint32_t stage_bytes) {
     constexpr int LPH = D / kQkEpl, HPW = 32 / LPH;
     extern __shared__ __align__(128) unsigned char ring[];
@@ -265,46 +344,87 @@ __global__ void __maxnreg__(RMSQ_QK_PIPE_MAXNREG)
     grid_dependency_wait();
     __syncthreads();
 
-    // Thread 0: start the copies of token k (position p) into stage s.
+    // One thread: start the copies of token k (positions p) into stage s.
+    constexpr int ROWS = kQkRows<AXES>;
     uint64_t pol_first = 0, pol_keep = 0;
-    auto issue = [&](int k, int s, int64_t p) {
+    auto issue = [&](int k, int s, const int64_t (&p)[ROWS]) {
         const int t = blockIdx.x + k * G;
         unsigned char* dst = ring + (size_t)s * stage_bytes;
-        const bool valid = p >= 0 && p < a.max_pos;
-        s_pos[s] = p;
-        mbar_arrive_expect_tx(&full[s], head_bytes + (valid ? D * 4u : 0u));
+        bool valid = true;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) valid = valid && p[i] >= 0 && p[i] < a.max_pos;
+        s_pos[s] = AXES == kOneAxis || valid ? p[0] : -1;
+        mbar_arrive_expect_tx(&full[s], head_bytes + (valid ? ROWS * D * 4u : 0u));
         bulk_g2s(dst, a.qkv + (int64_t)t * width_words, head_bytes, &full[s], pol_first);
-        if (valid) bulk_g2s(dst + head_bytes, a.cs + p * D, D * 4u, &full[s], pol_keep);
+        if (valid) {
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) bulk_g2s(dst + head_bytes + i * D * 4u, a.cs + p[i] * D, D * 4u, &full[s], pol_keep);
+        }
     };
-    int64_t p_next = -1;   // thread 0: position of the next token to issue
-    if (tid == 0) {
+    auto load_pos = [&](int t, int64_t (&p)[ROWS]) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) p[i] = __ldg(a.pos + static_cast<int64_t>(i) * a.n + t);
+    };
+    int64_t p_next[ROWS];   // thread 0: positions of the next token to issue
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) p_next[i] = -1;
+    if constexpr (AXES != kOneAxis) {
+        if (tid < 32) {
+            // a lane per stage: the first tokens' positions in one latency
+            pol_first = l2_policy_evict_first();
+            pol_keep = l2_policy_evict_normal();
+            if (tid < stages && blockIdx.x + tid * G < a.n) {
+                int64_t p[ROWS];
+                load_pos(blockIdx.x + tid * G, p);
+                issue(tid, tid, p);
+            }
+            const int t = blockIdx.x + stages * G;
+            if (tid == 0 && t < a.n) load_pos(t, p_next);
+        }
+    } else if (tid == 0) {
         pol_first = l2_policy_evict_first();
         pol_keep = l2_policy_evict_normal();
-        int64_t pp[kQkMaxStages];
+        int64_t pp[kQkMaxStages][1];
 #pragma unroll
         for (int k = 0; k < kQkMaxStages; ++k) {
             const int t = blockIdx.x + k * G;
-            pp[k] = (k < stages && t < a.n) ? __ldg(a.pos + t) : -1;
+            pp[k][0] = (k < stages && t < a.n) ? __ldg(a.pos + t) : -1;
         }
 #pragma unroll
         for (int k = 0; k < kQkMaxStages; ++k)
             if (k < stages && blockIdx.x + k * G < a.n) issue(k, k, pp[k]);
         const int t = blockIdx.x + stages * G;
-        if (t < a.n) p_next = __ldg(a.pos + t);
+        if (t < a.n) load_pos(t, p_next);
     }
 
     // The weight words of the warp's head group (the same for every token
     // while the warp has one group; reloaded per token otherwise).
-    uint32_t ww[8] = {};
+    const bool norm = AXES == kOneAxis || a.qw != nullptr;
+    uint32_t ww[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ww[i] = norm ? 0u : E::pack(1.0f, 1.0f);
     auto load_w = [&](int c) {
         const int hd = c * HPW + r;
-        if (hd < heads) {
+        if (norm && hd < heads) {
             const uint32_t* wp = hd < a.nq ? a.qw : a.kw;
             unpack2(__ldg(reinterpret_cast<const uint4*>(wp + qk_block_word<D>(g, 0))),
                     __ldg(reinterpret_cast<const uint4*>(wp + qk_block_word<D>(g, 1))), ww);
         }
     };
     load_w(warp);
+    // where the lane's angles lie in a token's rows
+    using Cs = typename std::conditional<AXES == kOneAxis, CsSmem<D, NEOX>, CsSmemAxes<D, AXES>>::type;
+    int off[AXES == kOneAxis ? 1 : AXES == kQuadAxes ? 2 : 8];
+    if constexpr (AXES == kOneAxis) {
+        off[0] = g;
+    } else {
+        constexpr int N = AXES == kQuadAxes ? 1 : 4;
+#pragma unroll
+        for (int i = 0; i < 2 * N; ++i) {
+            const int angle = qk_angle<D, NEOX>(g, i / N) + i % N;
+            off[i] = qk_axis(a, angle) * D + angle;
+        }
+    }
 
     int k = 0, s = 0;
     uint32_t parity = 0;   // stage s and its phase, advanced per token (no division)
@@ -315,9 +435,9 @@ __global__ void __maxnreg__(RMSQ_QK_PIPE_MAXNREG)
         // one answer per warp: the head math below shuffles across all lanes
         const bool ok = __all_sync(kFull, mbar_wait_bounded(&full[s], parity));
         const int64_t p = s_pos[s];
-        if (ok && p >= 0 && p < a.max_pos) {
+        if (ok && p >= 0 && (AXES != kOneAxis || p < a.max_pos)) {
             const unsigned char* st = ring + (size_t)s * stage_bytes;
-            const CsSmem<D, NEOX> cs{reinterpret_cast<const float*>(st + head_bytes), g};
+            const Cs cs{reinterpret_cast<const float*>(st + head_bytes), off};
             for (int c = warp; c < chunks; c += nwarps) {
                 const int hd = c * HPW + r;
                 const bool live = hd < heads;
@@ -329,10 +449,10 @@ __global__ void __maxnreg__(RMSQ_QK_PIPE_MAXNREG)
                             *reinterpret_cast<const uint4*>(sp + qk_block_word<D>(g, 1)), xw);
                 }
                 uint32_t ow[8];
-                qk_head_math<E, D, NEOX>(xw, ww, cs, a.eps, a.inv_d, ow);
+                qk_head_math<E, D, NEOX>(xw, ww, cs, a.eps, a.inv_d, ow, norm);
                 if (chunks > nwarps && c + nwarps >= chunks) load_w(warp);   // back to the first group
                 if (live) {
-                    uint32_t* hp = a.qkv + (int64_t)t * width_words + hd * (D / 2);
+                    uint32_t* hp = (AXES == kOneAxis ? a.qkv + (int64_t)t * width_words : a.out + t * a.out_words) + hd * (D / 2);
                     st_stream(reinterpret_cast<uint4*>(hp + qk_block_word<D>(g, 0)),
                               make_uint4(ow[0], ow[1], ow[2], ow[3]));
                     st_stream(reinterpret_cast<uint4*>(hp + qk_block_word<D>(g, 1)),
@@ -348,7 +468,7 @@ __global__ void __maxnreg__(RMSQ_QK_PIPE_MAXNREG)
         if (tid == 0 && blockIdx.x + (k + stages) * G < a.n) {
             issue(k + stages, s, p_next);
             const int tn = blockIdx.x + (k + stages + 1) * G;
-            if (tn < a.n) p_next = __ldg(a.pos + tn);
+            if (tn < a.n) load_pos(tn, p_next);
         }
         if (++s == stages) {
             s = 0;
@@ -365,9 +485,9 @@ __global__ void __maxnreg__(RMSQ_QK_PIPE_MAXNREG)
 }
 
 // Ring stage of the pipelined form: the q and k heads of a token and its
-// cos / sin row, rounded up to 128 bytes.
-inline uint32_t qk_stage_bytes(int heads, int head_dim) {
-    return (static_cast<uint32_t>(heads) * head_dim * 2 + head_dim * 4 + 127u) / 128u * 128u;
+// cos / sin rows, rounded up to 128 bytes.
+inline uint32_t qk_stage_bytes(int heads, int head_dim, int rows) {
+    return (static_cast<uint32_t>(heads) * head_dim * 2 + rows * head_dim * 4 + 127u) / 128u * 128u;
 }
 
 // Stages of the ring: about 24 KB of copies per CTA, 2 to kQkMaxStages
@@ -384,7 +504,7 @@ inline int qk_stages(uint32_t stage_bytes) {
 // Pipelined when asked for (or, for AUTO, from eight tokens per SM up: below
 // that the warp kernel's lower latency wins on GB300) and two stages fit the
 // shared-memory budget; otherwise the warp kernel.
-template <class E>
+template <class E, int AXES>
 cudaError_t launch_qk(const QkArgs& a, int head_dim, bool neox, int variant, cudaStream_t stream) {
     cudaError_t err = cudaSuccess;
     const int sms = sm_count(&err);
@@ -392,16 +512,16 @@ cudaError_t launch_qk(const QkArgs& a, int head_dim, bool neox, int variant, cud
     const int hpw = 32 * kQkEpl / head_dim;
     const int heads = a.nq + a.nkv;
     const int chunks = (heads + hpw - 1) / hpw;
-    const uint32_t stage_bytes = qk_stage_bytes(heads, head_dim);
+    const uint32_t stage_bytes = qk_stage_bytes(heads, head_dim, kQkRows<AXES>);
     const bool fits = 2u * stage_bytes <= static_cast<uint32_t>(kPipeSmemBudget);
     const bool pipe = fits && variant != kVariantDirect && (variant == kVariantPipelined || a.n >= 8 * sms);
     QkArgs args = a;
     if (pipe) {
         const void* fn = nullptr;
         switch (head_dim) {
-        case 64: fn = neox ? (const void*)&qk_pipe_kernel<E, 64, true> : (const void*)&qk_pipe_kernel<E, 64, false>; break;
-        case 128: fn = neox ? (const void*)&qk_pipe_kernel<E, 128, true> : (const void*)&qk_pipe_kernel<E, 128, false>; break;
-        case 256: fn = neox ? (const void*)&qk_pipe_kernel<E, 256, true> : (const void*)&qk_pipe_kernel<E, 256, false>; break;
+        case 64: fn = neox ? (const void*)&qk_pipe_kernel<E, 64, true, AXES> : (const void*)&qk_pipe_kernel<E, 64, false, AXES>; break;
+        case 128: fn = neox ? (const void*)&qk_pipe_kernel<E, 128, true, AXES> : (const void*)&qk_pipe_kernel<E, 128, false, AXES>; break;
+        case 256: fn = neox ? (const void*)&qk_pipe_kernel<E, 256, true, AXES> : (const void*)&qk_pipe_kernel<E, 256, false, AXES>; break;
         default: return cudaErrorInvalidValue;
         }
         // warps: the token's head groups spread evenly, at most 16
@@ -425,9 +545,9 @@ cudaError_t launch_qk(const QkArgs& a, int head_dim, bool neox, int variant, cud
     }
     const void* fn = nullptr;
     switch (head_dim) {
-    case 64: fn = neox ? (const void*)&qk_norm_rope_kernel<E, 64, true> : (const void*)&qk_norm_rope_kernel<E, 64, false>; break;
-    case 128: fn = neox ? (const void*)&qk_norm_rope_kernel<E, 128, true> : (const void*)&qk_norm_rope_kernel<E, 128, false>; break;
-    case 256: fn = neox ? (const void*)&qk_norm_rope_kernel<E, 256, true> : (const void*)&qk_norm_rope_kernel<E, 256, false>; break;
+    case 64: fn = neox ? (const void*)&qk_norm_rope_kernel<E, 64, true, AXES> : (const void*)&qk_norm_rope_kernel<E, 64, false, AXES>; break;
+    case 128: fn = neox ? (const void*)&qk_norm_rope_kernel<E, 128, true, AXES> : (const void*)&qk_norm_rope_kernel<E, 128, false, AXES>; break;
+    case 256: fn = neox ? (const void*)&qk_norm_rope_kernel<E, 256, true, AXES> : (const void*)&qk_norm_rope_kernel<E, 256, false, AXES>; break;
     default: return cudaErrorInvalidValue;
     }
     const int64_t warps = (int64_t)a.n * chunks;
