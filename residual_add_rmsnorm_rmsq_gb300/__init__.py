@@ -75,7 +75,7 @@ EXPORTS = ("rmsq_fused_add_rmsnorm_quant", "rmsq_fused_add_rmsnorm_quant_ex",
            "rmsq_allreduce_add_rmsnorm_quant",
            "rmsq_build_slot_map", "rmsq_kv_cache_store_nvfp4", "rmsq_kv_cache_load_nvfp4",
            "rmsq_paged_attention_nvfp4", "rmsq_paged_attention_nvfp4_ex", "rmsq_paged_attention_workspace_bytes",
-           "rmsq_kv_cache_store_fp8", "rmsq_kv_cache_load_fp8",
+           "rmsq_kv_cache_store_fp8", "rmsq_kv_cache_load_fp8", "rmsq_paged_attention_fp8",
            "rmsq_fp8_block_matmul",
            "rmsq_set_pipeline_config", "rmsq_set_programmatic_launch", "rmsq_take_fault_flags",
            "rmsq_query_sizes", "rmsq_query_launch", "rmsq_debug_convert", "rmsq_debug_activation", "rmsq_debug_bounded_wait",
@@ -144,6 +144,9 @@ def load(path: str | None = None):
         L.rmsq_paged_attention_nvfp4.restype = ci
         L.rmsq_paged_attention_nvfp4_ex.argtypes = L.rmsq_paged_attention_nvfp4.argtypes + [i64]
         L.rmsq_paged_attention_nvfp4_ex.restype = ci
+        L.rmsq_paged_attention_fp8.argtypes = [vp, i64, vp, vp, i64, i64, vp, i64, vp, vp, f32, i64, vp, vp, vp,
+                                               ctypes.c_size_t, i64, i64, ci, ci, ci, ci, vp, ci, i64]
+        L.rmsq_paged_attention_fp8.restype = ci
         L.rmsq_paged_attention_workspace_bytes.argtypes = [i64, i64, ci, ci, ci]
         L.rmsq_paged_attention_workspace_bytes.restype = ctypes.c_size_t
         L.rmsq_fp8_block_matmul.argtypes = [vp, vp, ci, vp, vp, vp, i64, i64, i64, ci, vp]
@@ -827,6 +830,61 @@ def paged_attention_nvfp4(q: torch.Tensor, cache: torch.Tensor, block_table: tor
                                          vcode, max_query)
     if st:
         raise RmsqError(st, "rmsq_paged_attention_nvfp4")
+    return out if lse is None else (out, lse)
+
+
+def paged_attention_fp8(q: torch.Tensor, cache: torch.Tensor, scales: torch.Tensor, block_table: torch.Tensor,
+                        query_start: torch.Tensor, seq_lens: torch.Tensor, softmax_scale: float | None = None, *,
+                        window: int = 0, return_lse: bool = False, out: torch.Tensor | None = None,
+                        lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None,
+                        variant: str = "auto", max_query: int = 0):
+    """rmsq_paged_attention_fp8: causal attention of q [tokens, heads, D] (token
+    stride free) over the paged FP8 cache (`cache` and `scales` of
+    kv_cache_shapes_fp8).  Everything else as in paged_attention_nvfp4: returns
+    out [tokens, heads, D], or (out, lse [tokens, heads] fp32) with return_lse or
+    a given lse.
+    """
+    vcode = _variant(variant)
+    L, empty = load(), _empty_for(stream)
+    dt = _act_types(q)
+    qs = _token_rows("q", q)
+    n, heads, d = q.shape
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [requests, width]")
+    pages, kv, page, dim = _cache_fp8(cache, scales)
+    if dim != d:
+        raise ValueError(f"q has heads of {d}, the cache of {dim}")
+    R, width = block_table.shape
+    if out is None:
+        out = empty(q.shape, dtype=dt, device=q.device)
+    if lse is None and return_lse:
+        lse = empty((n, heads), dtype=_F32, device=q.device)
+    if workspace is None:
+        workspace = empty(paged_attention_workspace_bytes(n, R, heads, kv, d), dtype=_U8, device=q.device)
+    i, size = q.get_device(), workspace.numel()
+    if not (_is_current(i) and cache.get_device() == i and scales.get_device() == i and
+            _fits(block_table, _I32, i, (R, width)) and _fits(query_start, _I32, i, (R + 1,)) and
+            _fits(seq_lens, _I32, i, (R,)) and _fits(out, dt, i, (n, heads, d)) and
+            (lse is None or _fits(lse, _F32, i, (n, heads))) and _fits(workspace, _U8, i, (size,))):
+        _check_tensors({"q": q, "cache": cache, "scales": scales, "block_table": block_table, "query_start": query_start,
+                        "seq_lens": seq_lens, "out": out, "lse": lse, "workspace": workspace},
+                       {"q": dt, "cache": cache.dtype, "scales": _U8, "block_table": _I32, "query_start": _I32,
+                        "seq_lens": _I32, "out": dt, "lse": _F32, "workspace": _U8})
+        _want_shape("block_table", block_table, R, width)
+        _want_shape("query_start", query_start, R + 1)
+        _want_shape("seq_lens", seq_lens, R)
+        _want_shape("out", out, n, heads, d)
+        if lse is not None:
+            _want_shape("lse", lse, n, heads)
+        _want_shape("workspace", workspace, size)
+    if softmax_scale is None:
+        softmax_scale = d ** -0.5
+    st = L.rmsq_paged_attention_fp8(q.data_ptr(), qs, cache.data_ptr(), scales.data_ptr(), pages, page,
+                                    block_table.data_ptr(), width, query_start.data_ptr(), seq_lens.data_ptr(),
+                                    softmax_scale, window, out.data_ptr(), _p(lse), workspace.data_ptr(), size, n, R, heads,
+                                    kv, d, DTYPES[dt], _stream(stream, i), vcode, max_query)
+    if st:
+        raise RmsqError(st, "rmsq_paged_attention_fp8")
     return out if lse is None else (out, lse)
 
 

@@ -22,7 +22,8 @@ LIBDIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(LIBDIR, "librmsq.so")
 
 UNITS = ["rmsq_api.cu", "rmsq_rows_bf16.cu", "rmsq_rows_fp16.cu", "rmsq_noalloc.cu", "rmsq_act.cu", "rmsq_qk.cu",
-         "rmsq_qk_axes.cu", "rmsq_allreduce.cu", "rmsq_kv.cu", "rmsq_kv8.cu", "rmsq_attn.cu", "rmsq_matmul.cu"]
+         "rmsq_qk_axes.cu", "rmsq_allreduce.cu", "rmsq_kv.cu", "rmsq_kv8.cu", "rmsq_attn.cu", "rmsq_attn8.cu",
+         "rmsq_matmul.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-ftz=false", "-prec-div=true",
                      "-prec-sqrt=true", "-fmad=true", "-Xcompiler", "-fPIC,-O2",

@@ -1,4 +1,6 @@
-// Attention over the paged NVFP4 cache, for few queries per request (decode).
+// Attention over a paged cache, for few queries per request (decode): the
+// kernels, with the NVFP4 cache's reader.  The FP8 cache's is in rmsq_attn8.cuh;
+// a reader is a struct C with its step's layout, its copies and its loads.
 //
 //   o_i = sum_j p_ij v_j,  p_ij = exp(scale q_i.k_j) / sum_j' exp(scale q_i.k_j'),
 //   keys j <= pos_i (and j > pos_i - window), pos_i = seq_len - query_len + i.
@@ -83,10 +85,11 @@ struct AttnArgs {
     const void* q;
     int64_t q_stride;       // elements between tokens
     const uint8_t* cache;
+    const uint8_t* scales;  // of the FP8 cache's blocks
     const int* table;       // [requests, width]
     const int* q_start;     // [requests + 1]
     const int* seq_lens;    // [requests]
-    const float* k_gs;
+    const float* k_gs;      // global scales of the NVFP4 cache (null: 1)
     const float* v_gs;
     void* out;              // [tokens, heads, D]
     float* lse;             // [tokens, heads] or null
@@ -274,6 +277,24 @@ struct Step {
     static constexpr int ring = stages * 2 * half;            // per warp
 };
 
+// The reader of the NVFP4 cache.
+struct Nvfp4Cache {
+    static constexpr bool block_scales = false;     // its scales are multiplied into the elements
+    template <int D> using Step = rmsq::Step<D>;
+    template <int D> using Regs = KeyRegs<D>;
+    // first of the lane's j-th eight dims
+    template <int D>
+    static __device__ __forceinline__ int q_dim(int t, int j) { return t * (D / 4) + 8 * j; }
+    template <int D>
+    static __device__ __forceinline__ void copy_half(unsigned char* dst, const AttnArgs& a, int in, int page, int head, int l);
+};
+
+// What a reader with block_scales has of a step's two halves: their scale
+// bytes, 0 for a half that is not there.
+struct HalfScales {
+    uint32_t k[2], v[2];
+};
+
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(smem_u32(dst)), "l"(src) : "memory");
 }
@@ -281,7 +302,7 @@ __device__ __forceinline__ void copy16(void* dst, const void* src) {
 // Starts the copies of a half from row `in` of a page: 16 lanes, lane l takes
 // every 16th 16-byte chunk.
 template <int D>
-__device__ __forceinline__ void copy_half(unsigned char* dst, const AttnArgs& a, int in, int page, int head, int l) {
+__device__ __forceinline__ void Nvfp4Cache::copy_half(unsigned char* dst, const AttnArgs& a, int in, int page, int head, int l) {
     using S = Step<D>;
     const uint32_t tile = static_cast<uint32_t>(D / 16 * 9) << a.page_shift;
     const uint8_t* kt = a.cache + (static_cast<int64_t>(page) * 2 * a.kv_heads + head) * tile;
@@ -368,15 +389,23 @@ __device__ __forceinline__ float lag_limit(float t, float f) { return t == -INFI
 __device__ __forceinline__ float weight_shift(float m, float f) { return m == -INFINITY ? 0.0f : fmaf(-m, f, kPShift); }
 __device__ __forceinline__ bool is_far(float shift) { return !(fabsf(shift) <= kFar); }
 
+// 2^(a - b) of two exponent bytes a <= b, 2^-126 at least.
+__device__ __forceinline__ float pow2_diff(uint32_t a, uint32_t b) {
+    return __uint_as_float(static_cast<uint32_t>(max(static_cast<int>(a + 127u - b), 1)) << 23);
+}
+
 // A warp's running state over its keys for one item.  The logits and their
 // maximum m stay in the units of the product; f turns them into units of log2;
 // limit is the logit above which the maximum has to move; far: some row's
-// maximum is beyond kFar.
+// maximum is beyond kFar.  With block_scales a half's keys share one power of two,
+// a factor of its logits, and its values another, a factor of its weights
+// relative to the largest such scale so far (ve): neither is applied per element.
 template <int D, int NB>
 struct WarpState {
     float o[D / 16][NB][4];
     float m[NB][2], l[NB][2], limit[NB][2];
     bool far;
+    uint32_t ve;        // block_scales: the byte of the value scale that o is in units of
 };
 
 // S^T of 16 keys: s[b][0..1] key kappa(g), rows 2t and 2t + 1; s[b][2..3] key + 8.
@@ -459,16 +488,24 @@ __device__ __forceinline__ void values16(WarpState<D, NB>& w, const KeyRegs<D>& 
 // One step: 32 keys from `base`.  pos / lo: last and first key each of the
 // lane's columns may see; `full`: every key is inside for every row; bit i of
 // `have`: half i is there.
-template <int D, int NB>
+template <class C, int D, int NB>
 __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned char* st, const uint32_t (&qf)[D / 16][NB][2],
                                          const float (&f)[NB][2], const int (&pos)[NB][2], const int (&lo)[NB][2],
-                                         bool full, uint32_t have, int base, int g, int t) {
+                                         bool full, uint32_t have, int base, int g, int t, const HalfScales& sc) {
+    using S = typename C::template Step<D>;
     float s[2][NB][4];
-    KeyRegs<D> x[2];
+    typename C::template Regs<D> x[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        read_keys<D>(x[h], st + h * Step<D>::half, g, t);
+        read_keys<D>(x[h], st + h * S::half, g, t);
         scores16<D, NB>(s[h], x[h], qf);
+        if constexpr (C::block_scales) {
+            const float ks = __uint_as_float(sc.k[h] << 23);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[h][b][j] *= ks;
+        }
     }
     if (!full) {
         const int key = base + (g >> 1) + ((g & 1) << 2);
@@ -492,8 +529,15 @@ __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned cha
             top[b][j] = fmaxf(fmaxf(s[0][b][j], s[0][b][j + 2]), fmaxf(s[1][b][j], s[1][b][j + 2]));
             grow |= top[b][j] > w.limit[b][j];
         }
+    if constexpr (C::block_scales) grow |= max(sc.v[0], sc.v[1]) > w.ve;
     if (__any_sync(kFull, grow)) {
         bool far = false;
+        float rv = 1.0f;
+        if constexpr (C::block_scales) {
+            const uint32_t ve = max(w.ve, max(sc.v[0], sc.v[1]));
+            rv = pow2_diff(w.ve, ve);
+            w.ve = ve;
+        }
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -509,8 +553,8 @@ __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned cha
                 w.l[b][j] *= r;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    w.o[i][b][j] *= r;
-                    w.o[i][b][j + 2] *= r;
+                    w.o[i][b][j] *= C::block_scales ? r * rv : r;
+                    w.o[i][b][j + 2] *= C::block_scales ? r * rv : r;
                 }
             }
         w.far = __any_sync(kFull, far);
@@ -545,13 +589,18 @@ __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned cha
             for (int j = 0; j < 4; ++j) p[j] = exp2_approx(fmaf(s[h][b][j], f[b][j & 1], shift[b][j & 1]));
             w.l[b][0] += p[0] + p[2];
             w.l[b][1] += p[1] + p[3];
+            if constexpr (C::block_scales) {
+                const float v = pow2_diff(sc.v[h], w.ve);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) p[j] *= v;
+            }
             pf[h][b][0] = transpose8x8(Fp16T::pack(p[0], p[1]));
             pf[h][b][1] = transpose8x8(Fp16T::pack(p[2], p[3]));
         }
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        read_values<D>(x[h], st + h * Step<D>::half, g, t);
+        read_values<D>(x[h], st + h * S::half, g, t);
         values16<D, NB>(w, x[h], pf[h]);
     }
 }
@@ -565,9 +614,9 @@ struct AttnSmem {
 };
 
 // Bytes of the ring, or of the join if that is more.
-template <int D, int NB>
-constexpr int kAttnMem = (kAttnWarps * Step<D>::ring > static_cast<int>(sizeof(AttnSmem<D, NB>))
-                              ? kAttnWarps * Step<D>::ring : static_cast<int>(sizeof(AttnSmem<D, NB>)) + 127) / 128 * 128;
+template <class C, int D, int NB>
+constexpr int kAttnMem = (kAttnWarps * C::template Step<D>::ring > static_cast<int>(sizeof(AttnSmem<D, NB>))
+                              ? kAttnWarps * C::template Step<D>::ring : static_cast<int>(sizeof(AttnSmem<D, NB>)) + 127) / 128 * 128;
 
 // Four dims of an output row, times the row's factor.
 template <class E>
@@ -581,13 +630,13 @@ __device__ __forceinline__ float row_lse(float m, float l, float f) {
     return l == 0.0f ? -INFINITY : fmaf(m, f, log2f(l) - kPShift) * 0.693147180559945309f;
 }
 
-template <class E, int D, int NB>
+template <class C, class E, int D, int NB>
 __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
     constexpr int ROWS = 8 * NB;
-    using S = Step<D>;
+    using S = typename C::template Step<D>;
     extern __shared__ __align__(128) unsigned char mem[];
     AttnSmem<D, NB>& sm = *reinterpret_cast<AttnSmem<D, NB>*>(mem);
-    int64_t* prefix = reinterpret_cast<int64_t*>(mem + kAttnMem<D, NB>);
+    int64_t* prefix = reinterpret_cast<int64_t*>(mem + kAttnMem<C, D, NB>);
     allow_dependents();
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -598,7 +647,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
     const int64_t run = run_length(total, a.workers);
     int64_t x = blockIdx.x * run;
     const int64_t end = x + run < total ? x + run : total;
-    const float k_gs = __ldg(a.k_gs), v_gs = __ldg(a.v_gs);
+    const float k_gs = C::block_scales ? 1.0f : __ldg(a.k_gs), v_gs = C::block_scales ? 1.0f : __ldg(a.v_gs);
     CutItem cut = {};
     unsigned char* ring = mem + warp * S::ring;
 
@@ -625,6 +674,9 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
             if (j >= ntiles || k > pos_max || k + 15 < lo_min) return -1;
             return __ldg(row_table + (k >> a.page_shift));
         };
+        // block_scales: bytes of the lane's half of the steps in flight, keys'
+        // then values', loaded with the copies and not touched before their turn
+        uint32_t raw[S::stages][2] = {};
         uint32_t have = 0;      // bits 2s, 2s + 1: halves of stage s
         // (a page is compared with their number here and not where it is
         // loaded: the warp would wait for the load there)
@@ -632,8 +684,24 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
             if (page >= a.num_pages) page = -1;
             const uint32_t there = __ballot_sync(kFull, page >= 0);
             have = (have & ~(3u << (2 * s))) | (((there & 1u) | (there >> 16 & 1u) << 1) << (2 * s));
+            if constexpr (C::block_scales) {
+#pragma unroll
+                for (int i = 0; i < S::stages - 1; ++i) {
+                    raw[i][0] = raw[i + 1][0];
+                    raw[i][1] = raw[i + 1][1];
+                }
+                raw[S::stages - 1][0] = raw[S::stages - 1][1] = 0u;
+                if (page >= 0) {
+                    const int in = (first_key + j * kAttnKeyTile + my_half * 16) & ((1 << a.page_shift) - 1);
+                    const int64_t side = static_cast<int64_t>(a.kv_heads) << (a.page_shift - 4);
+                    const uint8_t* p = a.scales + (static_cast<int64_t>(page) * 2 * a.kv_heads + at.head) *
+                                                      (int64_t(1) << (a.page_shift - 4)) + (in >> 4);
+                    raw[S::stages - 1][0] = __ldg(p);
+                    raw[S::stages - 1][1] = __ldg(p + side);
+                }
+            }
             if (page >= 0)
-                copy_half<D>(ring + (s * 2 + my_half) * S::half, a,
+                C::template copy_half<D>(ring + (s * 2 + my_half) * S::half, a,
                              (first_key + j * kAttnKeyTile + my_half * 16) & ((1 << a.page_shift) - 1), page, at.head,
                              lane & 15);
             asm volatile("cp.async.commit_group;" ::: "memory");
@@ -654,10 +722,10 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
             for (int i = 0; i < D / 8; ++i) w[i] = 0u;
             if (row < rows) {
                 const int i = row / a.group, h = at.head * a.group + row % a.group;
-                const uint16_t* p = static_cast<const uint16_t*>(a.q) + (rq.q0 + i) * a.q_stride + h * D + t * (D / 4);
+                const uint16_t* p = static_cast<const uint16_t*>(a.q) + (rq.q0 + i) * a.q_stride + h * D;
 #pragma unroll
                 for (int j = 0; j < D / 32; ++j) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + j);
+                    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p + C::template q_dim<D>(t, j)));
                     w[4 * j] = u.x; w[4 * j + 1] = u.y; w[4 * j + 2] = u.z; w[4 * j + 3] = u.w;
                 }
             }
@@ -690,6 +758,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
         }
         WarpState<D, NB> w;
         w.far = false;
+        w.ve = 0u;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -713,8 +782,14 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
             const uint32_t here = have >> (2 * s) & 3u;
             if (here) {
                 const int base = first_key + j * kAttnKeyTile;
-                attend32<D, NB>(w, ring + s * 2 * S::half, qf, fs, pos, lo,
-                                here == 3u && base + 31 <= pos_min && base >= lo_max, here, base, g, t);
+                HalfScales sc = {};
+                if constexpr (C::block_scales) {
+                    const uint32_t own = (here >> my_half & 1u) ? C::scale_codes(raw[0][0], raw[0][1]) : 0u;
+                    const uint32_t first = __shfl_sync(kFull, own, 0), second = __shfl_sync(kFull, own, 16);
+                    sc = {{first & 0xffu, second & 0xffu}, {first >> 8, second >> 8}};
+                }
+                attend32<C, D, NB>(w, ring + s * 2 * S::half, qf, fs, pos, lo,
+                                   here == 3u && base + 31 <= pos_min && base >= lo_max, here, base, g, t, sc);
             }
             __syncwarp();   // every lane has read the stage that the next copy overwrites
         }
@@ -744,7 +819,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
                 float top = sm.m[0][row];
 #pragma unroll
                 for (int i = 1; i < kAttnWarps; ++i) top = fmaxf(top, sm.m[i][row]);
-                const float f = w.m[b][j] == -INFINITY ? 0.0f : exp2_approx((w.m[b][j] - top) * fs[b][j]);
+                float f = w.m[b][j] == -INFINITY ? 0.0f : exp2_approx((w.m[b][j] - top) * fs[b][j]);
+                if constexpr (C::block_scales) f *= __uint_as_float(w.ve << 23);
                 float* dst = &sm.o[warp][row][g * (D / 8)];
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
@@ -827,7 +903,7 @@ __device__ __forceinline__ void merge(Partial& a, const Partial& b, float factor
     a.m = m;
 }
 
-template <class E, int D, int NB>
+template <class C, class E, int D, int NB>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a) {
     constexpr int ROWS = 8 * NB;
     __shared__ __align__(16) Partial met[kJoinThreads];
@@ -839,7 +915,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a) {
     if (parts == 0) return;
     const Req rq = {c0.z, c0.w, 0, 0, 0};
     const int w0 = blockIdx.x;
-    const float v_gs = __ldg(a.v_gs);
+    const float v_gs = a.v_gs ? __ldg(a.v_gs) : 1.0f;
     const int rows = rq.qlen * a.group, row0 = c1.x * ROWS;
     const int64_t slot = ROWS * kPartRow<D>;
     const int quads = ROWS * (D / 4) / static_cast<int>(gridDim.y);      // of this share; a power of two

@@ -1,5 +1,6 @@
-// Attention over the paged NVFP4 cache for many queries per request (prompts),
-// on the fifth-generation tensor cores.  The mathematics, the f16 operands and
+// Attention over a paged cache for many queries per request (prompts), on the
+// fifth-generation tensor cores; the NVFP4 cache's reader (the FP8 cache's is in
+// rmsq_attn8.cuh).  The mathematics, the f16 operands and
 // the scaling of queries and probabilities are those of rmsq_attn.cuh.
 //
 // A CTA takes 256 rows (query token, head of the group) of a request and kv
@@ -38,6 +39,7 @@
 
 #include <type_traits>
 
+#include "rmsq.h"
 #include "rmsq_attn.cuh"
 #include "rmsq_tc.cuh"
 
@@ -215,6 +217,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
+// What a reader with block_scales tells of a 128-key tile's eight blocks: the
+// factors of their logits, and the bytes of their values' scales (0: not there).
+struct TileScales {
+    float k[8];
+    uint32_t v[8];
+};
+
+template <int D>
+struct Nvfp4Prompt : Nvfp4Cache {
+    using Raw = RawTile<D>;
+};
+
 // A row's 128 logits.  They stay in registers from the maximum to the weights:
 // read from tensor memory twice, 16 at a time, the two passes waited out
 // sixteen load latencies per tile (260 us for the prompt step of 147 GFLOP).
@@ -270,6 +284,54 @@ __device__ __forceinline__ float weigh_half(const Row& d, int h, uint32_t s_at, 
     return (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
 }
 
+// The same with block_scales: every 16 logits have a factor of their own, and
+// what is stored is the weights times their value scale relative to the row's, a
+// power of two that only changes the exponent's addend; the sum is of the
+// weights themselves.  `done`: the factors are in the logits already.
+__device__ __forceinline__ float weigh_half_scaled(const Row& d, int h, uint32_t s_at, float f, float shift,
+                                                   const TileScales& sc, uint32_t ve, bool done) {
+    float total = 0.0f;
+#pragma unroll
+    for (int c = 2 * h; c < 2 * h + 2; ++c) {
+        uint32_t p[16];
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const float(&x16)[16] = d[2 * c + q];
+            // (within the normal numbers: a masked logit times zero would be NaN)
+            const float fk = done ? f : clamp_factor(f * sc.k[2 * c + q]);
+            const int down = max(static_cast<int>(sc.v[2 * c + q]) - static_cast<int>(ve), -90);
+            const float add = shift + static_cast<float>(down);
+            const float2 f2 = make_float2(fk, fk), s2 = make_float2(add, add);
+            float2 sum[2] = {};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float2 x = fma2_rn(make_float2(x16[2 * j], x16[2 * j + 1]), f2, s2);
+                x.x = exp2_approx(x.x);
+                x.y = exp2_approx(x.y);
+                sum[j & 1] = add2_rn(sum[j & 1], x);
+                p[8 * q + j] = Fp16T::pack(x.x, x.y);
+            }
+            total = fmaf((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y),
+                         __uint_as_float(static_cast<uint32_t>(127 - down) << 23), total);
+        }
+        tmem_st16(s_at + c * 16, p);
+    }
+    return total;
+}
+
+// Maximum of a half's logits times their factors.
+__device__ __forceinline__ float max_half_scaled(const Row& d, int h, const TileScales& sc) {
+    float top = -INFINITY;
+#pragma unroll
+    for (int c = 4 * h; c < 4 * h + 4; ++c) {
+        float t[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t[j & 1] = max3(t[j & 1], d[c][2 * j], d[c][2 * j + 1]);
+        top = fmaxf(top, fmaxf(t[0], t[1]) * sc.k[c]);
+    }
+    return top;
+}
+
 // The CTA's item, counted from its request's first one, and the request; -1 if
 // there are not that many.  Up to 32 requests every warp finds it for itself, a
 // lane per request; more are scanned in `scratch` (the key and value tiles' space,
@@ -316,13 +378,14 @@ __device__ __forceinline__ int64_t find_item(const AttnArgs& a, int64_t* scratch
     return item < 0 ? -1 : item;
 }
 
-template <class E, int D>
+template <class P, class E, int D>
 __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs a) {
     using Tile = PromptTile<D>;
     extern __shared__ unsigned char dyn[];
     __shared__ __align__(8) uint64_t qfull[2], kfull[2], kempty[2], vfull[2], vempty[2], sfull[2], pready[2],
         ofull[2], drained;
     __shared__ __align__(16) uint32_t valid[4][4];  // which keys of a tile lie on a page, four tiles deep
+    __shared__ __align__(16) TileScales scales[P::block_scales ? 4 : 1];
     __shared__ uint32_t tmem_base;
     unsigned char* qs = dyn + ((1024u - (smem_u32(dyn) & 1023u)) & 1023u);
     unsigned char* ks = qs + 2 * Tile::q;
@@ -434,7 +497,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
         // the load the comparison would make the warp wait for it every time.
         auto page_of = [&](int key) { return key > last_pos ? -1 : __ldg(table + (key >> a.page_shift)); };
         auto checked = [&](int p) { return p < a.num_pages ? p : -1; };
-        RawTile<D> raw;
+        typename P::Raw raw;
         int kkey = key_begin + t, vkey = key_begin + octet * 8;
         bool here = checked(page_of(kkey)) >= 0;
         load_keys<D>(raw, a, kkey, checked(page_of(kkey)), head);
@@ -448,6 +511,13 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
             if (!ok) break;
             const uint32_t there = __ballot_sync(kFull, here);
             if (lane == 0) valid[n & 3][w] = there;
+            if constexpr (P::block_scales) {
+                if ((t & 15) == 0) {
+                    const uint32_t c = here ? P::scale_codes(raw.ks, raw.vs) : 1u;
+                    scales[n & 3].k[t >> 4] = __uint_as_float((c & 0xffu) << 23);
+                    scales[n & 3].v[t >> 4] = c >> 8;
+                }
+            }
             write_keys<D>(ks + s * Tile::k, raw, t);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -484,7 +554,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                     q[4 * j] = u.x; q[4 * j + 1] = u.y; q[4 * j + 2] = u.z; q[4 * j + 3] = u.w;
                 }
             }
-            float f = a.scale_log2 / __ldg(a.k_gs);
+            float f = P::block_scales ? a.scale_log2 : a.scale_log2 / __ldg(a.k_gs);
             if constexpr (E::kBits87 == Bf16T::kBits87) {
                 float top = 0.0f;
 #pragma unroll
@@ -509,6 +579,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
             const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
             const uint32_t s_at = tmem + i * 128 + lanes, o_at = tmem + 256 + i * D + lanes;
             float m = -INFINITY, l = 0.0f, limit = -INFINITY, shift = 0.0f;
+            uint32_t ve = 0;        // block_scales: byte of the value scale that the row's O is in units of
             for (int n = 0; n < steps; ++n) {
                 const int key0 = key_begin + n * 128;
                 ok = warp_wait(&sfull[i], n & 1);
@@ -534,20 +605,33 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                 start_half(d, s_at, 0);
                 finish_half(d, 0);
                 start_half(d, s_at, 1);
+                const TileScales& sc = scales[P::block_scales ? n & 3 : 0];
                 if (!full) mask_half(d, 0, see);
-                float top = max_half(d, 0);
+                float top = P::block_scales ? max_half_scaled(d, 0, sc) : max_half(d, 0);
                 finish_half(d, 1);
                 if (!full) mask_half(d, 1, see);
-                top = fmaxf(top, max_half(d, 1));
-                if (__any_sync(kFull, top > limit)) {
+                top = fmaxf(top, P::block_scales ? max_half_scaled(d, 1, sc) : max_half(d, 1));
+                uint32_t most = 0;      // largest value scale that the row sees here
+                if constexpr (P::block_scales) {
+#pragma unroll
+                    for (int c = 0; c < 8; ++c)
+                        if (full || (see[c >> 1] >> ((c & 1) * 16) & 0xffffu) != 0u) most = max(most, sc.v[c]);
+                }
+                bool done = false;      // the factors are in the logits
+                if (__any_sync(kFull, top > limit || most > ve)) {
                     // sfull of this step says that the previous P . V has
                     // completed too: O may be rescaled here
                     const float m1 = top > limit ? fmaxf(top, m) : m;   // whatever shares the warp
-                    const float r = m1 == -INFINITY ? 1.0f : exp2_approx((m - m1) * f);
+                    float r = m1 == -INFINITY ? 1.0f : exp2_approx((m - m1) * f);
                     m = m1;
                     limit = lag_limit(m, f);
                     shift = weight_shift(m, f);
                     l *= r;
+                    if constexpr (P::block_scales) {
+                        most = max(most, ve);
+                        r *= pow2_diff(ve, most);
+                        ve = most;
+                    }
                     if (n > 0) {
 #pragma unroll
                         for (int c = 0; c < D / 16; ++c) {
@@ -572,11 +656,16 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
 #pragma unroll
                         for (int c = 0; c < 8; ++c)
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) d[c][j] -= t;
+                            for (int j = 0; j < 16; ++j) {
+                                if constexpr (P::block_scales) d[c][j] *= sc.k[c];
+                                d[c][j] -= t;
+                            }
+                        done = P::block_scales;
                     }
                 }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) l += weigh_half(d, h, s_at, f, shift);
+                for (int h = 0; h < 2; ++h)
+                    l += P::block_scales ? weigh_half_scaled(d, h, s_at, f, shift, sc, ve, done) : weigh_half(d, h, s_at, f, shift);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -587,7 +676,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                 ok = warp_wait(&ofull[i], 0);
                 tc_fence_after();
             }
-            const float inv = l > 0.0f ? 1.0f / (l * __ldg(a.v_gs)) : (l == 0.0f ? 0.0f : l);
+            float inv;
+            if constexpr (P::block_scales) inv = l > 0.0f ? __uint_as_float(ve << 23) / l : (l == 0.0f ? 0.0f : l);
+            else inv = l > 0.0f ? 1.0f / (l * __ldg(a.v_gs)) : (l == 0.0f ? 0.0f : l);
             const int64_t oh = static_cast<int64_t>(rq.q0 + token) * a.heads + qh;
             uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + oh * D);
 #pragma unroll

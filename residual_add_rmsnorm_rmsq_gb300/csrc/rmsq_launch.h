@@ -106,6 +106,7 @@ cudaError_t take_pipe_fault_qk_axes(unsigned int* out);
 cudaError_t take_pipe_fault_ar(unsigned int* out);
 cudaError_t take_mm_fault(unsigned int* out);
 cudaError_t take_prompt_fault(unsigned int* out);
+cudaError_t take_prompt_fault_fp8(unsigned int* out);
 cudaError_t launch_convert(int kind, const float* in, uint8_t* out, int64_t n, cudaStream_t stream);
 
 }  // namespace rmsq

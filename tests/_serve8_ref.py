@@ -110,7 +110,8 @@ def attention(q, codes, scales, table, q_lens, seq_lens, softmax_scale, window, 
     """out, lse in float64 and their tolerances.
 
     Per output element, with p the exact weights (sum 1) and A = sum p |v|:
-      - the output's rounding, half a step: eps / 2 |out|;
+      - the output's rounding, half a step: eps / 2 |out|, and among fp16's
+        subnormal numbers (below 2^-14, steps of 2^-24) 2^-25;
       - weights rounded to f16: 2^-11 A; they are held relative to the largest
         value scale S of the request's head, and where that product is below
         2^-23 of the largest weight it is subnormal, off by 2^-34 of it times a
@@ -158,7 +159,7 @@ def attention(q, codes, scales, table, q_lens, seq_lens, softmax_scale, window, 
                     cnt = len(s)
                     big = sv[at[ok], 1, h // G, off[ok] // 16].max()
                     tol[t, h] = eps / 2 * np.abs(out[t, h]) + A * (2.0 ** -11 + 2 * ds + 2 * cnt * 2.0 ** -23) + \
-                        cnt * 2.0 ** -34 * 448 * big
+                        cnt * 2.0 ** -34 * 448 * big + (2.0 ** -25 if eps == 2.0 ** -10 else 0.0)
                     tol_lse[t, h] = ds + cnt * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -23 * abs(lse[t, h])
             t += 1
     return out, lse, tol, tol_lse
