@@ -18,7 +18,7 @@
 // by a power of two per row into f16's range, exact unless an element is
 // 2^-28 of the row's largest (then off by 2^-39 of it).  Probabilities are
 // rounded to f16 (11 bits; 8 would be as many as a bf16 output has), scaled by
-// 2^kPShift so that those down to 2^-23 of the maximum keep all their bits.  With
+// 2^9 so that those down to 2^-23 of the maximum keep all their bits (p_shift).  With
 // 32-bit weights the relative error of fp16 outputs is 2.1e-4 and with these
 // 2.9e-4 (3 requests of up to 131071 keys, against 64 bits); bf16 outputs hide it
 // (1.7e-3 both ways).  The matrix unit's next wider type would halve its rate.
@@ -68,8 +68,6 @@ constexpr int kAttnThreads = kAttnWarps * 32;
 constexpr int kAttnKeyTile = kAttnWarps * 32;   // keys per CTA step: 32 per warp
 constexpr int kAttnMaxWorkers = 1216;           // CTAs of the split launch: 8 per SM of 152
 constexpr int kPromptRows = 64;                 // see launch_attn
-constexpr float kPShift = 9.0f;                 // probabilities are scaled by 2^9 ...
-constexpr float kLazy = 6.0f;                   // ... and by up to 2^6 more while the maximum lags: < 2^16 in f16
 constexpr float kFar = 1024.0f;                 // maximum (in powers of two) from which it is subtracted first
 
 // What the join has to know of an item that starts in a run and goes past its
@@ -280,6 +278,9 @@ struct Step {
 // The reader of the NVFP4 cache.
 struct Nvfp4Cache {
     static constexpr bool block_scales = false;     // its scales are multiplied into the elements
+    static constexpr float p_shift = 9.0f;          // weights are scaled by 2^9 ...
+    static constexpr float lazy = 6.0f;             // ... and by up to 2^6 more while the maximum lags: < 2^16 in f16
+    static constexpr uint32_t lazy_scale = 0;
     template <int D> using Step = rmsq::Step<D>;
     template <int D> using Regs = KeyRegs<D>;
     // first of the lane's j-th eight dims
@@ -381,15 +382,17 @@ __device__ __forceinline__ uint32_t dup_half(uint32_t pair, int hi) { return __b
 __device__ __forceinline__ float clamp_factor(float f) { return fminf(fmaxf(f, 1.17549435e-38f), 3.40282347e38f); }
 
 // The logit above which a maximum of t has to move.  Rounded down: half a unit of
-// t's last place can be more than kLazy.
-__device__ __forceinline__ float lag_limit(float t, float f) { return t == -INFINITY ? t : __fadd_rd(t, kLazy / f); }
+// t's last place can be more than C::lazy.
+template <class C>
+__device__ __forceinline__ float lag_limit(float t, float f) { return t == -INFINITY ? t : __fadd_rd(t, C::lazy / f); }
 
 // What the exponents of a row with maximum m are shifted by, and whether m is
 // so far out that it is to be subtracted from the logits instead.
-__device__ __forceinline__ float weight_shift(float m, float f) { return m == -INFINITY ? 0.0f : fmaf(-m, f, kPShift); }
+template <class C>
+__device__ __forceinline__ float weight_shift(float m, float f) { return m == -INFINITY ? 0.0f : fmaf(-m, f, C::p_shift); }
 __device__ __forceinline__ bool is_far(float shift) { return !(fabsf(shift) <= kFar); }
 
-// 2^(a - b) of two exponent bytes a <= b, 2^-126 at least.
+// 2^(a - b) of two exponent bytes, 2^-126 at least.
 __device__ __forceinline__ float pow2_diff(uint32_t a, uint32_t b) {
     return __uint_as_float(static_cast<uint32_t>(max(static_cast<int>(a + 127u - b), 1)) << 23);
 }
@@ -519,7 +522,7 @@ __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned cha
                     if (k > pos[b][j & 1] || k < lo[b][j & 1] || !(have >> h & 1u)) s[h][b][j] = -INFINITY;
                 }
     }
-    // The maximum is moved only when some logit passes it by more than kLazy.
+    // The maximum is moved only when some logit passes it by more than C::lazy.
     float top[NB][2];
     bool grow = false;
 #pragma unroll
@@ -529,7 +532,7 @@ __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned cha
             top[b][j] = fmaxf(fmaxf(s[0][b][j], s[0][b][j + 2]), fmaxf(s[1][b][j], s[1][b][j + 2]));
             grow |= top[b][j] > w.limit[b][j];
         }
-    if constexpr (C::block_scales) grow |= max(sc.v[0], sc.v[1]) > w.ve;
+    if constexpr (C::block_scales) grow |= max(sc.v[0], sc.v[1]) > w.ve + C::lazy_scale;
     if (__any_sync(kFull, grow)) {
         bool far = false;
         float rv = 1.0f;
@@ -548,8 +551,8 @@ __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned cha
                 const float m = fmaxf(x, w.m[b][j]);
                 const float r = m == -INFINITY ? 1.0f : exp2_approx((w.m[b][j] - m) * f[b][j]);
                 w.m[b][j] = m;
-                w.limit[b][j] = lag_limit(m, f[b][j]);
-                far |= is_far(weight_shift(m, f[b][j]));
+                w.limit[b][j] = lag_limit<C>(m, f[b][j]);
+                far |= is_far(weight_shift<C>(m, f[b][j]));
                 w.l[b][j] *= r;
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
@@ -563,7 +566,7 @@ __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned cha
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) shift[b][j] = weight_shift(w.m[b][j], f[b][j]);
+        for (int j = 0; j < 2; ++j) shift[b][j] = weight_shift<C>(w.m[b][j], f[b][j]);
     if (w.far) {    // the rows that are (the others as ever, whatever shares their warp)
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -571,7 +574,7 @@ __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned cha
             for (int j = 0; j < 2; ++j) {
                 const bool far = is_far(shift[b][j]);
                 const float m = far ? w.m[b][j] : 0.0f;
-                if (far) shift[b][j] = kPShift;
+                if (far) shift[b][j] = C::p_shift;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     s[h][b][j] -= m;
@@ -625,9 +628,10 @@ __device__ __forceinline__ void store_quad(void* out, int64_t at, float4 o, floa
         make_uint2(E::pack(o.x * inv, o.y * inv), E::pack(o.z * inv, o.w * inv));
 }
 
-// ln of the sum of the weights: l of them relative to the maximum m, times 2^kPShift.
+// ln of the sum of the weights: l of them relative to the maximum m, times 2^p_shift.
+template <class C>
 __device__ __forceinline__ float row_lse(float m, float l, float f) {
-    return l == 0.0f ? -INFINITY : fmaf(m, f, log2f(l) - kPShift) * 0.693147180559945309f;
+    return l == 0.0f ? -INFINITY : fmaf(m, f, log2f(l) - C::p_shift) * 0.693147180559945309f;
 }
 
 template <class C, class E, int D, int NB>
@@ -851,7 +855,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
                     const int64_t tok = rq.q0 + (row0 + row) / a.group;
                     const int64_t oh = tok * a.heads + at.head * a.group + (row0 + row) % a.group;
                     store_quad<E>(a.out, oh * D + d, o, l > 0.0f ? 1.0f / (l * v_gs) : (l == 0.0f ? 0.0f : l));
-                    if (a.lse && d == 0) a.lse[oh] = row_lse(top, l, f);
+                    if (a.lse && d == 0) a.lse[oh] = row_lse<C>(top, l, f);
                 }
             } else {
                 *reinterpret_cast<float4*>(part + row * kPartRow<D> + d) = o;
@@ -946,7 +950,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a) {
             const int64_t oh = tok * a.heads + head * a.group + (row0 + row) % a.group;
             const float l = acc.l;
             store_quad<E>(a.out, oh * D + d, acc.o, l > 0.0f ? 1.0f / (l * v_gs) : (l == 0.0f ? 0.0f : l));
-            if (a.lse && d == 0) a.lse[oh] = row_lse(acc.m, l, factor);
+            if (a.lse && d == 0) a.lse[oh] = row_lse<C>(acc.m, l, factor);
         }
         __syncthreads();
     }

@@ -43,6 +43,12 @@ struct Step8 {
 
 struct Fp8Cache {
     static constexpr bool block_scales = true;
+    // Weights are scaled by 2^5, up to 2^8 more while the maximum lags and 2^2 more
+    // while the value scale does: moving either costs a pass over O (the maximum had
+    // to move at one step in nine with 2^9 and 2^6, on tokens of uneven strength).
+    // Weights below 2^-19 of the largest are subnormal f16, off by 2^-30 of it.
+    static constexpr float p_shift = 5.0f, lazy = 8.0f;
+    static constexpr uint32_t lazy_scale = 2;
     template <int D> using Step = Step8<D>;
     template <int D> using Regs = KeyRegs8<D>;
     // first of the lane's j-th eight dims: 16 of every 64
@@ -147,44 +153,37 @@ __device__ __forceinline__ void values16(WarpState<D, NB>& w, const KeyRegs8<D>&
     }
 }
 
-// A converting thread's share of a 128-key tile of the prompt kernel.
+// The prompt kernel's tiles of 128 keys.  A warp of their own (`fetch`) finds the
+// pages and scales of a tile's eight blocks and copies their keys, D * 16
+// contiguous bytes each, into a ring of two raw tiles; four warps (`convert`) turn
+// those into operand rows, and values from registers that are loaded a tile
+// ahead.
+//
+// The prompt step of rmsq_attn_prompt.cuh's figures (2478 and 2445 queries of 32
+// heads, 192 GFLOP) takes 251 us, over the NVFP4 cache 203.  Tried on the way: keys
+// loaded into registers, a row per thread, with a factor for each 16 logits in the
+// softmax 278; the same with lines read whole 295; the blocks that are far apart
+// handled in the softmax, which then holds code for both, 305; keys converted by
+// two warps of the issuing group 283.
 template <int D>
-struct RawTile8 {
-    uint32_t k[D / 4], v[8][D / 32];
-    uint32_t ks, vs;        // scale bytes of the key's block, keys' and values'
+struct RawValues {
+    static constexpr int VW = D / 32;           // words of a key's values (D/8 dims)
+    uint32_t v[8][VW];
 };
 
+// First byte of a key (side 0) or value (1) of a page.
 template <int D>
-struct Fp8Prompt : Fp8Cache {
-    using Raw = RawTile8<D>;
-};
-
-template <int D>
-__device__ __forceinline__ void load_keys(RawTile8<D>& x, const AttnArgs& a, int key, int kpage, int head) {
-    if (kpage >= 0) {
-        const int64_t at = static_cast<int64_t>(kpage) * 2 * a.kv_heads + head;
-        const int in = key & ((1 << a.page_shift) - 1);
-        const uint4* p = reinterpret_cast<const uint4*>(a.cache + ((at << a.page_shift) + in) * D);
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) set4(&x.k[4 * j], __ldg(p + j));
-        const uint8_t* s = a.scales + (at << (a.page_shift - 4)) + (in >> 4);
-        x.ks = __ldg(s);
-        x.vs = __ldg(s + (static_cast<int64_t>(a.kv_heads) << (a.page_shift - 4)));
-    } else {
-#pragma unroll
-        for (int j = 0; j < D / 4; ++j) x.k[j] = 0u;
-        x.ks = x.vs = 0u;
-    }
+__device__ __forceinline__ const uint8_t* row_of(const AttnArgs& a, int page, int side, int head, int key) {
+    const int64_t at = (static_cast<int64_t>(page) * 2 + side) * a.kv_heads + head;
+    return a.cache + ((at << a.page_shift) + (key & ((1 << a.page_shift) - 1))) * D;
 }
 
 template <int D>
-__device__ __forceinline__ void load_values(RawTile8<D>& x, const AttnArgs& a, int key, int vpage, int head, int unit) {
-    const int64_t at = (static_cast<int64_t>(max(vpage, 0)) * 2 + 1) * a.kv_heads + head;
-    const int in = key & ((1 << a.page_shift) - 1);
-    const uint8_t* p = a.cache + ((at << a.page_shift) + in) * D + unit * (D / 8);
+__device__ __forceinline__ void load_values(RawValues<D>& x, const AttnArgs& a, int key, int page, int head, int unit) {
+    const uint8_t* p = row_of<D>(a, max(page, 0), 1, head, key) + unit * (D / 8);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (vpage >= 0) {
+        if (page >= 0) {
             if constexpr (D == 128) {
                 set4(x.v[i], __ldg(reinterpret_cast<const uint4*>(p + i * D)));
             } else {
@@ -193,31 +192,55 @@ __device__ __forceinline__ void load_values(RawTile8<D>& x, const AttnArgs& a, i
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < D / 32; ++j) x.v[i][j] = 0u;
+            for (int j = 0; j < RawValues<D>::VW; ++j) x.v[i][j] = 0u;
         }
     }
 }
 
-// K of the thread's key as a row of the operand tile.
+// A lane's share of the warp's 32 raw keys: 8 codes of a row, D / 8 lanes to a row.
 template <int D>
-__device__ __forceinline__ void write_keys(unsigned char* dst, const RawTile8<D>& x, int row) {
+struct RawKeys {
+    static constexpr int LT = D / 8, ROWS = 32 / LT, N = 32 / ROWS;     // lanes of a row; rows of an access; accesses
+    uint2 k[N];
+};
+
+template <int D>
+__device__ __forceinline__ void read_raw(RawKeys<D>& x, const unsigned char* raw, int warp, int lane) {
+    using R = RawKeys<D>;
+    raw += (warp * 32 + lane / R::LT) * D + lane % R::LT * 8;
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j) {       // 8 dims: a 16-byte chunk
-        const uint32_t a = x.k[2 * j], b = x.k[2 * j + 1];
-        *reinterpret_cast<uint4*>(dst + (j >> 3) * (128 * 128) + row * 128 + (((j & 7) ^ (row & 7)) << 4)) =
-            make_uint4(e4m3x2_to_f16x2(a), e4m3x2_to_f16x2(a >> 16), e4m3x2_to_f16x2(b), e4m3x2_to_f16x2(b >> 16));
+    for (int i = 0; i < R::N; ++i) x.k[i] = *reinterpret_cast<const uint2*>(raw + i * R::ROWS * D);
+}
+
+// They as rows of the operand tile, times their blocks' factors (f16 pairs).
+template <int D>
+__device__ __forceinline__ void write_keys(unsigned char* dst, const RawKeys<D>& x, int warp, int lane, uint32_t f0, uint32_t f1) {
+    using R = RawKeys<D>;
+    const int piece = lane % R::LT, row = warp * 32 + lane / R::LT;
+    dst += (piece >> 3) * (128 * 128) + row * 128;
+#pragma unroll
+    for (int i = 0; i < R::N; ++i) {
+        const uint32_t f = i < R::N / 2 ? f0 : f1;
+        *reinterpret_cast<uint4*>(dst + i * R::ROWS * 128 + (((piece & 7) ^ ((row + i * R::ROWS) & 7)) << 4)) =
+            make_uint4(mul_f16x2(e4m3x2_to_f16x2(x.k[i].x), f), mul_f16x2(e4m3x2_to_f16x2(x.k[i].x >> 16), f),
+                       mul_f16x2(e4m3x2_to_f16x2(x.k[i].y), f), mul_f16x2(e4m3x2_to_f16x2(x.k[i].y >> 16), f));
     }
 }
 
-// V of the thread's 8 keys and D/8 dims as 16-byte pieces of V^T's rows.
+// V of the thread's 8 keys and D/8 dims, times their block's factor, as 16-byte
+// pieces of V^T's rows.
 template <int D>
-__device__ __forceinline__ void write_values(unsigned char* dst, const RawTile8<D>& x, int octet, int unit) {
+__device__ __forceinline__ void write_values(unsigned char* dst, const RawValues<D>& x, int octet, int unit, uint32_t f) {
     unsigned char* base = dst + (octet >> 3) * (D * 128);
 #pragma unroll
-    for (int j = 0; j < D / 32; ++j) {
+    for (int j = 0; j < RawValues<D>::VW; ++j) {
         uint32_t v[4][4];       // [pair of keys][dim]
 #pragma unroll
-        for (int p = 0; p < 4; ++p) pair_values(x.v[2 * p][j], x.v[2 * p + 1][j], v[p]);
+        for (int p = 0; p < 4; ++p) {
+            pair_values(x.v[2 * p][j], x.v[2 * p + 1][j], v[p]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[p][c] = mul_f16x2(v[p][c], f);
+        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int row = unit * (D / 8) + 4 * j + c;
@@ -226,5 +249,148 @@ __device__ __forceinline__ void write_values(unsigned char* dst, const RawTile8<
         }
     }
 }
+
+// The f16 pair 2^-down, twice; down at most 15 (2^-15 is a subnormal number).
+__device__ __forceinline__ uint32_t f16_factor(uint32_t down) { return (down < 15u ? (15u - down) << 10 : 0x200u) * 0x10001u; }
+
+// How far apart the scales of a step's blocks may be for every code times its
+// scale relative to the largest to be exact in f16: 2^-9 times 2^-15 is its
+// smallest number.
+constexpr uint32_t kNarrow = 15;
+
+template <int D>
+struct Fp8Prompt : Fp8Cache {
+    static constexpr int ring = 2 * 128 * D;        // bytes of the raw keys
+
+    // One warp; lane l cares for block l % 8 of a tile.  A tile's pages are loaded
+    // two tiles before its copies, its scales one.  A tile is a step, unless its
+    // blocks' scales are too far apart: then each step takes those of the blocks left
+    // that are near the first of them.  `info` is eight steps deep: when a slot of the
+    // ring is free again, the step four before has only been multiplied and may still
+    // be in its softmax, the one five before is through.
+    static __device__ __forceinline__ bool fetch(const AttnArgs& a, int req, int head, int key_begin, int last_pos, int tiles,
+                                                 unsigned char* raw, uint64_t* full, uint64_t* empty, StepInfo* info) {
+        constexpr int kBlock = kBlockTokens * D;
+        const int lane = threadIdx.x & 31, block = lane & 7;
+        const int* table = a.table + static_cast<int64_t>(req) * a.width;
+        auto page_of = [&](int tile) {
+            const int key = key_begin + tile * 128 + block * kBlockTokens;
+            return key > last_pos ? -1 : __ldg(table + (key >> a.page_shift));
+        };
+        // (a page is compared with their number when it is used: next to its load
+        // the warp would wait for it)
+        auto checked = [&](int p) { return p < a.num_pages ? p : -1; };
+        uint32_t kraw = 0u, vraw = 0u;
+        auto load_scales = [&](int page, int tile) {
+            if (page < 0) return;
+            const int64_t at = static_cast<int64_t>(page) * 2 * a.kv_heads + head;
+            const int in = (key_begin + tile * 128 + block * kBlockTokens) & ((1 << a.page_shift) - 1);
+            const uint8_t* p = a.scales + (at << (a.page_shift - 4)) + (in >> 4);
+            kraw = __ldg(p);
+            vraw = __ldg(p + (static_cast<int64_t>(a.kv_heads) << (a.page_shift - 4)));
+        };
+        const uint64_t keep = l2_policy_evict_normal();
+        int page = checked(page_of(0)), next = page_of(1), n = 0;
+        bool ok = true;
+        load_scales(page, 0);
+#pragma unroll 1
+        for (int tile = 0; tile < tiles && ok; ++tile) {
+            uint32_t todo = __ballot_sync(kFull, page >= 0) & 0xffu, kc = 0u, vc = 0u;
+            if (page >= 0) {
+                kc = cache_scale_code(kraw);
+                vc = cache_scale_code(vraw);
+            }
+#pragma unroll 1
+            do {
+                const int s = n & 1;
+                ok = warp_wait(&empty[s], ((n >> 1) & 1) ^ 1);
+                if (!ok) break;
+                bool take = todo >> block & 1u;
+                uint32_t kmost = __reduce_max_sync(kFull, take ? kc : 0u), vmost = __reduce_max_sync(kFull, take ? vc : 0u);
+                if (__any_sync(kFull, take && (kc + kNarrow < kmost || vc + kNarrow < vmost))) {
+                    const int first = __ffs(todo) - 1;
+                    const uint32_t k0 = __shfl_sync(kFull, kc, first), v0 = __shfl_sync(kFull, vc, first);
+                    // 7 below to 8 above
+                    take = take && kc + 7u >= k0 && kc <= k0 + 8u && vc + 7u >= v0 && vc <= v0 + 8u;
+                    kmost = __reduce_max_sync(kFull, take ? kc : 0u);
+                    vmost = __reduce_max_sync(kFull, take ? vc : 0u);
+                }
+                const uint32_t taken = __ballot_sync(kFull, take) & 0xffu;
+                todo &= ~taken;
+                StepInfo& t = info[n & 7];
+                if (lane < 4)
+                    t.valid[lane] = (taken >> (2 * lane) & 1u) * 0xffffu | (taken >> (2 * lane + 1) & 1u) * 0xffff0000u;
+                if (lane < 8) {
+                    t.page[lane] = take ? page : -1;
+                    t.fk[lane] = f16_factor(take ? kmost - kc : 0u);
+                    t.fv[lane] = f16_factor(take ? vmost - vc : 0u);
+                }
+                if (lane == 0) {
+                    t.k = cache_scale_value(max(kmost, 1u));
+                    t.v = vmost;
+                    t.key0 = key_begin + tile * 128;
+                    t.last = tile + 1 == tiles && todo == 0u;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(&full[s], __popc(taken) * kBlock);
+                __syncwarp();
+                if (lane < 8 && take)
+                    bulk_g2s(raw + s * 128 * D + block * kBlock,
+                             row_of<D>(a, page, 0, head, key_begin + tile * 128 + block * kBlockTokens), kBlock, &full[s], keep);
+                ++n;
+            } while (todo != 0u);
+            page = checked(next);
+            next = page_of(tile + 2);
+            load_scales(page, tile + 1);
+        }
+        // its copies are through before it leaves
+#pragma unroll 1
+        for (int i = max(n - 2, 0); i < n; ++i) ok = warp_wait(&full[i & 1], (i >> 1) & 1) && ok;
+        return ok;
+    }
+
+    // Four warps, keys and values in turn.  A step's raw keys are read, and its
+    // values loaded, into the registers that the step before has just left: shared
+    // memory is as busy with the matrix unit's operands that a read takes 400 clocks.
+    static __device__ __forceinline__ bool convert(const AttnArgs& a, int head, const unsigned char* raw, unsigned char* ks,
+                                                   unsigned char* vs, uint64_t* rawfull, uint64_t* rawempty, uint64_t* kfull,
+                                                   uint64_t* kempty, uint64_t* vfull, uint64_t* vempty, const StepInfo* info) {
+        constexpr int kTile = 128 * D * 2;      // bytes of an operand tile
+        const int lane = threadIdx.x & 31, w = threadIdx.x >> 5 & 3;
+        const int octet = (w & 1) * 8 + (lane & 7), unit = (w >> 1) * 4 + (lane >> 3), block = octet >> 1;
+        RawKeys<D> keys;
+        RawValues<D> values;
+        if (!warp_wait(&rawfull[0], 0)) return false;
+        read_raw<D>(keys, raw, w, lane);
+        load_values<D>(values, a, info[0].key0 + octet * 8, info[0].page[block], head, unit);
+#pragma unroll 1
+        for (int n = 0;; ++n) {
+            const int s = n & 1;
+            const uint32_t parity = (n >> 1) & 1;
+            const StepInfo& t = info[n & 7];
+            const int last = t.last;
+            if (!warp_wait(&kempty[s], parity ^ 1)) return false;
+            write_keys<D>(ks + s * kTile, keys, w, lane, t.fk[2 * w], t.fk[2 * w + 1]);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&kfull[s]);
+                mbar_arrive(&rawempty[s]);
+            }
+            if (!last) {
+                if (!warp_wait(&rawfull[s ^ 1], ((n + 1) >> 1) & 1)) return false;
+                read_raw<D>(keys, raw + (s ^ 1) * 128 * D, w, lane);
+            }
+            if (!warp_wait(&vempty[s], parity ^ 1)) return false;
+            write_values<D>(vs + s * kTile, values, octet, unit, t.fv[block]);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&vfull[s]);
+            if (last) return true;
+            const StepInfo& u = info[(n + 1) & 7];
+            load_values<D>(values, a, u.key0 + octet * 8, u.page[block], head, unit);
+        }
+    }
+};
 
 }  // namespace rmsq

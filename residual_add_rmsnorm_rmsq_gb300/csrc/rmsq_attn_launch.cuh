@@ -70,7 +70,9 @@ cudaError_t launch_split(AttnArgs a, int64_t max_tiles, cudaStream_t stream) {
 template <class P, class E, int D>
 cudaError_t launch_prompt(AttnArgs a, cudaStream_t stream) {
     const void* fn = (const void*)&attn_prompt_kernel<P, E, D>;
-    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, PromptTile<D>::smem);
+    constexpr int smem = PromptTile<D>::with_ring(P::ring);
+    static_assert(smem <= 230400, "the rest is the kernel's static shared memory");
+    const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // as many 256-row items as these sizes can hold; those without one return at once
     const int64_t rows = static_cast<int64_t>(a.tokens) * a.group;
@@ -78,7 +80,7 @@ cudaError_t launch_prompt(AttnArgs a, cudaStream_t stream) {
     const int64_t items = rows / 256 + (few < a.requests ? few : a.requests);
     void* params[] = {&a};
     return launch_kernel(fn, dim3(static_cast<unsigned>(items * a.kv_heads)), dim3(kPromptThreads), params,
-                         PromptTile<D>::smem, stream);
+                         smem, stream);
 }
 
 // What the kernels take for 128 keys, in us: the split kernel for 48 (row, kv

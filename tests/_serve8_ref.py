@@ -113,9 +113,10 @@ def attention(q, codes, scales, table, q_lens, seq_lens, softmax_scale, window, 
       - the output's rounding, half a step: eps / 2 |out|, and among fp16's
         subnormal numbers (below 2^-14, steps of 2^-24) 2^-25;
       - weights rounded to f16: 2^-11 A; they are held relative to the largest
-        value scale S of the request's head, and where that product is below
-        2^-23 of the largest weight it is subnormal, off by 2^-34 of it times a
-        code of at most 448: n 2^-34 448 S;
+        value scale S of the request's head, the largest of them as 2^5 at least,
+        and where that product is below 2^-19 of it it is subnormal in f16, off by
+        2^-25 (half a step), so 2^-30 of it, times a code of at most 448:
+        n 2^-30 448 S;
       - logits: a dot product of D exact products summed in fp32, counted with
         a full step (2^-23) per addition because the matrix unit may truncate:
         ds = (D + 8) 2^-23 scale sum|q||k|, 2^-21 for the exponential and
@@ -159,7 +160,7 @@ def attention(q, codes, scales, table, q_lens, seq_lens, softmax_scale, window, 
                     cnt = len(s)
                     big = sv[at[ok], 1, h // G, off[ok] // 16].max()
                     tol[t, h] = eps / 2 * np.abs(out[t, h]) + A * (2.0 ** -11 + 2 * ds + 2 * cnt * 2.0 ** -23) + \
-                        cnt * 2.0 ** -34 * 448 * big + (2.0 ** -25 if eps == 2.0 ** -10 else 0.0)
+                        cnt * 2.0 ** -30 * 448 * big + (2.0 ** -25 if eps == 2.0 ** -10 else 0.0)
                     tol_lse[t, h] = ds + cnt * 2.0 ** -23 + 2.0 ** -20 + 2.0 ** -23 * abs(lse[t, h])
             t += 1
     return out, lse, tol, tol_lse
