@@ -28,7 +28,11 @@
 // angles in registers for all tokens, so that a token costs no selection: two
 // 16-byte reads each of cos and sin where every aligned group of four angles
 // has one axis (sections that are multiples of four), eight 4-byte ones
-// otherwise (axes that alternate).
+// otherwise (axes that alternate).  16384 tokens of 32 + 4 heads of 128 take 53.3
+// and 56.5 us (5.5 TB/s; one axis 49.7): the kernel waits for each token's chain of
+// reads, so that CTAs per SM decide.  The next positions therefore wait in shared
+// memory, which leaves 56 registers for four of them; in registers they were 61 us
+// with three CTAs.  Each warp putting the token's own row together first was 65.
 #pragma once
 
 #include <type_traits>
@@ -321,7 +325,7 @@ constexpr int kQkPipeMaxThreads = 512;
 static_assert(RMSQ_QK_PIPE_MAXNREG <= 64, "a 512-thread CTA must fit the SM's registers");
 
 template <class E, int D, bool NEOX, int AXES>
-__global__ void __maxnreg__(AXES == kOneAxis ? RMSQ_QK_PIPE_MAXNREG : 64)
+__global__ void __maxnreg__(RMSQ_QK_PIPE_MAXNREG)
     qk_pipe_kernel(const QkArgs a, const int stages, const uint32_t stage_bytes) {
     constexpr int LPH = D / kQkEpl, HPW = 32 / LPH;
     extern __shared__ __align__(128) unsigned char ring[];
@@ -365,9 +369,29 @@ __global__ void __maxnreg__(AXES == kOneAxis ? RMSQ_QK_PIPE_MAXNREG : 64)
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) p[i] = __ldg(a.pos + static_cast<int64_t>(i) * a.n + t);
     };
-    int64_t p_next[ROWS];   // thread 0: positions of the next token to issue
+    // Thread 0: position of the next token to issue, in a register, or three of them
+    // copied to shared memory (registers are what four CTAs per SM lack).
+    int64_t p_next[1] = {-1};
+    __shared__ int64_t s_next[ROWS];
+    auto fetch_next = [&](int t) {
+        if constexpr (AXES == kOneAxis) {
+            load_pos(t, p_next);
+        } else {
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) p_next[i] = -1;
+            for (int i = 0; i < ROWS; ++i)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8;"
+                             :: "r"(smem_u32(&s_next[i])), "l"(a.pos + static_cast<int64_t>(i) * a.n + t) : "memory");
+        }
+    };
+    auto issue_next = [&](int k, int s) {
+        if constexpr (AXES == kOneAxis) {
+            issue(k, s, p_next);
+        } else {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            const int64_t p[ROWS] = {s_next[0], s_next[1], s_next[2]};
+            issue(k, s, p);
+        }
+    };
     if constexpr (AXES != kOneAxis) {
         if (tid < 32) {
             // a lane per stage: the first tokens' positions in one latency
@@ -379,7 +403,7 @@ __global__ void __maxnreg__(AXES == kOneAxis ? RMSQ_QK_PIPE_MAXNREG : 64)
                 issue(tid, tid, p);
             }
             const int t = blockIdx.x + stages * G;
-            if (tid == 0 && t < a.n) load_pos(t, p_next);
+            if (tid == 0 && t < a.n) fetch_next(t);
         }
     } else if (tid == 0) {
         pol_first = l2_policy_evict_first();
@@ -394,7 +418,7 @@ __global__ void __maxnreg__(AXES == kOneAxis ? RMSQ_QK_PIPE_MAXNREG : 64)
         for (int k = 0; k < kQkMaxStages; ++k)
             if (k < stages && blockIdx.x + k * G < a.n) issue(k, k, pp[k]);
         const int t = blockIdx.x + stages * G;
-        if (t < a.n) load_pos(t, p_next);
+        if (t < a.n) fetch_next(t);
     }
 
     // The weight words of the warp's head group (the same for every token
@@ -466,9 +490,9 @@ __global__ void __maxnreg__(AXES == kOneAxis ? RMSQ_QK_PIPE_MAXNREG : 64)
             break;
         }
         if (tid == 0 && blockIdx.x + (k + stages) * G < a.n) {
-            issue(k + stages, s, p_next);
+            issue_next(k + stages, s);
             const int tn = blockIdx.x + (k + stages + 1) * G;
-            if (tn < a.n) load_pos(tn, p_next);
+            if (tn < a.n) fetch_next(tn);
         }
         if (++s == stages) {
             s = 0;
