@@ -29,7 +29,9 @@ template <int D>
 struct Step8 {
     static constexpr int codes = 16 * D;                      // bytes of a half, keys or values
     static constexpr int half = 2 * codes;
-    static constexpr int stages = D == 64 ? 4 : 2;            // 12, 8 or 16 KB in flight per warp
+    // 8, 16 or 16 KB in flight per warp (128 requests of up to 8192 keys: 122 us with
+    // two stages of D = 128, which let three CTAs on an SM, 118 with three and two)
+    static constexpr int stages = D == 256 ? 2 : 3;
     static constexpr int ring = stages * 2 * half;            // per warp
     // Keys are read by lanes (g, t) at row kappa(g), which for eight lanes are two
     // rows four apart, 64 bytes each: those go to different halves of the banks.

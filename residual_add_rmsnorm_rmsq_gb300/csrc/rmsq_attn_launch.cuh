@@ -85,12 +85,18 @@ cudaError_t launch_prompt(AttnArgs a, cudaStream_t stream) {
 
 // What the kernels take for 128 keys, in us: the split kernel for 48 (row, kv
 // head) per SM, the prompt kernel for a CTA's 256 rows on every SM.  Measured on
-// 20000 to 100000 keys: 1.92 to 2.07 and 1.80 to 1.92 (D = 128), 1.16 to 1.27 and
-// 1.44 to 1.52 (64).
+// 20000 to 100000 keys of the NVFP4 cache: 1.92 to 2.07 and 1.80 to 1.92 (D = 128),
+// 1.16 to 1.27 and 1.44 to 1.52 (64); on 20000 of the FP8 cache, 64 to 160 queries
+// of 8 x 8 heads: 2.21 and 2.06, 1.43 and 1.51 (96 queries of D = 128 296 us split
+// and 320, 112 342 and 321; of D = 64 112 219 and 237, 128 250 and 236).
 struct Cost {
     double split, prompt;
 };
-inline Cost cost_of(int head_dim) { return head_dim <= 64 ? Cost{1.21, 1.48} : Cost{1.97, 1.86}; }
+template <class C>
+Cost cost_of(int head_dim) {
+    if (C::block_scales) return head_dim <= 64 ? Cost{1.43, 1.51} : Cost{2.21, 2.06};
+    return head_dim <= 64 ? Cost{1.21, 1.48} : Cost{1.97, 1.86};
+}
 
 // Requests of more than kPromptRows rows go to the prompt kernel (AUTO: if they
 // are worth it there, see prompt_takes), the others to the split kernel, whichever
@@ -123,7 +129,7 @@ cudaError_t launch_attn(AttnArgs a, int head_dim, int64_t max_query, int64_t max
     const int64_t tokens = max_query > 0 && max_query < a.tokens / a.requests ? max_query * a.requests : a.tokens;
     const int64_t rows = tokens * a.group;
     const int64_t items = (rows / 256 + 1) * a.kv_heads;
-    const Cost cost = cost_of(head_dim);
+    const Cost cost = cost_of<C>(head_dim);
     const bool sooner = cost.split * static_cast<double>(rows * a.kv_heads) / (48.0 * sms) >
                         cost.prompt * static_cast<double>((items + sms - 1) / sms);
     const int64_t rest = a.tokens >= a.requests ? a.tokens - a.requests + 1 : 1;    // left for one request
