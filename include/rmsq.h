@@ -518,32 +518,6 @@ int rmsq_paged_attention_nvfp4_ex(const void *q, int64_t q_stride, const void *k
                                   void *stream, int variant, int64_t max_query);
 
 /*
- * rmsq_paged_attention_fp8 — the same attention over the paged FP8 cache (codes
- * and scales as above), with rmsq_paged_attention_nvfp4_ex's arguments, rules,
- * variants, workspace and errors otherwise.  The products with the codes are
- * exact and summed in fp32; a block's key scale multiplies its 16 logits in fp32,
- * its value scale its 16 weights before those are rounded to f16, relative to the
- * largest value scale met so far.
- * A NaN among a key's elements gives NaN in the out and lse of the queries that
- * attend to it, and of no others (the store marks a token whose value has one in
- * this way); NaN codes of values read as 448.  What unwritten slots and scales
- * behind a request's last token hold does not matter.
- *  cache         16-byte aligned;  scales  no alignment.
- */
-int rmsq_paged_attention_fp8(const void *q, int64_t q_stride, const void *cache, const uint8_t *scales,
-                             int64_t num_pages, int64_t page_size, const int32_t *block_table, int64_t table_width,
-                             const int32_t *query_start, const int32_t *seq_lens, float softmax_scale,
-                             int64_t window, void *out, float *lse, void *workspace, size_t workspace_bytes,
-                             int64_t n_tokens, int64_t num_requests, int num_heads, int num_kv_heads, int head_dim,
-                             int dtype, void *stream, int variant, int64_t max_query);
-
-/* Bytes of workspace rmsq_paged_attention_nvfp4 and _fp8 need (0 for arguments it
- * refuses; else the same for every number of tokens and requests, 10 to 21
- * MB: one workspace serves the calls of a program that follow one another). */
-size_t rmsq_paged_attention_workspace_bytes(int64_t n_tokens, int64_t num_requests, int num_heads,
-                                            int num_kv_heads, int head_dim);
-
-/*
  * The paged FP8 cache: codes, device, u8 (E4M3) [num_pages, 2, num_kv_heads,
  * page_size, head_dim], 16-byte aligned, keys at index 0 and values at index 1
  * of the second axis; and scales, device, u8 [num_pages, 2, num_kv_heads,
@@ -582,6 +556,32 @@ int rmsq_kv_cache_store_fp8(const void *k, int64_t k_stride, const void *v, int6
 int rmsq_kv_cache_load_fp8(const void *cache, const uint8_t *scales, int64_t num_pages, int64_t page_size,
                            const int64_t *slot_map, void *k, int64_t k_stride, void *v, int64_t v_stride,
                            int64_t n_tokens, int num_kv_heads, int head_dim, int dtype, void *stream);
+
+/*
+ * rmsq_paged_attention_fp8 — the same attention over the paged FP8 cache (codes
+ * and scales as above), with rmsq_paged_attention_nvfp4_ex's arguments, rules,
+ * variants, workspace and errors otherwise.  The products with the codes are
+ * exact and summed in fp32; a block's key scale multiplies its 16 logits in fp32,
+ * its value scale its 16 weights before those are rounded to f16, relative to the
+ * largest value scale met so far.
+ * A NaN among a key's elements gives NaN in the out and lse of the queries that
+ * attend to it, and of no others (the store marks a token whose value has one in
+ * this way); NaN codes of values read as 448.  What unwritten slots and scales
+ * behind a request's last token hold does not matter.
+ *  cache         16-byte aligned;  scales  no alignment.
+ */
+int rmsq_paged_attention_fp8(const void *q, int64_t q_stride, const void *cache, const uint8_t *scales,
+                             int64_t num_pages, int64_t page_size, const int32_t *block_table, int64_t table_width,
+                             const int32_t *query_start, const int32_t *seq_lens, float softmax_scale,
+                             int64_t window, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                             int64_t n_tokens, int64_t num_requests, int num_heads, int num_kv_heads, int head_dim,
+                             int dtype, void *stream, int variant, int64_t max_query);
+
+/* Bytes of workspace rmsq_paged_attention_nvfp4 and _fp8 need (0 for arguments it
+ * refuses; else the same for every number of tokens and requests, 10 to 21
+ * MB: one workspace serves the calls of a program that follow one another). */
+size_t rmsq_paged_attention_workspace_bytes(int64_t n_tokens, int64_t num_requests, int num_heads,
+                                            int num_kv_heads, int head_dim);
 
 /* Most ranks rmsq_allreduce_add_rmsnorm_quant sums. */
 #define RMSQ_MAX_ALLREDUCE_RANKS 8
