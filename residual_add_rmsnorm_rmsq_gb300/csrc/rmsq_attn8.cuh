@@ -162,11 +162,13 @@ __device__ __forceinline__ void values16(WarpState<D, NB>& w, const KeyRegs8<D>&
 // ahead.
 //
 // The prompt step of rmsq_attn_prompt.cuh's figures (2478 and 2445 queries of 32
-// heads, 192 GFLOP) takes 251 us, over the NVFP4 cache 203.  Tried on the way: keys
-// loaded into registers, a row per thread, with a factor for each 16 logits in the
-// softmax 278; the same with lines read whole 295; the blocks that are far apart
-// handled in the softmax, which then holds code for both, 305; keys converted by
-// two warps of the issuing group 283.
+// heads, 192 GFLOP) takes 236 us, over the NVFP4 cache 199; 128 keys 1.97 us on a
+// context of 20000 (1.67).  What it is sensitive to is the size of the roles' code
+// (see the issuing loop) and the latency of reads.  Tried on the way: keys loaded into
+// registers, a row per thread, with a factor for each 16 logits in the softmax 278;
+// the same with lines read whole 295; the blocks that are far apart handled in the
+// softmax, which then holds code for both, 305; keys converted by two warps of the
+// issuing group 283; values converted in a rolled loop 246 where it was 251.
 template <int D>
 struct RawValues {
     static constexpr int VW = D / 32;           // words of a key's values (D/8 dims)
@@ -297,16 +299,19 @@ struct Fp8Prompt : Fp8Cache {
         load_scales(page, 0);
 #pragma unroll 1
         for (int tile = 0; tile < tiles && ok; ++tile) {
-            uint32_t todo = __ballot_sync(kFull, page >= 0) & 0xffu, kc = 0u, vc = 0u;
-            if (page >= 0) {
-                kc = cache_scale_code(kraw);
-                vc = cache_scale_code(vraw);
-            }
+            uint32_t todo = __ballot_sync(kFull, page >= 0) & 0xffu;
 #pragma unroll 1
             do {
                 const int s = n & 1;
                 ok = warp_wait(&empty[s], ((n >> 1) & 1) ^ 1);
                 if (!ok) break;
+                // The keys of all blocks left, before anything waits for their scales.
+                if (lane == 0) mbar_expect_tx(&full[s], __popc(todo) * kBlock);
+                __syncwarp();
+                if (lane < 8 && (todo >> block & 1u))
+                    bulk_g2s(raw + s * 128 * D + block * kBlock,
+                             row_of<D>(a, page, 0, head, key_begin + tile * 128 + block * kBlockTokens), kBlock, &full[s], keep);
+                const uint32_t kc = cache_scale_code(kraw), vc = cache_scale_code(vraw);
                 bool take = todo >> block & 1u;
                 uint32_t kmost = __reduce_max_sync(kFull, take ? kc : 0u), vmost = __reduce_max_sync(kFull, take ? vc : 0u);
                 if (__any_sync(kFull, take && (kc + kNarrow < kmost || vc + kNarrow < vmost))) {
@@ -334,11 +339,7 @@ struct Fp8Prompt : Fp8Cache {
                     t.last = tile + 1 == tiles && todo == 0u;
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive_expect_tx(&full[s], __popc(taken) * kBlock);
-                __syncwarp();
-                if (lane < 8 && take)
-                    bulk_g2s(raw + s * 128 * D + block * kBlock,
-                             row_of<D>(a, page, 0, head, key_begin + tile * 128 + block * kBlockTokens), kBlock, &full[s], keep);
+                if (lane == 0) mbar_arrive(&full[s]);
                 ++n;
             } while (todo != 0u);
             page = checked(next);
@@ -384,13 +385,17 @@ struct Fp8Prompt : Fp8Cache {
                 read_raw<D>(keys, raw + (s ^ 1) * 128 * D, w, lane);
             }
             if (!warp_wait(&vempty[s], parity ^ 1)) return false;
-            write_values<D>(vs + s * kTile, values, octet, unit, t.fv[block]);
+            const RawValues<D> now = values;
+            const uint32_t fv = t.fv[block];
+            if (!last) {
+                const StepInfo& u = info[(n + 1) & 7];
+                load_values<D>(values, a, u.key0 + octet * 8, u.page[block], head, unit);
+            }
+            write_values<D>(vs + s * kTile, now, octet, unit, fv);
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) mbar_arrive(&vfull[s]);
             if (last) return true;
-            const StepInfo& u = info[(n + 1) & 7];
-            load_values<D>(values, a, u.key0 + octet * 8, u.page[block], head, unit);
         }
     }
 };

@@ -94,7 +94,7 @@ struct Cost {
 };
 template <class C>
 Cost cost_of(int head_dim) {
-    if (C::block_scales) return head_dim <= 64 ? Cost{1.43, 1.51} : Cost{2.21, 2.06};
+    if (C::block_scales) return head_dim <= 64 ? Cost{1.43, 1.45} : Cost{2.21, 1.97};
     return head_dim <= 64 ? Cost{1.21, 1.48} : Cost{1.97, 1.86};
 }
 

@@ -18,12 +18,13 @@
 // One is the chain of a tile: its products (1150 clocks), the hand-over (200), its
 // softmax (2100: 520 to read the logits, 330 for the maximum, 1040 for the
 // weights, the rest hand-over) and the next products; two tiles hide half of
-// that.  128 keys take 1.80 to 1.92 us on contexts of 20000 to 100000.  The other
+// that.  128 keys take 1.67 us on a context of 20000 (1.70 with all products of a
+// tile unrolled).  The other
 // is what lies outside it: a CTA has all of tensor memory, so the next one's
 // request, queries and first conversion, and the last one's output, overlap with
 // nothing (8 to 10 us a CTA: 128 queries of 8 x 8 heads take 12 us on 128 keys and
 // 74 on 4000).  2478 and 2445 queries of 32 heads on contexts of 732 and 1574
-// keys: 204 us, 192 GFLOP (0.94 PFLOP/s; half the measured bf16 rate, 101 us), of
+// keys: 199 us, 192 GFLOP (0.96 PFLOP/s; half the measured bf16 rate, 101 us), of
 // which the 80 steps of an SM are 147 and the starts and ends of its 4.1 CTAs and
 // the last round the rest.  Heads of 64: 2000 queries of 32 heads on 4000 keys 88
 // us, of 128 115.  Measured and not kept (against
@@ -73,7 +74,7 @@ constexpr uint32_t kF16Idesc = (1u << 4) | (static_cast<uint32_t>(N / 8) << 17) 
 // apart.
 template <int N, int STEPS, int A_BLOCK, int B_BLOCK>
 __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint32_t a, uint32_t b) {
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < STEPS; ++i)
         asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %4, 0;\n\t"
                      "mov.b64 da, {%1, %5};\n\tmov.b64 db, {%2, %5};\n\t"
@@ -86,7 +87,7 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint32_t a, uint32_t b) {
 // D (+)= A . B^T with A in tensor memory (8 columns per step).
 template <int N, int STEPS, int B_BLOCK>
 __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b, bool add) {
-#pragma unroll
+#pragma unroll 4
     for (int i = 0; i < STEPS; ++i)
         asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %4, 0;\n\tmov.b64 db, {%2, %5};\n\t"
                      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
@@ -240,6 +241,11 @@ struct Nvfp4Prompt : Nvfp4Cache {
 // read from tensor memory twice, 16 at a time, the two passes waited out
 // sixteen load latencies per tile (260 us for the prompt step of 147 GFLOP).
 using Row = float[8][16];
+
+// A stage that is not a constant.
+struct StageOf {
+    int value;
+};
 
 // Half h (0, 1) of a row: 64 logits.
 __device__ __forceinline__ void start_half(Row& d, uint32_t s_at, int h) {
@@ -407,8 +413,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
         fewer_registers<kIssueRegs>();
         if (warp == 12 && steps > 0) {
             // The whole warp walks the loop, so that its addresses stay
-            // uniform, and twice a round, so that its stages are constants;
-            // one lane issues.  Tile by tile: O += P . V of the step before, then
+            // uniform, and twice a round, so that its stages are constants
+            // (with block_scales once, and a tile after the other: the roles' code
+            // together does not fit the instruction cache there, and a step of
+            // 128 keys took 2.49 us with all SMs at work and 1.89 with a fifth of
+            // them, now 1.97 either way); one lane issues.  Tile by tile: O += P . V of the step before, then
             // S = Q . K^T of this one.  (One issuing warp per tile let the two
             // fall into step, both tiles' softmax at once and then both tiles'
             // products: 260 us instead of 212 for the prompt step.)
@@ -417,7 +426,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
             for (int i = 0; i < tiles && ok; ++i) ok = mbar_wait(&qfull[i], 0);
             ok = __all_sync(kFull, ok);
             auto step = [&](auto stage, int n) {
-                constexpr int s = decltype(stage)::value, z = s ^ 1;
+                const int s = stage.value, z = s ^ 1;
                 if (n < steps) {
                     ok = ok && mbar_wait(&kfull[s], (n >> 1) & 1);
                     if constexpr (P::block_scales) {
@@ -425,7 +434,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                     }
                 }
                 if (n > 0) ok = ok && mbar_wait(&vfull[z], ((n - 1) >> 1) & 1);
-#pragma unroll
+#pragma unroll (P::block_scales ? 1 : 2)
                 for (int i = 0; i < 2; ++i) {
                     if (i >= tiles) break;
                     const uint32_t s_at = tmem + i * 128, o_at = tmem + 256 + i * D;
@@ -451,9 +460,14 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                     }
                 }
             };
-            for (int n = 0; n <= steps && ok; n += 2) {
-                step(std::integral_constant<int, 0>{}, n);
-                if (ok && n < steps) step(std::integral_constant<int, 1>{}, n + 1);
+            if constexpr (P::block_scales) {
+#pragma unroll 1
+                for (int n = 0; n <= steps && ok; ++n) step(StageOf{n & 1}, n);
+            } else {
+                for (int n = 0; n <= steps && ok; n += 2) {
+                    step(std::integral_constant<int, 0>{}, n);
+                    if (ok && n < steps) step(std::integral_constant<int, 1>{}, n + 1);
+                }
             }
             if (!ok && issuer) {
                 mma_commit(&drained);
