@@ -86,15 +86,15 @@ cudaError_t launch_prompt(AttnArgs a, cudaStream_t stream) {
 // What the kernels take for 128 keys, in us: the split kernel for 48 (row, kv
 // head) per SM, the prompt kernel for a CTA's 256 rows on every SM.  Measured on
 // 20000 to 100000 keys of the NVFP4 cache: 1.92 to 2.07 and 1.80 to 1.92 (D = 128),
-// 1.16 to 1.27 and 1.44 to 1.52 (64); on 20000 of the FP8 cache, 64 to 160 queries
-// of 8 x 8 heads: 2.21 and 2.06, 1.43 and 1.51 (96 queries of D = 128 296 us split
-// and 320, 112 342 and 321; of D = 64 112 219 and 237, 128 250 and 236).
+// 1.16 to 1.27 and 1.44 to 1.52 (64); on 20000 of the FP8 cache 2.21 and 1.97, 1.43
+// and 1.52 (64 to 160 queries of 8 x 8 heads: 96 of D = 128 296 us split and 307, 112
+// 342 and 306; of D = 64 112 219 and 238, 128 250 and 238).
 struct Cost {
     double split, prompt;
 };
 template <class C>
 Cost cost_of(int head_dim) {
-    if (C::block_scales) return head_dim <= 64 ? Cost{1.43, 1.45} : Cost{2.21, 1.97};
+    if (C::block_scales) return head_dim <= 64 ? Cost{1.43, 1.52} : Cost{2.21, 1.97};
     return head_dim <= 64 ? Cost{1.21, 1.48} : Cost{1.97, 1.86};
 }
 

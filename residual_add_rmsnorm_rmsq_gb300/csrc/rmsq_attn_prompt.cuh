@@ -427,12 +427,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
             ok = __all_sync(kFull, ok);
             auto step = [&](auto stage, int n) {
                 const int s = stage.value, z = s ^ 1;
-                if (n < steps) {
-                    ok = ok && mbar_wait(&kfull[s], (n >> 1) & 1);
-                    if constexpr (P::block_scales) {
-                        if (__all_sync(kFull, ok && info[n & 7].last)) steps = n + 1;
-                    }
-                }
+                if (n < steps) ok = ok && mbar_wait(&kfull[s], (n >> 1) & 1);
                 if (n > 0) ok = ok && mbar_wait(&vfull[z], ((n - 1) >> 1) & 1);
 #pragma unroll (P::block_scales ? 1 : 2)
                 for (int i = 0; i < 2; ++i) {
@@ -462,7 +457,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
             };
             if constexpr (P::block_scales) {
 #pragma unroll 1
-                for (int n = 0; n <= steps && ok; ++n) step(StageOf{n & 1}, n);
+                for (int n = 0; n <= steps && ok; ++n) {
+                    step(StageOf{n & 1}, n);
+                    if (ok && n < steps && info[n & 7].last) steps = n + 1;     // (read behind the products)
+                }
             } else {
                 for (int n = 0; n <= steps && ok; n += 2) {
                     step(std::integral_constant<int, 0>{}, n);
@@ -574,8 +572,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                 ok = warp_wait(&sfull[i], n & 1);
                 if (!ok) break;
                 tc_fence_after();
-                // (read once, together: shared memory is busy with the products' operands,
-                // and every read after another here was 400 clocks of the step)
+                Row d;
+                start_half(d, s_at, 0);
+                // (read together, beside the logits: shared memory is busy with the
+                // products' operands, a read takes up to 400 clocks)
                 const StepInfo& at = info[P::block_scales ? n & 7 : 0];
                 const uint4 have = *reinterpret_cast<const uint4*>(P::block_scales ? at.valid : valid[n & 3]);
                 const uint4 rest = P::block_scales ? *reinterpret_cast<const uint4*>(&at.k) : make_uint4(0u, 0u, 0u, 0u);
@@ -598,8 +598,6 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                         see[c] = below & above & hv[c];
                     }
                 }
-                Row d;
-                start_half(d, s_at, 0);
                 finish_half(d, 0);
                 start_half(d, s_at, 1);
                 if (!full) mask_half(d, 0, see);
@@ -655,7 +653,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                     // two that only changes the addend; the sum without it.  (The factor
                     // within the normal numbers: a masked logit times zero would be NaN.)
                     const float fk = done ? f : clamp_factor(f * tile_k);
-                    const int down = max(static_cast<int>(tile_v) - static_cast<int>(ve), -90);
+                    // (a row that sees nothing here may be in units of any scale, or none)
+                    const int down = min(max(static_cast<int>(tile_v) - static_cast<int>(ve), -90),
+                                         static_cast<int>(P::lazy_scale));
                     float sum = 0.0f;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) sum += weigh_half(d, h, s_at, fk, shift + static_cast<float>(down));

@@ -146,6 +146,16 @@ def test_scales_over_their_range(rmsq_gpu, k_scale, v_scale, variant):
 
 
 @pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [1, 40])
+def test_large_values_before_the_window(rmsq_gpu, D, window, variant):
+    """Rows that see nothing of the first tiles, whose value scales are far above
+    one, and rows that see nothing at all."""
+    c = make([150, 70, 3], [290, 60, 200], 4, 2, D, 16, "bf16", seed=window, v_scale=(128, 187))
+    check(rmsq_gpu, c, window=window, variant=variant)
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
 @pytest.mark.parametrize("rising", [True, False])
 def test_values_that_grow_along_the_keys(rmsq_gpu, rising, variant):
     """The value scale of a block 2^1 (2^-1) times the one before it, and equal
