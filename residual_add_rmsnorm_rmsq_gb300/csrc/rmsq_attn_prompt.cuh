@@ -18,14 +18,14 @@
 // One is the chain of a tile: its products (1150 clocks), the hand-over (200), its
 // softmax (2100: 520 to read the logits, 330 for the maximum, 1040 for the
 // weights, the rest hand-over) and the next products; two tiles hide half of
-// that.  128 keys take 1.67 us on a context of 20000 (1.70 with all products of a
+// that.  128 keys take 1.66 us on a context of 20000 (1.70 with all products of a
 // tile unrolled).  The other
 // is what lies outside it: a CTA has all of tensor memory, so the next one's
 // request, queries and first conversion, and the last one's output, overlap with
 // nothing (8 to 10 us a CTA: 128 queries of 8 x 8 heads take 12 us on 128 keys and
 // 74 on 4000).  2478 and 2445 queries of 32 heads on contexts of 732 and 1574
-// keys: 199 us, 192 GFLOP (0.96 PFLOP/s; half the measured bf16 rate, 101 us), of
-// which the 80 steps of an SM are 147 and the starts and ends of its 4.1 CTAs and
+// keys: 197 us, 192 GFLOP (0.97 PFLOP/s; half the measured bf16 rate, 101 us), of
+// which the 80 steps of an SM are 133 and the starts and ends of its 4.1 CTAs and
 // the last round the rest.  Heads of 64: 2000 queries of 32 heads on 4000 keys 88
 // us, of 128 115.  Measured and not kept (against
 // 212 to 215 us): two threads per row (326: 88 registers a thread spill), one
@@ -417,7 +417,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
             // (with block_scales once, and a tile after the other: the roles' code
             // together does not fit the instruction cache there, and a step of
             // 128 keys took 2.49 us with all SMs at work and 1.89 with a fifth of
-            // them, now 1.97 either way); one lane issues.  Tile by tile: O += P . V of the step before, then
+            // them, so 1.96 either way); one lane issues.  Tile by tile: O += P . V of the step before, then
             // S = Q . K^T of this one.  (One issuing warp per tile let the two
             // fall into step, both tiles' softmax at once and then both tiles'
             // products: 260 us instead of 212 for the prompt step.)

@@ -47,7 +47,10 @@ __device__ __forceinline__ uint8_t* scale_at(const Cache8Args& a, int64_t slot, 
 // all runs of the range to their end; no token is looked after twice and no
 // warp waits for another.  A lane holds 8 elements of a token, D / 8 lanes a
 // token, all of a run's tokens are in registers before the maximum is taken: one
-// pass.
+// pass.  Prompts are bound by HBM and, as much, by the chain of a run (slots, tokens,
+// maximum, codes) that a warp walks a side after the other with 80 registers a
+// thread; 16000 tokens of 4 + 4 heads of 128, 49 MB, take about 11 us (4.4 TB/s), 256
+// decodes of 8 + 8 heads 4.0 us (latency: slots, then tokens and the old scale).
 //
 // Not finite elements do not count for the scale.  They become NaN, and so do all
 // of the token's key codes of that head: the attention's reader can then leave
@@ -223,7 +226,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) cache8_st
 // ---------------------------------------------------------------------------
 // Load: T(code * scale), exact before its rounding; zeros for a slot outside the
 // cache.  One thread per 16 elements, a token's (keys, then values) on a power of
-// two of lanes up to 32, as in the NVFP4 load.
+// two of lanes up to 32, as in the NVFP4 load.  Bound by HBM: 16016 tokens of 4 + 4
+// heads of 128, 49 MB, take 10.0 us (4.9 TB/s), 2134 of 8 + 8 heads 6.4 us.
 // ---------------------------------------------------------------------------
 template <class E, int D>
 __global__ void __launch_bounds__(256) cache8_load_kernel(Cache8Args a) {
@@ -332,10 +336,16 @@ cudaError_t launch_cache8(bool store, int head_dim, int dtype, Cache8Args& a, cu
     const void* fn = dtype == RMSQ_FP16 ? cache8_kernel<Fp16T>(store, head_dim) : cache8_kernel<Bf16T>(store, head_dim);
     int64_t threads;
     if (store) {
-        // one token per warp while the warps of one token each fit the card
-        // a few times over: then 16, a block of a prompt
+        // Tokens of a warp: one for a decode (each token starts a run: a warp of
+        // several takes them one after the other), more for a prompt (most of its
+        // tokens start none).  The host sees only how many there are.  Measured, in
+        // us for 1, 2, 4, 8, 16: 256 decodes of 8 heads of 128 4.2 6.0 8.2 14.1 26.4, a
+        // prompt of 1000 6.7 6.2 6.1 5.3 6.3; 1000 decodes 8.7 9.5 12.4 18.9 28.3, a
+        // prompt of 2000 8.9 7.9 7.5 7.2 7.3; 3000 decodes 21.4 20.2 20.1 23.7 42.1, a
+        // prompt of 4000 13.1 10.3 8.7 8.1 8.5; 8000 decodes 53 50 49 51 62, a prompt of
+        // 8000 21.7 16.6 13.9 12.4 11.6; a prompt of 30000 70 50 40 36 34.
         const int64_t warps = static_cast<int64_t>(a.n) * a.heads;
-        a.range_shift = warps <= 16384 ? 0 : warps <= 65536 ? 2 : 4;
+        a.range_shift = warps < 8192 ? 0 : warps < 24576 ? 1 : warps < 49152 ? 2 : warps < 131072 ? 3 : 4;
         const int64_t ranges = (static_cast<int64_t>(a.n) + (1 << a.range_shift) - 1) >> a.range_shift;
         threads = ranges * a.heads * 32;
     } else {

@@ -71,9 +71,9 @@ def test_store(rmsq_gpu, dtype, h, D, page, lens):
     _check(rmsq_gpu, *_cache(rng, pages, h, D, page), _kv(rng, n, h, D, dtype), _kv(rng, n, h, D, dtype), slots)
 
 
-@pytest.mark.parametrize("n, h", [(5000, 4), (20000, 4), (9000, 8)])
+@pytest.mark.parametrize("n, h", [(5000, 4), (20000, 4), (9000, 8), (7000, 4), (33000, 4)])
 def test_store_of_a_prompt(rmsq_gpu, n, h):
-    """Sizes for which a warp looks after 4 and 16 tokens; decodes between them."""
+    """Sizes for which a warp looks after 2, 4, 8 and 16 tokens; decodes between them."""
     rng = np.random.default_rng(n)
     lens = [(9, n // 2)] + [(i % 30, 1) for i in range(40)] + [(3, n - n // 2 - 40)]
     pages = sum(-(-(c + m) // 64) for c, m in lens) + 2
