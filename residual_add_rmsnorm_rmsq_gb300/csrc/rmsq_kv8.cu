@@ -49,7 +49,7 @@ __device__ __forceinline__ uint8_t* scale_at(const Cache8Args& a, int64_t slot, 
 // token, all of a run's tokens are in registers before the maximum is taken: one
 // pass.  Prompts are bound by HBM and, as much, by the chain of a run (slots, tokens,
 // maximum, codes) that a warp walks a side after the other with 80 registers a
-// thread; 16000 tokens of 4 + 4 heads of 128, 49 MB, take about 11 us (4.4 TB/s), 256
+// thread; 16000 tokens of 4 + 4 heads of 128, 49 MB, take 9.6 us (5.1 TB/s), 256
 // decodes of 8 + 8 heads 4.0 us (latency: slots, then tokens and the old scale).
 //
 // Not finite elements do not count for the scale.  They become NaN, and so do all
