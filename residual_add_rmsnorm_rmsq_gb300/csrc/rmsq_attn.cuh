@@ -55,7 +55,11 @@
 // Work is split evenly over the CTAs whatever the lengths: the (request, row
 // tile, kv head, 128-key tile) tiles form one sequence, cut into equal runs; a CTA
 // writes the items its run holds whole, and leaves (O, m, l, f) in the workspace
-// for the two that its ends may cut, which a second launch joins in order.
+// for the two that its ends may cut, which a second launch joins in order.  A
+// reader with a `piece` counts that many tiles more for each item, places of the
+// sequence without work: what a CTA does once per item it touches (queries, first
+// copies, the warps' join) then counts like tiles, and a CTA of many short items
+// gets fewer tiles.
 #pragma once
 
 #include "rmsq_device.cuh"
@@ -135,12 +139,15 @@ __device__ __forceinline__ Req load_request(const AttnArgs& a, int r) {
     return x;
 }
 
-// prefix[r] = count(rows, key tiles, the prompt kernel's or not) summed over the
-// requests before r, prefix[requests] over all, in shared memory.  Ends with a
-// barrier.  (Compact on purpose: it is cold code at the start of every CTA.)
-template <int THREADS, class Count>
-__device__ __forceinline__ void scan_requests(const AttnArgs& a, int64_t* prefix, Count count) {
+// prefix[r] = items(rows, the prompt kernel's or not) summed over the requests
+// before r, prefix[requests] over all, in shared memory; with TILES their tiles, and
+// where those of all kv heads are more than the workers, PIECE more for each item.
+// Returns what was added to an item.  Ends with a barrier.  (Compact on purpose:
+// it is cold code at the start of every CTA.)
+template <int THREADS, bool TILES, int PIECE, class Items>
+__device__ __forceinline__ int scan_requests(const AttnArgs& a, int64_t* prefix, Items items) {
     __shared__ int64_t wsum[THREADS / 32];
+    __shared__ int witems[THREADS / 32];
     __shared__ int longer[32];      // candidates of 2^i key tiles and more
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (a.requests + THREADS - 1) / THREADS;
@@ -160,41 +167,65 @@ __device__ __forceinline__ void scan_requests(const AttnArgs& a, int64_t* prefix
     }
     if (a.share != 0) __syncthreads();
     int64_t sum = 0;
+    int count = 0;
 #pragma unroll 1
     for (int r = r0; r < r1; ++r) {
         const int64_t rows = prefix[r + 1] >> 32;
-        const int ktiles = static_cast<int>(prefix[r + 1]);
-        const int64_t c = count(rows, ktiles, prompt_takes(a, rows, ktiles, longer));
-        prefix[r + 1] = c;
-        sum += c;
+        const int ktiles = static_cast<int>(prefix[r + 1]), length = TILES ? ktiles : 1;
+        const int n = static_cast<int>(items(rows, prompt_takes(a, rows, ktiles, longer)));
+        prefix[r + 1] = static_cast<int64_t>(n) << 32 | length;
+        sum += static_cast<int64_t>(n) * length;
+        count += n;
     }
     int64_t inc = sum;
+    int inc_items = count;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int64_t u = __shfl_up_sync(kFull, inc, o);
         if (lane >= o) inc += u;
+        if constexpr (PIECE != 0) {
+            const int v = __shfl_up_sync(kFull, inc_items, o);
+            if (lane >= o) inc_items += v;
+        }
     }
-    if (lane == 31) wsum[warp] = inc;
+    if (lane == 31) {
+        wsum[warp] = inc;
+        if constexpr (PIECE != 0) witems[warp] = inc_items;
+    }
     __syncthreads();
     int64_t run = inc - sum;
+    int more = 0;
+    if constexpr (PIECE != 0) {
+        int64_t total = 0;
+#pragma unroll
+        for (int w = 0; w < THREADS / 32; ++w) total += wsum[w];
+        if (total * a.kv_heads > a.workers) more = PIECE;
+        int before = inc_items - count;
+#pragma unroll 1
+        for (int w = 0; w < warp; ++w) before += witems[w];
+        run += static_cast<int64_t>(before) * more;
+    }
 #pragma unroll 1
     for (int w = 0; w < warp; ++w) run += wsum[w];
 #pragma unroll 1
     for (int r = r0; r < r1; ++r) {
-        run += prefix[r + 1];
+        const int64_t x = prefix[r + 1];
+        run += (x >> 32) * (static_cast<int>(x) + more);
         prefix[r + 1] = run;
     }
     if (tid == 0) prefix[0] = 0;
     __syncthreads();
+    return more;
 }
 
-// Where tile x of the whole sequence lies.
+// Where tile x of the whole sequence lies, whose items have `more` places behind
+// their tiles.
 struct Place {
     int r, head, qtile, tile;   // tile: index inside the item
     int64_t item0;              // first tile of the item in the sequence
 };
 
-__device__ __forceinline__ Place locate(const AttnArgs& a, const int64_t* prefix, int64_t x, Req& req) {
+__device__ __forceinline__ Place locate(const AttnArgs& a, const int64_t* prefix, int64_t x, int more, Req& req) {
     int lo = 0, hi = a.requests;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -203,10 +234,11 @@ __device__ __forceinline__ Place locate(const AttnArgs& a, const int64_t* prefix
     }
     req = load_request(a, lo);
     const int64_t rest = x - prefix[lo] * a.kv_heads;
-    const int64_t item = rest / req.ktiles;
+    const int length = req.ktiles + more;
+    const int64_t item = rest / length;
     Place p;
     p.r = lo;
-    p.tile = static_cast<int>(rest - item * req.ktiles);
+    p.tile = static_cast<int>(rest - item * length);
     p.qtile = static_cast<int>(item / a.kv_heads);
     p.head = static_cast<int>(item - static_cast<int64_t>(p.qtile) * a.kv_heads);
     p.item0 = x - p.tile;
@@ -281,6 +313,7 @@ struct Nvfp4Cache {
     static constexpr float p_shift = 9.0f;          // weights are scaled by 2^9 ...
     static constexpr float lazy = 6.0f;             // ... and by up to 2^6 more while the maximum lags: < 2^16 in f16
     static constexpr uint32_t lazy_scale = 0;
+    static constexpr int piece = 0;                 // items are cut by their tiles alone
     template <int D> using Step = rmsq::Step<D>;
     template <int D> using Regs = KeyRegs<D>;
     // first of the lane's j-th eight dims
@@ -644,9 +677,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
     allow_dependents();
     grid_dependency_wait();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    scan_requests<kAttnThreads>(a, prefix, [](int64_t r, int ktiles, bool taken) {
-        return taken ? 0 : (r + ROWS - 1) / ROWS * ktiles;
-    });
+    const int more = scan_requests<kAttnThreads, true, C::piece>(
+        a, prefix, [](int64_t r, bool taken) { return taken ? 0 : (r + ROWS - 1) / ROWS; });
     const int64_t total = prefix[a.requests] * a.kv_heads;
     const int64_t run = run_length(total, a.workers);
     int64_t x = blockIdx.x * run;
@@ -657,7 +689,11 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
 
     while (x < end) {
         Req rq;
-        const Place at = locate(a, prefix, x, rq);
+        const Place at = locate(a, prefix, x, more, rq);
+        if (C::piece != 0 && at.tile >= rq.ktiles) {
+            x = at.item0 + rq.ktiles + more;
+            continue;
+        }
         const int ntiles = static_cast<int>(min(static_cast<int64_t>(rq.ktiles - at.tile), end - x));
         const int rows = rq.qlen * a.group;      // of the request
         const int row0 = at.qtile * ROWS;

@@ -2,8 +2,8 @@
 // rmsq_attn_prompt.cuh).
 //
 // Decode is bound by HBM: 128 requests of 2048 to 8192 keys, 8 heads on each of 4 kv
-// heads of 128, take 118 us for 697 MB (5.9 TB/s, 44 % of the issue slots; the NVFP4
-// cache's 390 MB 81 us), 3 requests of up to 131071 keys on 8 kv heads 106 us for 635
+// heads of 128, take 114 us for 697 MB (6.1 TB/s, 45 % of the issue slots; the NVFP4
+// cache's 390 MB 81 us), 3 requests of up to 131071 keys on 8 kv heads 105 us for 635
 // MB (6.0 TB/s).
 //
 // An E4M3 code is exact in f16, so that a code is converted and nothing else: the
@@ -34,8 +34,9 @@ template <int D>
 struct Step8 {
     static constexpr int codes = 16 * D;                      // bytes of a half, keys or values
     static constexpr int half = 2 * codes;
-    // 8, 16 or 16 KB in flight per warp (128 requests of up to 8192 keys: 122 us with
-    // two stages of D = 128, which let three CTAs on an SM, 118 with three and two)
+    // 8, 16 or 16 KB in flight per warp (128 requests of up to 8192 keys, items cut by
+    // their tiles alone: 122 us with two stages of D = 128, which let three CTAs on an
+    // SM, 118 with three and two)
     static constexpr int stages = D == 256 ? 2 : 3;
     static constexpr int ring = stages * 2 * half;            // per warp
     // Keys are read by lanes (g, t) at row kappa(g), which for eight lanes are two
@@ -56,6 +57,14 @@ struct Fp8Cache {
     // Weights below 2^-19 of the largest are subnormal f16, off by 2^-30 of it.
     static constexpr float p_shift = 5.0f, lazy = 8.0f;
     static constexpr uint32_t lazy_scale = 2;
+    // Tiles that starting and ending an item counts for, where there are more tiles
+    // than CTAs.  For 0, 1, 2, 3, 4, 6, in us: 32 decodes of 100 to 2000 keys, 8 x 4
+    // heads of 128, 26.0 20.9 19.7 17.7 18.6 20.5, 128 of 16 to 2000 66.5 51.7 47.1 42.6
+    // 41.6 44.8, 256 of 100 to 1000 104 88 81 74 72 73, 128 of 2000 to 8192 (4 x 8)
+    // 103.9 103.5 100.8 100.4 99.9 100.1; heads of 64, 128 of 16 to 2000 34.6 31.5 29.0
+    // 26.1 26.7 27.6; of 256 41.5 30.2 28.8 26.9 26.4 28.2.  (One tile per CTA is
+    // the best cut there is: 8 decodes of up to 500 keys 9.5, with 4 more 10.7.)
+    static constexpr int piece = 4;
     template <int D> using Step = Step8<D>;
     template <int D> using Regs = KeyRegs8<D>;
     // first of the lane's j-th eight dims: 16 of every 64

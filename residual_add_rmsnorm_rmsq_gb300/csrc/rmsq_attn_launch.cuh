@@ -259,7 +259,7 @@ int attend(const AttnCall& c, int per_token) {
     a.window = c.window > INT32_MAX / 2 ? 0 : static_cast<int>(c.window);
     a.scale_log2 = c.softmax_scale * 1.44269504088896341f;
     // most (row tile, kv head, key tile) tiles these sizes can hold
-    const int64_t ktiles = (static_cast<int64_t>(c.width) << shift) / kAttnKeyTile + 1;
+    const int64_t ktiles = (static_cast<int64_t>(c.width) << shift) / kAttnKeyTile + 1 + C::piece;
     constexpr int64_t kMaxTiles = int64_t(1) << 40;
     const int64_t qtiles = c.tokens * a.group / 8 + c.requests;
     const int64_t max_tiles = qtiles > kMaxTiles / ktiles / c.kv_heads ? kMaxTiles : qtiles * ktiles * c.kv_heads;

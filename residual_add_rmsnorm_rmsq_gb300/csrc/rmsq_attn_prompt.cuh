@@ -328,7 +328,7 @@ __device__ __forceinline__ int64_t find_item(const AttnArgs& a, int64_t* scratch
         req = __ffs(__ballot_sync(kFull, inc > item)) - 1;
         return item - __shfl_sync(kFull, inc - items, req);
     }
-    scan_requests<kPromptThreads>(a, scratch, [](int64_t r, int, bool taken) { return taken ? (r + 255) / 256 : 0; });
+    scan_requests<kPromptThreads, false, 0>(a, scratch, [](int64_t r, bool taken) { return taken ? (r + 255) / 256 : 0; });
     int64_t item = scratch[a.requests] - 1 - skip;
     if (item >= 0) {
         int hi = a.requests;

@@ -241,6 +241,16 @@ def test_long_ragged_decode_and_determinism(rmsq_gpu, D, heads, kv):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+@pytest.mark.parametrize("requests", [30, 130, 500])
+@pytest.mark.parametrize("D, heads, kv", [(64, 8, 8), (128, 12, 4), (256, 6, 2)])
+def test_many_requests_of_one_to_three_tiles(rmsq_gpu, D, heads, kv, requests):
+    """Fewer and more tiles of 128 keys than CTAs; requests without queries or keys among them."""
+    rng = np.random.default_rng(requests + D)
+    q_lens = rng.integers(0, 4, requests).tolist()
+    seq = [0 if q == 0 and r % 2 else q + int(rng.integers(0, 380)) for r, q in enumerate(q_lens)]
+    check(rmsq_gpu, make(q_lens, seq, heads, kv, D, 16, "bf16", seed=requests), variant="direct")
+
+
 def test_no_tokens_no_requests_no_pages(rmsq_gpu):
     rq = rmsq_gpu
     c = make([1], [20], 2, 1, 64, 16, "bf16")
