@@ -100,6 +100,7 @@ struct AttnArgs {
     int requests, width, tokens, heads, kv_heads, group;
     int page_shift, num_pages, window, workers;
     int most_rows;          // rows of a request above which it may be the prompt kernel's, see prompt_takes
+    int half_items;         // prompt items of 128 rows per kv head up to which they have 128 and not 256
     int64_t share;          // 0, or what rows times requests have to reach for that
     float scale_log2;       // softmax scale * log2(e)
 };

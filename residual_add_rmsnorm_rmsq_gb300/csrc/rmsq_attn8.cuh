@@ -2,9 +2,9 @@
 // rmsq_attn_prompt.cuh).
 //
 // Decode is bound by HBM: 128 requests of 2048 to 8192 keys, 8 heads on each of 4 kv
-// heads of 128, take 114 us for 697 MB (6.1 TB/s, 45 % of the issue slots; the NVFP4
-// cache's 390 MB 81 us), 3 requests of up to 131071 keys on 8 kv heads 105 us for 635
-// MB (6.0 TB/s).
+// heads of 128, take 113 us for 697 MB (6.2 TB/s, 45 % of the issue slots; the NVFP4
+// cache's 390 MB 81 us), 3 requests of up to 131071 keys on 8 kv heads 104 us for 635
+// MB (6.1 TB/s).
 //
 // An E4M3 code is exact in f16, so that a code is converted and nothing else: the
 // scale of a block of 16 tokens, which is a step's half and a chunk of a logit
@@ -176,7 +176,7 @@ __device__ __forceinline__ void values16(WarpState<D, NB>& w, const KeyRegs8<D>&
 // ahead.
 //
 // The prompt step of rmsq_attn_prompt.cuh's figures (2478 and 2445 queries of 32
-// heads, 192 GFLOP) takes 235 us, over the NVFP4 cache 197; 128 keys 1.96 us on a
+// heads, 192 GFLOP) takes 234 us, over the NVFP4 cache 198; 128 keys 1.96 us on a
 // context of 20000 (1.66).  What it is sensitive to is the size of the roles' code
 // (see the issuing loop) and the latency of reads.  Tried on the way: keys loaded into
 // registers, a row per thread, with a factor for each 16 logits in the softmax 278;

@@ -74,10 +74,14 @@ cudaError_t launch_prompt(AttnArgs a, cudaStream_t stream) {
     static_assert(smem <= 230400, "the rest is the kernel's static shared memory");
     const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    // as many 256-row items as these sizes can hold; those without one return at once
+    // as many items of 256 rows as these sizes can hold, and of 128 as they and the card
+    // can; those without one return at once
     const int64_t rows = static_cast<int64_t>(a.tokens) * a.group;
-    const int64_t few = rows / (a.most_rows + 1);
-    const int64_t items = rows / 256 + (few < a.requests ? few : a.requests);
+    int64_t few = rows / (a.most_rows + 1);
+    if (few > a.requests) few = a.requests;
+    int64_t items = rows / 256 + few;
+    const int64_t halves = rows / 128 + few < a.half_items ? rows / 128 + few : a.half_items;
+    if (halves > items) items = halves;
     void* params[] = {&a};
     return launch_kernel(fn, dim3(static_cast<unsigned>(items * a.kv_heads)), dim3(kPromptThreads), params,
                          smem, stream);
@@ -87,15 +91,15 @@ cudaError_t launch_prompt(AttnArgs a, cudaStream_t stream) {
 // head) per SM, the prompt kernel for a CTA's 256 rows on every SM.  Measured on
 // 20000 to 100000 keys of the NVFP4 cache: 1.92 to 2.07 and 1.80 to 1.92 (D = 128),
 // 1.16 to 1.27 and 1.44 to 1.52 (64); on 20000 of the FP8 cache 2.21 and 1.97, 1.43
-// and 1.52 (64 to 160 queries of 8 x 8 heads: 96 of D = 128 296 us split and 307, 112
-// 342 and 306; of D = 64 112 219 and 238, 128 250 and 238).
+// and 1.52, with 128 rows per CTA 1.78 and 1.38 (96 queries of 8 x 8 heads of 128 299 us
+// split and 277, 64 204 and 275; of 64 96 191 and 216, 112 220 and 217).
 struct Cost {
-    double split, prompt;
+    double split, prompt, half;
 };
 template <class C>
 Cost cost_of(int head_dim) {
-    if (C::block_scales) return head_dim <= 64 ? Cost{1.43, 1.52} : Cost{2.21, 1.97};
-    return head_dim <= 64 ? Cost{1.21, 1.48} : Cost{1.97, 1.86};
+    if (C::block_scales) return head_dim <= 64 ? Cost{1.43, 1.52, 1.38} : Cost{2.21, 1.97, 1.78};
+    return head_dim <= 64 ? Cost{1.21, 1.48, 1.48} : Cost{1.97, 1.86, 1.86};
 }
 
 // Requests of more than kPromptRows rows go to the prompt kernel (AUTO: if they
@@ -130,8 +134,9 @@ cudaError_t launch_attn(AttnArgs a, int head_dim, int64_t max_query, int64_t max
     const int64_t rows = tokens * a.group;
     const int64_t items = (rows / 256 + 1) * a.kv_heads;
     const Cost cost = cost_of<C>(head_dim);
+    const double step = (rows / 128 + 1) * a.kv_heads <= sms ? cost.half : cost.prompt;
     const bool sooner = cost.split * static_cast<double>(rows * a.kv_heads) / (48.0 * sms) >
-                        cost.prompt * static_cast<double>((items + sms - 1) / sms);
+                        step * static_cast<double>((items + sms - 1) / sms);
     const int64_t rest = a.tokens >= a.requests ? a.tokens - a.requests + 1 : 1;    // left for one request
     const int64_t longest = max_query > 0 ? (max_query < a.tokens ? max_query : a.tokens)
                             : variant == kVariantPipelined ? a.tokens : rest;
@@ -140,7 +145,8 @@ cudaError_t launch_attn(AttnArgs a, int head_dim, int64_t max_query, int64_t max
     // (a single request is the prompt kernel's whatever its length)
     a.most_rows = !prompt ? INT32_MAX : a.requests == 1 ? 0 : kPromptRows;
     if (prompt && variant == kVariantAuto && a.requests > 1)
-        a.share = static_cast<int64_t>(cost.prompt / cost.split * 48.0 * sms / a.kv_heads) + 1;
+        a.share = static_cast<int64_t>(step / cost.split * 48.0 * sms / a.kv_heads) + 1;
+    a.half_items = C::block_scales ? sms / a.kv_heads : 0;      // (over the NVFP4 cache items have 256 rows)
     if (prompt) {
         const cudaError_t e = head_dim == 64 ? launch_prompt<P<64>, E, 64>(a, stream) : launch_prompt<P<128>, E, 128>(a, stream);
         if (e != cudaSuccess || a.requests == 1) return e;

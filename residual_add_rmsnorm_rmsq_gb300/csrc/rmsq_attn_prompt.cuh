@@ -4,7 +4,7 @@
 // the scaling of queries and probabilities are those of rmsq_attn.cuh.
 //
 // A CTA takes 256 rows (query token, head of the group) of a request and kv
-// head as two tiles of 128, and walks the keys 128 at a time:
+// head as two tiles of 128 (or one, see find_item), and walks the keys 128 at a time:
 //   S = Q . K^T (128 x 128 x D)  ->  P = 2^(f (S - m))  ->  O += P . V (128 x D x 128)
 // with S, P (f16, in S's place) and O in tensor memory, a thread per row in the
 // softmax.  While one tile is in its softmax the matrix unit works for the
@@ -24,7 +24,7 @@
 // request, queries and first conversion, and the last one's output, overlap with
 // nothing (8 to 10 us a CTA: 128 queries of 8 x 8 heads take 12 us on 128 keys and
 // 74 on 4000).  2478 and 2445 queries of 32 heads on contexts of 732 and 1574
-// keys: 197 us, 192 GFLOP (0.97 PFLOP/s; half the measured bf16 rate, 101 us), of
+// keys: 198 us, 192 GFLOP (0.97 PFLOP/s; half the measured bf16 rate, 101 us), of
 // which the 80 steps of an SM are 133 and the starts and ends of its 4.1 CTAs and
 // the last round the rest.  Heads of 64: 2000 queries of 32 heads on 4000 keys 88
 // us, of 128 115.  Measured and not kept (against
@@ -301,7 +301,14 @@ __device__ __forceinline__ float weigh_half(const Row& d, int h, uint32_t s_at, 
 // there are not that many.  Up to 32 requests every warp finds it for itself, a
 // lane per request; more are scanned in `scratch` (the key and value tiles' space,
 // which is theirs on return).
-__device__ __forceinline__ int64_t find_item(const AttnArgs& a, int64_t* scratch, int& req) {
+//
+// An item has 256 rows, or 128 where all items of 128 fit the card's SMs at once: a
+// CTA then has one row tile, whose step is shorter, and a prompt twice the CTAs.  In
+// us for 256 and 128 (FP8, heads of 128): 452 queries of 4 x 4 heads on 1510 keys (60
+// CTAs of 128 rows) 34.6 28.3, 600 of 4 x 8 on 2000 (152) 42.5 36.2, 900 (228) 42.5
+// 55.7, 280 of 8 x 8 on 20000 (144) 309 284, 320 (160) 309 529; heads of 64, 1100 of 4 x
+// 4 on 1500 (140) 25.9 22.7, 320 of 8 x 8 on 20000 240 418.  `shift`: log2 of the rows.
+__device__ __forceinline__ int64_t find_item(const AttnArgs& a, int64_t* scratch, int& req, int& shift) {
     const int skip = static_cast<int>(blockIdx.x) / a.kv_heads;
     if (a.requests <= 32) {
         const int lane = threadIdx.x & 31;
@@ -316,7 +323,10 @@ __device__ __forceinline__ int64_t find_item(const AttnArgs& a, int64_t* scratch
         if (a.share != 0)
 #pragma unroll 1
             for (uint32_t rest = all; rest != 0; rest &= rest - 1) n += __shfl_sync(kFull, own, __ffs(rest) - 1) >= own;
-        const int items = open && (a.share == 0 || static_cast<int64_t>(rows) * n >= a.share) ? (rows + 255) >> 8 : 0;
+        if (!open || (a.share != 0 && static_cast<int64_t>(rows) * n < a.share)) rows = 0;
+        const int halves = (rows + 127) >> 7;
+        shift = __reduce_add_sync(kFull, min(halves, 1 << 24)) <= a.half_items ? 7 : 8;
+        const int items = shift == 7 ? halves : (halves + 1) >> 1;
         int inc = items;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -328,7 +338,18 @@ __device__ __forceinline__ int64_t find_item(const AttnArgs& a, int64_t* scratch
         req = __ffs(__ballot_sync(kFull, inc > item)) - 1;
         return item - __shfl_sync(kFull, inc - items, req);
     }
-    scan_requests<kPromptThreads, false, 0>(a, scratch, [](int64_t r, bool taken) { return taken ? (r + 255) / 256 : 0; });
+    auto scan = [&](int rows) {
+        scan_requests<kPromptThreads, false, 0>(a, scratch, [rows](int64_t r, bool taken) { return taken ? (r + rows - 1) / rows : 0; });
+    };
+    shift = 8;
+#pragma unroll 1
+    for (;;) {
+        scan(1 << shift);
+        const int64_t total = scratch[a.requests];
+        if (shift == 7 || total == 0 || 2 * total > a.half_items) break;    // (at most twice as many of 128)
+        shift = 7;
+        __syncthreads();    // the total has been read
+    }
     int64_t item = scratch[a.requests] - 1 - skip;
     if (item >= 0) {
         int hi = a.requests;
@@ -382,9 +403,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
     // The item of this CTA: tiles of a request from the last rows (most keys)
     // to the first, kv heads innermost.
     const int head = blockIdx.x % a.kv_heads;
-    int req = 0;
-    const int64_t item = find_item(a, reinterpret_cast<int64_t*>(ks), req);
-    const int row0 = static_cast<int>(item) * 256;
+    int req = 0, shift = 8;
+    const int64_t item = find_item(a, reinterpret_cast<int64_t*>(ks), req, shift);
+    const int row0 = static_cast<int>(item) << shift;
     if (item < 0) {
         allow_dependents();
         return;
@@ -398,8 +419,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
 
     const Req rq = load_request(a, req);
     const int rows = rq.qlen * a.group, first_pos = rq.seq - rq.qlen;
-    const int tiles = min(rows - row0, 256) > 128 ? 2 : 1;
-    const int last_pos = first_pos + (min(row0 + 256, rows) - 1) / a.group;
+    const int end_row = min(rows - row0, 1 << shift) + row0;
+    const int tiles = end_row - row0 > 128 ? 2 : 1;
+    const int last_pos = first_pos + (end_row - 1) / a.group;
     const int low_pos = first_pos + row0 / a.group;
     const int low_key = a.window > 0 ? max(low_pos - a.window + 1, 0) : 0;
     const int key_begin = low_key / 128 * 128;

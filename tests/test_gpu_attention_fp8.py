@@ -116,6 +116,15 @@ def test_prompts_of_the_automatic_choice(rmsq_gpu):
     assert rmsq_gpu.take_fault_flags() == 0
 
 
+@pytest.mark.parametrize("q_lens", [
+    [76], [77], [300], [4000], [64, 1, 33, 0, 40], [20, 2, 90] * 11, [1] * 37 + [95], [1] * 40, [17] * 40 + [200]])
+@pytest.mark.parametrize("D, heads, kv", [(64, 8, 4), (128, 4, 1)])
+def test_prompts_in_tiles_and_pairs_of_tiles(rmsq_gpu, D, heads, kv, q_lens):
+    """CTAs of 128 rows where they fit the card together, of 256 where not; up to 32 requests and more."""
+    seq = [q + 11 * r % 170 for r, q in enumerate(q_lens)]
+    check(rmsq_gpu, make(q_lens, seq, heads, kv, D, 32, "bf16", seed=len(q_lens)), variant="pipelined")
+
+
 @pytest.mark.parametrize("variant", VARIANTS)
 @pytest.mark.parametrize("D", [64, 128])
 def test_bad_pages_empty_rows_padding(rmsq_gpu, D, variant):
