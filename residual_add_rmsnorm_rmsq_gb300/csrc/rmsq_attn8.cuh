@@ -58,9 +58,9 @@ struct Fp8Cache {
     static constexpr float p_shift = 5.0f, lazy = 8.0f;
     static constexpr uint32_t lazy_scale = 2;
     // Tiles that starting and ending an item counts for, where there are more tiles
-    // than CTAs.  For 0, 1, 2, 3, 4, 6, in us: 32 decodes of 100 to 2000 keys, 8 x 4
+    // than CTAs.  For 0, 1, 2, 3, 4, 6, in us: 32 decodes of 100 to 2000 keys, 4 x 8
     // heads of 128, 26.0 20.9 19.7 17.7 18.6 20.5, 128 of 16 to 2000 66.5 51.7 47.1 42.6
-    // 41.6 44.8, 256 of 100 to 1000 104 88 81 74 72 73, 128 of 2000 to 8192 (4 x 8)
+    // 41.6 44.8, 256 of 100 to 1000 104 88 81 74 72 73, 128 of 2000 to 8192 (8 x 4)
     // 103.9 103.5 100.8 100.4 99.9 100.1; heads of 64, 128 of 16 to 2000 34.6 31.5 29.0
     // 26.1 26.7 27.6; of 256 41.5 30.2 28.8 26.9 26.4 28.2.  (One tile per CTA is
     // the best cut there is: 8 decodes of up to 500 keys 9.5, with 4 more 10.7.)

@@ -305,7 +305,7 @@ __device__ __forceinline__ float weigh_half(const Row& d, int h, uint32_t s_at, 
 // An item has 256 rows, or 128 where all items of 128 fit the card's SMs at once: a
 // CTA then has one row tile, whose step is shorter, and a prompt twice the CTAs.  In
 // us for 256 and 128 (FP8, heads of 128): 452 queries of 4 x 4 heads on 1510 keys (60
-// CTAs of 128 rows) 34.6 28.3, 600 of 4 x 8 on 2000 (152) 42.5 36.2, 900 (228) 42.5
+// CTAs of 128 rows) 34.6 28.3, 600 of 8 x 4 on 2000 (152) 42.5 36.2, 900 (228) 42.5
 // 55.7, 280 of 8 x 8 on 20000 (144) 309 284, 320 (160) 309 529; heads of 64, 1100 of 4 x
 // 4 on 1500 (140) 25.9 22.7, 320 of 8 x 8 on 20000 240 418.  `shift`: log2 of the rows.
 __device__ __forceinline__ int64_t find_item(const AttnArgs& a, int64_t* scratch, int& req, int& shift) {
