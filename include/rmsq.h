@@ -562,8 +562,13 @@ int rmsq_kv_cache_load_fp8(const void *cache, const uint8_t *scales, int64_t num
  * and scales as above), with rmsq_paged_attention_nvfp4_ex's arguments, rules,
  * variants, workspace and errors otherwise.  The products with the codes are
  * exact and summed in fp32; a block's key scale multiplies its 16 logits in fp32,
- * its value scale its 16 weights before those are rounded to f16, relative to the
- * largest value scale met so far.
+ * its value scale its 16 weights, relative to the largest weight times value scale
+ * among the keys that the query sees, before those are rounded to f16.  With w the
+ * weights (sum 1), S_j the value scale of key j's block and U = max w_j S_j over the
+ * n keys seen, that rounding puts an output off by at most 2^-11 sum w_j |v_j| +
+ * n 2^-30 448 U, whatever the scales of keys that it does not see (fp16 outputs of
+ * ordinary values are off by 2.5e-4 of their magnitude where 32-bit weights give
+ * 2.1e-4, bf16 ones by 1.7e-3 either way).
  * A NaN among a key's elements gives NaN in the out and lse of the queries that
  * attend to it, and of no others (the store marks a token whose value has one in
  * this way); NaN codes of values read as 448.  What unwritten slots and scales

@@ -313,7 +313,6 @@ struct Nvfp4Cache {
     static constexpr bool block_scales = false;     // its scales are multiplied into the elements
     static constexpr float p_shift = 9.0f;          // weights are scaled by 2^9 ...
     static constexpr float lazy = 6.0f;             // ... and by up to 2^6 more while the maximum lags: < 2^16 in f16
-    static constexpr uint32_t lazy_scale = 0;
     static constexpr int piece = 0;                 // items are cut by their tiles alone
     template <int D> using Step = rmsq::Step<D>;
     template <int D> using Regs = KeyRegs<D>;
@@ -426,24 +425,55 @@ template <class C>
 __device__ __forceinline__ float weight_shift(float m, float f) { return m == -INFINITY ? 0.0f : fmaf(-m, f, C::p_shift); }
 __device__ __forceinline__ bool is_far(float shift) { return !(fabsf(shift) <= kFar); }
 
-// 2^(a - b) of two exponent bytes, 2^-126 at least.
-__device__ __forceinline__ float pow2_diff(uint32_t a, uint32_t b) {
-    return __uint_as_float(static_cast<uint32_t>(max(static_cast<int>(a + 127u - b), 1)) << 23);
-}
+// 2^e, e from -126 to 127.
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
 // A warp's running state over its keys for one item.  The logits and their
 // maximum m stay in the units of the product; f turns them into units of log2;
 // limit is the logit above which the maximum has to move; far: some row's
-// maximum is beyond kFar.  With block_scales a half's keys share one power of two,
-// a factor of its logits, and its values another, a factor of its weights
-// relative to the largest such scale so far (ve): neither is applied per element.
+// maximum is beyond kFar.
+//
+// With block_scales a half's keys share one power of two, a factor of its logits, and
+// its values another, 2^v, a factor of its weights: neither is applied per element.
+// What counts is then the weighted value, 2^(f s + v), so that the row's
+// reference is the largest of those it has seen: m is the logit of that key and e
+// the v of its block, and weights are 2^(f (s - m) + v - e + p_shift), whatever lies in
+// places that the row does not see, or sees with a large scale and next to no weight.
+// The sum l of the weights proper has v left out and would leave fp32's range if it
+// were relative to the same key: it is in units of 2^(e - C::middle).  limit is e +
+// lazy, shift what the exponent of a key with the reference's v is shifted by.
 template <int D, int NB>
 struct WarpState {
     float o[D / 16][NB][4];
-    float m[NB][2], l[NB][2], limit[NB][2];
+    float m[NB][2], l[NB][2], limit[NB][2], shift[NB][2];
     bool far;
-    uint32_t ve;        // block_scales: the byte of the value scale that o is in units of
 };
+
+// A row's reference: a maximum, with block_scales its block's exponent beside it.
+struct Peak {
+    float m, e;
+};
+// log2 of what a is relative to b
+template <class C>
+__device__ __forceinline__ float above(Peak a, Peak b, float f) {
+    return C::block_scales ? fmaf(a.m - b.m, f, a.e - b.e) : (a.m - b.m) * f;
+}
+// A sum of weights that is to be relative to a peak 2^x times as high.  (With
+// block_scales x may be below the normal numbers' exponents where the result is not.)
+template <class C>
+__device__ __forceinline__ float lowered(float l, float x) {
+    if constexpr (C::block_scales) {
+        const float half = exp2_approx(0.5f * x);
+        return l * half * half;
+    } else {
+        return l * exp2_approx(x);
+    }
+}
+template <class C>
+__device__ __forceinline__ Peak higher(Peak a, Peak b, float f) {
+    if constexpr (C::block_scales) return above<C>(b, a, f) > 0.0f ? b : a;   // (-inf below -inf: NaN, a)
+    else return {fmaxf(a.m, b.m), 0.0f};
+}
 
 // S^T of 16 keys: s[b][0..1] key kappa(g), rows 2t and 2t + 1; s[b][2..3] key + 8.
 template <int D, int NB>
@@ -556,7 +586,9 @@ __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned cha
                     if (k > pos[b][j & 1] || k < lo[b][j & 1] || !(have >> h & 1u)) s[h][b][j] = -INFINITY;
                 }
     }
-    // The maximum is moved only when some logit passes it by more than C::lazy.
+    // The maximum is moved only when some logit (weighted value) passes it by more than
+    // C::lazy.
+    const float v[2] = {static_cast<float>(sc.v[0]), static_cast<float>(sc.v[1])}, larger = fmaxf(v[0], v[1]);
     float top[NB][2];
     bool grow = false;
 #pragma unroll
@@ -564,34 +596,42 @@ __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned cha
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             top[b][j] = fmaxf(fmaxf(s[0][b][j], s[0][b][j + 2]), fmaxf(s[1][b][j], s[1][b][j + 2]));
-            grow |= top[b][j] > w.limit[b][j];
+            // (as if both halves had the larger scale: which has it is looked at below;
+            // nothing yet and nothing here is NaN)
+            grow |= (C::block_scales ? fmaf(top[b][j] - w.m[b][j], f[b][j], larger) : top[b][j]) > w.limit[b][j];
         }
-    if constexpr (C::block_scales) grow |= max(sc.v[0], sc.v[1]) > w.ve + C::lazy_scale;
     if (__any_sync(kFull, grow)) {
         bool far = false;
-        float rv = 1.0f;
-        if constexpr (C::block_scales) {
-            const uint32_t ve = max(w.ve, max(sc.v[0], sc.v[1]));
-            rv = pow2_diff(w.ve, ve);
-            w.ve = ve;
-        }
+        // Two scales that are near each other count as the larger one, which puts the
+        // reference too high by 2^close at most: one maximum over the lanes instead of
+        // two (for a block that is not there v is 0).
+        const float smaller = fminf(v[0], v[1]);
+        bool near = true;
+        if constexpr (C::block_scales) near = smaller == 0.0f || larger - smaller <= C::close;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                float x = top[b][j];
+                const Peak was = {w.m[b][j], w.limit[b][j] - C::lazy};
+                auto over_lanes = [](float x) {
 #pragma unroll
-                for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
-                const float m = fmaxf(x, w.m[b][j]);
-                const float r = m == -INFINITY ? 1.0f : exp2_approx((w.m[b][j] - m) * f[b][j]);
-                w.m[b][j] = m;
-                w.limit[b][j] = lag_limit<C>(m, f[b][j]);
-                far |= is_far(weight_shift<C>(m, f[b][j]));
-                w.l[b][j] *= r;
+                    for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+                    return x;
+                };
+                const float first = near ? top[b][j] : fmaxf(s[0][b][j], s[0][b][j + 2]);
+                Peak now = higher<C>(was, {over_lanes(first), near ? larger : v[0]}, f[b][j]);
+                if (!near) now = higher<C>(now, {over_lanes(fmaxf(s[1][b][j], s[1][b][j + 2])), v[1]}, f[b][j]);
+                const float x = now.m == -INFINITY ? 0.0f : above<C>(was, now, f[b][j]), r = exp2_approx(x);
+                w.m[b][j] = now.m;
+                w.limit[b][j] = C::block_scales ? now.e + C::lazy : lag_limit<C>(now.m, f[b][j]);
+                const float shift = weight_shift<C>(now.m, f[b][j]);
+                w.shift[b][j] = shift;
+                far |= is_far(shift);
+                w.l[b][j] = lowered<C>(w.l[b][j], x);
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
-                    w.o[i][b][j] *= C::block_scales ? r * rv : r;
-                    w.o[i][b][j + 2] *= C::block_scales ? r * rv : r;
+                    w.o[i][b][j] *= r;
+                    w.o[i][b][j + 2] *= r;
                 }
             }
         w.far = __any_sync(kFull, far);
@@ -600,7 +640,7 @@ __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned cha
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) shift[b][j] = weight_shift<C>(w.m[b][j], f[b][j]);
+        for (int j = 0; j < 2; ++j) shift[b][j] = C::block_scales ? w.shift[b][j] : weight_shift<C>(w.m[b][j], f[b][j]);
     if (w.far) {    // the rows that are (the others as ever, whatever shares their warp)
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -617,19 +657,38 @@ __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned cha
             }
     }
     uint32_t pf[2][NB][2];
+    // block_scales: the weighted values, 2^(f (s - m) + v - e + p_shift), and from them the
+    // weights in units of 2^(e - middle), by 2^(middle - v); where v is below middle the
+    // other way round, so that neither underflows for the other.
+    int over[2] = {0, 0};
+    if constexpr (C::block_scales) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) over[h] = static_cast<int>(sc.v[h]) - C::middle;
+    }
+    const bool low = min(over[0], over[1]) < 0;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float p[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) p[j] = exp2_approx(fmaf(s[h][b][j], f[b][j & 1], shift[b][j & 1]));
-            w.l[b][0] += p[0] + p[2];
-            w.l[b][1] += p[1] + p[3];
             if constexpr (C::block_scales) {
-                const float v = pow2_diff(sc.v[h], w.ve);
+                // (v - e first, a whole number: shift keeps its bits)
+                const float up = fmaxf(v[h], static_cast<float>(C::middle)) + C::lazy, weight = pow2(-max(over[h], 0));
+                const float x[2] = {shift[b][0] + (up - w.limit[b][0]), shift[b][1] + (up - w.limit[b][1])};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) p[j] *= v;
+                for (int j = 0; j < 4; ++j) p[j] = exp2_approx(fmaf(s[h][b][j], f[b][j & 1], x[j & 1]));
+                w.l[b][0] = fmaf(p[0] + p[2], weight, w.l[b][0]);
+                w.l[b][1] = fmaf(p[1] + p[3], weight, w.l[b][1]);
+                if (low) {
+                    const float value = pow2(min(over[h], 0));
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) p[j] *= value;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) p[j] = exp2_approx(fmaf(s[h][b][j], f[b][j & 1], shift[b][j & 1]));
+                w.l[b][0] += p[0] + p[2];
+                w.l[b][1] += p[1] + p[3];
             }
             pf[h][b][0] = transpose8x8(Fp16T::pack(p[0], p[1]));
             pf[h][b][1] = transpose8x8(Fp16T::pack(p[2], p[3]));
@@ -646,7 +705,7 @@ __device__ __forceinline__ void attend32(WarpState<D, NB>& w, const unsigned cha
 template <int D, int NB>
 struct AttnSmem {
     float o[kAttnWarps][8 * NB][D + 4];
-    float m[kAttnWarps][8 * NB], l[kAttnWarps][8 * NB];
+    float m[kAttnWarps][8 * NB], l[kAttnWarps][8 * NB], e[kAttnWarps][8 * NB];
     float f[8 * NB];
 };
 
@@ -662,10 +721,21 @@ __device__ __forceinline__ void store_quad(void* out, int64_t at, float4 o, floa
         make_uint2(E::pack(o.x * inv, o.y * inv), E::pack(o.z * inv, o.w * inv));
 }
 
-// ln of the sum of the weights: l of them relative to the maximum m, times 2^p_shift.
+// ln of the sum of the weights: l of them relative to the maximum, times 2^p_shift, and
+// with block_scales in units of 2^(e - middle).  (The exponents are added as whole
+// numbers: log2f(l) alone may be large, and its rounding with it.)
 template <class C>
-__device__ __forceinline__ float row_lse(float m, float l, float f) {
-    return l == 0.0f ? -INFINITY : fmaf(m, f, log2f(l) - C::p_shift) * 0.693147180559945309f;
+__device__ __forceinline__ float row_lse(Peak top, float l, float f) {
+    if (l == 0.0f) return -INFINITY;
+    float log2_l = log2f(l);
+    if constexpr (C::block_scales) {
+        if (l > 0.0f && l < INFINITY) {
+            const uint32_t u = __float_as_uint(l);
+            const float whole = static_cast<float>(static_cast<int>(u >> 23) - 127 - C::middle) + top.e;
+            log2_l = whole + log2f(__uint_as_float((u & 0x7fffffu) | 0x3f800000u));
+        }
+    }
+    return fmaf(top.m, f, log2_l - C::p_shift) * 0.693147180559945309f;
 }
 
 template <class C, class E, int D, int NB>
@@ -799,12 +869,13 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
         }
         WarpState<D, NB> w;
         w.far = false;
-        w.ve = 0u;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                w.m[b][j] = w.limit[b][j] = -INFINITY;
+                w.m[b][j] = -INFINITY;
+                w.limit[b][j] = C::block_scales ? C::lazy : -INFINITY;
+                w.shift[b][j] = 0.0f;
                 w.l[b][j] = 0.0f;
             }
 #pragma unroll
@@ -845,23 +916,34 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
                 float l = w.l[b][j];
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(kFull, l, o);
+                w.l[b][j] = l;
                 if (g == 0) {
                     sm.m[warp][8 * b + 2 * t + j] = w.m[b][j];
-                    sm.l[warp][8 * b + 2 * t + j] = l;
+                    if constexpr (C::block_scales) sm.e[warp][8 * b + 2 * t + j] = w.limit[b][j] - C::lazy;
                     if (warp == 0) sm.f[8 * b + 2 * t + j] = fs[b][j];
                 }
             }
         __syncthreads();
+        auto peak_of = [&](int k, int row) { return Peak{sm.m[k][row], C::block_scales ? sm.e[k][row] : 0.0f}; };
+        auto top_of = [&](int row, float f) {
+            Peak top = peak_of(0, row);
+#pragma unroll
+            for (int k = 1; k < kAttnWarps; ++k) top = higher<C>(top, peak_of(k, row), f);
+            return top;
+        };
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int row = 8 * b + 2 * t + j;
-                float top = sm.m[0][row];
-#pragma unroll
-                for (int i = 1; i < kAttnWarps; ++i) top = fmaxf(top, sm.m[i][row]);
-                float f = w.m[b][j] == -INFINITY ? 0.0f : exp2_approx((w.m[b][j] - top) * fs[b][j]);
-                if constexpr (C::block_scales) f *= __uint_as_float(w.ve << 23);
+                const Peak top = top_of(row, fs[b][j]);
+                const float x = above<C>({w.m[b][j], w.limit[b][j] - C::lazy}, top, fs[b][j]);
+                float f = w.m[b][j] == -INFINITY ? 0.0f : exp2_approx(x);
+                // (without a maximum the sum is 0, or NaN where the logits are)
+                if (g == 0) sm.l[warp][row] = w.m[b][j] == -INFINITY ? w.l[b][j] : lowered<C>(w.l[b][j], x);
+                // (sums of weighted values in units of 2^(e - 127), of weights in 2^(e -
+                // middle): e drops out of their quotient)
+                if constexpr (C::block_scales) f *= pow2(C::middle - 127);
                 float* dst = &sm.o[warp][row][g * (D / 8)];
 #pragma unroll
                 for (int i = 0; i < D / 16; ++i) {
@@ -874,29 +956,27 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
         float* part = a.part + (static_cast<int64_t>(blockIdx.x) * 2 + (x == blockIdx.x * run ? 0 : 1)) * ROWS * kPartRow<D>;
         for (int i = tid; i < ROWS * (D / 4); i += kAttnThreads) {
             const int row = i / (D / 4), d = i % (D / 4) * 4;
-            const float f = sm.f[row];
-            float top = sm.m[0][row], l = 0.0f;
-#pragma unroll
-            for (int k = 1; k < kAttnWarps; ++k) top = fmaxf(top, sm.m[k][row]);
+            float l = 0.0f;
             float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int k = 0; k < kAttnWarps; ++k) {
                 const float4 u = *reinterpret_cast<const float4*>(&sm.o[k][row][d]);
                 o.x += u.x; o.y += u.y; o.z += u.z; o.w += u.w;
-                const float mk = sm.m[k][row];
-                // (without a maximum the sum is 0, or NaN where the logits are)
-                l += mk == -INFINITY ? sm.l[k][row] : sm.l[k][row] * exp2_approx((mk - top) * f);
+                l += sm.l[k][row];
             }
             if (whole) {
                 if (row0 + row < rows) {
                     const int64_t tok = rq.q0 + (row0 + row) / a.group;
                     const int64_t oh = tok * a.heads + at.head * a.group + (row0 + row) % a.group;
                     store_quad<E>(a.out, oh * D + d, o, l > 0.0f ? 1.0f / (l * v_gs) : (l == 0.0f ? 0.0f : l));
-                    if (a.lse && d == 0) a.lse[oh] = row_lse<C>(top, l, f);
+                    if (a.lse && d == 0) a.lse[oh] = row_lse<C>(top_of(row, sm.f[row]), l, sm.f[row]);
                 }
             } else {
                 *reinterpret_cast<float4*>(part + row * kPartRow<D> + d) = o;
-                if (d == 0) *reinterpret_cast<float4*>(part + row * kPartRow<D> + D) = make_float4(top, l, f, 0.0f);
+                if (d == 0) {
+                    const Peak top = top_of(row, sm.f[row]);
+                    *reinterpret_cast<float4*>(part + row * kPartRow<D> + D) = make_float4(top.m, l, sm.f[row], top.e);
+                }
             }
         }
         __syncthreads();
@@ -922,26 +1002,30 @@ constexpr int kJoinShares = 8;
 
 struct Partial {
     float4 o;
-    float m, l;
+    Peak top;
+    float l;
 };
 
 // The parts of a row have one factor, `factor`.
 __device__ __forceinline__ Partial load_partial(const float* p, int d, int D, float& factor) {
     const float4 o = __ldcg(reinterpret_cast<const float4*>(p + d)), ml = __ldcg(reinterpret_cast<const float4*>(p + D));
     factor = ml.z;
-    return {o, ml.x, ml.y};
+    return {o, {ml.x, ml.w}, ml.y};
 }
 
+template <class C>
 __device__ __forceinline__ void merge(Partial& a, const Partial& b, float factor) {
-    const float m = fmaxf(a.m, b.m);
-    const float f = a.m == -INFINITY ? 0.0f : exp2_approx((a.m - m) * factor);
-    const float h = b.m == -INFINITY ? 0.0f : exp2_approx((b.m - m) * factor);
+    const Peak top = higher<C>(a.top, b.top, factor);
+    const float x = a.top.m == -INFINITY ? -INFINITY : above<C>(a.top, top, factor);
+    const float y = b.top.m == -INFINITY ? -INFINITY : above<C>(b.top, top, factor);
+    const float f = exp2_approx(x), h = exp2_approx(y);
     a.o.x = a.o.x * f + b.o.x * h;
     a.o.y = a.o.y * f + b.o.y * h;
     a.o.z = a.o.z * f + b.o.z * h;
     a.o.w = a.o.w * f + b.o.w * h;
-    a.l = a.l * f + b.l * h;
-    a.m = m;
+    if constexpr (C::block_scales) a.l = lowered<C>(a.l, x) + lowered<C>(b.l, y);
+    else a.l = a.l * f + b.l * h;
+    a.top = top;
 }
 
 template <class C, class E, int D, int NB>
@@ -964,7 +1048,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a) {
     const int quad = threadIdx.x % across, group = threadIdx.x / across;
     for (int q0 = 0; q0 < quads; q0 += across) {
         const int at_quad = blockIdx.y * quads + q0 + quad, row = at_quad / (D / 4), d = at_quad % (D / 4) * 4;
-        Partial acc = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, 0.0f};
+        Partial acc = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), {-INFINITY, 0.0f}, 0.0f};
         auto part = [&](int w) {
             return a.part + (static_cast<int64_t>(w0 + w) * 2 + (w == 0 ? first_slot : 0)) * slot + row * kPartRow<D>;
         };
@@ -973,21 +1057,21 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a) {
             Partial p[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                p[i] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), -INFINITY, 0.0f};
+                p[i] = {make_float4(0.0f, 0.0f, 0.0f, 0.0f), {-INFINITY, 0.0f}, 0.0f};
                 if (w + i * split < parts) p[i] = load_partial(part(w + i * split), d, D, factor);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) merge(acc, p[i], factor);
+            for (int i = 0; i < 4; ++i) merge<C>(acc, p[i], factor);
         }
         met[threadIdx.x] = acc;
         __syncthreads();
         if (group == 0 && row0 + row < rows) {
-            for (int i = 1; i < split; ++i) merge(acc, met[i * across + quad], factor);
+            for (int i = 1; i < split; ++i) merge<C>(acc, met[i * across + quad], factor);
             const int64_t tok = rq.q0 + (row0 + row) / a.group;
             const int64_t oh = tok * a.heads + head * a.group + (row0 + row) % a.group;
             const float l = acc.l;
             store_quad<E>(a.out, oh * D + d, acc.o, l > 0.0f ? 1.0f / (l * v_gs) : (l == 0.0f ? 0.0f : l));
-            if (a.lse && d == 0) a.lse[oh] = row_lse<C>(acc.m, l, factor);
+            if (a.lse && d == 0) a.lse[oh] = row_lse<C>(acc.top, l, factor);
         }
         __syncthreads();
     }

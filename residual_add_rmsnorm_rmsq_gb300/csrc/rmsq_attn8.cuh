@@ -9,7 +9,7 @@
 // An E4M3 code is exact in f16, so that a code is converted and nothing else: the
 // scale of a block of 16 tokens, which is a step's half and a chunk of a logit
 // row in the two kernels, is a factor of the block's logits (keys) and of its
-// weights (values), and costs nothing per element.  NaN codes of values read as
+// weights (values; relative to what, see WarpState), and costs nothing per element.  NaN codes of values read as
 // 448: a masked place meets a weight of 0, which a NaN would survive (the store
 // turns the token's keys to NaN as well, so that queries that see it are told).
 #pragma once
@@ -51,12 +51,16 @@ struct Step8 {
 
 struct Fp8Cache {
     static constexpr bool block_scales = true;
-    // Weights are scaled by 2^5, up to 2^8 more while the maximum lags and 2^2 more
-    // while the value scale does: moving either costs a pass over O (the maximum had
-    // to move at one step in nine with 2^9 and 2^6, on tokens of uneven strength).
-    // Weights below 2^-19 of the largest are subnormal f16, off by 2^-30 of it.
-    static constexpr float p_shift = 5.0f, lazy = 8.0f;
-    static constexpr uint32_t lazy_scale = 2;
+    // Weights, times their values' scale, are held as 2^6 at the row's largest (2^5 where
+    // that was taken for larger, see attend32), up to 2^9 more while it lags: moving it
+    // costs a pass over O (it had to move at one step in nine with 2^9 and 2^6, on tokens
+    // of uneven strength).  Those below 2^-19 of the largest are subnormal f16, off by
+    // 2^-30 of it.
+    static constexpr float p_shift = 6.0f, lazy = 9.0f, close = 1.0f;
+    // Scale bytes v are 1 to 187 as they are read.  A weight in units of 2^(e - middle) is
+    // 2^(middle - v) times its weighted value: from 2^(5 - 107) for a row's largest at v =
+    // 187, with 24 bits below it within fp32, to 2^(15 + 79) at 1.
+    static constexpr int middle = 80;
     // Tiles that starting and ending an item counts for, where there are more tiles
     // than CTAs.  For 0, 1, 2, 3, 4, 6, in us: 32 decodes of 100 to 2000 keys, 4 x 8
     // heads of 128, 26.0 20.9 19.7 17.7 18.6 20.5, 128 of 16 to 2000 66.5 51.7 47.1 42.6
@@ -348,7 +352,7 @@ struct Fp8Prompt : Fp8Cache {
                 }
                 if (lane == 0) {
                     t.k = cache_scale_value(max(kmost, 1u));
-                    t.v = vmost;
+                    t.v = static_cast<float>(vmost);
                     t.key0 = key_begin + tile * 128;
                     t.last = tile + 1 == tiles && todo == 0u;
                 }

@@ -221,12 +221,11 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // What a reader with block_scales tells of a step: the 128 keys it is about and
 // which of them it takes, the factor of their logits and the byte of their values'
-// scale (0: there is none), whether it is the last one, and the eight blocks'
+// scale (as a number; 0: there is none), whether it is the last one, and the eight blocks'
 // pages (-1: not taken) and the f16 factors of their keys and values.
 struct StepInfo {
     uint32_t valid[4];
-    float k;
-    uint32_t v;
+    float k, v;
     int key0, last;
     int page[8];
     uint32_t fk[8], fv[8];
@@ -588,8 +587,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
             const int pos = live ? first_pos + token : -1, lo = a.window > 0 ? pos - a.window + 1 : 0;
             const uint32_t lanes = static_cast<uint32_t>(quad * 32) << 16;
             const uint32_t s_at = tmem + i * 128 + lanes, o_at = tmem + 256 + i * D + lanes;
-            float m = -INFINITY, l = 0.0f, limit = -INFINITY, shift = 0.0f;
-            uint32_t ve = 0;        // block_scales: byte of the value scale that the row's O is in units of
+            // (block_scales: limit is what the weighted values may pass the reference by)
+            Peak peak = {-INFINITY, 0.0f};
+            float l = 0.0f, limit = P::block_scales ? P::lazy : -INFINITY, shift = 0.0f;
             for (int n = 0; n < steps; ++n) {
                 ok = warp_wait(&sfull[i], n & 1);
                 if (!ok) break;
@@ -602,7 +602,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                 const uint4 have = *reinterpret_cast<const uint4*>(P::block_scales ? at.valid : valid[n & 3]);
                 const uint4 rest = P::block_scales ? *reinterpret_cast<const uint4*>(&at.k) : make_uint4(0u, 0u, 0u, 0u);
                 const float tile_k = __uint_as_float(rest.x);
-                const uint32_t tile_v = rest.y;
+                const float tile_v = __uint_as_float(rest.y);
                 const int key0 = P::block_scales ? static_cast<int>(rest.z) : key_begin + n * 128;
                 if (P::block_scales && rest.w != 0u) steps = n + 1;
                 const uint32_t hv[4] = {have.x, have.y, have.z, have.w};
@@ -627,35 +627,35 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                 finish_half(d, 1);
                 if (!full) mask_half(d, 1, see);
                 top = fmaxf(top, max_half(d, 1));
-                uint32_t most = 0;      // block_scales: largest value scale that the row sees here
+                float gain = 0.0f;      // block_scales: log2 of the largest weighted value relative to the row's
+                bool high = top > limit;
                 if constexpr (P::block_scales) {
                     top *= tile_k;
-                    if (full || (see[0] | see[1] | see[2] | see[3]) != 0u) most = tile_v;
+                    gain = above<P>({top, tile_v}, peak, f);    // (nothing yet, nothing here: NaN)
+                    high = (limit == -INFINITY ? top : gain) > limit;
                 }
                 float move = 1.0f;      // factor of the row's O
                 bool moved = false;
                 bool done = false;      // the factors are in the logits
-                if (__any_sync(kFull, top > limit || most > ve + P::lazy_scale)) {
+                if (__any_sync(kFull, high)) {
                     // sfull of this step says that the previous P . V has
                     // completed too: O may be rescaled here
-                    const float m1 = top > limit ? fmaxf(top, m) : m;   // whatever shares the warp
-                    float r = m1 == -INFINITY ? 1.0f : exp2_approx((m - m1) * f);
-                    m = m1;
-                    limit = lag_limit<P>(m, f);
-                    shift = weight_shift<P>(m, f);
-                    l *= r;
+                    const Peak was = peak;
+                    if (high) peak = higher<P>(peak, {top, tile_v}, f);     // whatever shares the warp
+                    const float x = peak.m == -INFINITY ? 0.0f : above<P>(was, peak, f);
+                    limit = P::block_scales ? P::lazy : lag_limit<P>(peak.m, f);
+                    shift = weight_shift<P>(peak.m, f);
+                    l = lowered<P>(l, x);
                     if constexpr (P::block_scales) {
-                        most = max(most, ve);
-                        r *= pow2_diff(ve, most);
-                        ve = most;
+                        if (high) gain = fminf(gain, 0.0f);     // (relative to where it is now)
                     }
-                    move = r;
+                    move = exp2_approx(x);
                     moved = n > 0;
                     // A row that is far out comes here at every step (its limit
                     // is passed by any logit); the others subtract zero.
                     if (__any_sync(kFull, is_far(shift))) {
                         const bool own = is_far(shift);
-                        const float t = own ? m : 0.0f;
+                        const float t = own ? peak.m : 0.0f;
                         if (own) {
                             shift = P::p_shift;
                             limit = -INFINITY;
@@ -671,17 +671,19 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                     }
                 }
                 if constexpr (P::block_scales) {
-                    // Weights times their values' scale relative to the row's, a power of
-                    // two that only changes the addend; the sum without it.  (The factor
+                    // Weights times their values' scale, a power of two that only changes
+                    // the addend; the sum of the weights from theirs.  Where all of a step's
+                    // are far below what f16 holds they are brought just below it, so that
+                    // the sum, in which they may be the largest, has them whole.  (The factor
                     // within the normal numbers: a masked logit times zero would be NaN.)
                     const float fk = done ? f : clamp_factor(f * tile_k);
-                    // (a row that sees nothing here may be in units of any scale, or none)
-                    const int down = min(max(static_cast<int>(tile_v) - static_cast<int>(ve), -90),
-                                         static_cast<int>(P::lazy_scale));
+                    const float up = fminf(fmaxf(ceilf(-30.0f - P::p_shift - gain), 0.0f), 100.0f);
                     float sum = 0.0f;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) sum += weigh_half(d, h, s_at, fk, shift + static_cast<float>(down));
-                    l = fmaf(sum, __uint_as_float(static_cast<uint32_t>(127 - down) << 23), l);
+                    for (int h = 0; h < 2; ++h) sum += weigh_half(d, h, s_at, fk, shift + (tile_v - peak.e + up));
+                    // 2^(middle - v - up); 0 below the normal numbers
+                    const int unit = 127 + P::middle - static_cast<int>(tile_v + up);
+                    l = fmaf(sum, __uint_as_float(static_cast<uint32_t>(max(unit, 0)) << 23), l);
                 } else {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) l += weigh_half(d, h, s_at, f, shift);
@@ -714,9 +716,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                 ok = warp_wait(&ofull[i], 0);
                 tc_fence_after();
             }
-            float inv;
-            if constexpr (P::block_scales) inv = l > 0.0f ? __uint_as_float(ve << 23) / l : (l == 0.0f ? 0.0f : l);
-            else inv = l > 0.0f ? 1.0f / (l * __ldg(a.v_gs)) : (l == 0.0f ? 0.0f : l);
+            const float inv = l > 0.0f ? 1.0f / (P::block_scales ? l : l * __ldg(a.v_gs)) : (l == 0.0f ? 0.0f : l);
             const int64_t oh = static_cast<int64_t>(rq.q0 + token) * a.heads + qh;
             uint4* out = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + oh * D);
 #pragma unroll
@@ -726,6 +726,10 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                     __syncwarp();   // the lanes come from the stores below, which not all of them make
                     tmem_ld16(o, o_at + c * 16);
                     tmem_wait(o);
+                    if constexpr (P::block_scales) {    // O is in units of 2^(e - 127), l of 2^(e - middle)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] *= pow2(P::middle - 127);
+                    }
                 } else {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) o[j] = 0.0f;
@@ -739,7 +743,7 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                                                     E::pack(o[8 * h + 6] * inv, o[8 * h + 7] * inv));
                 }
             }
-            if (live && ok && a.lse) a.lse[oh] = row_lse<P>(m, l, f);
+            if (live && ok && a.lse) a.lse[oh] = row_lse<P>(peak, l, f);
         }
     }
     if (!ok) atomicOr(&g_prompt_fault, 1u);
