@@ -530,11 +530,12 @@ int rmsq_paged_attention_nvfp4_ex(const void *q, int64_t q_stride, const void *k
  * into the cache.  For each block of 16 slots and head that receives tokens, with
  * amax their largest finite magnitude,
  *   s = 2^ceil(log2 max(amax / 448, 1e-12))       (at most 2^60)
- * as RMSQ_QUANT_E8M0 has it; if the block's first slot is not among those
- * received the block is one that is partly filled, and s is at least the scale it
- * has.  Codes are e4m3(x / s).  The block's other slots keep their values: if the
- * scale has grown their codes are rounded to it (exact unless they become
- * subnormal).  Magnitudes above 448 * 2^60 saturate.  An element that is not
+ * as RMSQ_QUANT_E8M0 has it.  Codes are e4m3(x / s).  A block whose first slot is
+ * among those received is begun anew: what its other slots held is lost (their codes
+ * stay and are read with the new scale).  Else it is one that is partly filled, s is
+ * at least the scale it has, and its other slots keep their values: if the scale has
+ * grown their codes are rounded to it (exact unless they become subnormal).
+ * Magnitudes above 448 * 2^60 saturate.  An element that is not
  * finite is stored as NaN, and so are then all key codes of that token and head,
  * so that every query that attends to the token gives NaN, and no other.
  * rmsq_kv_cache_load_fp8 — reads tokens back: T(code * scale), rounded once.
@@ -542,11 +543,12 @@ int rmsq_paged_attention_nvfp4_ex(const void *q, int64_t q_stride, const void *k
  *  slot_map      device, int64[n_tokens].  A token whose slot lies outside
  *                [0, num_pages * page_size) is skipped by the store and read as
  *                zeros by the load.  Of the store's, those of one block of 16
- *                have to be consecutive entries and ascend, as
- *                rmsq_build_slot_map writes them; what a block holds after a
- *                call where they do not is not specified (other blocks are not
- *                concerned).  The load takes any slots.
- * Deterministic.  No output may overlap an input; the load's k and v rows may
+ *                have to ascend (each slot once) within 16 consecutive entries,
+ *                with none but skipped ones between them: as rmsq_build_slot_map
+ *                writes them, whichever of them are then taken out.  What a
+ *                block holds after a call where they do not is not specified
+ *                (other blocks are not concerned).  The load takes any slots.
+ * Deterministic with such a map.  No output may overlap an input; the load's k and v rows may
  * interleave in one buffer.  Asynchronous on `stream`.
  */
 int rmsq_kv_cache_store_fp8(const void *k, int64_t k_stride, const void *v, int64_t v_stride,

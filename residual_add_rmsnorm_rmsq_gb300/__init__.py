@@ -703,8 +703,8 @@ def kv_cache_store_fp8(k: torch.Tensor, v: torch.Tensor, slot_map: torch.Tensor,
     """rmsq_kv_cache_store_fp8: k, v [n, kv heads, D] (token stride free, so
     slices of a qkv buffer serve) quantised into `cache` and `scales`
     (kv_cache_shapes_fp8) at slot_map (int64 [n], as build_slot_map writes it:
-    the slots of a block of 16 stand together and ascend); a slot outside the
-    cache skips its token."""
+    the slots of a block of 16 ascend within 16 entries that are no other
+    block's); a slot outside the cache skips its token, wherever it stands."""
     L = load()
     dt = _act_types(k)
     ks, vs = _token_rows("k", k), _token_rows("v", v)

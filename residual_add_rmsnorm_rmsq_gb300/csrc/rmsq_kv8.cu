@@ -43,9 +43,10 @@ __device__ __forceinline__ uint8_t* scale_at(const Cache8Args& a, int64_t slot, 
 //
 // A warp looks after a range of tokens (a power of two up to 16) of one kv head,
 // and takes the runs of tokens of one block that start there.  The slots of a run
-// are consecutive entries of the slot map, so that 32 entries, one per lane, show
-// all runs of the range to their end; no token is looked after twice and no
-// warp waits for another.  A lane holds 8 elements of a token, D / 8 lanes a
+// ascend within 16 consecutive entries of the slot map, with none but skipped ones
+// between them, so that 16 entries before the range and 16 behind it show which
+// runs start in it, and all of them to their end; no token is looked after twice and
+// no warp waits for another.  A lane holds 8 elements of a token, D / 8 lanes a
 // token, all of a run's tokens are in registers before the maximum is taken: one
 // pass.  Prompts are bound by HBM and, as much, by the chain of a run (slots, tokens,
 // maximum, codes) that a warp walks a side after the other with 80 registers a
@@ -125,21 +126,41 @@ __global__ void __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) cache8_st
     const int head = static_cast<int>(w % a.heads);
     const int64_t base = w / a.heads << a.range_shift;
     if (base >= a.n) return;
-    // lane i: entry base - 1 + i of the slot map
-    const int64_t mine = base - 1 + lane;
-    int64_t slot = mine >= 0 && mine < a.n ? __ldg(reinterpret_cast<const long long*>(a.slots) + mine) : -1;
-    if (slot >= a.slots_total) slot = -1;
-    const int64_t before = __shfl_up_sync(kFull, slot, 1);
-    const bool goes_on = lane > 0 && slot >= 0 && before >= 0 && slot > before && slot / kBlockTokens == before / kBlockTokens;
-    const uint32_t on = __ballot_sync(kFull, goes_on);
-    uint32_t starts = __ballot_sync(kFull, slot >= 0 && !goes_on) & (((1u << (1 << a.range_shift)) - 1u) << 1);
+    // lane i: entry base - 1 + i of the slot map; -1: skipped
+    auto entry = [&](int64_t i) {
+        const int64_t s = i >= 0 && i < a.n ? __ldg(reinterpret_cast<const long long*>(a.slots) + i) : -1;
+        return s < a.slots_total ? s : -1;
+    };
+    // A token goes on a run if the entry before it that is not skipped, at most 15
+    // away, is a smaller slot of its block.
+    auto goes_on = [](int64_t s, int64_t before) {
+        return s >= 0 && before >= 0 && s > before && s / kBlockTokens == before / kBlockTokens;
+    };
+    const int64_t slot = entry(base - 1 + lane);
+    const uint32_t valid = __ballot_sync(kFull, slot >= 0);
+    int64_t before = __shfl_up_sync(kFull, slot, 1);
+    if (__any_sync(kFull, slot < 0 && base - 1 + lane >= 0 && base - 1 + lane < a.n)) {
+        // something is skipped: the one before may be further off, or before these
+        const int64_t prior = lane < kBlockTokens ? entry(base - kBlockTokens + lane) : -1;
+        const uint32_t below = valid & ((1u << lane) - 1u), valid_prior = __ballot_sync(kFull, prior >= 0);
+        const int last = 31 - __clz(below), last_prior = 31 - __clz(valid_prior);       // -1: none
+        const int64_t near = __shfl_sync(kFull, slot, max(last, 0)), far = __shfl_sync(kFull, prior, max(last_prior, 0));
+        before = last >= 0 ? near : last_prior >= 0 ? far : -1;
+        if ((last >= 0 ? lane - last : lane + kBlockTokens - 1 - last_prior) >= kBlockTokens) before = -1;
+    }
+    const uint32_t begins = valid & ~__ballot_sync(kFull, lane > 0 && goes_on(slot, before));
+    uint32_t starts = begins & (((1u << (1 << a.range_shift)) - 1u) << 1);
     const int sub = lane / LT, chunk = lane % LT;
     while (starts != 0) {
         const int first = __ffs(starts) - 1;
         starts &= starts - 1;
-        const uint32_t rest = first < 31 ? ~(on >> (first + 1)) : 0xffffffffu;
-        const int len = min(__ffs(rest), kBlockTokens);       // ascending in one block: at most 16
+        // bit j: the j-th entry from there is the run's, up to the next one that begins another
+        const uint32_t next = begins >> first & ~1u;
+        const uint32_t members = valid >> first & 0xffffu & ((next & (0u - next)) - 1u);
+        const int len = 32 - __clz(members);
         const int64_t slot0 = __shfl_sync(kFull, slot, first);
+        // lane j: where the j-th entry's slot lies in its block
+        const int offset = __shfl_sync(kFull, static_cast<int>(slot) & (kBlockTokens - 1), (first + lane) & 31);
         // The values, then the keys; the keys' first tokens are loaded with the
         // values' (a decode has no others), the rest only when the values'
         // registers are free.
@@ -158,9 +179,8 @@ __global__ void __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) cache8_st
             old[0] = *sp[0];
             old[1] = *sp[1];
         }
-        // offsets that the run takes; lane's tokens' own
-        const bool member = lane >= first && lane < first + len;
-        const uint32_t taken = __reduce_or_sync(kFull, member ? 1u << (slot & (kBlockTokens - 1)) : 0u);
+        // offsets that the run takes
+        const uint32_t taken = __reduce_or_sync(kFull, members >> lane & 1u ? 1u << offset : 0u);
         uint32_t poison = 0u;       // tokens of the run with an element that is not finite
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
@@ -168,6 +188,11 @@ __global__ void __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) cache8_st
             in[0] = i == 0 ? front[0] : front[1];
 #pragma unroll
             for (int p = 1; p < PASSES; ++p) in[p] = load(i, p);
+            if ((members & (members + 1u)) != 0u) {     // tokens between the run's that are skipped
+#pragma unroll
+                for (int p = 0; p < PASSES; ++p)
+                    if (!(members >> (p * TP + sub) & 1u)) in[p] = make_uint4(0u, 0u, 0u, 0u);
+            }
             uint32_t m = 0u;
 #pragma unroll
             for (int p = 0; p < PASSES; ++p)
@@ -214,9 +239,9 @@ __global__ void __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) cache8_st
             for (int p = 0; p < PASSES; ++p) {
                 if (p * TP >= len) break;
                 const int j = p * TP + sub;
-                const int at = static_cast<int>(__shfl_sync(kFull, slot, min(first + j, 31))) & (kBlockTokens - 1);
+                const int at = __shfl_sync(kFull, offset, j);
                 const uint2 c = codes8<E>(in[p], f);
-                if (j < len) *reinterpret_cast<uint2*>(block + at * D + chunk * 8) = c;
+                if (members >> j & 1u) *reinterpret_cast<uint2*>(block + at * D + chunk * 8) = c;
             }
             if (lane == 0) *(i == 0 ? sp[0] : sp[1]) = static_cast<uint8_t>(e);
         }
