@@ -1,5 +1,6 @@
 """The FP8 cache's store where the tokens of a block are interrupted by skipped
-entries of the slot map: codes and scales byte for byte the plain reference's."""
+entries of the slot map, and where a warp looks after several of them: codes and
+scales byte for byte the plain reference's."""
 import numpy as np
 import pytest
 import torch
@@ -45,6 +46,27 @@ def test_prompts_and_decodes_with_holes(rmsq_gpu, n, h, D, share):
     pages = sum(-(-(c + m) // 64) for c, m in lens) + 2
     slots = _holes(rng, kv._requests(rng, pages, 64, lens), share)
     kv._check(rmsq_gpu, *kv._cache(rng, pages, h, D, 64), kv._kv(rng, n, h, D, "bf16"), kv._kv(rng, n, h, D, "bf16"), slots)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n, h", [(1100, 1), (2500, 8), (5000, 8), (9000, 8), (4200, 32)])
+def test_several_runs_of_a_warp(rmsq_gpu, n, h, D, dtype):
+    """The same sizes for every head length and type: prompts, decodes side by side, and
+    tokens that are not finite in runs that share a warp with others."""
+    rng = np.random.default_rng(n + D)
+    lens = [(9, n // 2)] + [(i % 31, 1 + i % 3) for i in range(60)]
+    lens.append((3, n - sum(m for _, m in lens)))
+    pages = sum(-(-(c + m) // 32) for c, m in lens) + 2
+    slots = kv._requests(rng, pages, 32, lens)
+    k, v = kv._kv(rng, n, h, D, dtype), kv._kv(rng, n, h, D, dtype)
+    odd = rng.choice(n, 40, replace=False)
+    odd[:20] = n // 2 + np.arange(20) * 3                   # among the short requests
+    for i, t in enumerate(odd):
+        x = (k, v)[i % 2]
+        x[t, rng.integers(h), rng.integers(D)] = (float("nan"), float("inf"), -float("inf"))[i % 3]
+    k[odd[0]] = float("nan")
+    kv._check(rmsq_gpu, *kv._cache(rng, pages, h, D, 32), k, v, slots)
 
 
 def test_a_store_with_holes_gives_the_same_every_time(rmsq_gpu):
