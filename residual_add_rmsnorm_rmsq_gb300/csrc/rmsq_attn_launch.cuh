@@ -14,7 +14,9 @@
 
 namespace rmsq {
 
-inline cudaError_t take_fault_of_unit(unsigned int* out) {
+// Reads and clears this unit's fault flag.  Static as the flag is: one copy for all
+// units would read one unit's.
+static cudaError_t take_fault_of_unit(unsigned int* out) {
     const unsigned int zero = 0;
     cudaError_t e = cudaMemcpyFromSymbol(out, g_prompt_fault, sizeof(unsigned int));
     if (e == cudaSuccess && *out) e = cudaMemcpyToSymbol(g_prompt_fault, &zero, sizeof(zero));

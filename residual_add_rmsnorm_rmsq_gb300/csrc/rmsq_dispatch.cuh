@@ -426,8 +426,9 @@ cudaError_t launch_nvfp4_dynamic(const LaunchArgs& la, void* workspace, float* o
     return launch_kernel(fn, dim3((unsigned)grid), dim3(256), params, 0, stream);
 }
 
-// Reads and clears this unit's pipeline fault flag (current device).
-inline cudaError_t take_pipe_fault(unsigned int* out) {
+// Reads and clears this unit's pipeline fault flag (current device).  Static as the
+// flag is: one copy for all units would read one unit's.
+static cudaError_t take_pipe_fault(unsigned int* out) {
     unsigned int zero = 0;
     cudaError_t e = cudaMemcpyFromSymbol(out, g_pipe_fault, sizeof(unsigned int));
     if (e == cudaSuccess) e = cudaMemcpyToSymbol(g_pipe_fault, &zero, sizeof(unsigned int));
