@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(256, D == 64 ? 4 : D == 128 ? 3 : 2) cache8_st
     int64_t before = __shfl_up_sync(kFull, slot, 1);
     if (__any_sync(kFull, slot < 0 && base - 1 + lane >= 0 && base - 1 + lane < a.n)) {
         // something is skipped: the one before may be further off, or before these
-        const int64_t prior = lane < kBlockTokens ? entry(base - kBlockTokens + lane) : -1;
+        const int64_t prior = (valid & 1u) == 0u && lane < kBlockTokens ? entry(base - kBlockTokens + lane) : -1;
         const uint32_t below = valid & ((1u << lane) - 1u), valid_prior = __ballot_sync(kFull, prior >= 0);
         const int last = 31 - __clz(below), last_prior = 31 - __clz(valid_prior);       // -1: none
         const int64_t near = __shfl_sync(kFull, slot, max(last, 0)), far = __shfl_sync(kFull, prior, max(last_prior, 0));

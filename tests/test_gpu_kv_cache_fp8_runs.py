@@ -37,7 +37,7 @@ def test_runs_with_holes(rmsq_gpu, slots, h, D, page, dtype):
     kv._check(rmsq_gpu, *kv._cache(rng, 64 // page + 1, h, D, page), kv._kv(rng, n, h, D, dtype), kv._kv(rng, n, h, D, dtype), slots)
 
 
-@pytest.mark.parametrize("share", [0.05, 0.5, 0.9])
+@pytest.mark.parametrize("share", [0.05, 0.5])
 @pytest.mark.parametrize("n, h, D", [(700, 2, 128), (3000, 4, 64), (2200, 8, 128), (7000, 4, 128), (5000, 8, 256), (16500, 8, 64)])
 def test_prompts_and_decodes_with_holes(rmsq_gpu, n, h, D, share):
     """Sizes for which a warp looks after 1, 2, 4, 8 and 16 tokens."""
@@ -48,11 +48,10 @@ def test_prompts_and_decodes_with_holes(rmsq_gpu, n, h, D, share):
     kv._check(rmsq_gpu, *kv._cache(rng, pages, h, D, 64), kv._kv(rng, n, h, D, "bf16"), kv._kv(rng, n, h, D, "bf16"), slots)
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("D, dtype", [(64, "fp16"), (128, "bf16"), (256, "fp16")])
 @pytest.mark.parametrize("n, h", [(1100, 1), (2500, 8), (5000, 8), (9000, 8), (4200, 32)])
 def test_several_runs_of_a_warp(rmsq_gpu, n, h, D, dtype):
-    """The same sizes for every head length and type: prompts, decodes side by side, and
+    """The same sizes for every head length: prompts, decodes side by side, and
     tokens that are not finite in runs that share a warp with others."""
     rng = np.random.default_rng(n + D)
     lens = [(9, n // 2)] + [(i % 31, 1 + i % 3) for i in range(60)]
