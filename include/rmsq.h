@@ -568,9 +568,11 @@ int rmsq_kv_cache_load_fp8(const void *cache, const uint8_t *scales, int64_t num
  * among the keys that the query sees, before those are rounded to f16.  With w the
  * weights (sum 1), S_j the value scale of key j's block and U = max w_j S_j over the
  * n keys seen, that rounding puts an output off by at most 2^-11 sum w_j |v_j| +
- * n 2^-30 448 U, whatever the scales of keys that it does not see (fp16 outputs of
- * ordinary values are off by 2.5e-4 of their magnitude where 32-bit weights give
- * 2.1e-4, bf16 ones by 1.7e-3 either way).
+ * n 2^-30 448 U (n 2^-24 448 U for prompts in the pipelined variant, where blocks of
+ * one tile of 128 keys whose value scales are up to 2^7 apart share the largest),
+ * whatever the scales of keys that it does not see.  fp16 outputs of ordinary
+ * values are off by 2.5e-4 of their magnitude where 32-bit weights give 2.1e-4,
+ * bf16 ones by 1.7e-3 either way.
  * A NaN among a key's elements gives NaN in the out and lse of the queries that
  * attend to it, and of no others (the store marks a token whose value has one in
  * this way); NaN codes of values read as 448.  What unwritten slots and scales

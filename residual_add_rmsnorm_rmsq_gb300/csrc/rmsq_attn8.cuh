@@ -52,7 +52,7 @@ struct Step8 {
 struct Fp8Cache {
     static constexpr bool block_scales = true;
     // Weights, times their values' scale, are held as 2^6 at the row's largest (2^5 where
-    // that was taken for larger, see attend32), up to 2^9 more while it lags: moving it
+    // that was taken for larger, see attend32; prompts: see kNarrowValues), up to 2^9 more while it lags: moving it
     // costs a pass over O (it had to move at one step in nine with 2^9 and 2^6, on tokens
     // of uneven strength).  Those below 2^-19 of the largest are subnormal f16, off by
     // 2^-30 of it.
@@ -275,10 +275,12 @@ __device__ __forceinline__ void write_values(unsigned char* dst, const RawValues
 // The f16 pair 2^-down, twice; down at most 15 (2^-15 is a subnormal number).
 __device__ __forceinline__ uint32_t f16_factor(uint32_t down) { return (down < 15u ? (15u - down) << 10 : 0x200u) * 0x10001u; }
 
-// How far apart the scales of a step's blocks may be for every code times its
-// scale relative to the largest to be exact in f16: 2^-9 times 2^-15 is its
-// smallest number.
-constexpr uint32_t kNarrow = 15;
+// How far apart the scales of a step's blocks may be.  Keys: for every code times its
+// scale relative to the largest to be exact in f16, whose smallest number is 2^-9 times
+// 2^-15.  Values: a row's reference takes the step's largest scale for its own key's,
+// so that its weighted values may be held lower than it says by as much: 2^-1 at the
+// largest, and weights that are subnormal in f16 off by 2^-24 of it in place of 2^-30.
+constexpr uint32_t kNarrowKeys = 15, kNarrowValues = 7;
 
 template <int D>
 struct Fp8Prompt : Fp8Cache {
@@ -332,11 +334,11 @@ struct Fp8Prompt : Fp8Cache {
                 const uint32_t kc = cache_scale_code(kraw), vc = cache_scale_code(vraw);
                 bool take = todo >> block & 1u;
                 uint32_t kmost = __reduce_max_sync(kFull, take ? kc : 0u), vmost = __reduce_max_sync(kFull, take ? vc : 0u);
-                if (__any_sync(kFull, take && (kc + kNarrow < kmost || vc + kNarrow < vmost))) {
+                if (__any_sync(kFull, take && (kc + kNarrowKeys < kmost || vc + kNarrowValues < vmost))) {
                     const int first = __ffs(todo) - 1;
                     const uint32_t k0 = __shfl_sync(kFull, kc, first), v0 = __shfl_sync(kFull, vc, first);
-                    // 7 below to 8 above
-                    take = take && kc + 7u >= k0 && kc <= k0 + 8u && vc + 7u >= v0 && vc <= v0 + 8u;
+                    // 7 below to 8 above, 3 below to 4 above
+                    take = take && kc + 7u >= k0 && kc <= k0 + 8u && vc + 3u >= v0 && vc <= v0 + 4u;
                     kmost = __reduce_max_sync(kFull, take ? kc : 0u);
                     vmost = __reduce_max_sync(kFull, take ? vc : 0u);
                 }

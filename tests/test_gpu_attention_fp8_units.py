@@ -15,15 +15,17 @@ pytestmark = pytest.mark.gpu
 VARIANTS = ("direct", "pipelined")
 
 
-def exact(c, window):
+def exact(c, window, variant="direct"):
     """out and lse in float64, and their tolerances.
 
     With w the exact weights (sum 1), S_j the value scale of key j's block, A = sum
     w |v| and U = max w_j S_j, all over the keys that the row sees:
       - the output's rounding, half a step, and 2^-25 (bf16: 2^-134) among subnormal numbers;
       - weights rounded to f16: half a step is 2^-11 of each, 2^-11 A;
-      - they are held so that the largest w_j S_j is 2^5 at least; below 2^-14 f16 has
-        steps of 2^-24: off by 2^-25 each, 2^-30 U, times a code of at most 448;
+      - they are held so that the largest w_j S_j is 2^5 at least, 2^-1 in the kernel for
+        prompts (blocks up to 2^7 apart share the scale of the largest); below 2^-14 f16
+        has steps of 2^-24: off by 2^-25 each, 2^-30 U or 2^-24 U, times a code of at
+        most 448;
       - logits: D + 8 full steps of 2^-23 of scale sum |q||k|, 2^-21 for the exponential,
         2^-22 |logit| for subtraction and factor, and 2^-16 for the exponent of a value
         scale (up to 186, 2^-24 of it, times ln 2, twice) added to them: ds, which moves
@@ -57,7 +59,7 @@ def exact(c, window):
             o = w @ v
             out[t: t + m, h], lse[t: t + m, h] = o, (top + np.log(total))[:, 0]
             tol[t: t + m, h] = eps / 2 * np.abs(o) + A * (2.0 ** -11 + 2 * ds + 2 * cnt * 2.0 ** -23) + \
-                cnt * 2.0 ** -30 * 448 * U + (2.0 ** -25 if eps == 2.0 ** -10 else 2.0 ** -134)
+                cnt * 2.0 ** (-30 if variant == "direct" else -24) * 448 * U + (2.0 ** -25 if eps == 2.0 ** -10 else 2.0 ** -134)
             tol_lse[t: t + m, h] = (ds + cnt * 2.0 ** -23 + 2.0 ** -20)[:, 0] + 2.0 ** -23 * np.abs(lse[t: t + m, h])
         t += m
     return out, lse, tol, tol_lse
@@ -65,7 +67,7 @@ def exact(c, window):
 
 def check(rq, c, *, window=0, variant="direct"):
     out, lse = attn.run(rq, c, window=window, variant=variant)
-    want, w_lse, tol, tol_lse = exact(c, window)
+    want, w_lse, tol, tol_lse = exact(c, window, variant)
     assert (np.abs(want) > tol).mean() > 0.9, "the tolerance would let zeros pass"
     off = np.abs(out.double().cpu().numpy() - want) - tol
     assert not (off > 0).any() and not np.isnan(off).any(), \
@@ -150,6 +152,24 @@ def test_small_values_of_large_weight(rmsq_gpu, D, dtype, apart, variant):
         for b in range(0, (n - 1) // 16 + 1, 2):
             set_block(c, r, b, v_byte=118 + apart, logit=-apart * math.log(2))
     check(rmsq_gpu, c, variant=variant)
+
+
+@pytest.mark.parametrize("variant", VARIANTS)
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("apart", [4, 7, 8, 14])
+def test_large_values_of_little_weight(rmsq_gpu, D, apart, variant):
+    """Every second block's values 2^apart larger and of weight e^-20; where the others'
+    are next to nothing (every second dim) it is these that count."""
+    c = attn.make([150, 70], [300, 200], 4, 2, D, 16, "bf16", seed=D, k_scale=(117, 118), v_scale=(110, 111))
+    near_ones(c)
+    c["codes"][:, 1, :, :, 1::2] = 1
+    rng = np.random.default_rng(apart)
+    for r, n in enumerate(c["seq"]):
+        for b in range(1, (n - 1) // 16 + 1, 2):
+            set_block(c, r, b, v_byte=110 + apart, logit=-20.0)
+            page, at = blocks_of(c, r, b)[0]
+            c["codes"][page, 1, :, 16 * at: 16 * at + 16] = rng.integers(0, 127, (2, 16, D)) | 128 * rng.integers(0, 2, (2, 16, D))
+    check(rmsq_gpu, c, window=32, variant=variant)
 
 
 @pytest.mark.parametrize("variant", VARIANTS)
