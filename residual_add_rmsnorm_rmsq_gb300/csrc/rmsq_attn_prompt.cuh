@@ -627,17 +627,21 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                 finish_half(d, 1);
                 if (!full) mask_half(d, 1, see);
                 top = fmaxf(top, max_half(d, 1));
-                float gain = 0.0f;      // block_scales: log2 of the largest weighted value relative to the row's
-                bool high = top > limit;
+                // block_scales: log2 of the largest weighted value relative to the row's; all of
+                // them far below what f16 holds
+                float gain = 0.0f;
+                bool high = top > limit, low = false;
                 if constexpr (P::block_scales) {
                     top *= tile_k;
                     gain = above<P>({top, tile_v}, peak, f);    // (nothing yet, nothing here: NaN)
                     high = (limit == -INFINITY ? top : gain) > limit;
+                    low = gain < -30.0f - P::p_shift;
                 }
+                float up = 0.0f;        // block_scales: what these weights are raised by
                 float move = 1.0f;      // factor of the row's O
                 bool moved = false;
                 bool done = false;      // the factors are in the logits
-                if (__any_sync(kFull, high)) {
+                if (__any_sync(kFull, high || low)) {
                     // sfull of this step says that the previous P . V has
                     // completed too: O may be rescaled here
                     const Peak was = peak;
@@ -646,11 +650,11 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                     limit = P::block_scales ? P::lazy : lag_limit<P>(peak.m, f);
                     shift = weight_shift<P>(peak.m, f);
                     l = lowered<P>(l, x);
-                    if constexpr (P::block_scales) {
-                        if (high) gain = fminf(gain, 0.0f);     // (relative to where it is now)
-                    }
                     move = exp2_approx(x);
-                    moved = n > 0;
+                    moved = n > 0 && (!P::block_scales || __any_sync(kFull, high));
+                    // They are brought just below what f16 holds, so that the sum of the
+                    // weights, in which they may be the largest, has them whole.
+                    if (low) up = fminf(ceilf(-30.0f - P::p_shift - gain), 100.0f);
                     // A row that is far out comes here at every step (its limit
                     // is passed by any logit); the others subtract zero.
                     if (__any_sync(kFull, is_far(shift))) {
@@ -672,12 +676,9 @@ __global__ void __launch_bounds__(kPromptThreads, 1) attn_prompt_kernel(AttnArgs
                 }
                 if constexpr (P::block_scales) {
                     // Weights times their values' scale, a power of two that only changes
-                    // the addend; the sum of the weights from theirs.  Where all of a step's
-                    // are far below what f16 holds they are brought just below it, so that
-                    // the sum, in which they may be the largest, has them whole.  (The factor
-                    // within the normal numbers: a masked logit times zero would be NaN.)
+                    // the addend; the sum of the weights from theirs.  (The factor within the
+                    // normal numbers: a masked logit times zero would be NaN.)
                     const float fk = done ? f : clamp_factor(f * tile_k);
-                    const float up = fminf(fmaxf(ceilf(-30.0f - P::p_shift - gain), 0.0f), 100.0f);
                     float sum = 0.0f;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) sum += weigh_half(d, h, s_at, fk, shift + (tile_v - peak.e + up));
