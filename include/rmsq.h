@@ -350,7 +350,7 @@ int rmsq_qk_norm_rope_ex(void *qkv, const int64_t *positions, const float *cos_s
  *  cos_sin_cache  as there.  Angle i takes its cos and sin from the row of its
  *                 axis's position.
  *  q_weight, k_weight  as there, or both NULL: no norm, the heads are rotated
- *                 only (eps is then not used).
+ *                 only (eps is then not used, but checked).
  *  section_t, section_h, section_w  number of angles of each axis, together
  *                 head_dim / 2.
  *  interleaved    0: the first section_t angles are the time's, the next

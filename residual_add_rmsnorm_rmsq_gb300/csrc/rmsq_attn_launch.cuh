@@ -92,9 +92,14 @@ cudaError_t launch_prompt(AttnArgs a, cudaStream_t stream) {
 // What the kernels take for 128 keys, in us: the split kernel for 48 (row, kv
 // head) per SM, the prompt kernel for a CTA's 256 rows on every SM.  Measured on
 // 20000 to 100000 keys of the NVFP4 cache: 1.92 to 2.07 and 1.80 to 1.92 (D = 128),
-// 1.16 to 1.27 and 1.44 to 1.52 (64); on 20000 of the FP8 cache 2.21 and 1.97, 1.43
-// and 1.52, with 128 rows per CTA 1.78 and 1.38 (96 queries of 8 x 8 heads of 128 299 us
-// split and 277, 64 204 and 275; of 64 96 191 and 216, 112 220 and 217).
+// 1.16 to 1.27 and 1.44 to 1.52 (64).  The prompt kernel's steps have become shorter
+// since, 1.67 at D = 128: it would be sooner from 96 queries of 8 x 8 heads on (270
+// us split and 261, 104 290 and 261) and is taken from 108.  The border has stayed,
+// and with it what calls in between give to the last bit.
+// On 20000 keys of the FP8 cache 2.31 and 1.98, 1.50 and 1.54, with 128 rows per CTA
+// 1.82 and 1.39, up to 5 % more than the constants; the two kernels meet where these
+// say: 88 queries of 8 x 8 heads of 128 279 us split and 283, 96 304 and 285, heads of
+// 64 104 213 and 218, 112 228 and 216.
 struct Cost {
     double split, prompt, half;
 };
@@ -114,11 +119,11 @@ Cost cost_of(int head_dim) {
 // belong to the split kernel, although it reads the keys once per 16 rows.  Both
 // costs are proportional to the length, which the host does not know, so that
 // what decides is the rows.  Measured with one request of 8 x 8 heads of 128 and
-// 20000 keys, split and prompt: 88 queries 250 and 300 us, 104 292 and 301, 112
-// 313 and 300, 128 355 and 301 (on 2000 keys already 96 queries 49 and 42); heads
-// of 64, 128 queries: 218 and 237.  8 queries of 16 x 8 heads on 50000 keys 124
-// and 675; 8 requests of 50 queries (8 x 4 heads) on 2000 82 and 46; 4 of 200 (4 x
-// 8) on 500 66 and 23.
+// 20000 keys of the NVFP4 cache, split and prompt: 88 queries 249 and 262 us, 96 270
+// and 261, 112 311 and 261, 128 353 and 261 (on 2000 keys 96 queries 48 and 36);
+// heads of 64, 128 queries: 214 and 225.  8 queries of 16 x 8 heads on 50000 keys 123
+// and 603; 8 requests of 50 queries (8 x 4 heads) on 2000 82 and 40; 4 of 200 (4 x
+// 8) on 500 65 and 21.
 //
 // It is not launched where no request can be its: the caller's bound on the
 // queries of a request says so, or, without one, that there are no more than one

@@ -306,7 +306,12 @@ __device__ __forceinline__ float weigh_half(const Row& d, int h, uint32_t s_at, 
 // us for 256 and 128 (FP8, heads of 128): 452 queries of 4 x 4 heads on 1510 keys (60
 // CTAs of 128 rows) 34.6 28.3, 600 of 8 x 4 on 2000 (152) 42.5 36.2, 900 (228) 42.5
 // 55.7, 280 of 8 x 8 on 20000 (144) 309 284, 320 (160) 309 529; heads of 64, 1100 of 4 x
-// 4 on 1500 (140) 25.9 22.7, 320 of 8 x 8 on 20000 240 418.  `shift`: log2 of the rows.
+// 4 on 1500 (140) 25.9 22.7, 320 of 8 x 8 on 20000 240 418 (the taken ones are up to
+// 1.5 % longer now: 28.8, 36.7, 290).  More than 32 requests are scanned by all
+// threads with a barrier each time, for items of 256 rows first; a second scan, for
+// 128, is made only where it is sure to fit, at most twice as many: between half of
+// the card's SMs and all of them a batch of so many requests keeps its 256.  `shift`:
+// log2 of the rows.
 __device__ __forceinline__ int64_t find_item(const AttnArgs& a, int64_t* scratch, int& req, int& shift) {
     const int skip = static_cast<int>(blockIdx.x) / a.kv_heads;
     if (a.requests <= 32) {
